@@ -17,6 +17,7 @@ cu_seqlens int32 [n_max + 1].
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -31,6 +32,9 @@ __all__ = [
     "gdn_chunk_fwd_conv", "gdn_chunk_fwd_conv_timed", "gdn_recurrent_fwd",
     "gdn_recurrent_fwd_timed", "recurrent_gated_delta_rule", "GDN_SEGMENT_MIN_TOKENS", "GDN_FOUR_TILE_MIN_TOKENS",
     "GDN_T_MAX_LIMIT", "GDN_N_MAX_LIMIT", "gdn_chunk_fwd_noalloc", "GDN_NOALLOC_SCRATCH_BYTES",
+    "gdn_attn_config", "make_attn_config", "gdn_attn_workspace_size", "gdn_qk_norm_rope",
+    "gdn_kv_append", "gdn_attn_prefill", "gdn_attn_paged", "rope_inv_freq", "qk_norm_rope",
+    "append_paged_kv", "causal_attention", "paged_attention",
 ]
 
 GDN_BF16 = 0
@@ -49,7 +53,8 @@ EXPORTED_SYMBOLS = ("gdn_nt_max", "gdn_workspace_layout", "gdn_workspace_size",
                     "gdn_chunk_fwd_inter", "gdn_chunk_fwd", "gdn_status_str",
                     "gdn_chunk_fwd_timed", "gdn_front_conv_silu_l2_timed", "gdn_chunk_fwd_conv",
                     "gdn_chunk_fwd_conv_timed", "gdn_recurrent_fwd", "gdn_recurrent_fwd_timed",
-                    "gdn_chunk_fwd_noalloc")
+                    "gdn_chunk_fwd_noalloc", "gdn_attn_workspace_size", "gdn_qk_norm_rope",
+                    "gdn_kv_append", "gdn_attn_prefill", "gdn_attn_paged")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libgdn.so")
@@ -67,6 +72,16 @@ class gdn_workspace_layout_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in
                 ("w16", "q16", "kimg", "uimg", "pimg", "gimg", "table", "order", "seg_sa", "seg_z",
                  "seg_phi", "seg_oh", "total")]
+
+
+class gdn_attn_config(ctypes.Structure):
+    _fields_ = [("t_max", ctypes.c_int32), ("n_max", ctypes.c_int32), ("h", ctypes.c_int32),
+                ("hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float), ("rot_dim", ctypes.c_int32),
+                ("rot_interleaved", ctypes.c_int32), ("rot_scale", ctypes.c_float),
+                ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("tk_max", ctypes.c_int32),
+                ("shared_max", ctypes.c_int32)]
 
 
 class GDNError(RuntimeError):
@@ -107,6 +122,15 @@ def load_library():
     lib.gdn_recurrent_fwd.argtypes = [cfgp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.gdn_chunk_fwd_noalloc.argtypes = [cfgp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.gdn_recurrent_fwd_timed.argtypes = [cfgp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    acfg, i64 = ctypes.POINTER(gdn_attn_config), ctypes.c_int64
+    lib.gdn_attn_workspace_size.argtypes = [acfg, ctypes.POINTER(sz)]
+    lib.gdn_qk_norm_rope.argtypes = [acfg, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.gdn_kv_append.argtypes = [acfg, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.gdn_attn_prefill.argtypes = [acfg, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, sz, vp]
+    lib.gdn_attn_paged.argtypes = [acfg, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    for name in ("gdn_attn_workspace_size", "gdn_qk_norm_rope", "gdn_kv_append",
+                 "gdn_attn_prefill", "gdn_attn_paged"):
+        getattr(lib, name).restype = ctypes.c_int
     for name in ("gdn_workspace_size", "gdn_workspace_layout", "gdn_build_chunk_indices", "gdn_front_conv_silu_l2",
                  "gdn_chunk_fwd_intra", "gdn_chunk_fwd_inter", "gdn_chunk_fwd",
                  "gdn_chunk_fwd_timed", "gdn_front_conv_silu_l2_timed", "gdn_chunk_fwd_conv",
@@ -428,3 +452,303 @@ def chunk_gated_delta_rule(q, k, v, g, beta, cu_seqlens, initial_state=None,
     gdn_chunk_fwd(cfg, q, k, v, g, beta, initial_state, cu_seqlens, chunk_indices, o, hT,
                   workspace)
     return o, hT
+
+
+# ---- softmax-attention layers of a hybrid stack (include/gdn.h, last section)
+
+def make_attn_config(t_max, n_max, h, hkv, d=128, dtype=GDN_BF16, scale=0.0, eps=1e-6, rot_dim=0,
+                     rot_interleaved=False, rot_scale=0.0, page_size=16, n_pages=0, max_pages=0,
+                     tk_max=0, shared_max=0) -> gdn_attn_config:
+    """A gdn_attn_config; dtype is GDN_BF16 / GDN_F16 or the torch dtype."""
+    if isinstance(dtype, torch.dtype):
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"attention dtype {dtype}: bfloat16 or float16 expected")
+        dtype = _TORCH_DTYPE[dtype]
+    return gdn_attn_config(int(t_max), int(n_max), int(h), int(hkv), int(d), int(dtype),
+                           float(scale), float(eps), int(rot_dim), int(bool(rot_interleaved)),
+                           float(rot_scale), int(page_size), int(n_pages), int(max_pages),
+                           int(tk_max), int(shared_max))
+
+
+def gdn_attn_workspace_size(cfg: gdn_attn_config) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().gdn_attn_workspace_size(ctypes.byref(cfg), ctypes.byref(out)),
+           "gdn_attn_workspace_size")
+    return int(out.value)
+
+
+class _Args:
+    """Tensor arguments of one attention call: every check, and the device the
+    call runs on (that of its tensors; all must share it, and the call is made
+    with it current, on its current stream unless `stream` is given)."""
+
+    __slots__ = ("device", "dtype")
+
+    def __init__(self, cfg):
+        self.device = None
+        self.dtype = _GDN_DTYPE.get(cfg.dtype)
+
+    def _on(self, x, name):
+        if not x.is_cuda:
+            raise ValueError(f"{name}: device tensor expected")
+        if self.device is None:
+            self.device = x.device
+        elif x.device != self.device:
+            raise ValueError(f"{name}: on {x.device}, {self.device} expected")
+        return x.data_ptr()
+
+    def dense(self, x, name, elems, dtype, last=None):
+        """Pointer of a contiguous tensor of at least `elems` elements (None and
+        raw pointers pass through)."""
+        if not isinstance(x, torch.Tensor):
+            return x
+        _need(x, name, elems, dtype, last)
+        if not x.is_contiguous():
+            raise ValueError(f"{name}: contiguous tensor expected")
+        return self._on(x, name)
+
+    def rows(self, x, name, tokens, heads, d):
+        """Pointer and row stride of packed rows: [tokens, heads, d] (or [tokens,
+        heads * d]), each token's values in one piece, any distance apart."""
+        if not isinstance(x, torch.Tensor):
+            return x, 0
+        if x.dtype != self.dtype:
+            raise ValueError(f"{name}: dtype {x.dtype}, {self.dtype} expected")
+        shape, stride = x.shape, x.stride()
+        if len(shape) == 3:
+            ok = shape[1] == heads and shape[2] == d and stride[2] == 1 and \
+                (stride[1] == d or heads == 1)
+        else:
+            ok = len(shape) == 2 and shape[1] == heads * d and stride[1] == 1
+        # (a single row's stride says nothing: torch may report any value)
+        if shape[0] > 1 and stride[0] < heads * d:
+            ok = False  # rows that overlap, or one row broadcast
+        if not ok or shape[0] < tokens:
+            raise ValueError(f"{name}: {tuple(shape)} with strides {stride}, [{tokens}, {heads}, "
+                             f"{d}] with every token's row in one piece expected")
+        return self._on(x, name), stride[0] if shape[0] > 1 else 0
+
+    def workspace(self, x, ws_bytes):
+        if not isinstance(x, torch.Tensor):
+            return x, int(ws_bytes)
+        have = x.numel() * x.element_size()
+        if ws_bytes is not None and int(ws_bytes) > have:
+            raise ValueError(f"workspace: {have} bytes, ws_bytes = {int(ws_bytes)}")
+        if not x.is_contiguous():
+            raise ValueError("workspace: contiguous tensor expected")
+        return self._on(x, "workspace"), have if ws_bytes is None else int(ws_bytes)
+
+    def call(self, where, stream, *args):
+        fn = getattr(load_library(), where)
+        dev = self.device
+        if dev is None or dev.index == torch.cuda.current_device():
+            st = fn(*args, _stream(stream))
+        else:
+            with torch.cuda.device(dev):
+                st = fn(*args, _stream(stream))
+        _check(st, where)
+
+
+def _front_args(c, cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens):
+    if not isinstance(qkv, torch.Tensor):
+        p, row = qkv, 0
+    else:
+        p, row = c.rows(qkv, "qkv", cfg.t_max, cfg.h + 2 * cfg.hkv, cfg.d)
+    return (ctypes.byref(cfg), p, row, c.dense(q_w, "q_w", cfg.d, torch.float32),
+            c.dense(k_w, "k_w", cfg.d, torch.float32),
+            c.dense(inv_freq, "inv_freq", cfg.rot_dim // 2, torch.float32),
+            c.dense(cu_seqlens, "cu_seqlens", cfg.n_max + 1, torch.int32),
+            c.dense(kv_lens, "kv_lens", cfg.n_max, torch.int32))
+
+
+def gdn_qk_norm_rope(cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens, q, k, stream=None):
+    """RMS norm of every query and key head and rotation by the token's position.
+    qkv [t_max, (h + 2 hkv) d] may have any row stride (a multiple of 8)."""
+    c = _Args(cfg)
+    a = _front_args(c, cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens)
+    c.call("gdn_qk_norm_rope", stream, *a,
+           c.dense(q, "q", cfg.t_max * cfg.h * cfg.d, c.dtype, cfg.d),
+           c.dense(k, "k", cfg.t_max * cfg.hkv * cfg.d, c.dtype, cfg.d))
+
+
+def _pool(c, cfg, x, name):
+    return c.dense(x, name, cfg.n_pages * cfg.hkv * cfg.page_size * cfg.d, c.dtype, cfg.d)
+
+
+def gdn_kv_append(cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens, block_table, q, k, k_pages,
+                  v_pages, stream=None):
+    """gdn_qk_norm_rope that also writes k and v into the pages of the cache; q and
+    k may be None."""
+    c = _Args(cfg)
+    a = _front_args(c, cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens)
+    c.call("gdn_kv_append", stream, *a,
+           c.dense(block_table, "block_table", cfg.n_max * cfg.max_pages, torch.int32,
+                   cfg.max_pages),
+           c.dense(q, "q", cfg.t_max * cfg.h * cfg.d, c.dtype, cfg.d),
+           c.dense(k, "k", cfg.t_max * cfg.hkv * cfg.d, c.dtype, cfg.d),
+           _pool(c, cfg, k_pages, "k_pages"), _pool(c, cfg, v_pages, "v_pages"))
+
+
+def gdn_attn_prefill(cfg, q, k, v, cu_q, cu_k, o, workspace, ws_bytes=None, stream=None):
+    """Causal attention over packed prompts; q, k, v [tokens, heads, d] may have any
+    row stride (a multiple of 8); cu_k None = cu_q."""
+    c = _Args(cfg)
+    tk = cfg.tk_max or cfg.t_max
+    q, q_row = c.rows(q, "q", cfg.t_max, cfg.h, cfg.d)
+    k, k_row = c.rows(k, "k", tk, cfg.hkv, cfg.d)
+    v, v_row = c.rows(v, "v", tk, cfg.hkv, cfg.d)
+    ws, ws_bytes = c.workspace(workspace, ws_bytes)
+    c.call("gdn_attn_prefill", stream, ctypes.byref(cfg), q, q_row, k, k_row, v, v_row,
+           c.dense(cu_q, "cu_q", cfg.n_max + 1, torch.int32),
+           c.dense(cu_k, "cu_k", cfg.n_max + 1, torch.int32),
+           c.dense(o, "o", cfg.t_max * cfg.h * cfg.d, c.dtype, cfg.d), ws, ws_bytes)
+
+
+def gdn_attn_paged(cfg, q, k_pages, v_pages, cu_seqlens, kv_lens, block_table, shared_len, o,
+                   workspace, ws_bytes=None, stream=None):
+    """Attention of each sequence's new tokens to the pages of the cache; shared_len
+    (int32 [1] on the device, or None) positions lie in the same pages for all."""
+    c = _Args(cfg)
+    q, q_row = c.rows(q, "q", cfg.t_max, cfg.h, cfg.d)
+    ws, ws_bytes = c.workspace(workspace, ws_bytes)
+    c.call("gdn_attn_paged", stream, ctypes.byref(cfg), q, q_row,
+           _pool(c, cfg, k_pages, "k_pages"), _pool(c, cfg, v_pages, "v_pages"),
+           c.dense(cu_seqlens, "cu_seqlens", cfg.n_max + 1, torch.int32),
+           c.dense(kv_lens, "kv_lens", cfg.n_max, torch.int32),
+           c.dense(block_table, "block_table", cfg.n_max * cfg.max_pages, torch.int32,
+                   cfg.max_pages),
+           c.dense(shared_len, "shared_len", 1, torch.int32),
+           c.dense(o, "o", cfg.t_max * cfg.h * cfg.d, c.dtype, cfg.d), ws, ws_bytes)
+
+
+def rope_inv_freq(rot_dim, base=10000.0, factor=1.0, original_len=None, low_turns=1.0,
+                  high_turns=32.0, device=None):
+    """Radians per position of each pair, fp32 [rot_dim / 2]: base^(-2 i / rot_dim).
+
+    factor > 1 stretches positions for contexts `factor` times longer than the
+    model was trained on: without original_len every frequency is divided by it;
+    with original_len (the trained length) a pair that makes at least high_turns
+    turns over it keeps its frequency, one that makes at most low_turns is
+    divided, and those between are blended linearly in the number of turns.
+    """
+    if rot_dim < 0 or rot_dim % 2:
+        raise ValueError(f"rot_dim {rot_dim}: an even number expected")
+    if not factor > 0 or not base > 0:
+        raise ValueError(f"base {base}, factor {factor}: positive numbers expected")
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    f = float(base) ** (-2.0 * i / max(rot_dim, 1))
+    if original_len is None:
+        f = f / factor
+    else:
+        if not high_turns > low_turns:
+            raise ValueError(f"high_turns {high_turns}: more than low_turns {low_turns} expected")
+        turns = original_len * f / (2.0 * math.pi)
+        keep = ((turns - low_turns) / (high_turns - low_turns)).clamp(0.0, 1.0)
+        f = f * keep + f / factor * (1.0 - keep)
+    return f.float().to(device) if device is not None else f.float()
+
+
+def _packed_qkv(qkv, heads, kv_heads):
+    if qkv.dim() != 2 or qkv.shape[1] % (heads + 2 * kv_heads):
+        raise ValueError(f"qkv [T, ({heads} + 2 * {kv_heads}) * d] expected: {tuple(qkv.shape)}")
+    return qkv.shape[0], qkv.shape[1] // (heads + 2 * kv_heads)
+
+
+def qk_norm_rope(qkv, heads, kv_heads, cu_seqlens, q_weight=None, k_weight=None, inv_freq=None,
+                 kv_lens=None, eps=1e-6, interleaved=False, rot_scale=1.0):
+    """Allocate outputs with torch and run gdn_qk_norm_rope on the current stream.
+
+    qkv [T, (heads + 2 kv_heads) d] bf16 or fp16; weights fp32 [d] or None (no
+    norm); inv_freq fp32 [rot_dim / 2] or None (no rotation). Returns (q [T,
+    heads, d], k [T, kv_heads, d]); v is qkv's last kv_heads d columns."""
+    T, d = _packed_qkv(qkv, heads, kv_heads)
+    cfg = make_attn_config(T, cu_seqlens.numel() - 1, heads, kv_heads, d, qkv.dtype, eps=eps,
+                           rot_dim=0 if inv_freq is None else 2 * inv_freq.numel(),
+                           rot_interleaved=interleaved, rot_scale=rot_scale)
+    q = torch.empty((T, heads, d), dtype=qkv.dtype, device=qkv.device)
+    k = torch.empty((T, kv_heads, d), dtype=qkv.dtype, device=qkv.device)
+    gdn_qk_norm_rope(cfg, qkv, q_weight, k_weight, inv_freq, cu_seqlens, kv_lens, q, k)
+    return q, k
+
+
+def _pages(k_pages, v_pages, block_table):
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or block_table.dim() != 2:
+        raise ValueError(f"k_pages, v_pages [pages, kv_heads, page_size, d] and block_table [N, "
+                         f"columns] expected: {tuple(k_pages.shape)}, {tuple(v_pages.shape)}, "
+                         f"{tuple(block_table.shape)}")
+    return k_pages.shape
+
+
+def append_paged_kv(qkv, heads, cu_seqlens, kv_lens, block_table, k_pages, v_pages, q_weight=None,
+                    k_weight=None, inv_freq=None, eps=1e-6, interleaved=False, rot_scale=1.0,
+                    output_k=False):
+    """Run gdn_kv_append on the current stream: q and k normed and rotated, k and v
+    written into the cache pages of their positions (kv_lens: tokens of each
+    sequence in all, these included). Returns q [T, heads, d], or (q, k) with
+    output_k."""
+    pages, hkv, size, d = _pages(k_pages, v_pages, block_table)
+    T, dq = _packed_qkv(qkv, heads, hkv)
+    if dq != d:
+        raise ValueError(f"qkv: head dim {dq}, {d} expected")
+    cfg = make_attn_config(T, cu_seqlens.numel() - 1, heads, hkv, d, qkv.dtype, eps=eps,
+                           rot_dim=0 if inv_freq is None else 2 * inv_freq.numel(),
+                           rot_interleaved=interleaved, rot_scale=rot_scale, page_size=size,
+                           n_pages=pages, max_pages=block_table.shape[1])
+    q = torch.empty((T, heads, d), dtype=qkv.dtype, device=qkv.device)
+    k = torch.empty((T, hkv, d), dtype=qkv.dtype, device=qkv.device) if output_k else None
+    gdn_kv_append(cfg, qkv, q_weight, k_weight, inv_freq, cu_seqlens, kv_lens, block_table, q, k,
+                  k_pages, v_pages)
+    return (q, k) if output_k else q
+
+
+def _attn_workspace(cfg, device, workspace):
+    if workspace is not None:
+        return workspace
+    with torch.cuda.device(device):
+        return torch.empty(gdn_attn_workspace_size(cfg), dtype=torch.uint8, device=device)
+
+
+def causal_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, scale=None, workspace=None):
+    """Allocate the output with torch and run gdn_attn_prefill on the current stream.
+
+    q [T, heads, d], k and v [Tk, kv_heads, d], bf16 or fp16, rows of any stride;
+    the queries are the last tokens of their keys (cu_seqlens_k None: the same
+    tokens). Returns o [T, heads, d]; rows behind the last sequence are not
+    written."""
+    if q.dim() != 3 or k.dim() != 3 or v.shape != k.shape or k.shape[2] != q.shape[2] or \
+            not q.dtype == k.dtype == v.dtype:
+        raise ValueError(f"q [T, heads, d] and k, v [Tk, kv_heads, d] of one dtype expected: "
+                         f"{tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
+    if cu_seqlens_k is not None and cu_seqlens_k.numel() != cu_seqlens.numel():
+        raise ValueError("cu_seqlens and cu_seqlens_k: the same number of sequences expected")
+    T, H, d = q.shape
+    if cu_seqlens_k is None and k.shape[0] < T:
+        raise ValueError(f"k, v: {k.shape[0]} rows, at least {T} expected")
+    cfg = make_attn_config(T, cu_seqlens.numel() - 1, H, k.shape[1], d, q.dtype, scale or 0.0,
+                           tk_max=k.shape[0])
+    workspace = _attn_workspace(cfg, q.device, workspace)
+    o = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+    gdn_attn_prefill(cfg, q, k, v, cu_seqlens, cu_seqlens_k, o, workspace)
+    return o
+
+
+def paged_attention(q, k_pages, v_pages, cu_seqlens, kv_lens, block_table, shared_len=None,
+                    scale=None, workspace=None):
+    """Allocate the output with torch and run gdn_attn_paged on the current stream.
+
+    q [T, heads, d]: the new tokens of every sequence (one each when decoding),
+    whose keys and values the cache already holds; shared_len: int32 [1] on the
+    device, positions that lie in the same pages for the whole batch (read once
+    for all). Returns o [T, heads, d]."""
+    pages, hkv, size, d = _pages(k_pages, v_pages, block_table)
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError(f"q [T, heads, {d}] expected: {tuple(q.shape)}")
+    cols = block_table.shape[1]
+    cfg = make_attn_config(q.shape[0], cu_seqlens.numel() - 1, q.shape[1], hkv, d, q.dtype,
+                           scale or 0.0, page_size=size, n_pages=pages, max_pages=cols,
+                           shared_max=0 if shared_len is None else cols * size)
+    workspace = _attn_workspace(cfg, q.device, workspace)
+    o = torch.empty((q.shape[0], q.shape[1], d), dtype=q.dtype, device=q.device)
+    gdn_attn_paged(cfg, q, k_pages, v_pages, cu_seqlens, kv_lens, block_table, shared_len, o,
+                   workspace)
+    return o

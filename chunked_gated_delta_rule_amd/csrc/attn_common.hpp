@@ -1,0 +1,78 @@
+// Device-side building blocks shared by the softmax-attention kernels: 16-bit
+// element types, packing, cross-lane steps, and the search of a packed batch.
+#pragma once
+
+#include "gdn_common.hpp"
+
+namespace gdn {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma32(f16x8 a, f16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+// The two 16-bit element types: the MFMA operand vector, the rounding of a
+// pair (to nearest even), and the value of the low and high half of a word.
+template <typename T>
+struct Elem;
+template <>
+struct Elem<__bf16> {
+  typedef bf16x8 vec8;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+  }
+  static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+  static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+};
+template <>
+struct Elem<_Float16> {
+  typedef f16x8 vec8;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack_f16(a, b); }
+  static __device__ __forceinline__ float lo(uint32_t w) {
+    return static_cast<float>(__builtin_bit_cast(f16x2, w)[0]);
+  }
+  static __device__ __forceinline__ float hi(uint32_t w) {
+    return static_cast<float>(__builtin_bit_cast(f16x2, w)[1]);
+  }
+};
+
+// The value of lane l ^ 16 / l ^ 32.
+__device__ __forceinline__ float swap16(float x) { return __shfl_xor(x, 16, 64); }
+__device__ __forceinline__ float swap32(float x) { return __shfl_xor(x, 32, 64); }
+
+constexpr float kNegInf = -__builtin_inff();
+
+// Softmax statistics move only when a row's maximum (log2 scale) has grown by
+// more than this: the weights then stay below 2^8, exact enough in 16 bits and
+// in the fp32 sums, and the output sums are rescaled a few times per row only.
+constexpr float kRescaleLog2 = 8.f;
+
+// Last s in [0, n) with key(s) <= x, for a non-decreasing key with key(0) <= x,
+// by one wave: 64 probes per level (n <= 16384: at most three levels). With a
+// key that is not sorted the answer is some s in [0, n).
+template <typename F>
+__device__ __forceinline__ int wave_search(int n, int x, int lane, F key) {
+  int lo = 0, len = n;
+  while (len > 1) {
+    const int step = (len + 63) / 64;
+    const int at = lane * step;
+    const bool in = at < len && key(lo + at) <= x;
+    const int hits = max(__popcll(__ballot(in)), 1);
+    const int skip = (hits - 1) * step;
+    lo += skip;
+    len = min(step, len - skip);
+  }
+  return lo;
+}
+
+// Sequence of packed row t (t < cu[n_max]).
+__device__ __forceinline__ int seq_of_row(const int32_t *__restrict__ cu, int n_max, int t_max,
+                                          int t, int lane) {
+  return wave_search(n_max, t, lane, [&](int s) { return cu_at(cu, s, t_max); });
+}
+
+}  // namespace gdn

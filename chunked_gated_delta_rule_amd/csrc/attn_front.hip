@@ -1,0 +1,215 @@
+// Front of a softmax-attention layer: RMS norm of every query and key head,
+// rotation by the token's position, and (gdn_kv_append) the write of k and v
+// into the pages of the cache, in one pass over the packed q | k | v rows.
+//
+//   x' = x / sqrt(mean(x^2) + eps) * w
+//   (a, b) -> s (a cos t - b sin t, b cos t + a sin t),  t = position * inv_freq[i]
+//
+// HBM-bound: each row is read once and written once. One 256-thread work-group
+// per token; D / 8 lanes own a head, eight channels each, and the work-group
+// walks the heads 2048 / D at a time. The channels of a lane are chosen so that
+// both members of its pairs are its own (half layout: four channels and the
+// four rot_dim / 2 further; interleaved: eight in a row), so the rotation needs
+// no other lane. cos and sin of the token's rot_dim / 2 angles are formed once
+// per work-group, in LDS, while the first heads' loads are in flight.
+#include "attn_common.hpp"
+#include "attn_launch.hpp"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kFrontThreads = 256;
+
+// How a lane's eight channels are placed: pairs inside the lane (half layout
+// with rot_dim a multiple of 8, or interleaved), or (half layout with any other
+// rot_dim) eight channels in a row whose partners are read one by one.
+enum class Pairs { kHalf = 0, kInterleaved = 1, kHalfOdd = 2 };
+
+// 1 / (2 pi), for angles counted in turns.
+constexpr double kInvTwoPi = 0.15915494309189533577;
+
+template <typename T>
+__device__ __forceinline__ void unpack4(const u32x2 &w, float *f) {
+  f[0] = Elem<T>::lo(w[0]);
+  f[1] = Elem<T>::hi(w[0]);
+  f[2] = Elem<T>::lo(w[1]);
+  f[3] = Elem<T>::hi(w[1]);
+}
+
+template <typename T, int D, Pairs kPairs, bool kCache>
+__global__ __launch_bounds__(kFrontThreads) void attn_front_kernel(FrontArgs a) {
+  constexpr int kLanes = D / 8;                    // lanes per head
+  constexpr int kHeads = kFrontThreads / kLanes;   // heads per pass
+  __shared__ __attribute__((aligned(16))) float cs[D / 2], sn[D / 2];
+  const int t = flat_block();
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int li = tid % kLanes;
+  if (t >= cu_at(a.cu, a.n_max, a.t_max)) return;
+  const int half = a.rot_dim >> 1;
+
+  // this lane's channels: c0 .. c0 + 3 and c1 .. c1 + 3
+  int c0 = 8 * li, c1 = c0 + 4;
+  bool turned = c0 < a.rot_dim;
+  if constexpr (kPairs == Pairs::kHalf) {
+    turned = li < half / 4;
+    c0 = turned ? 4 * li : a.rot_dim + 8 * (li - half / 4);
+    c1 = turned ? half + 4 * li : c0 + 4;
+  }
+  const int heads = a.h + (kCache ? 2 : 1) * a.hkv;
+  const T *row = static_cast<const T *>(a.qkv) + t * a.qkv_row;
+  const int first = a.q ? 0 : a.h;
+  int hd = first + tid / kLanes;
+  u32x2 x0{0u, 0u}, x1{0u, 0u};
+  auto load = [&](int head) __attribute__((always_inline)) {
+    if (head < heads) {
+      x0 = *reinterpret_cast<const u32x2 *>(row + head * D + c0);
+      x1 = *reinterpret_cast<const u32x2 *>(row + head * D + c1);
+    }
+  };
+  load(hd);
+
+  const int s = seq_of_row(a.cu, a.n_max, a.t_max, t, lane);
+  const int bos = cu_at(a.cu, s, a.t_max), eos = cu_end(a.cu, s, bos, a.t_max);
+  // kv_lens is the caller's: the position is formed in 64 bits
+  const int64_t pos = a.kv_lens ? (int64_t)a.kv_lens[s] - (eos - t) : t - bos;
+  for (int i = tid; i < half; i += kFrontThreads) {
+    const double turns = (double)pos * (double)a.inv_freq[i] * kInvTwoPi;
+    const float f = (float)(turns - __builtin_rint(turns));  // -1/2 .. 1/2
+    cs[i] = a.rot_scale * __builtin_amdgcn_cosf(f);  // cos(2 pi f)
+    sn[i] = a.rot_scale * __builtin_amdgcn_sinf(f);
+  }
+  int64_t slot = -1;  // the token's row in a page pool of one head
+  if constexpr (kCache) {
+    const int64_t col = pos >> a.page_shift;
+    if (pos >= 0 && col < a.max_pages) {
+      const int page = a.table[(int64_t)s * a.max_pages + col];
+      if (page >= 0 && page < a.n_pages)
+        slot = (((int64_t)page * a.hkv) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+    }
+  }
+  float wq[8], wk[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int c = j < 4 ? c0 + j : c1 + j - 4;
+    wq[j] = a.q_w ? a.q_w[c] : 1.f;
+    wk[j] = a.k_w ? a.k_w[c] : 1.f;
+  }
+  __syncthreads();
+
+  for (int base = first; base < heads; base += kHeads) {
+    const bool in = hd < heads;
+    const u32x2 y0 = x0, y1 = x1;
+    const int head = hd;
+    hd += kHeads;
+    load(hd);
+    const bool is_q = head < a.h, is_v = head >= a.h + a.hkv;
+    const bool norm = (is_q ? a.q_w : a.k_w) != nullptr && !is_v;
+    float x[8];
+    unpack4<T>(y0, x);
+    unpack4<T>(y1, x + 4);
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+    ss = sum16(ss);
+    if constexpr (kLanes == 32) ss += swap16(ss);
+    const float r = norm ? 1.f / sqrtf(ss * (1.f / D) + a.eps) : 1.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] *= r * (is_q ? wq[j] : wk[j]);
+    if (!is_v) {
+      if constexpr (kPairs == Pairs::kHalf) {
+        if (turned) {
+          const f32x4 c = *reinterpret_cast<const f32x4 *>(cs + c0);
+          const f32x4 d = *reinterpret_cast<const f32x4 *>(sn + c0);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float u = x[j], w = x[j + 4];
+            x[j] = u * c[j] - w * d[j];
+            x[j + 4] = w * c[j] + u * d[j];
+          }
+        }
+      } else if constexpr (kPairs == Pairs::kInterleaved) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (c0 + 2 * j < a.rot_dim) {
+            const float c = cs[(c0 >> 1) + j], d = sn[(c0 >> 1) + j];
+            const float u = x[2 * j], w = x[2 * j + 1];
+            x[2 * j] = u * c - w * d;
+            x[2 * j + 1] = w * c + u * d;
+          }
+        }
+      } else {
+        if (in) {
+          const float *wp = is_q ? a.q_w : a.k_w;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int c = c0 + j;
+            if (c < a.rot_dim) {
+              const bool low = c < half;
+              const int p = low ? c + half : c - half, i = low ? c : p;
+              const float y = static_cast<float>(row[head * D + p]) * r * (wp ? wp[p] : 1.f);
+              x[j] = x[j] * cs[i] + (low ? -y : y) * sn[i];
+            }
+          }
+        }
+      }
+    }
+    if (!in) continue;
+    // v is copied as it is, bit for bit
+    const u32x2 z0 = is_v ? y0 : u32x2{Elem<T>::pack(x[0], x[1]), Elem<T>::pack(x[2], x[3])};
+    const u32x2 z1 = is_v ? y1 : u32x2{Elem<T>::pack(x[4], x[5]), Elem<T>::pack(x[6], x[7])};
+    auto store = [&](T *p) __attribute__((always_inline)) {
+      *reinterpret_cast<u32x2 *>(p + c0) = z0;
+      *reinterpret_cast<u32x2 *>(p + c1) = z1;
+    };
+    if (is_q) {
+      store(static_cast<T *>(a.q) + ((int64_t)t * a.h + head) * D);
+      continue;
+    }
+    const int kh = head - a.h - (is_v ? a.hkv : 0);
+    if (!is_v && a.k) store(static_cast<T *>(a.k) + ((int64_t)t * a.hkv + kh) * D);
+    if constexpr (kCache) {
+      if (slot >= 0)
+        store(static_cast<T *>(is_v ? a.v_pages : a.k_pages) +
+              (slot + ((int64_t)kh << a.page_shift)) * D);
+    }
+  }
+}
+
+template <typename T, int D, bool kCache>
+void run(const FrontArgs &a, bool interleaved, dim3 grid, hipStream_t stream) {
+  const dim3 block(kFrontThreads);
+  if (interleaved)
+    hipLaunchKernelGGL((attn_front_kernel<T, D, Pairs::kInterleaved, kCache>), grid, block, 0,
+                       stream, a);
+  else if (a.rot_dim % 8 == 0)
+    hipLaunchKernelGGL((attn_front_kernel<T, D, Pairs::kHalf, kCache>), grid, block, 0, stream, a);
+  else
+    hipLaunchKernelGGL((attn_front_kernel<T, D, Pairs::kHalfOdd, kCache>), grid, block, 0, stream,
+                       a);
+}
+
+template <typename T>
+void run_of(const FrontArgs &a, int d, bool interleaved, dim3 grid, hipStream_t stream) {
+  if (d == 128)
+    a.k_pages ? run<T, 128, true>(a, interleaved, grid, stream)
+              : run<T, 128, false>(a, interleaved, grid, stream);
+  else
+    a.k_pages ? run<T, 256, true>(a, interleaved, grid, stream)
+              : run<T, 256, false>(a, interleaved, grid, stream);
+}
+
+}  // namespace
+
+hipError_t launch_attn_front(const gdn_attn_config *cfg, FrontArgs a, hipStream_t stream) {
+  if (cfg->t_max == 0) return hipSuccess;
+  dim3 grid;
+  if (!flat_grid(cfg->t_max, kFrontThreads, grid)) return hipErrorInvalidValue;
+  if (cfg->dtype == GDN_BF16)
+    run_of<__bf16>(a, cfg->d, cfg->rot_interleaved != 0, grid, stream);
+  else
+    run_of<_Float16>(a, cfg->d, cfg->rot_interleaved != 0, grid, stream);
+  return hipGetLastError();
+}
+
+}  // namespace gdn

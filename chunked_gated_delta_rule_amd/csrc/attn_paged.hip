@@ -1,0 +1,567 @@
+// Attention of a few new tokens per sequence to a paged cache (decode, verify),
+// with the pages that the whole batch shares read once.
+//
+// The rows of an item are the new tokens of one sequence times the query heads
+// of one key / value head (of every sequence, for the shared prefix), 16 kRT at
+// a time; an item's keys are cut into units of 128. HBM-bound on the keys and
+// values: each unit is read once per item.
+//
+//  * Work: all units of the batch in one line (key head, prefix, sequences in
+//    order, row tiles, units), cut into equal runs, one per work-group of a
+//    fixed grid. So lengths need not be known on the host, a single long
+//    sequence fills the device, and a ragged batch is balanced to one unit. A
+//    run covers the end of one item, whole items, and the start of another.
+//    Whole items are written at once; the others leave (maximum, sum, output
+//    sum) in the workspace, at most two per work-group, and the join kernel
+//    adds them up, row by row.
+//  * Each of the four waves takes 32 keys of a unit on its own, with a running
+//    maximum and sum of its own; the waves meet once per item, in LDS. There is
+//    no barrier in the loop over keys.
+//  * K and V go from the pages to registers in 16-byte loads, in the layout of
+//    the matrix instructions: scores S^T = K Q^T (a lane's column is one row),
+//    O^T += V^T P^T. K's fragment is 8 consecutive dims of one key, as stored.
+//    For V a lane loads 8 keys x 8 dims (each instruction four whole rows of
+//    256 bytes) and transposes the block inside its registers, one byte permute
+//    per pair of values; fragment j then has the dims 8 c + j. The keys of a
+//    lane are the ones its scores hold, so weights never leave the lane.
+#include "attn_common.hpp"
+#include "attn_launch.hpp"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kUnit = 128;  // keys per unit: 32 per wave
+
+// Items of the batch, the same in the main kernel and in the join.
+struct Plan {
+  int prefix;       // shared positions: whole pages, before every new token
+  int tokens;       // packed rows
+  int first;        // a sequence with new tokens (its table leads to the prefix)
+  int per_wg;       // units per work-group
+  int64_t total;    // units
+  int64_t head;     // units per key head
+  int64_t lead;     // of these, the prefix's
+};
+// workspace: the plan, then units before each sequence (int64 [n_max + 1])
+constexpr int kPlanInts = 16;
+
+__device__ __forceinline__ int units_of(int keys) { return (keys + kUnit - 1) / kUnit; }
+
+// New tokens and keys of sequence s.
+struct Seq {
+  int bos, n, kv;
+};
+__device__ __forceinline__ Seq seq_at(const PagedArgs &a, int s) {
+  Seq q;
+  q.bos = cu_at(a.cu, s, a.t_max);
+  q.n = cu_end(a.cu, s, q.bos, a.t_max) - q.bos;
+  const int64_t room = (int64_t)a.max_pages << a.page_shift;  // positions the table reaches
+  const int kv = max(a.kv_lens[s], 0);
+  q.kv = kv < room ? kv : (int)room;
+  return q;
+}
+
+template <int kRT>
+__device__ __forceinline__ int row_tiles(int64_t rows) {
+  return (int)((rows + 16 * kRT - 1) / (16 * kRT));
+}
+
+// The work of one wave-set on one item's run of units, and what it leaves.
+template <typename T, int D, int kRT>
+__global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_paged_kernel(PagedArgs a) {
+  typedef typename Elem<T>::vec8 vec8;
+  constexpr int kRows = 16 * kRT;
+  constexpr int kDC = D / 128;   // 128-dim blocks
+  constexpr int kPad = D + 4;    // floats per row of the meeting place
+  __shared__ __attribute__((aligned(16))) T qs[kRows][D + 8];
+  __shared__ __attribute__((aligned(16))) float os[4][16][kPad];
+  __shared__ float wm[4][kRows], wl[4][kRows];
+  __shared__ int64_t scan64[5];
+  __shared__ int scan32[4][3];
+
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int c = lane & 15, g = lane >> 4;
+  const int G = a.h / a.hkv;
+  // consecutive runs on one XCD: its L2 then holds the rows that they share
+  const int wg = (blockIdx.x & 7) * ((a.grid + 7) / 8) + (blockIdx.x >> 3);
+  if (wg >= a.grid) return;
+
+  // ---- the plan: shared prefix, units of every sequence
+  const int tokens = cu_at(a.cu, a.n_max, a.t_max);
+  const int per = (a.n_max + 255) / 256;
+  const int s0 = min(tid * per, a.n_max), s1 = min(s0 + per, a.n_max);
+  int prefix = 0, first = a.n_max;
+  if (a.shared_len && a.shared_max > 0) {
+    int least = min(max(a.shared_len[0], 0), a.shared_max);
+    for (int s = s0; s < s1; ++s) {
+      const Seq q = seq_at(a, s);
+      if (q.n > 0) {
+        least = min(least, q.kv - q.n);
+        first = min(first, s);
+      }
+    }
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      least = min(least, __shfl_xor(least, off, 64));
+      first = min(first, __shfl_xor(first, off, 64));
+    }
+    if (lane == 0) scan32[w][0] = least, scan32[w][1] = first;
+    __syncthreads();
+    for (int i = 0; i < 4; ++i) {
+      least = min(least, scan32[i][0]);
+      first = min(first, scan32[i][1]);
+    }
+    prefix = first < a.n_max ? max(least, 0) >> a.page_shift << a.page_shift : 0;
+  }
+  auto units_in = [&](int s) __attribute__((always_inline)) -> int64_t {
+    const Seq q = seq_at(a, s);
+    return q.n > 0 && q.kv > prefix
+               ? (int64_t)row_tiles<kRT>((int64_t)q.n * G) * units_of(q.kv - prefix)
+               : 0;
+  };
+  int64_t mine = 0;
+  for (int s = s0; s < s1; ++s) mine += units_in(s);
+  int64_t incl = mine;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int64_t y = __shfl_up(incl, off, 64);
+    if (lane >= off) incl += y;
+  }
+  if (lane == 63) scan64[w] = incl;
+  __syncthreads();
+  int64_t before = incl - mine, seqs = 0;
+  for (int i = 0; i < 4; ++i) {
+    if (i < w) before += scan64[i];
+    seqs += scan64[i];
+  }
+  const int64_t lead = prefix > 0 ? (int64_t)row_tiles<kRT>((int64_t)tokens * G) * units_of(prefix) : 0;
+  const int64_t per_head = lead + seqs, total = per_head * a.hkv;
+  const int64_t per_wg = max((total + a.grid - 1) / a.grid, (int64_t)1);
+  if (wg == 0) {
+    int64_t *starts = reinterpret_cast<int64_t *>(a.plan + kPlanInts);
+    int64_t at = before;
+    for (int s = s0; s < s1; ++s) {
+      starts[s] = at;
+      at += units_in(s);
+    }
+    if (tid == 0) {
+      a.plan[0] = prefix;
+      reinterpret_cast<int64_t *>(a.plan)[1] = per_head;
+      reinterpret_cast<int64_t *>(a.plan)[2] = lead;
+      reinterpret_cast<int64_t *>(a.plan)[3] = per_wg;
+    }
+  }
+  const int64_t u0 = (int64_t)wg * per_wg, u1 = min(u0 + per_wg, total);
+  if (u0 >= u1) return;
+
+  // ---- the item of u0: the thread whose sequences hold it names it
+  int kh = (int)(u0 / per_head);
+  int64_t in_head = u0 - kh * per_head;
+  int s = -1;  // -1: the prefix
+  int64_t in_seq = in_head;
+  if (in_head >= lead) {
+    const int64_t x = in_head - lead;
+    if (x >= before && x < before + mine) {
+      int64_t at = before;
+      int i = s0;
+      for (int64_t n = units_in(i); x >= at + n; n = units_in(i)) {
+        at += n;
+        ++i;
+      }
+      scan32[0][2] = i;
+      scan64[4] = x - at;
+    }
+    __syncthreads();
+    s = scan32[0][2];
+    in_seq = scan64[4];
+  }
+
+  const T *kpool = static_cast<const T *>(a.k_pages), *vpool = static_cast<const T *>(a.v_pages);
+  int64_t u = u0;
+  while (u < u1) {
+    // the item: its rows, its keys, the units of it in this run
+    Seq q{0, tokens, prefix};
+    int key0 = 0, row0 = first;
+    if (s >= 0) {
+      q = seq_at(a, s);
+      key0 = prefix;
+      row0 = s;
+    }
+    const int nu = units_of(q.kv - key0);
+    const int rt = (int)(in_seq / nu), un = (int)(in_seq - (int64_t)rt * nu);
+    const int run = (int)min((int64_t)(nu - un), u1 - u);
+    const int64_t rows = (int64_t)q.n * G, r0 = (int64_t)rt * kRows;
+    const int32_t *table = a.table + (int64_t)row0 * a.max_pages;
+
+    __syncthreads();  // the item before may still be read
+    for (int i = tid; i < kRows * (D / 8); i += 256) {
+      const int row = i / (D / 8), ch = i % (D / 8);
+      const int64_t r = min(r0 + row, rows - 1);
+      const int tok = (int)(r / G);
+      *reinterpret_cast<u32x4 *>(&qs[row][8 * ch]) = *reinterpret_cast<const u32x4 *>(
+          static_cast<const T *>(a.q) + (int64_t)(q.bos + tok) * a.q_row +
+          ((int64_t)kh * G + (r - (int64_t)tok * G)) * D + 8 * ch);
+    }
+    int lim[kRT];  // the last key that this lane's row of each tile sees
+#pragma unroll
+    for (int t = 0; t < kRT; ++t) {
+      const int64_t r = r0 + 16 * t + c;
+      lim[t] = s < 0 ? q.kv - 1 : q.kv - q.n + (int)(min(r, rows - 1) / G);
+    }
+    const int all_see = s < 0 ? q.kv - 1 : q.kv - q.n + (int)(r0 / G);  // every row sees these
+    __syncthreads();
+
+    f32x4 o[kRT][kDC][8];
+    float m[kRT], l[kRT];
+#pragma unroll
+    for (int t = 0; t < kRT; ++t) {
+      m[t] = kNegInf;
+      l[t] = 0.f;
+#pragma unroll
+      for (int b = 0; b < kDC; ++b)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[t][b][j] = zero4();
+    }
+    for (int i = 0; i < run; ++i) {
+      const int k0 = key0 + (un + i) * kUnit + 32 * w;  // the wave's 32 keys
+      if (k0 >= q.kv) continue;
+      // two tiles of 16 keys, each inside one page
+      const T *kt[2], *vt[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int key = min(k0 + 16 * t, (q.kv - 1) & ~15);
+        const int page = min(max(table[key >> a.page_shift], 0), a.n_pages - 1);
+        const int64_t at = ((((int64_t)page * a.hkv + kh) << a.page_shift) +
+                            (key & ((1 << a.page_shift) - 1))) * D;
+        kt[t] = kpool + at;
+        vt[t] = vpool + at;
+      }
+      vec8 kf[2][D / 32];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int p = 0; p < D / 32; ++p)
+          kf[t][p] = *reinterpret_cast<const vec8 *>(kt[t] + c * D + 32 * p + 8 * g);
+      // keys 4 g + e of tile 0, then of tile 1
+      u32x4 vr[kDC][8];
+#pragma unroll
+      for (int b = 0; b < kDC; ++b)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          vr[b][e] = *reinterpret_cast<const u32x4 *>(vt[e >> 2] + (4 * g + (e & 3)) * D + 128 * b +
+                                                      8 * c);
+      if (k0 + 32 > q.kv) {  // rows past the length may hold anything
+#pragma unroll
+        for (int b = 0; b < kDC; ++b)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (k0 + 16 * (e >> 2) + 4 * g + (e & 3) >= q.kv) vr[b][e] = u32x4{0u, 0u, 0u, 0u};
+      }
+      vec8 vf[kDC][8];
+#pragma unroll
+      for (int b = 0; b < kDC; ++b)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          u32x4 x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[e] = __builtin_amdgcn_perm(vr[b][2 * e + 1][j >> 1], vr[b][2 * e][j >> 1],
+                                         j & 1 ? 0x07060302u : 0x05040100u);
+          vf[b][j] = __builtin_bit_cast(vec8, x);
+        }
+      const bool masked = k0 + 31 > all_see;
+#pragma unroll
+      for (int t = 0; t < kRT; ++t) {
+        f32x4 sc[2] = {zero4(), zero4()};
+#pragma unroll
+        for (int p = 0; p < D / 32; ++p) {
+          const vec8 qf = *reinterpret_cast<const vec8 *>(&qs[16 * t + c][32 * p + 8 * g]);
+          sc[0] = mfma(kf[0][p], qf, sc[0]);
+          sc[1] = mfma(kf[1][p], qf, sc[1]);
+        }
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (k0 + 16 * (e >> 2) + 4 * g + (e & 3) > lim[t]) sc[e >> 2][e & 3] = kNegInf;
+        }
+        float mx = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])),
+                         fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3])));
+        mx = fmaxf(mx, swap16(mx));
+        mx = fmaxf(mx, swap32(mx)) * a.scale_log2;
+        if (__any(mx > m[t] + kRescaleLog2)) {
+          const float mn = fmaxf(m[t], mx);
+          const float al = mn == kNegInf ? 1.f : fast_exp2(m[t] - mn);
+          m[t] = mn;
+          l[t] *= al;
+#pragma unroll
+          for (int b = 0; b < kDC; ++b)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[t][b][j] *= al;
+        }
+        const float ms = m[t] == kNegInf ? 0.f : m[t];
+        u32x4 pw;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float e0 = fast_exp2(fmaf(sc[e >> 1][2 * (e & 1)], a.scale_log2, -ms));
+          const float e1 = fast_exp2(fmaf(sc[e >> 1][2 * (e & 1) + 1], a.scale_log2, -ms));
+          l[t] += e0 + e1;
+          pw[e] = Elem<T>::pack(e0, e1);
+        }
+        const vec8 pf = __builtin_bit_cast(vec8, pw);
+#pragma unroll
+        for (int b = 0; b < kDC; ++b)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[t][b][j] = mfma(vf[b][j], pf, o[t][b][j]);
+      }
+    }
+
+    // ---- the four waves meet, one 16-row tile at a time
+#pragma unroll
+    for (int t = 0; t < kRT; ++t) {
+      l[t] += swap16(l[t]);
+      l[t] += swap32(l[t]);
+      if (g == 0) {
+        wm[w][16 * t + c] = m[t];
+        wl[w][16 * t + c] = l[t];
+      }
+    }
+    const bool from_start = un == 0, to_end = un + run == nu;
+    const bool whole = from_start && to_end;
+    // whole and alone: the output; whole beside a prefix: the row's place; else
+    // this work-group's place 0 (the item began before it) or 1 (it goes on)
+    const bool last = whole && prefix == 0;
+    const int64_t place = (int64_t)wg * 2 + (from_start ? 1 : 0);
+#pragma unroll
+    for (int t = 0; t < kRT; ++t) {
+      __syncthreads();
+      float big = kNegInf;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) big = fmaxf(big, wm[i][16 * t + c]);
+      const float f = m[t] == kNegInf ? 0.f : fast_exp2(m[t] - big);
+#pragma unroll
+      for (int b = 0; b < kDC; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float *p = &os[w][c][128 * b + 32 * g + 8 * i];
+          const auto &x = o[t][b];
+          *reinterpret_cast<f32x4 *>(p) = f32x4{x[0][i] * f, x[1][i] * f, x[2][i] * f, x[3][i] * f};
+          *reinterpret_cast<f32x4 *>(p + 4) =
+              f32x4{x[4][i] * f, x[5][i] * f, x[6][i] * f, x[7][i] * f};
+        }
+      __syncthreads();
+      // sixteen threads per row, 4 dims each at a time
+      const int row = tid >> 4, q4 = 4 * (tid & 15);
+      const int64_t r = r0 + 16 * t + row;
+      if (r < rows) {
+        float mm = kNegInf, ll = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mm = fmaxf(mm, wm[i][16 * t + row]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          ll += wm[i][16 * t + row] == kNegInf ? 0.f
+                                               : wl[i][16 * t + row] * fast_exp2(wm[i][16 * t + row] - mm);
+        const int tok = (int)(r / G);
+        const int64_t orow = (int64_t)(q.bos + tok) * a.h + (int64_t)kh * G + (r - (int64_t)tok * G);
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        float *po, *pm;
+        if (whole) {
+          const int64_t at = (s < 0 ? 0 : (int64_t)a.t_max * a.h) + orow;
+          po = a.done_o + at * D;
+          pm = a.done_ml + at * 2;
+        } else {
+          po = a.part_o + (place * kRows + 16 * t + row) * D;
+          pm = a.part_ml + (place * kRows + 16 * t + row) * 2;
+        }
+        if (!last && (tid & 15) == 0) {
+          pm[0] = mm;
+          pm[1] = ll;
+        }
+#pragma unroll
+        for (int b = 0; b < D / 64; ++b) {
+          f32x4 sum = zero4();
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            sum += *reinterpret_cast<const f32x4 *>(&os[i][row][64 * b + q4]);
+          if (last)
+            *reinterpret_cast<u32x2 *>(static_cast<T *>(a.o) + orow * D + 64 * b + q4) =
+                u32x2{Elem<T>::pack(sum[0] * inv, sum[1] * inv),
+                      Elem<T>::pack(sum[2] * inv, sum[3] * inv)};
+          else
+            *reinterpret_cast<f32x4 *>(po + 64 * b + q4) = sum;
+        }
+      }
+    }
+
+    // ---- the next item
+    u += run;
+    in_seq += run;
+    in_head += run;
+    if (u >= u1) break;
+    if (in_head == per_head) {
+      ++kh;
+      in_head = in_seq = 0;
+      s = -1;
+    }
+    if (s < 0) {
+      if (in_head < lead) continue;
+      in_seq = 0;
+      s = 0;
+      while (units_in(s) == 0) ++s;
+    } else if (in_seq == units_in(s)) {
+      in_seq = 0;
+      ++s;
+      while (units_in(s) == 0) ++s;
+    }
+  }
+}
+
+// Joins what several work-groups, or the prefix and a sequence, left of a row,
+// and writes zeros where a row sees no key. One work-group per (token, query
+// head); rows that the main kernel finished are left alone.
+template <typename T, int D, int kRT>
+__global__ __launch_bounds__(256) void attn_join_kernel(PagedArgs a) {
+  constexpr int kRows = 16 * kRT;
+  constexpr int kLanes = D / 4;            // threads per partial result
+  constexpr int kPar = 256 / kLanes;       // partial results at a time
+  __shared__ __attribute__((aligned(16))) float os[kPar][D];
+  __shared__ float ms[4], ls[kPar];
+  const int wg = flat_block();
+  const int t = wg / a.h, head = wg % a.h;
+  const int tid = threadIdx.x, lane = tid & 63;
+  if (t >= cu_at(a.cu, a.n_max, a.t_max)) return;
+  const int G = a.h / a.hkv, kh = head / G;
+  const int s = seq_of_row(a.cu, a.n_max, a.t_max, t, lane);
+  const Seq q = seq_at(a, s);
+  if (t < q.bos || t >= q.bos + q.n) return;  // an unsorted cu_seqlens: a row of no sequence
+  const int prefix = a.plan[0];
+  const int64_t per_head = reinterpret_cast<const int64_t *>(a.plan)[1];
+  const int64_t lead = reinterpret_cast<const int64_t *>(a.plan)[2];
+  const int64_t per_wg = reinterpret_cast<const int64_t *>(a.plan)[3];
+  const int64_t start = reinterpret_cast<const int64_t *>(a.plan + kPlanInts)[s];
+
+  // the two items of the row: units [lo, hi), and the row's number in its tile
+  int64_t lo[2] = {0, 0}, hi[2] = {0, 0};
+  int in_tile[2] = {0, 0};
+  if (prefix > 0) {
+    const int64_t r = (int64_t)t * G + head % G;
+    const int nu = units_of(prefix);
+    lo[0] = kh * per_head + r / kRows * nu;
+    hi[0] = lo[0] + nu;
+    in_tile[0] = (int)(r % kRows);
+  }
+  if (q.kv > prefix) {
+    const int64_t r = (int64_t)(t - q.bos) * G + head % G;
+    const int nu = units_of(q.kv - prefix);
+    lo[1] = kh * per_head + lead + start + r / kRows * nu;
+    hi[1] = lo[1] + nu;
+    in_tile[1] = (int)(r % kRows);
+  }
+  int64_t w0[2], cnt[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    w0[i] = lo[i] / per_wg;
+    cnt[i] = hi[i] > lo[i] ? (hi[i] - 1) / per_wg - w0[i] + 1 : 0;
+  }
+  if (prefix == 0 && cnt[1] == 1) return;  // the main kernel wrote it
+  const int64_t orow = (int64_t)t * a.h + head;
+  const int64_t n = cnt[0] + cnt[1];
+  // partial result i of the row: its output sum and its statistics
+  auto where = [&](int64_t i, const float *&po, const float *&pm) __attribute__((always_inline)) {
+    const int k = i < cnt[0] ? 0 : 1;
+    const int64_t j = i - (k ? cnt[0] : 0);
+    if (cnt[k] == 1) {
+      const int64_t at = (k ? (int64_t)a.t_max * a.h : 0) + orow;
+      po = a.done_o + at * D;
+      pm = a.done_ml + at * 2;
+    } else {
+      const int64_t wgi = w0[k] + j;
+      const int64_t at = (wgi * 2 + (lo[k] >= wgi * per_wg ? 1 : 0)) * kRows + in_tile[k];
+      po = a.part_o + at * D;
+      pm = a.part_ml + at * 2;
+    }
+  };
+  float big = kNegInf;
+  for (int64_t i = tid; i < n; i += 256) {
+    const float *po, *pm;
+    where(i, po, pm);
+    big = fmaxf(big, pm[0]);
+  }
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) big = fmaxf(big, __shfl_xor(big, off, 64));
+  if (lane == 0) ms[tid >> 6] = big;
+  __syncthreads();
+  big = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3]));
+  f32x4 sum = zero4();
+  float l = 0.f;
+  const int part = tid / kLanes, d4 = 4 * (tid % kLanes);
+  for (int64_t i = part; i < n; i += kPar) {
+    const float *po, *pm;
+    where(i, po, pm);
+    if (pm[0] == kNegInf) continue;
+    const float f = fast_exp2(pm[0] - big);
+    l = fmaf(pm[1], f, l);
+    sum += *reinterpret_cast<const f32x4 *>(po + d4) * f;
+  }
+  *reinterpret_cast<f32x4 *>(&os[part][d4]) = sum;
+  if (tid % kLanes == 0) ls[part] = l;
+  __syncthreads();
+  if (part > 0) return;
+#pragma unroll
+  for (int i = 1; i < kPar; ++i) {
+    sum += *reinterpret_cast<const f32x4 *>(&os[i][d4]);
+    l += ls[i];
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  *reinterpret_cast<u32x2 *>(static_cast<T *>(a.o) + orow * D + d4) =
+      u32x2{Elem<T>::pack(sum[0] * inv, sum[1] * inv), Elem<T>::pack(sum[2] * inv, sum[3] * inv)};
+}
+
+template <typename T, int D, int kRT>
+hipError_t run(const PagedArgs &a, dim3 join, hipStream_t stream) {
+  hipLaunchKernelGGL((attn_paged_kernel<T, D, kRT>), dim3((a.grid + 7) / 8 * 8), dim3(256), 0,
+                     stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((attn_join_kernel<T, D, kRT>), join, dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t run_of(const PagedArgs &a, int d, int rt, dim3 join, hipStream_t stream) {
+  if (d == 128)
+    return rt == 1   ? run<T, 128, 1>(a, join, stream)
+           : rt == 2 ? run<T, 128, 2>(a, join, stream)
+                     : run<T, 128, 4>(a, join, stream);
+  return rt == 1 ? run<T, 256, 1>(a, join, stream) : run<T, 256, 2>(a, join, stream);
+}
+
+}  // namespace
+
+// One 16-row tile per item holds a decoding sequence's heads; where the rows of
+// an average sequence, or of the batch on its shared prefix, are more, wider
+// items read the keys fewer times.
+int paged_row_tiles(const gdn_attn_config *cfg) {
+  const int64_t rows = cfg->shared_max > 0
+                           ? (int64_t)cfg->t_max * (cfg->h / cfg->hkv)
+                           : (int64_t)cfg->t_max * (cfg->h / cfg->hkv) / cfg->n_max;
+  const int most = cfg->d == 128 ? 4 : 2;
+  int rt = 1;
+  while (rt < most && rows > 16 * rt) rt *= 2;
+  return rt;
+}
+
+int paged_grid(const gdn_attn_config *cfg) {
+  return cu_count() * (paged_row_tiles(cfg) * cfg->d <= 256 ? 2 : 1);
+}
+
+hipError_t launch_attn_paged(const gdn_attn_config *cfg, PagedArgs a, hipStream_t stream) {
+  if (cfg->t_max == 0) return hipSuccess;
+  dim3 join;
+  if (!flat_grid((int64_t)cfg->t_max * cfg->h, 256, join)) return hipErrorInvalidValue;
+  const int rt = paged_row_tiles(cfg);
+  return cfg->dtype == GDN_BF16 ? run_of<__bf16>(a, cfg->d, rt, join, stream)
+                                : run_of<_Float16>(a, cfg->d, rt, join, stream);
+}
+
+}  // namespace gdn

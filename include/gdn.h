@@ -371,6 +371,123 @@ gdn_status gdn_recurrent_fwd_timed(const gdn_config *cfg, const void *q, const v
                                    const float *h0, const int32_t *cu_seqlens, void *o, float *hT,
                                    void *stream, void *ev_start, void *ev_stop);
 
+/* ---------------------------------------------------------------------------
+ * Softmax-attention layers of a hybrid stack
+ *
+ * A stack that mixes gated-delta-rule layers with softmax-attention layers
+ * needs, beside the front, the prefill and the decode above, the same three
+ * steps for the latter: a front (per-head norm and position rotation, with
+ * the write into a paged key / value cache), causal attention over whole
+ * prompts, and attention of a few new tokens per sequence to the cache. The
+ * conventions at the top of this file hold here too: packed varlen rows,
+ * cu_seqlens and every other device-side index clamped to the buffers cfg
+ * sizes, host checks before any HIP call, nothing allocated, nothing
+ * synchronised, launches only on `stream`. Rows past cu_seqlens[n_max] are
+ * left as they were. Outputs must not overlap inputs.
+ *
+ *  - Query head i reads key / value head i / (h / hkv).
+ *  - kv_lens (device, int32 [n_max]): tokens of each sequence in all, this
+ *    call's included: the n tokens of a sequence in this call are its
+ *    positions kv_lens - n .. kv_lens - 1.
+ *  - The cache: k_pages, v_pages (device) [n_pages, hkv, page_size, d], and
+ *    block_table (device) int32 [n_max, max_pages]: position p of sequence s
+ *    lies in page block_table[s][p / page_size], row p % page_size. Rows of a
+ *    page past a sequence's length may hold anything, NaN included.
+ *  - Types: q, k, v, qkv, the pages and o share cfg->dtype (GDN_BF16 or
+ *    GDN_F16). Scores, softmax statistics and output sums are fp32; softmax
+ *    weights are rounded to the 16-bit type for their product with v, and the
+ *    output is rounded once.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t t_max;           /* token capacity (rows of q, qkv, o; query tokens) */
+  int32_t n_max;           /* sequence capacity */
+  int32_t h, hkv;          /* query heads; key / value heads, h a multiple of hkv */
+  int32_t d;               /* head dim: 128 or 256 */
+  gdn_dtype dtype;         /* GDN_BF16 or GDN_F16 */
+  float scale;             /* score scale; <= 0 selects 1 / sqrt(d) */
+  float eps;               /* RMS norm: added to the mean square; finite, >= 0 */
+  int32_t rot_dim;         /* leading dims of each head that are rotated: even, 0 .. d */
+  int32_t rot_interleaved; /* 0: dims (i, i + rot_dim / 2) form pair i; 1: (2 i, 2 i + 1) */
+  float rot_scale;         /* factor on cos and sin (long-context scaling); 0 selects 1 */
+  int32_t page_size;       /* tokens per page: 16, 32, 64, 128 or 256 */
+  int32_t n_pages;         /* pages of k_pages and v_pages */
+  int32_t max_pages;       /* columns of block_table */
+  int32_t tk_max;          /* rows of k and v in gdn_attn_prefill; 0 selects t_max */
+  int32_t shared_max;      /* largest *shared_len (gdn_attn_paged); 0: no shared prefix */
+} gdn_attn_config;
+
+/* Bytes of workspace gdn_attn_prefill and gdn_attn_paged need for `cfg` on the
+ * current device (its compute units bound the number of partial results).
+ * Nothing in a workspace has to start at any value; calls that overlap in
+ * time need workspaces of their own. */
+gdn_status gdn_attn_workspace_size(const gdn_attn_config *cfg, size_t *bytes);
+
+/* RMS norm of every query and key head and rotation by the token's position,
+ * one pass:  x' = x / sqrt(mean(x^2) + eps) * w,  then pair i of the first
+ * rot_dim dims, (a, b) -> rot_scale (a cos t - b sin t, b cos t + a sin t),
+ * t = position * inv_freq[i].
+ *   qkv      (device) [t_max, (h + 2 hkv) d], channels q | k | v, head-major;
+ *            qkv_row elements from one row to the next (0 = dense; a multiple
+ *            of 8)
+ *   q_w, k_w (device, nullable = no norm of that kind of head) fp32 [d]
+ *   inv_freq (device; NULL if and only if rot_dim is 0) fp32 [rot_dim / 2]:
+ *            radians per position. The angle is formed and reduced in 64 bits.
+ *   kv_lens  (nullable: positions count from 0 in each sequence)
+ *   q (device) [t_max, h, d], k (device) [t_max, hkv, d], written. */
+gdn_status gdn_qk_norm_rope(const gdn_attn_config *cfg, const void *qkv, int64_t qkv_row,
+                            const float *q_w, const float *k_w, const float *inv_freq,
+                            const int32_t *cu_seqlens, const int32_t *kv_lens, void *q, void *k,
+                            void *stream);
+
+/* gdn_qk_norm_rope that writes the rotated keys, and v as it is, into the
+ * cache pages of their positions in the same pass.
+ *   q (nullable = not wanted), k (nullable = only the pages are written)
+ *   kv_lens (required). A token whose position is negative, or whose page is
+ *   outside block_table's columns or names no page (< 0 or >= n_pages), is
+ *   not written to the cache. Two tokens of one call must not share a page
+ *   row. */
+gdn_status gdn_kv_append(const gdn_attn_config *cfg, const void *qkv, int64_t qkv_row,
+                         const float *q_w, const float *k_w, const float *inv_freq,
+                         const int32_t *cu_seqlens, const int32_t *kv_lens,
+                         const int32_t *block_table, void *q, void *k, void *k_pages,
+                         void *v_pages, void *stream);
+
+/* Causal attention over packed prompts:  o_r = sum_c softmax_c(scale q_r . k_c) v_c
+ * over the keys c of the row's sequence up to its own position. Sequence s has
+ * the rows cu_q[s] .. of q and o and the rows cu_k[s] .. of k and v, and its
+ * queries are the last of its keys: query i of lq sees keys 0 .. lk - lq + i.
+ * A row that sees no key (lq > lk) gives zeros.
+ *   q (device) [t_max, h, d]; k, v (device) [tk_max, hkv, d]; q_row, k_row,
+ *   v_row elements from one token to the next (0 = dense; multiples of 8), so
+ *   each may be read where a projection left it
+ *   cu_q, cu_k (device) int32 [n_max + 1]; cu_k NULL = cu_q
+ *   o (device) [t_max, h, d], dense: valid rows written
+ *   workspace (device) >= gdn_attn_workspace_size bytes, 256-byte aligned.
+ * A value that is not finite in k or v reaches at most the rows of its own
+ * sequence. */
+gdn_status gdn_attn_prefill(const gdn_attn_config *cfg, const void *q, int64_t q_row,
+                            const void *k, int64_t k_row, const void *v, int64_t v_row,
+                            const int32_t *cu_q, const int32_t *cu_k, void *o, void *workspace,
+                            size_t ws_bytes, void *stream);
+
+/* Attention of each sequence's n new tokens (one when decoding, a few when
+ * verifying, any number) to its cache, which already holds them: token i sees
+ * positions 0 .. kv_lens - n + i. A row that sees no key gives zeros.
+ *   q (device) [t_max, h, d], q_row as above
+ *   shared_len (device, nullable = 0) int32 [1]: a promise that the batch's
+ *            sequences have their first *shared_len positions in the same
+ *            pages (equal leading block_table entries). Those pages are then
+ *            read once for the whole batch, as whole pages and as far as all
+ *            the sequences' new tokens come after them. At most
+ *            cfg->shared_max (a larger value counts as that).
+ *   o (device) [t_max, h, d], dense
+ * A block_table entry that names no page reads page 0 or n_pages - 1. */
+gdn_status gdn_attn_paged(const gdn_attn_config *cfg, const void *q, int64_t q_row,
+                          const void *k_pages, const void *v_pages, const int32_t *cu_seqlens,
+                          const int32_t *kv_lens, const int32_t *block_table,
+                          const int32_t *shared_len, void *o, void *workspace, size_t ws_bytes,
+                          void *stream);
+
 /* Static string for a status code (never NULL). */
 const char *gdn_status_str(gdn_status status);
 

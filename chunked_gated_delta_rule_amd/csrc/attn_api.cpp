@@ -80,10 +80,12 @@ gdn_status check_workspace(const Layout &l, const void *ws, size_t bytes) {
   return GDN_OK;
 }
 
-// A row stride in elements: 0 = dense; else at least one row, 16-byte steps.
+// A row stride in elements: 0 = dense; else at least one row, 16-byte steps, and
+// at most what lets 64 rows be indexed in 32 bits.
+constexpr int64_t kMaxRow = 1 << 24;
 bool row_of(int64_t given, int64_t dense, int64_t &row) {
   row = given == 0 ? dense : given;
-  return row >= dense && row % 8 == 0;
+  return row >= dense && row % 8 == 0 && row <= kMaxRow;
 }
 
 float scale_log2(const gdn_attn_config *cfg) {

@@ -40,9 +40,38 @@ struct Elem<_Float16> {
   }
 };
 
-// The value of lane l ^ 16 / l ^ 32.
-__device__ __forceinline__ float swap16(float x) { return __shfl_xor(x, 16, 64); }
-__device__ __forceinline__ float swap32(float x) { return __shfl_xor(x, 32, 64); }
+// Maximum and sum over lanes l and l ^ 32 (l ^ 16), in both: the swap of half
+// (quarter) waves leaves the lower ones' values in one register and the upper
+// ones' in the other.
+struct Halves {
+  float a, b;
+};
+__device__ __forceinline__ Halves halves32(float x) {
+  const uint32_t u = __float_as_uint(x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return {__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+__device__ __forceinline__ Halves halves16(float x) {
+  const uint32_t u = __float_as_uint(x);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return {__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+__device__ __forceinline__ float max32(float x) {
+  const Halves h = halves32(x);
+  return fmaxf(h.a, h.b);
+}
+__device__ __forceinline__ float sum32(float x) {
+  const Halves h = halves32(x);
+  return h.a + h.b;
+}
+__device__ __forceinline__ float max16(float x) {
+  const Halves h = halves16(x);
+  return fmaxf(h.a, h.b);
+}
+__device__ __forceinline__ float sum16x(float x) {
+  const Halves h = halves16(x);
+  return h.a + h.b;
+}
 
 constexpr float kNegInf = -__builtin_inff();
 

@@ -112,7 +112,7 @@ __global__ __launch_bounds__(kFrontThreads) void attn_front_kernel(FrontArgs a) 
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
     ss = sum16(ss);
-    if constexpr (kLanes == 32) ss += swap16(ss);
+    if constexpr (kLanes == 32) ss = sum16x(ss);
     const float r = norm ? 1.f / sqrtf(ss * (1.f / D) + a.eps) : 1.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] *= r * (is_q ? wq[j] : wk[j]);

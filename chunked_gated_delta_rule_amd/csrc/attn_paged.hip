@@ -287,8 +287,7 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_paged_kernel
         }
         float mx = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])),
                          fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3])));
-        mx = fmaxf(mx, swap16(mx));
-        mx = fmaxf(mx, swap32(mx)) * a.scale_log2;
+        mx = max32(max16(mx)) * a.scale_log2;
         if (__any(mx > m[t] + kRescaleLog2)) {
           const float mn = fmaxf(m[t], mx);
           const float al = mn == kNegInf ? 1.f : fast_exp2(m[t] - mn);
@@ -319,8 +318,7 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_paged_kernel
     // ---- the four waves meet, one 16-row tile at a time
 #pragma unroll
     for (int t = 0; t < kRT; ++t) {
-      l[t] += swap16(l[t]);
-      l[t] += swap32(l[t]);
+      l[t] = sum32(sum16x(l[t]));
       if (g == 0) {
         wm[w][16 * t + c] = m[t];
         wl[w][16 * t + c] = l[t];

@@ -43,19 +43,141 @@ __host__ __device__ inline int64_t tile_slots(int64_t t_max, int64_t n_max) {
   return t_max / kBM + n_max;
 }
 
+// Head and tile slot of a work-group. The last (longest) tiles come first. With
+// a multiple of 8 heads, neighbouring heads (which read the same keys) go to one
+// XCD, whose L2 then holds their keys and values.
+__device__ __forceinline__ void place(int wg, int h, int slots, int &head, int &slot) {
+  if (h % 8 == 0) {
+    const int per = h / 8, i = wg >> 3;
+    head = (wg & 7) * per + i % per;
+    slot = slots - 1 - i / per;
+  } else {
+    head = wg % h;
+    slot = slots - 1 - wg / h;
+  }
+}
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+template <typename T, int D>
+struct Tile {
+  static constexpr int kRowBytes = D * 2;
+  static constexpr int kLoads = kBN * kRowBytes / 4096;  // per wave: 1 KB each
+  static constexpr int kRowsPerLoad = 4096 / kRowBytes;  // of the work-group's four waves
+  // Chunk (16 bytes) in which row r keeps its chunk c. For K, whose fragments
+  // take one chunk of 32 rows, the rows differ in the low bits; for V, whose
+  // transposing reads take four neighbouring chunks of four rows, in bits 2, 3.
+  static __device__ __forceinline__ int k_swz(int r) { return r & 15; }
+  static __device__ __forceinline__ int v_swz(int r) { return (r & 3) << 2; }
+};
+
+// Copies 64 rows (those of them that the descriptor's range holds, zeros for the
+// others) straight to LDS: lane l of wave w fills the 16 bytes at 4096 i + 1024 w +
+// 16 l with the chunk that belongs there.
+template <typename T, int D, bool kV>
+__device__ __forceinline__ void fetch(T *dst, rsrc_t src, int row_bytes, int lane, int w) {
+  typedef Tile<T, D> L;
+#pragma unroll
+  for (int i = 0; i < L::kLoads; ++i) {
+    const int in = 1024 * w + 16 * lane;
+    const int row = i * L::kRowsPerLoad + in / L::kRowBytes, at = in % L::kRowBytes / 16;
+    const int ch = at ^ (kV ? L::v_swz(row) : L::k_swz(row));
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        src, (lds_void *)(reinterpret_cast<char *>(dst) + 4096 * i + 1024 * w), 16,
+        row * row_bytes + 16 * ch, 0, 0, 0);
+  }
+}
+
+// One query tile's running state, and its step over one tile of keys.
+template <typename T, int D>
+struct Rows {
+  typedef typename Elem<T>::vec8 vec8;
+  vec8 q[D / 16];
+  f32x16 o[D / 32];
+  float m, l;  // maximum (log2 scale) and this lane's part of the sum
+
+  __device__ __forceinline__ void step(const T *kt, const T *vt, int k0, int lim, bool masked,
+                                       float scale_log2, int lane) {
+    typedef Tile<T, D> L;
+    const int col = lane & 31, hh = lane >> 5;
+    f32x16 sc[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sc[t][i] = 0.f;
+    const T *kr = kt + col * D;
+    const int kx = L::k_swz(col) ^ hh;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      const T *p = kr + 8 * ((2 * i) ^ kx);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        sc[t] = mfma32(*reinterpret_cast<const vec8 *>(p + 32 * t * D), q[i], sc[t]);
+    }
+    if (masked) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          sc[t][i] = k0 + 32 * t + 8 * (i >> 2) + 4 * hh + (i & 3) <= lim ? sc[t][i] : kNegInf;
+    }
+    float mx = kNegInf;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, sc[t][i]);
+    mx = max32(mx) * scale_log2;
+    if (__any(mx > m + kRescaleLog2)) {
+      const float mn = fmaxf(m, mx);
+      const float al = mn == kNegInf ? 1.f : fast_exp2(m - mn);
+      m = mn;
+      l *= al;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[i][k] *= al;
+    }
+    const float ms = m == kNegInf ? 0.f : m;
+    // lane's part of a transposing read: row 4 hh + (s16 >> 2) (+ 8), columns 32 i +
+    // 16 gb + 4 (s16 & 3)
+    const int s16 = lane & 15, gb = (lane >> 4) & 1, r0 = 4 * hh + (s16 >> 2);
+    const T *vr = vt + r0 * D + 4 * (s16 & 1);
+    const int vx = L::v_swz(r0) ^ (2 * gb + ((s16 & 3) >> 1));
+    // 16 keys at a time: the weights of the next are formed while the products
+    // of these run
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      uint32_t wd[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float e0 = fast_exp2(fmaf(sc[b >> 1][8 * (b & 1) + 2 * i], scale_log2, -ms));
+        const float e1 = fast_exp2(fmaf(sc[b >> 1][8 * (b & 1) + 2 * i + 1], scale_log2, -ms));
+        l += e0 + e1;
+        wd[i] = Elem<T>::pack(e0, e1);
+      }
+      const vec8 p = __builtin_bit_cast(vec8, u32x4{wd[0], wd[1], wd[2], wd[3]});
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const T *p0 = vr + 8 * ((4 * i) ^ vx);
+        const u32x2 x = tr_read(p0 + 16 * b * D), y = tr_read(p0 + (16 * b + 8) * D);
+        o[i] = mfma32(__builtin_bit_cast(vec8, u32x4{x[0], x[1], y[0], y[1]}), p, o[i]);
+      }
+    }
+  }
+};
+
 template <typename T, int D>
 __global__ __launch_bounds__(256, D == 128 ? 2 : 1) void attn_prefill_kernel(PrefillArgs a,
                                                                             int slots) {
-  typedef typename Elem<T>::vec8 vec8;
-  constexpr int kCh = D / 8;                  // 16-byte chunks per row
-  constexpr int kStage = kBN * kCh / 256;     // chunks per thread and tile
-  __shared__ __attribute__((aligned(16))) T lds[2][2][kBN * D];
+  // four arrays of their own, so that a tile in flight is known to be another
+  // than the ones being read
+  __shared__ __attribute__((aligned(16))) T k_a[kBN * D], v_a[kBN * D], k_b[kBN * D], v_b[kBN * D];
 
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, hh = lane >> 5;
-  // heads fastest, the last (longest) tiles first
   const int wg = flat_block();
-  const int head = wg % a.h, slot = slots - 1 - wg / a.h;
+  int head, slot;
+  place(wg, a.h, slots, head, slot);
   if (slot < 0) return;  // past the grid's count (last row)
   const int s = wave_search(a.n_max, slot, lane,
                             [&](int i) { return cu_at(a.cu_q, i, a.t_max) / kBM + i; });
@@ -73,121 +195,46 @@ __global__ __launch_bounds__(256, D == 128 ? 2 : 1) void attn_prefill_kernel(Pre
   const int keys = min(past + min(q0 + kBM, lq), lk);  // keys any row of the tile sees
   const int tiles = keys > 0 ? (keys + kBN - 1) / kBN : 0;
 
-  vec8 qf[D / 16];
+  Rows<T, D> x;
   {
     const T *qp = static_cast<const T *>(a.q) + (int64_t)(qb + r) * a.q_row + head * D + 8 * hh;
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) qf[i] = *reinterpret_cast<const vec8 *>(qp + 16 * i);
+    for (int i = 0; i < D / 16; ++i)
+      x.q[i] = *reinterpret_cast<const typename Rows<T, D>::vec8 *>(qp + 16 * i);
   }
-  const T *kp = static_cast<const T *>(a.k) + (int64_t)kb * a.k_row + kvh * D;
-  const T *vp = static_cast<const T *>(a.v) + (int64_t)kb * a.v_row + kvh * D;
-
-  u32x4 ks[kStage], vs[kStage];
-  auto load = [&](int k0) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < kStage; ++i) {
-      const int idx = i * 256 + tid, row = min(k0 + idx / kCh, lk - 1), ch = idx % kCh;
-      ks[i] = *reinterpret_cast<const u32x4 *>(kp + (int64_t)row * a.k_row + 8 * ch);
-      vs[i] = *reinterpret_cast<const u32x4 *>(vp + (int64_t)row * a.v_row + 8 * ch);
-    }
-  };
-  auto stage = [&](int buf) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < kStage; ++i) {
-      const int idx = i * 256 + tid, row = idx / kCh, ch = idx % kCh;
-      const int at = row * D + 8 * (ch ^ (row & 15));
-      *reinterpret_cast<u32x4 *>(&lds[buf][0][at]) = ks[i];
-      *reinterpret_cast<u32x4 *>(&lds[buf][1][at]) = vs[i];
-    }
-  };
-
-  f32x16 o[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-    for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
-  float m = kNegInf, l = 0.f;  // maximum (log2 scale) and this lane's part of the sum
+    for (int j = 0; j < 16; ++j) x.o[i][j] = 0.f;
+  x.m = kNegInf;
+  x.l = 0.f;
 
-  if (tiles > 0) {
-    load(0);
-    stage(0);
-  }
-  __syncthreads();
-  for (int j = 0; j < tiles; ++j) {
-    const int k0 = j * kBN, buf = j & 1;
-    if (j + 1 < tiles) load(k0 + kBN);
-    if (k0 <= wave_hi) {
-      f32x16 sc[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sc[t][i] = 0.f;
-        const int row = 32 * t + col;
-        const T *base = &lds[buf][0][row * D];
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const vec8 kf = *reinterpret_cast<const vec8 *>(base + 8 * ((2 * i + hh) ^ (row & 15)));
-          sc[t] = mfma32(kf, qf[i], sc[t]);
-        }
-      }
-      if (k0 + kBN - 1 > wave_lo) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            sc[t][i] = k0 + 32 * t + 8 * (i >> 2) + 4 * hh + (i & 3) <= lim ? sc[t][i] : kNegInf;
-      }
-      float mx = kNegInf;
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, sc[t][i]);
-      mx = fmaxf(mx, swap32(mx)) * a.scale_log2;
-      if (__any(mx > m + kRescaleLog2)) {
-        const float mn = fmaxf(m, mx);
-        const float al = mn == kNegInf ? 1.f : fast_exp2(m - mn);
-        m = mn;
-        l *= al;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-          for (int k = 0; k < 16; ++k) o[i][k] *= al;
-      }
-      const float ms = m == kNegInf ? 0.f : m;
-      vec8 p[4];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          uint32_t wd[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float e0 = fast_exp2(fmaf(sc[t][8 * b + 2 * i], a.scale_log2, -ms));
-            const float e1 = fast_exp2(fmaf(sc[t][8 * b + 2 * i + 1], a.scale_log2, -ms));
-            l += e0 + e1;
-            wd[i] = Elem<T>::pack(e0, e1);
-          }
-          p[2 * t + b] = __builtin_bit_cast(vec8, u32x4{wd[0], wd[1], wd[2], wd[3]});
-        }
-      const T *vt = lds[buf][1];
-      const int s16 = lane & 15, gb = (lane >> 4) & 1;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const int ch = 4 * i + 2 * gb + ((s16 & 3) >> 1);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int ra = 16 * b + 4 * hh + (s16 >> 2), rb = ra + 8;
-          const u32x2 x = tr_read(vt + ra * D + 8 * (ch ^ (ra & 15)) + 4 * (s16 & 1));
-          const u32x2 y = tr_read(vt + rb * D + 8 * (ch ^ (rb & 15)) + 4 * (s16 & 1));
-          o[i] = mfma32(__builtin_bit_cast(vec8, u32x4{x[0], x[1], y[0], y[1]}), p[b], o[i]);
-        }
-      }
-    }
-    if (j + 1 < tiles) stage(buf ^ 1);
+  const T *kp = static_cast<const T *>(a.k) + (int64_t)kb * a.k_row + kvh * D;
+  const T *vp = static_cast<const T *>(a.v) + (int64_t)kb * a.v_row + kvh * D;
+  const int k_bytes = (int)a.k_row * 2, v_bytes = (int)a.v_row * 2;
+  // a tile's rows as a range that ends with the sequence's last key
+  auto get = [&](int j, T *kt, T *vt) __attribute__((always_inline)) {
+    const int64_t k0 = (int64_t)j * kBN;
+    const int rows = min(kBN, lk - (int)k0);
+    fetch<T, D, false>(kt, make_rsrc(kp + k0 * a.k_row, (rows - 1) * k_bytes + D * 2), k_bytes, lane, w);
+    fetch<T, D, true>(vt, make_rsrc(vp + k0 * a.v_row, (rows - 1) * v_bytes + D * 2), v_bytes, lane, w);
+  };
+  auto step = [&](int j, const T *kt, const T *vt) __attribute__((always_inline)) {
+    const int k0 = j * kBN;
+    if (k0 <= wave_hi) x.step(kt, vt, k0, lim, k0 + kBN - 1 > wave_lo, a.scale_log2, lane);
+  };
+  if (tiles > 0) get(0, k_a, v_a);
+  for (int j = 0; j < tiles; j += 2) {
+    __syncthreads();  // tile j is there, and the other pair is no longer read
+    if (j + 1 < tiles) get(j + 1, k_b, v_b);
+    step(j, k_a, v_a);
+    if (j + 1 >= tiles) break;
     __syncthreads();
+    if (j + 2 < tiles) get(j + 2, k_a, v_a);
+    step(j + 1, k_b, v_b);
   }
 
-  l += swap32(l);
+  const float l = sum32(x.l);
   const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees no key gives zeros
   if (r0 + col >= lq) return;
   T *op = static_cast<T *>(a.o) + ((int64_t)(qb + r0 + col) * a.h + head) * D + 4 * hh;
@@ -196,8 +243,8 @@ __global__ __launch_bounds__(256, D == 128 ? 2 : 1) void attn_prefill_kernel(Pre
 #pragma unroll
     for (int b = 0; b < 4; ++b)
       *reinterpret_cast<u32x2 *>(op + 32 * i + 8 * b) =
-          u32x2{Elem<T>::pack(o[i][4 * b] * inv, o[i][4 * b + 1] * inv),
-                Elem<T>::pack(o[i][4 * b + 2] * inv, o[i][4 * b + 3] * inv)};
+          u32x2{Elem<T>::pack(x.o[i][4 * b] * inv, x.o[i][4 * b + 1] * inv),
+                Elem<T>::pack(x.o[i][4 * b + 2] * inv, x.o[i][4 * b + 3] * inv)};
 }
 
 }  // namespace

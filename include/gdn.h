@@ -428,7 +428,7 @@ gdn_status gdn_attn_workspace_size(const gdn_attn_config *cfg, size_t *bytes);
  * t = position * inv_freq[i].
  *   qkv      (device) [t_max, (h + 2 hkv) d], channels q | k | v, head-major;
  *            qkv_row elements from one row to the next (0 = dense; a multiple
- *            of 8)
+ *            of 8, at most 2^24)
  *   q_w, k_w (device, nullable = no norm of that kind of head) fp32 [d]
  *   inv_freq (device; NULL if and only if rot_dim is 0) fp32 [rot_dim / 2]:
  *            radians per position. The angle is formed and reduced in 64 bits.
@@ -458,8 +458,8 @@ gdn_status gdn_kv_append(const gdn_attn_config *cfg, const void *qkv, int64_t qk
  * queries are the last of its keys: query i of lq sees keys 0 .. lk - lq + i.
  * A row that sees no key (lq > lk) gives zeros.
  *   q (device) [t_max, h, d]; k, v (device) [tk_max, hkv, d]; q_row, k_row,
- *   v_row elements from one token to the next (0 = dense; multiples of 8), so
- *   each may be read where a projection left it
+ *   v_row elements from one token to the next (0 = dense; multiples of 8, at
+ *   most 2^24), so each may be read where a projection left it
  *   cu_q, cu_k (device) int32 [n_max + 1]; cu_k NULL = cu_q
  *   o (device) [t_max, h, d], dense: valid rows written
  *   workspace (device) >= gdn_attn_workspace_size bytes, 256-byte aligned.

@@ -477,148 +477,156 @@ def gdn_attn_workspace_size(cfg: gdn_attn_config) -> int:
     return int(out.value)
 
 
-class _Args:
-    """Tensor arguments of one attention call: every check, and the device the
-    call runs on (that of its tensors; all must share it, and the call is made
-    with it current, on its current stream unless `stream` is given)."""
+# A small attention call is bound by the host, so its argument checks are kept to
+# one short function per tensor, with the message put together only on failure.
 
-    __slots__ = ("device", "dtype")
+# torch's raw handle of the current stream of a device (a Stream object for the
+# same question costs more than a kernel launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
-    def __init__(self, cfg):
-        self.device = None
-        self.dtype = _GDN_DTYPE.get(cfg.dtype)
 
-    def _on(self, x, name):
-        if not x.is_cuda:
-            raise ValueError(f"{name}: device tensor expected")
-        if self.device is None:
-            self.device = x.device
-        elif x.device != self.device:
-            raise ValueError(f"{name}: on {x.device}, {self.device} expected")
+def _dev(*tensors):
+    """Index of the device of the first tensor (None: raw pointers only; below 0: a
+    host tensor, which the call refuses after the other checks)."""
+    for x in tensors:
+        if isinstance(x, torch.Tensor):
+            return x.get_device()
+    return None
+
+
+def _at(x, name, dtype, elems, dev, last=None):
+    """Pointer of a contiguous tensor on device `dev` with at least `elems` elements
+    of `dtype` (None and raw pointers pass through)."""
+    if x is None or x.__class__ is int:
+        return x
+    if x.dtype is dtype and x.get_device() == dev and x.is_contiguous() and \
+            x.numel() >= elems and (last is None or x.shape[-1] == last):
         return x.data_ptr()
-
-    def dense(self, x, name, elems, dtype, last=None):
-        """Pointer of a contiguous tensor of at least `elems` elements (None and
-        raw pointers pass through)."""
-        if not isinstance(x, torch.Tensor):
-            return x
-        _need(x, name, elems, dtype, last)
-        if not x.is_contiguous():
-            raise ValueError(f"{name}: contiguous tensor expected")
-        return self._on(x, name)
-
-    def rows(self, x, name, tokens, heads, d):
-        """Pointer and row stride of packed rows: [tokens, heads, d] (or [tokens,
-        heads * d]), each token's values in one piece, any distance apart."""
-        if not isinstance(x, torch.Tensor):
-            return x, 0
-        if x.dtype != self.dtype:
-            raise ValueError(f"{name}: dtype {x.dtype}, {self.dtype} expected")
-        shape, stride = x.shape, x.stride()
-        if len(shape) == 3:
-            ok = shape[1] == heads and shape[2] == d and stride[2] == 1 and \
-                (stride[1] == d or heads == 1)
-        else:
-            ok = len(shape) == 2 and shape[1] == heads * d and stride[1] == 1
-        # (a single row's stride says nothing: torch may report any value)
-        if shape[0] > 1 and stride[0] < heads * d:
-            ok = False  # rows that overlap, or one row broadcast
-        if not ok or shape[0] < tokens:
-            raise ValueError(f"{name}: {tuple(shape)} with strides {stride}, [{tokens}, {heads}, "
-                             f"{d}] with every token's row in one piece expected")
-        return self._on(x, name), stride[0] if shape[0] > 1 else 0
-
-    def workspace(self, x, ws_bytes):
-        if not isinstance(x, torch.Tensor):
-            return x, int(ws_bytes)
-        have = x.numel() * x.element_size()
-        if ws_bytes is not None and int(ws_bytes) > have:
-            raise ValueError(f"workspace: {have} bytes, ws_bytes = {int(ws_bytes)}")
-        if not x.is_contiguous():
-            raise ValueError("workspace: contiguous tensor expected")
-        return self._on(x, "workspace"), have if ws_bytes is None else int(ws_bytes)
-
-    def call(self, where, stream, *args):
-        fn = getattr(load_library(), where)
-        dev = self.device
-        if dev is None or dev.index == torch.cuda.current_device():
-            st = fn(*args, _stream(stream))
-        else:
-            with torch.cuda.device(dev):
-                st = fn(*args, _stream(stream))
-        _check(st, where)
+    _need(x, name, elems, dtype, last)
+    if x.get_device() != dev:
+        raise ValueError(f"{name}: on {x.device}, device {dev} expected")
+    if not x.is_contiguous():
+        raise ValueError(f"{name}: contiguous tensor expected")
+    return x.data_ptr()
 
 
-def _front_args(c, cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens):
-    if not isinstance(qkv, torch.Tensor):
-        p, row = qkv, 0
+def _rows_at(x, name, dtype, tokens, heads, d, dev):
+    """Pointer and row stride of packed rows: [tokens, heads, d] (or [tokens,
+    heads * d]), each token's values in one piece, any distance apart."""
+    if x is None or x.__class__ is int:
+        return x, 0
+    shape, stride = x.shape, x.stride()
+    if x.dtype is not dtype:
+        raise ValueError(f"{name}: dtype {x.dtype}, {dtype} expected")
+    if len(shape) == 3:
+        ok = shape[1] == heads and shape[2] == d and stride[2] == 1 and \
+            (stride[1] == d or heads == 1)
     else:
-        p, row = c.rows(qkv, "qkv", cfg.t_max, cfg.h + 2 * cfg.hkv, cfg.d)
-    return (ctypes.byref(cfg), p, row, c.dense(q_w, "q_w", cfg.d, torch.float32),
-            c.dense(k_w, "k_w", cfg.d, torch.float32),
-            c.dense(inv_freq, "inv_freq", cfg.rot_dim // 2, torch.float32),
-            c.dense(cu_seqlens, "cu_seqlens", cfg.n_max + 1, torch.int32),
-            c.dense(kv_lens, "kv_lens", cfg.n_max, torch.int32))
+        ok = len(shape) == 2 and shape[1] == heads * d and stride[1] == 1
+    many = shape[0] > 1  # a single row's stride says nothing: torch may report any value
+    if not ok or shape[0] < tokens or (many and stride[0] < heads * d):
+        raise ValueError(f"{name}: {tuple(shape)} with strides {stride}, [{tokens}, {heads}, {d}] "
+                         f"with every token's row in one piece expected")
+    if x.get_device() != dev:
+        raise ValueError(f"{name}: on {x.device}, device {dev} expected")
+    return x.data_ptr(), stride[0] if many else 0
+
+
+def _ws_at(x, ws_bytes, dev):
+    if x is None or x.__class__ is int:
+        return x, int(ws_bytes)
+    have = x.numel() * x.element_size()
+    if ws_bytes is not None and int(ws_bytes) > have:
+        raise ValueError(f"workspace: {have} bytes, ws_bytes = {int(ws_bytes)}")
+    if x.get_device() != dev or not x.is_contiguous():
+        raise ValueError(f"workspace: contiguous tensor on device {dev} expected")
+    return x.data_ptr(), have if ws_bytes is None else int(ws_bytes)
+
+
+def _attn_call(where, dev, stream, *args):
+    """The call on its tensors' device, on that device's current stream unless
+    `stream` is given."""
+    fn = getattr(_lib or load_library(), where)
+    if stream is not None:
+        stream = _stream(stream)
+    elif dev is None:
+        stream = _stream(None)
+    elif dev >= 0:
+        stream = _raw_stream(dev)
+    if dev is not None and dev < 0:
+        raise ValueError("device tensor expected")
+    if dev is None or dev == torch.cuda.current_device():
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st:
+        raise GDNError(st, where)
+
+
+def _front_args(cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens, t, dev):
+    d = cfg.d
+    p, row = _rows_at(qkv, "qkv", t, cfg.t_max, cfg.h + 2 * cfg.hkv, d, dev)
+    f32, i32 = torch.float32, torch.int32
+    return (ctypes.byref(cfg), p, row, _at(q_w, "q_w", f32, d, dev), _at(k_w, "k_w", f32, d, dev),
+            _at(inv_freq, "inv_freq", f32, cfg.rot_dim // 2, dev),
+            _at(cu_seqlens, "cu_seqlens", i32, cfg.n_max + 1, dev),
+            _at(kv_lens, "kv_lens", i32, cfg.n_max, dev))
 
 
 def gdn_qk_norm_rope(cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens, q, k, stream=None):
     """RMS norm of every query and key head and rotation by the token's position.
     qkv [t_max, (h + 2 hkv) d] may have any row stride (a multiple of 8)."""
-    c = _Args(cfg)
-    a = _front_args(c, cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens)
-    c.call("gdn_qk_norm_rope", stream, *a,
-           c.dense(q, "q", cfg.t_max * cfg.h * cfg.d, c.dtype, cfg.d),
-           c.dense(k, "k", cfg.t_max * cfg.hkv * cfg.d, c.dtype, cfg.d))
-
-
-def _pool(c, cfg, x, name):
-    return c.dense(x, name, cfg.n_pages * cfg.hkv * cfg.page_size * cfg.d, c.dtype, cfg.d)
+    dev, t, n = _dev(qkv, q, k), _GDN_DTYPE.get(cfg.dtype), cfg.t_max * cfg.d
+    _attn_call("gdn_qk_norm_rope", dev, stream,
+               *_front_args(cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens, t, dev),
+               _at(q, "q", t, n * cfg.h, dev, cfg.d), _at(k, "k", t, n * cfg.hkv, dev, cfg.d))
 
 
 def gdn_kv_append(cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens, block_table, q, k, k_pages,
                   v_pages, stream=None):
     """gdn_qk_norm_rope that also writes k and v into the pages of the cache; q and
     k may be None."""
-    c = _Args(cfg)
-    a = _front_args(c, cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens)
-    c.call("gdn_kv_append", stream, *a,
-           c.dense(block_table, "block_table", cfg.n_max * cfg.max_pages, torch.int32,
-                   cfg.max_pages),
-           c.dense(q, "q", cfg.t_max * cfg.h * cfg.d, c.dtype, cfg.d),
-           c.dense(k, "k", cfg.t_max * cfg.hkv * cfg.d, c.dtype, cfg.d),
-           _pool(c, cfg, k_pages, "k_pages"), _pool(c, cfg, v_pages, "v_pages"))
+    dev, t, d, cols = _dev(qkv, k_pages), _GDN_DTYPE.get(cfg.dtype), cfg.d, cfg.max_pages
+    n, pool = cfg.t_max * d, cfg.n_pages * cfg.hkv * cfg.page_size * d
+    _attn_call("gdn_kv_append", dev, stream,
+               *_front_args(cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens, t, dev),
+               _at(block_table, "block_table", torch.int32, cfg.n_max * cols, dev, cols),
+               _at(q, "q", t, n * cfg.h, dev, d), _at(k, "k", t, n * cfg.hkv, dev, d),
+               _at(k_pages, "k_pages", t, pool, dev, d), _at(v_pages, "v_pages", t, pool, dev, d))
 
 
 def gdn_attn_prefill(cfg, q, k, v, cu_q, cu_k, o, workspace, ws_bytes=None, stream=None):
     """Causal attention over packed prompts; q, k, v [tokens, heads, d] may have any
     row stride (a multiple of 8); cu_k None = cu_q."""
-    c = _Args(cfg)
-    tk = cfg.tk_max or cfg.t_max
-    q, q_row = c.rows(q, "q", cfg.t_max, cfg.h, cfg.d)
-    k, k_row = c.rows(k, "k", tk, cfg.hkv, cfg.d)
-    v, v_row = c.rows(v, "v", tk, cfg.hkv, cfg.d)
-    ws, ws_bytes = c.workspace(workspace, ws_bytes)
-    c.call("gdn_attn_prefill", stream, ctypes.byref(cfg), q, q_row, k, k_row, v, v_row,
-           c.dense(cu_q, "cu_q", cfg.n_max + 1, torch.int32),
-           c.dense(cu_k, "cu_k", cfg.n_max + 1, torch.int32),
-           c.dense(o, "o", cfg.t_max * cfg.h * cfg.d, c.dtype, cfg.d), ws, ws_bytes)
+    dev, t = _dev(q, k, v, o), _GDN_DTYPE.get(cfg.dtype)
+    d, h, hkv, tq, n = cfg.d, cfg.h, cfg.hkv, cfg.t_max, cfg.n_max + 1
+    tk = cfg.tk_max or tq
+    q, q_row = _rows_at(q, "q", t, tq, h, d, dev)
+    k, k_row = _rows_at(k, "k", t, tk, hkv, d, dev)
+    v, v_row = _rows_at(v, "v", t, tk, hkv, d, dev)
+    ws, ws_bytes = _ws_at(workspace, ws_bytes, dev)
+    _attn_call("gdn_attn_prefill", dev, stream, ctypes.byref(cfg), q, q_row, k, k_row, v, v_row,
+               _at(cu_q, "cu_q", torch.int32, n, dev), _at(cu_k, "cu_k", torch.int32, n, dev),
+               _at(o, "o", t, tq * h * d, dev, d), ws, ws_bytes)
 
 
 def gdn_attn_paged(cfg, q, k_pages, v_pages, cu_seqlens, kv_lens, block_table, shared_len, o,
                    workspace, ws_bytes=None, stream=None):
     """Attention of each sequence's new tokens to the pages of the cache; shared_len
     (int32 [1] on the device, or None) positions lie in the same pages for all."""
-    c = _Args(cfg)
-    q, q_row = c.rows(q, "q", cfg.t_max, cfg.h, cfg.d)
-    ws, ws_bytes = c.workspace(workspace, ws_bytes)
-    c.call("gdn_attn_paged", stream, ctypes.byref(cfg), q, q_row,
-           _pool(c, cfg, k_pages, "k_pages"), _pool(c, cfg, v_pages, "v_pages"),
-           c.dense(cu_seqlens, "cu_seqlens", cfg.n_max + 1, torch.int32),
-           c.dense(kv_lens, "kv_lens", cfg.n_max, torch.int32),
-           c.dense(block_table, "block_table", cfg.n_max * cfg.max_pages, torch.int32,
-                   cfg.max_pages),
-           c.dense(shared_len, "shared_len", 1, torch.int32),
-           c.dense(o, "o", cfg.t_max * cfg.h * cfg.d, c.dtype, cfg.d), ws, ws_bytes)
+    dev, t, i32 = _dev(q, k_pages, v_pages, o), _GDN_DTYPE.get(cfg.dtype), torch.int32
+    d, h, tq, n, cols = cfg.d, cfg.h, cfg.t_max, cfg.n_max, cfg.max_pages
+    pool = cfg.n_pages * cfg.hkv * cfg.page_size * d
+    q, q_row = _rows_at(q, "q", t, tq, h, d, dev)
+    ws, ws_bytes = _ws_at(workspace, ws_bytes, dev)
+    _attn_call("gdn_attn_paged", dev, stream, ctypes.byref(cfg), q, q_row,
+               _at(k_pages, "k_pages", t, pool, dev, d), _at(v_pages, "v_pages", t, pool, dev, d),
+               _at(cu_seqlens, "cu_seqlens", i32, n + 1, dev), _at(kv_lens, "kv_lens", i32, n, dev),
+               _at(block_table, "block_table", i32, n * cols, dev, cols),
+               _at(shared_len, "shared_len", i32, 1, dev), _at(o, "o", t, tq * h * d, dev, d), ws,
+               ws_bytes)
 
 
 def rope_inv_freq(rot_dim, base=10000.0, factor=1.0, original_len=None, low_turns=1.0,

@@ -25,15 +25,24 @@ namespace {
 constexpr int kBM = 128;  // query rows per work-group
 constexpr int kBN = 64;   // keys per tile
 
+// instruction kinds of __builtin_amdgcn_sched_group_barrier
+constexpr int kSchedValu = 0x2, kSchedMfma = 0x8, kSchedLds = 0x100;
+
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// A tile in LDS. Tiles are passed in their own address space and indexed in one
+// step from their arrays' start: the compiler then sees which array a read is
+// from, and does not make it wait for copies in flight into the others.
+template <typename T>
+using Lds = __attribute__((address_space(3))) T *;
 
 // Transposing read: within each 16-lane group, lane s supplies four elements
 // of row (s >> 2), columns 4 (s & 3) .., and lane j receives column j of the
 // four rows.
-__device__ __forceinline__ u32x2 tr_read(const void *p) {
-  return __builtin_bit_cast(
-      u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(const_cast<void *>(p))));
+template <typename T>
+__device__ __forceinline__ u32x2 tr_read(Lds<T> tile, int at) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(tile + at)));
 }
 
 // Slots of the query tiles: sequence s starts at slot floor(cu[s] / kBM) + s,
@@ -57,8 +66,6 @@ __device__ __forceinline__ void place(int wg, int h, int slots, int &head, int &
   }
 }
 
-typedef __attribute__((address_space(3))) void lds_void;
-
 template <typename T, int D>
 struct Tile {
   static constexpr int kRowBytes = D * 2;
@@ -71,11 +78,15 @@ struct Tile {
   static __device__ __forceinline__ int v_swz(int r) { return (r & 3) << 2; }
 };
 
+// Waits for this wave's copies into LDS. A barrier alone does not: its ordering
+// covers the wave's own LDS accesses, not copies still in flight.
+__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
 // Copies 64 rows (those of them that the descriptor's range holds, zeros for the
 // others) straight to LDS: lane l of wave w fills the 16 bytes at 4096 i + 1024 w +
 // 16 l with the chunk that belongs there.
 template <typename T, int D, bool kV>
-__device__ __forceinline__ void fetch(T *dst, rsrc_t src, int row_bytes, int lane, int w) {
+__device__ __forceinline__ void fetch(Lds<T> dst, rsrc_t src, int row_bytes, int lane, int w) {
   typedef Tile<T, D> L;
 #pragma unroll
   for (int i = 0; i < L::kLoads; ++i) {
@@ -83,7 +94,7 @@ __device__ __forceinline__ void fetch(T *dst, rsrc_t src, int row_bytes, int lan
     const int row = i * L::kRowsPerLoad + in / L::kRowBytes, at = in % L::kRowBytes / 16;
     const int ch = at ^ (kV ? L::v_swz(row) : L::k_swz(row));
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        src, (lds_void *)(reinterpret_cast<char *>(dst) + 4096 * i + 1024 * w), 16,
+        src, (Lds<void>)(dst + 2048 * i + 512 * w), 16,
         row * row_bytes + 16 * ch, 0, 0, 0);
   }
 }
@@ -96,7 +107,7 @@ struct Rows {
   f32x16 o[D / 32];
   float m, l;  // maximum (log2 scale) and this lane's part of the sum
 
-  __device__ __forceinline__ void step(const T *kt, const T *vt, int k0, int lim, bool masked,
+  __device__ __forceinline__ void step(Lds<T> kt, Lds<T> vt, int k0, int lim, bool masked,
                                        float scale_log2, int lane) {
     typedef Tile<T, D> L;
     const int col = lane & 31, hh = lane >> 5;
@@ -105,15 +116,22 @@ struct Rows {
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int i = 0; i < 16; ++i) sc[t][i] = 0.f;
-    const T *kr = kt + col * D;
     const int kx = L::k_swz(col) ^ hh;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
-      const T *p = kr + 8 * ((2 * i) ^ kx);
+      const int at = col * D + 8 * ((2 * i) ^ kx);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
-        sc[t] = mfma32(*reinterpret_cast<const vec8 *>(p + 32 * t * D), q[i], sc[t]);
+        sc[t] = mfma32(*(Lds<const vec8>)(kt + at + 32 * t * D), q[i], sc[t]);
     }
+    // order: eight fragments ahead, then products and reads in turn
+    __builtin_amdgcn_sched_group_barrier(kSchedLds, D / 16, 0);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMfma, 2, 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedLds, 2, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(kSchedMfma, D / 16, 0);
     if (masked) {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -141,7 +159,6 @@ struct Rows {
     // lane's part of a transposing read: row 4 hh + (s16 >> 2) (+ 8), columns 32 i +
     // 16 gb + 4 (s16 & 3)
     const int s16 = lane & 15, gb = (lane >> 4) & 1, r0 = 4 * hh + (s16 >> 2);
-    const T *vr = vt + r0 * D + 4 * (s16 & 1);
     const int vx = L::v_swz(r0) ^ (2 * gb + ((s16 & 3) >> 1));
     // 16 keys at a time: the weights of the next are formed while the products
     // of these run
@@ -158,11 +175,22 @@ struct Rows {
       const vec8 p = __builtin_bit_cast(vec8, u32x4{wd[0], wd[1], wd[2], wd[3]});
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const T *p0 = vr + 8 * ((4 * i) ^ vx);
-        const u32x2 x = tr_read(p0 + 16 * b * D), y = tr_read(p0 + (16 * b + 8) * D);
+        const int at = r0 * D + 4 * (s16 & 1) + 8 * ((4 * i) ^ vx);
+        const u32x2 x = tr_read<T>(vt, at + 16 * b * D), y = tr_read<T>(vt, at + (16 * b + 8) * D);
         o[i] = mfma32(__builtin_bit_cast(vec8, u32x4{x[0], x[1], y[0], y[1]}), p, o[i]);
       }
     }
+    // order: the first keys' fragments and weights, then under each product the
+    // reads of a later one and a part of the next weights
+    __builtin_amdgcn_sched_group_barrier(kSchedLds, D / 16, 1);
+    __builtin_amdgcn_sched_group_barrier(kSchedValu, 28, 1);
+#pragma unroll
+    for (int i = 0; i < D / 8 - D / 32; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 1);
+      __builtin_amdgcn_sched_group_barrier(kSchedLds, 2, 1);
+      __builtin_amdgcn_sched_group_barrier(kSchedValu, 7, 1);
+    }
+    __builtin_amdgcn_sched_group_barrier(kSchedMfma, D / 32, 1);
   }
 };
 
@@ -213,25 +241,28 @@ __global__ __launch_bounds__(256, D == 128 ? 2 : 1) void attn_prefill_kernel(Pre
   const T *vp = static_cast<const T *>(a.v) + (int64_t)kb * a.v_row + kvh * D;
   const int k_bytes = (int)a.k_row * 2, v_bytes = (int)a.v_row * 2;
   // a tile's rows as a range that ends with the sequence's last key
-  auto get = [&](int j, T *kt, T *vt) __attribute__((always_inline)) {
+  auto get = [&](int j, Lds<T> kt, Lds<T> vt) __attribute__((always_inline)) {
     const int64_t k0 = (int64_t)j * kBN;
     const int rows = min(kBN, lk - (int)k0);
     fetch<T, D, false>(kt, make_rsrc(kp + k0 * a.k_row, (rows - 1) * k_bytes + D * 2), k_bytes, lane, w);
     fetch<T, D, true>(vt, make_rsrc(vp + k0 * a.v_row, (rows - 1) * v_bytes + D * 2), v_bytes, lane, w);
   };
-  auto step = [&](int j, const T *kt, const T *vt) __attribute__((always_inline)) {
+  auto step = [&](int j, Lds<T> kt, Lds<T> vt) __attribute__((always_inline)) {
     const int k0 = j * kBN;
     if (k0 <= wave_hi) x.step(kt, vt, k0, lim, k0 + kBN - 1 > wave_lo, a.scale_log2, lane);
   };
-  if (tiles > 0) get(0, k_a, v_a);
+  auto L = [](T *p) { return (Lds<T>)p; };
+  if (tiles > 0) get(0, L(k_a), L(v_a));
   for (int j = 0; j < tiles; j += 2) {
+    wait_copies();
     __syncthreads();  // tile j is there, and the other pair is no longer read
-    if (j + 1 < tiles) get(j + 1, k_b, v_b);
-    step(j, k_a, v_a);
+    if (j + 1 < tiles) get(j + 1, L(k_b), L(v_b));
+    step(j, L(k_a), L(v_a));
     if (j + 1 >= tiles) break;
+    wait_copies();
     __syncthreads();
-    if (j + 2 < tiles) get(j + 2, k_a, v_a);
-    step(j + 1, k_b, v_b);
+    if (j + 2 < tiles) get(j + 2, L(k_a), L(v_a));
+    step(j + 1, L(k_b), L(v_b));
   }
 
   const float l = sum32(x.l);

@@ -22,9 +22,6 @@ namespace gdn {
 
 namespace {
 
-constexpr int kBM = 128;  // query rows per work-group
-constexpr int kBN = 64;   // keys per tile
-
 // instruction kinds of __builtin_amdgcn_sched_group_barrier
 constexpr int kSchedValu = 0x2, kSchedMfma = 0x8, kSchedLds = 0x100;
 
@@ -45,12 +42,10 @@ __device__ __forceinline__ u32x2 tr_read(Lds<T> tile, int at) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(tile + at)));
 }
 
-// Slots of the query tiles: sequence s starts at slot floor(cu[s] / kBM) + s,
-// which is distinct for every tile of the batch and grows with s, so a slot's
-// sequence is found by a search and no table is needed.
-__host__ __device__ inline int64_t tile_slots(int64_t t_max, int64_t n_max) {
-  return t_max / kBM + n_max;
-}
+// Slots of the query tiles of bm rows: sequence s starts at slot floor(cu[s] / bm)
+// + s, which is distinct for every tile of the batch and grows with s, so a
+// slot's sequence is found by a search and no table is needed.
+inline int64_t tile_slots(int64_t t_max, int64_t n_max, int bm) { return t_max / bm + n_max; }
 
 // Head and tile slot of a work-group. The last (longest) tiles come first. With
 // a multiple of 8 heads, neighbouring heads (which read the same keys) go to one
@@ -66,82 +61,112 @@ __device__ __forceinline__ void place(int wg, int h, int slots, int &head, int &
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, int kBN, int kWaves>
 struct Tile {
   static constexpr int kRowBytes = D * 2;
-  static constexpr int kLoads = kBN * kRowBytes / 4096;  // per wave: 1 KB each
-  static constexpr int kRowsPerLoad = 4096 / kRowBytes;  // of the work-group's four waves
-  // Chunk (16 bytes) in which row r keeps its chunk c. For K, whose fragments
-  // take one chunk of 32 rows, the rows differ in the low bits; for V, whose
-  // transposing reads take four neighbouring chunks of four rows, in bits 2, 3.
-  static __device__ __forceinline__ int k_swz(int r) { return r & 15; }
-  static __device__ __forceinline__ int v_swz(int r) { return (r & 3) << 2; }
+  static constexpr int kPass = 1024 * kWaves;            // bytes the waves copy at a time
+  static constexpr int kLoads = kBN * kRowBytes / kPass;
+  static constexpr int kRowsPerLoad = kPass / kRowBytes;
 };
+// Chunk (16 bytes) in which row r keeps its chunk c: c ^ swizzle(r). For K, whose
+// fragments take one chunk of 32 rows, the rows differ in the low bits; for V,
+// whose transposing reads take four neighbouring chunks of four rows, in bits 2, 3.
+__device__ __forceinline__ int k_swz(int r) { return r & 15; }
+__device__ __forceinline__ int v_swz(int r) { return (r & 3) << 2; }
+
+// A value the compiler may not see through: what is derived from it is formed
+// anew at each use, where keeping it would cost registers all along the loop.
+template <bool kDo>
+__device__ __forceinline__ int opaque(int x) {
+  if constexpr (kDo) asm volatile("" : "+v"(x));
+  return x;
+}
 
 // Waits for this wave's copies into LDS. A barrier alone does not: its ordering
 // covers the wave's own LDS accesses, not copies still in flight.
-__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
-// Copies 64 rows (those of them that the descriptor's range holds, zeros for the
-// others) straight to LDS: lane l of wave w fills the 16 bytes at 4096 i + 1024 w +
-// 16 l with the chunk that belongs there.
-template <typename T, int D, bool kV>
-__device__ __forceinline__ void fetch(Lds<T> dst, rsrc_t src, int row_bytes, int lane, int w) {
-  typedef Tile<T, D> L;
-#pragma unroll
-  for (int i = 0; i < L::kLoads; ++i) {
-    const int in = 1024 * w + 16 * lane;
-    const int row = i * L::kRowsPerLoad + in / L::kRowBytes, at = in % L::kRowBytes / 16;
-    const int ch = at ^ (kV ? L::v_swz(row) : L::k_swz(row));
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        src, (Lds<void>)(dst + 2048 * i + 512 * w), 16,
-        row * row_bytes + 16 * ch, 0, 0, 0);
-  }
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+  asm volatile("" ::: "memory");
 }
 
-// One query tile's running state, and its step over one tile of keys.
-template <typename T, int D>
+// Copies kBN rows (those of them that the descriptor's range holds, zeros for the
+// others) straight to LDS: lane l of wave w fills the 16 bytes at kPass i + 1024 w +
+// 16 l with the chunk that belongs there.
+template <typename T, int D, int kBN, int kWaves, bool kV>
+__device__ __forceinline__ void fetch(Lds<T> dst, rsrc_t src, int row_bytes, int lane, int w) {
+  typedef Tile<T, D, kBN, kWaves> L;
+  // rows kRowsPerLoad apart (a multiple of 16) have the same swizzle, so a lane's
+  // places in one copy and the next differ by whole rows
+  static_assert(L::kRowsPerLoad % 16 == 0, "swizzles repeat every 16 rows");
+  const int in = 1024 * w + 16 * lane;
+  const int row = in / L::kRowBytes, ch = in % L::kRowBytes / 16 ^ (kV ? v_swz(row) : k_swz(row));
+  const int from = opaque<D == 256>(row * row_bytes + 16 * ch);
+#pragma unroll
+  for (int i = 0; i < L::kLoads; ++i)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (Lds<void>)(dst + L::kPass / 2 * i + 512 * w), 16,
+                                             from + i * L::kRowsPerLoad * row_bytes, 0, 0, 0);
+}
+
+// Running state of a wave's 32 query rows, and its two parts of a step over a
+// tile of keys.
+template <typename T, int D, int kBN>
 struct Rows {
   typedef typename Elem<T>::vec8 vec8;
+  static constexpr int kT = kBN / 32;
   vec8 q[D / 16];
   f32x16 o[D / 32];
+  f32x16 sc[kT];
   float m, l;  // maximum (log2 scale) and this lane's part of the sum
 
-  __device__ __forceinline__ void step(Lds<T> kt, Lds<T> vt, int k0, int lim, bool masked,
-                                       float scale_log2, int lane) {
-    typedef Tile<T, D> L;
-    const int col = lane & 31, hh = lane >> 5;
-    f32x16 sc[2];
+  __device__ __forceinline__ void load(const T *row, int hh) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int i = 0; i < D / 16; ++i)
+      q[i] = *reinterpret_cast<const vec8 *>(row + 8 * hh + 16 * i);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
+    m = kNegInf;
+    l = 0.f;
+  }
+
+  // Scores of the tile, and the running maximum.
+  __device__ __forceinline__ void score(Lds<T> kt, int k0, int lim, bool masked, float scale_log2,
+                                        int lane) {
+    const int col = lane & 31, hh = lane >> 5;
+#pragma unroll
+    for (int t = 0; t < kT; ++t)
 #pragma unroll
       for (int i = 0; i < 16; ++i) sc[t][i] = 0.f;
-    const int kx = L::k_swz(col) ^ hh;
+    // row col, chunk (2 i + hh) ^ swizzle: rows are multiples of 128 values, so the
+    // chunk's changes are bit flips of one address
+    const int base = opaque<D == 256>(col * D + 8 * (k_swz(col) ^ hh));
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
-      const int at = col * D + 8 * ((2 * i) ^ kx);
+      const int at = (base ^ (16 * (i & 7))) + 128 * (i >> 3);
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < kT; ++t)
         sc[t] = mfma32(*(Lds<const vec8>)(kt + at + 32 * t * D), q[i], sc[t]);
     }
     // order: eight fragments ahead, then products and reads in turn
-    __builtin_amdgcn_sched_group_barrier(kSchedLds, D / 16, 0);
+    __builtin_amdgcn_sched_group_barrier(kSchedLds, 8, 0);
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
+    for (int i = 0; i < D / 16 * kT / 2 - 4; ++i) {
       __builtin_amdgcn_sched_group_barrier(kSchedMfma, 2, 0);
       __builtin_amdgcn_sched_group_barrier(kSchedLds, 2, 0);
     }
-    __builtin_amdgcn_sched_group_barrier(kSchedMfma, D / 16, 0);
+    __builtin_amdgcn_sched_group_barrier(kSchedMfma, 8, 0);
     if (masked) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < kT; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           sc[t][i] = k0 + 32 * t + 8 * (i >> 2) + 4 * hh + (i & 3) <= lim ? sc[t][i] : kNegInf;
     }
     float mx = kNegInf;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < kT; ++t)
 #pragma unroll
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, sc[t][i]);
     mx = max32(mx) * scale_log2;
@@ -155,15 +180,20 @@ struct Rows {
 #pragma unroll
         for (int k = 0; k < 16; ++k) o[i][k] *= al;
     }
+  }
+
+  // Weights of the tile, and their products with its values.
+  __device__ __forceinline__ void weigh(Lds<T> vt, float scale_log2, int lane) {
     const float ms = m == kNegInf ? 0.f : m;
     // lane's part of a transposing read: row 4 hh + (s16 >> 2) (+ 8), columns 32 i +
     // 16 gb + 4 (s16 & 3)
-    const int s16 = lane & 15, gb = (lane >> 4) & 1, r0 = 4 * hh + (s16 >> 2);
-    const int vx = L::v_swz(r0) ^ (2 * gb + ((s16 & 3) >> 1));
+    const int hh = lane >> 5, s16 = lane & 15, gb = (lane >> 4) & 1, r0 = 4 * hh + (s16 >> 2);
+    const int base =
+        opaque<D == 256>(r0 * D + 4 * (s16 & 1) + 8 * (v_swz(r0) ^ (2 * gb + ((s16 & 3) >> 1))));
     // 16 keys at a time: the weights of the next are formed while the products
     // of these run
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
+    for (int b = 0; b < 2 * kT; ++b) {
       uint32_t wd[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -175,130 +205,202 @@ struct Rows {
       const vec8 p = __builtin_bit_cast(vec8, u32x4{wd[0], wd[1], wd[2], wd[3]});
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const int at = r0 * D + 4 * (s16 & 1) + 8 * ((4 * i) ^ vx);
+        const int at = (base ^ (32 * (i & 3))) + 128 * (i >> 2);
         const u32x2 x = tr_read<T>(vt, at + 16 * b * D), y = tr_read<T>(vt, at + (16 * b + 8) * D);
         o[i] = mfma32(__builtin_bit_cast(vec8, u32x4{x[0], x[1], y[0], y[1]}), p, o[i]);
       }
     }
     // order: the first keys' fragments and weights, then under each product the
     // reads of a later one and a part of the next weights
-    __builtin_amdgcn_sched_group_barrier(kSchedLds, D / 16, 1);
+    __builtin_amdgcn_sched_group_barrier(kSchedLds, 8, 1);
     __builtin_amdgcn_sched_group_barrier(kSchedValu, 28, 1);
 #pragma unroll
-    for (int i = 0; i < D / 8 - D / 32; ++i) {
+    for (int i = 0; i < D / 32 * 2 * kT - 4; ++i) {
       __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 1);
       __builtin_amdgcn_sched_group_barrier(kSchedLds, 2, 1);
-      __builtin_amdgcn_sched_group_barrier(kSchedValu, 7, 1);
+      __builtin_amdgcn_sched_group_barrier(kSchedValu, D == 128 ? 7 : 4, 1);
     }
-    __builtin_amdgcn_sched_group_barrier(kSchedMfma, D / 32, 1);
+    __builtin_amdgcn_sched_group_barrier(kSchedMfma, 4, 1);
+  }
+
+  __device__ __forceinline__ void store(T *row, int hh) const {
+    const float sum = sum32(l);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that sees no key gives zeros
+    if (!row) return;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        *reinterpret_cast<u32x2 *>(row + 4 * hh + 32 * i + 8 * b) =
+            u32x2{Elem<T>::pack(o[i][4 * b] * inv, o[i][4 * b + 1] * inv),
+                  Elem<T>::pack(o[i][4 * b + 2] * inv, o[i][4 * b + 3] * inv)};
   }
 };
 
-template <typename T, int D>
-__global__ __launch_bounds__(256, D == 128 ? 2 : 1) void attn_prefill_kernel(PrefillArgs a,
-                                                                            int slots) {
+// The tile of a work-group: its sequence, rows and keys.
+struct Where {
+  int head, qb, lq, kb, lk, q0, past;
+};
+template <int kBM>
+__device__ __forceinline__ bool find(const PrefillArgs &a, int slots, int lane, Where &t) {
+  int slot;
+  place(flat_block(), a.h, slots, t.head, slot);
+  if (slot < 0) return false;  // past the grid's count (last row)
+  const int s = wave_search(a.n_max, slot, lane,
+                            [&](int i) { return cu_at(a.cu_q, i, a.t_max) / kBM + i; });
+  t.qb = cu_at(a.cu_q, s, a.t_max);
+  t.lq = cu_end(a.cu_q, s, t.qb, a.t_max) - t.qb;
+  t.q0 = (slot - (t.qb / kBM + s)) * kBM;
+  if (t.q0 < 0 || t.q0 >= t.lq) return false;  // no tile of the sequence has this slot
+  t.kb = cu_at(a.cu_k, s, a.tk_max);
+  t.lk = cu_end(a.cu_k, s, t.kb, a.tk_max) - t.kb;
+  t.past = t.lk - t.lq;  // row r sees keys 0 .. past + r
+  return true;
+}
+
+// kWaves waves of 32 rows. With four, two work-groups share a CU (D = 128) and
+// overlap by chance. With eight, the two waves of a SIMD (w and w + 4) go through
+// the two parts of a step in opposite order, a barrier after each part: while one
+// runs its score products the other forms weights.
+template <typename T, int D, int kBN, int kWaves>
+__global__ __launch_bounds__(64 * kWaves, kWaves == 8 || D == 128 ? 2 : 1) void attn_prefill_kernel(
+    PrefillArgs a, int slots) {
+  constexpr int kBM = 32 * kWaves;
   // four arrays of their own, so that a tile in flight is known to be another
   // than the ones being read
   __shared__ __attribute__((aligned(16))) T k_a[kBN * D], v_a[kBN * D], k_b[kBN * D], v_b[kBN * D];
 
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, hh = lane >> 5;
-  const int wg = flat_block();
-  int head, slot;
-  place(wg, a.h, slots, head, slot);
-  if (slot < 0) return;  // past the grid's count (last row)
-  const int s = wave_search(a.n_max, slot, lane,
-                            [&](int i) { return cu_at(a.cu_q, i, a.t_max) / kBM + i; });
-  const int qb = cu_at(a.cu_q, s, a.t_max), lq = cu_end(a.cu_q, s, qb, a.t_max) - qb;
-  const int q0 = (slot - (qb / kBM + s)) * kBM;
-  if (q0 < 0 || q0 >= lq) return;  // no tile of the sequence has this slot
-  const int kb = cu_at(a.cu_k, s, a.tk_max), lk = cu_end(a.cu_k, s, kb, a.tk_max) - kb;
-  const int kvh = head / (a.h / a.hkv);
-  const int past = lk - lq;  // row r sees keys 0 .. past + r
-
-  const int r0 = q0 + 32 * w;                  // the wave's first row
-  const int r = min(r0 + col, lq - 1);         // this lane's row (the last one again past the end)
-  const int lim = past + r;
-  const int wave_lo = past + min(r0, lq - 1), wave_hi = past + min(r0 + 31, lq - 1);
-  const int keys = min(past + min(q0 + kBM, lq), lk);  // keys any row of the tile sees
+  Where t;
+  if (!find<kBM>(a, slots, lane, t)) return;
+  const int kvh = t.head / (a.h / a.hkv);
+  const int r0 = t.q0 + 32 * w;                // the wave's first row
+  const int r = min(r0 + col, t.lq - 1);       // this lane's row (the last one again past the end)
+  const int lim = t.past + r;
+  const int wave_lo = t.past + min(r0, t.lq - 1), wave_hi = t.past + min(r0 + 31, t.lq - 1);
+  const int keys = min(t.past + min(t.q0 + kBM, t.lq), t.lk);  // keys any row of the tile sees
   const int tiles = keys > 0 ? (keys + kBN - 1) / kBN : 0;
 
-  Rows<T, D> x;
-  {
-    const T *qp = static_cast<const T *>(a.q) + (int64_t)(qb + r) * a.q_row + head * D + 8 * hh;
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-      x.q[i] = *reinterpret_cast<const typename Rows<T, D>::vec8 *>(qp + 16 * i);
-  }
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-    for (int j = 0; j < 16; ++j) x.o[i][j] = 0.f;
-  x.m = kNegInf;
-  x.l = 0.f;
-
-  const T *kp = static_cast<const T *>(a.k) + (int64_t)kb * a.k_row + kvh * D;
-  const T *vp = static_cast<const T *>(a.v) + (int64_t)kb * a.v_row + kvh * D;
+  const T *kp = static_cast<const T *>(a.k) + (int64_t)t.kb * a.k_row + kvh * D;
+  const T *vp = static_cast<const T *>(a.v) + (int64_t)t.kb * a.v_row + kvh * D;
   const int k_bytes = (int)a.k_row * 2, v_bytes = (int)a.v_row * 2;
   // a tile's rows as a range that ends with the sequence's last key
-  auto get = [&](int j, Lds<T> kt, Lds<T> vt) __attribute__((always_inline)) {
+  auto get_k = [&](int j, T *kt) __attribute__((always_inline)) {
     const int64_t k0 = (int64_t)j * kBN;
-    const int rows = min(kBN, lk - (int)k0);
-    fetch<T, D, false>(kt, make_rsrc(kp + k0 * a.k_row, (rows - 1) * k_bytes + D * 2), k_bytes, lane, w);
-    fetch<T, D, true>(vt, make_rsrc(vp + k0 * a.v_row, (rows - 1) * v_bytes + D * 2), v_bytes, lane, w);
+    fetch<T, D, kBN, kWaves, false>((Lds<T>)kt,
+        make_rsrc(kp + k0 * a.k_row, (min(kBN, t.lk - (int)k0) - 1) * k_bytes + D * 2), k_bytes, lane, w);
   };
-  auto step = [&](int j, Lds<T> kt, Lds<T> vt) __attribute__((always_inline)) {
+  auto get_v = [&](int j, T *vt) __attribute__((always_inline)) {
+    const int64_t k0 = (int64_t)j * kBN;
+    fetch<T, D, kBN, kWaves, true>((Lds<T>)vt,
+        make_rsrc(vp + k0 * a.v_row, (min(kBN, t.lk - (int)k0) - 1) * v_bytes + D * 2), v_bytes, lane, w);
+  };
+  Rows<T, D, kBN> x;
+  if (tiles > 0) {
+    get_k(0, k_a);
+    get_v(0, v_a);
+  }
+  x.load(static_cast<const T *>(a.q) + (int64_t)(t.qb + r) * a.q_row + t.head * D, hh);
+  auto score = [&](int j, T *kt) __attribute__((always_inline)) {
     const int k0 = j * kBN;
-    if (k0 <= wave_hi) x.step(kt, vt, k0, lim, k0 + kBN - 1 > wave_lo, a.scale_log2, lane);
+    if (k0 <= wave_hi)
+      x.score((Lds<T>)kt, k0, lim, k0 + kBN - 1 > wave_lo, a.scale_log2, lane);
   };
-  auto L = [](T *p) { return (Lds<T>)p; };
-  if (tiles > 0) get(0, L(k_a), L(v_a));
-  for (int j = 0; j < tiles; j += 2) {
-    wait_copies();
-    __syncthreads();  // tile j is there, and the other pair is no longer read
-    if (j + 1 < tiles) get(j + 1, L(k_b), L(v_b));
-    step(j, L(k_a), L(v_a));
-    if (j + 1 >= tiles) break;
+  auto weigh = [&](int j, T *vt) __attribute__((always_inline)) {
+    if (j * kBN <= wave_hi) x.weigh((Lds<T>)vt, a.scale_log2, lane);
+  };
+  if constexpr (kWaves == 4) {
+    for (int j = 0; j < tiles; j += 2) {
+      wait_copies();
+      __syncthreads();  // tile j is there, and the other pair is no longer read
+      if (j + 1 < tiles) {
+        get_k(j + 1, k_b);
+        get_v(j + 1, v_b);
+      }
+      score(j, k_a);
+      weigh(j, v_a);
+      if (j + 1 >= tiles) break;
+      wait_copies();
+      __syncthreads();
+      if (j + 2 < tiles) {
+        get_k(j + 2, k_a);
+        get_v(j + 2, v_a);
+      }
+      score(j + 1, k_b);
+      weigh(j + 1, v_b);
+    }
+  } else {
+    // Phase p, one barrier each: waves 0 .. 3 score tile p / 2 in the even ones and
+    // weigh it in the odd ones, waves 4 .. 7 one phase later. K of tile j + 1 is
+    // copied from the end of phase 2 j (its place was last read in 2 j - 1) and
+    // first read in 2 j + 2; V of tile j + 1 from the end of 2 j + 1 (last read in
+    // 2 j) for 2 j + 3: each has a whole phase, and is waited for at its end.
+    auto k_end = [&](int j, T *kt) __attribute__((always_inline)) {
+      wait_copies();
+      if (j < tiles) get_k(j, kt);
+      __syncthreads();
+    };
+    auto v_end = [&](int j, T *vt) __attribute__((always_inline)) {
+      wait_copies();
+      if (j < tiles) get_v(j, vt);
+      __syncthreads();
+    };
     wait_copies();
     __syncthreads();
-    if (j + 2 < tiles) get(j + 2, L(k_a), L(v_a));
-    step(j + 1, L(k_b), L(v_b));
+    if (w < 4) {
+      for (int j = 0; j < tiles; j += 2) {
+        score(j, k_a);
+        k_end(j + 1, k_b);
+        weigh(j, v_a);
+        v_end(j + 1, v_b);
+        if (j + 1 >= tiles) break;
+        score(j + 1, k_b);
+        k_end(j + 2, k_a);
+        weigh(j + 1, v_b);
+        v_end(j + 2, v_a);
+      }
+      __syncthreads();
+    } else {
+      k_end(1, k_b);
+      for (int j = 0; j < tiles; j += 2) {
+        score(j, k_a);
+        v_end(j + 1, v_b);
+        weigh(j, v_a);
+        k_end(j + 2, k_a);
+        if (j + 1 >= tiles) break;
+        score(j + 1, k_b);
+        v_end(j + 2, v_a);
+        weigh(j + 1, v_b);
+        k_end(j + 3, k_b);
+      }
+    }
   }
+  x.store(r0 + col < t.lq
+              ? static_cast<T *>(a.o) + ((int64_t)(t.qb + r0 + col) * a.h + t.head) * D
+              : nullptr, hh);
+}
 
-  const float l = sum32(x.l);
-  const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees no key gives zeros
-  if (r0 + col >= lq) return;
-  T *op = static_cast<T *>(a.o) + ((int64_t)(qb + r0 + col) * a.h + head) * D + 4 * hh;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-      *reinterpret_cast<u32x2 *>(op + 32 * i + 8 * b) =
-          u32x2{Elem<T>::pack(x.o[i][4 * b] * inv, x.o[i][4 * b + 1] * inv),
-                Elem<T>::pack(x.o[i][4 * b + 2] * inv, x.o[i][4 * b + 3] * inv)};
+template <typename T, int D, int kBN, int kWaves>
+hipError_t run(const gdn_attn_config *cfg, const PrefillArgs &a, hipStream_t stream) {
+  const int64_t slots = tile_slots(cfg->t_max, cfg->n_max, 32 * kWaves);
+  dim3 grid;
+  if (!flat_grid(slots * cfg->h, 64 * kWaves, grid)) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((attn_prefill_kernel<T, D, kBN, kWaves>), grid, dim3(64 * kWaves), 0, stream, a,
+                     static_cast<int>(slots));
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t run_of(const gdn_attn_config *cfg, const PrefillArgs &a, hipStream_t stream) {
+  return cfg->d == 128 ? run<T, 128, 64, 4>(cfg, a, stream) : run<T, 256, 64, 8>(cfg, a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_attn_prefill(const gdn_attn_config *cfg, PrefillArgs a, hipStream_t stream) {
   if (cfg->t_max == 0) return hipSuccess;
-  const int64_t slots = tile_slots(cfg->t_max, cfg->n_max);
-  dim3 grid;
-  if (!flat_grid(slots * cfg->h, 256, grid)) return hipErrorInvalidValue;
-  const dim3 block(256);
-  const int n = static_cast<int>(slots);
-  if (cfg->dtype == GDN_BF16) {
-    if (cfg->d == 128)
-      hipLaunchKernelGGL((attn_prefill_kernel<__bf16, 128>), grid, block, 0, stream, a, n);
-    else
-      hipLaunchKernelGGL((attn_prefill_kernel<__bf16, 256>), grid, block, 0, stream, a, n);
-  } else {
-    if (cfg->d == 128)
-      hipLaunchKernelGGL((attn_prefill_kernel<_Float16, 128>), grid, block, 0, stream, a, n);
-    else
-      hipLaunchKernelGGL((attn_prefill_kernel<_Float16, 256>), grid, block, 0, stream, a, n);
-  }
-  return hipGetLastError();
+  return cfg->dtype == GDN_BF16 ? run_of<__bf16>(cfg, a, stream) : run_of<_Float16>(cfg, a, stream);
 }
 
 }  // namespace gdn

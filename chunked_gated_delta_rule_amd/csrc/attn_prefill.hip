@@ -82,11 +82,17 @@ __device__ __forceinline__ int opaque(int x) {
   return x;
 }
 
-// Waits for this wave's copies into LDS. A barrier alone does not: its ordering
-// covers the wave's own LDS accesses, not copies still in flight.
-__device__ __forceinline__ void wait_copies() {
+// Waits for this wave's reads of LDS and copies into it (lgkmcnt(0), vmcnt(0)).
+__device__ __forceinline__ void wait_lds() {
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+  __builtin_amdgcn_s_waitcnt(0x0070);
+  asm volatile("" ::: "memory");
+}
+// A barrier that leaves copies issued since wait_lds() in flight (__syncthreads
+// would wait for them).
+__device__ __forceinline__ void barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
 
@@ -312,8 +318,8 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 || D == 128 ? 2 : 1) void 
   };
   if constexpr (kWaves == 4) {
     for (int j = 0; j < tiles; j += 2) {
-      wait_copies();
-      __syncthreads();  // tile j is there, and the other pair is no longer read
+      wait_lds();
+      barrier();  // tile j is there, and the other pair is no longer read
       if (j + 1 < tiles) {
         get_k(j + 1, k_b);
         get_v(j + 1, v_b);
@@ -321,8 +327,8 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 || D == 128 ? 2 : 1) void 
       score(j, k_a);
       weigh(j, v_a);
       if (j + 1 >= tiles) break;
-      wait_copies();
-      __syncthreads();
+      wait_lds();
+      barrier();
       if (j + 2 < tiles) {
         get_k(j + 2, k_a);
         get_v(j + 2, v_a);
@@ -337,17 +343,17 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 || D == 128 ? 2 : 1) void 
     // first read in 2 j + 2; V of tile j + 1 from the end of 2 j + 1 (last read in
     // 2 j) for 2 j + 3: each has a whole phase, and is waited for at its end.
     auto k_end = [&](int j, T *kt) __attribute__((always_inline)) {
-      wait_copies();
+      wait_lds();
       if (j < tiles) get_k(j, kt);
-      __syncthreads();
+      barrier();
     };
     auto v_end = [&](int j, T *vt) __attribute__((always_inline)) {
-      wait_copies();
+      wait_lds();
       if (j < tiles) get_v(j, vt);
-      __syncthreads();
+      barrier();
     };
-    wait_copies();
-    __syncthreads();
+    wait_lds();
+    barrier();
     if (w < 4) {
       for (int j = 0; j < tiles; j += 2) {
         score(j, k_a);
@@ -360,7 +366,7 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 || D == 128 ? 2 : 1) void 
         weigh(j + 1, v_b);
         v_end(j + 2, v_a);
       }
-      __syncthreads();
+      barrier();
     } else {
       k_end(1, k_b);
       for (int j = 0; j < tiles; j += 2) {

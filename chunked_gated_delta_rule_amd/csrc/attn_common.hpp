@@ -80,28 +80,59 @@ constexpr float kNegInf = -__builtin_inff();
 // in the fp32 sums, and the output sums are rescaled a few times per row only.
 constexpr float kRescaleLog2 = 8.f;
 
-// Last s in [0, n) with key(s) <= x, for a non-decreasing key with key(0) <= x,
-// by one wave: 64 probes per level (n <= 16384: at most three levels). With a
-// key that is not sorted the answer is some s in [0, n).
+// Narrows [0, n) to at most 64 indexes that hold the last s with key(s) <= x, for
+// a non-decreasing key with key(0) <= x, by one wave: 64 probes per level (n <=
+// 16384: at most two levels). [lo, lo + len) stays inside [0, n) for any key.
 template <typename F>
-__device__ __forceinline__ int wave_search(int n, int x, int lane, F key) {
-  int lo = 0, len = n;
-  while (len > 1) {
+__device__ __forceinline__ void narrow(int n, int x, int lane, int &lo, int &len, F key) {
+  lo = 0;
+  len = n;
+  while (len > 64) {
     const int step = (len + 63) / 64;
     const int at = lane * step;
     const bool in = at < len && key(lo + at) <= x;
-    const int hits = max(__popcll(__ballot(in)), 1);
-    const int skip = (hits - 1) * step;
+    const int skip = (max(__popcll(__ballot(in)), 1) - 1) * step;
     lo += skip;
     len = min(step, len - skip);
   }
-  return lo;
 }
 
-// Sequence of packed row t (t < cu[n_max]).
-__device__ __forceinline__ int seq_of_row(const int32_t *__restrict__ cu, int n_max, int t_max,
-                                          int t, int lane) {
-  return wave_search(n_max, t, lane, [&](int s) { return cu_at(cu, s, t_max); });
+// A packed sequence: index, first row, rows.
+struct Packed {
+  int s, b, n;
+};
+
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// The last sequence s of the batch whose key(s, first row of s) is at most x. Each
+// lane of the last level loads what belongs to its sequence, extra(s) included,
+// and the chosen lane's values are handed out: one round trip to memory for up to
+// 64 sequences.
+template <int kExtra, typename F, typename G>
+__device__ __forceinline__ Packed locate(const int32_t *__restrict__ cu, int n_max, int t_max, int x,
+                                         int lane, F key, G extra, int (&out)[kExtra]) {
+  int lo, len;
+  narrow(n_max, x, lane, lo, len, [&](int s) { return key(s, cu_at(cu, s, t_max)); });
+  const int s = min(lo + lane, n_max - 1);
+  const int b = cu_at(cu, s, t_max), n = cu_end(cu, s, b, t_max) - b;
+  int mine[kExtra];
+  extra(s, mine);
+  const int hit = max(__popcll(__ballot(lane < len && key(s, b) <= x)), 1) - 1;
+#pragma unroll
+  for (int i = 0; i < kExtra; ++i) out[i] = __builtin_amdgcn_readlane(mine[i], hit);
+  return {uniform(lo + hit), __builtin_amdgcn_readlane(b, hit), __builtin_amdgcn_readlane(n, hit)};
+}
+
+// Sequence of packed row t (t < cu[n_max]) and its value of `extra`.
+template <typename G>
+__device__ __forceinline__ Packed seq_of_row(const int32_t *__restrict__ cu, int n_max, int t_max,
+                                             int t, int lane, G extra, int &out) {
+  int v[1];
+  const Packed p = locate(
+      cu, n_max, t_max, t, lane, [](int, int b) { return b; },
+      [&](int s, int(&o)[1]) { o[0] = extra(s); }, v);
+  out = v[0];
+  return p;
 }
 
 }  // namespace gdn

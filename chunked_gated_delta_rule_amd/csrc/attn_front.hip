@@ -69,10 +69,12 @@ __global__ __launch_bounds__(kFrontThreads) void attn_front_kernel(FrontArgs a) 
   };
   load(hd);
 
-  const int s = seq_of_row(a.cu, a.n_max, a.t_max, t, lane);
-  const int bos = cu_at(a.cu, s, a.t_max), eos = cu_end(a.cu, s, bos, a.t_max);
+  int len = 0;
+  const Packed p = seq_of_row(
+      a.cu, a.n_max, a.t_max, t, lane, [&](int i) { return a.kv_lens ? a.kv_lens[i] : 0; }, len);
+  const int s = p.s;
   // kv_lens is the caller's: the position is formed in 64 bits
-  const int64_t pos = a.kv_lens ? (int64_t)a.kv_lens[s] - (eos - t) : t - bos;
+  const int64_t pos = a.kv_lens ? (int64_t)len - (p.b + p.n - t) : t - p.b;
   for (int i = tid; i < half; i += kFrontThreads) {
     const double turns = (double)pos * (double)a.inv_freq[i] * kInvTwoPi;
     const float f = (float)(turns - __builtin_rint(turns));  // -1/2 .. 1/2

@@ -31,6 +31,7 @@ struct PrefillArgs {
   void *o;
   int t_max, tk_max, n_max, h, hkv;
   float scale_log2;  // score scale * log2(e)
+  int share;         // query heads of one key head that a tile's rows share
 };
 hipError_t launch_attn_prefill(const gdn_attn_config *cfg, PrefillArgs a, hipStream_t stream);
 

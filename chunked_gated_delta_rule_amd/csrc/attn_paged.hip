@@ -429,8 +429,11 @@ __global__ __launch_bounds__(256) void attn_join_kernel(PagedArgs a) {
   const int tid = threadIdx.x, lane = tid & 63;
   if (t >= cu_at(a.cu, a.n_max, a.t_max)) return;
   const int G = a.h / a.hkv, kh = head / G;
-  const int s = seq_of_row(a.cu, a.n_max, a.t_max, t, lane);
-  const Seq q = seq_at(a, s);
+  int kv;
+  const Packed p = seq_of_row(
+      a.cu, a.n_max, a.t_max, t, lane, [&](int i) { return seq_at(a, i).kv; }, kv);
+  const int s = p.s;
+  const Seq q{p.b, p.n, kv};
   if (t < q.bos || t >= q.bos + q.n) return;  // an unsorted cu_seqlens: a row of no sequence
   const int prefix = a.plan[0];
   const int64_t per_head = reinterpret_cast<const int64_t *>(a.plan)[1];

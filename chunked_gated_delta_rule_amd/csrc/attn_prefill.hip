@@ -42,22 +42,30 @@ __device__ __forceinline__ u32x2 tr_read(Lds<T> tile, int at) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(tile + at)));
 }
 
-// Slots of the query tiles of bm rows: sequence s starts at slot floor(cu[s] / bm)
-// + s, which is distinct for every tile of the batch and grows with s, so a
-// slot's sequence is found by a search and no table is needed.
-inline int64_t tile_slots(int64_t t_max, int64_t n_max, int bm) { return t_max / bm + n_max; }
+// A tile's rows are tokens times the query heads that share a key head, as many
+// of those as divide their number and are at most 16 (`share`): tiles then span
+// few tokens, so little is computed beyond the diagonal or past a sequence's end.
+// Tiles of tt tokens have slots: sequence s starts at slot floor(cu[s] / tt) + s,
+// which is distinct for every tile of the batch and grows with s, so a slot's
+// sequence is found by a search and no table is needed.
+constexpr int kMostShare = 16;
+int share_of(int group) {
+  int g = group < kMostShare ? group : kMostShare;
+  while (group % g) --g;
+  return g;
+}
 
-// Head and tile slot of a work-group. The last (longest) tiles come first. With
-// a multiple of 8 heads, neighbouring heads (which read the same keys) go to one
-// XCD, whose L2 then holds their keys and values.
-__device__ __forceinline__ void place(int wg, int h, int slots, int &head, int &slot) {
-  if (h % 8 == 0) {
-    const int per = h / 8, i = wg >> 3;
-    head = (wg & 7) * per + i % per;
+// Head group and tile slot of a work-group. The last (longest) tiles come first.
+// With a multiple of 8 groups, neighbouring groups (which may read the same keys)
+// go to one XCD, whose L2 then holds their keys and values.
+__device__ __forceinline__ void place(int wg, int groups, int slots, int &group, int &slot) {
+  if (groups % 8 == 0) {
+    const int per = groups / 8, i = wg >> 3;
+    group = (wg & 7) * per + i % per;
     slot = slots - 1 - i / per;
   } else {
-    head = wg % h;
-    slot = slots - 1 - wg / h;
+    group = wg % groups;
+    slot = slots - 1 - wg / groups;
   }
 }
 
@@ -164,11 +172,12 @@ struct Rows {
     }
     __builtin_amdgcn_sched_group_barrier(kSchedMfma, 8, 0);
     if (masked) {
+      const int last = opaque<true>(lim - k0 - 4 * hh);
 #pragma unroll
       for (int t = 0; t < kT; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          sc[t][i] = k0 + 32 * t + 8 * (i >> 2) + 4 * hh + (i & 3) <= lim ? sc[t][i] : kNegInf;
+          sc[t][i] = 32 * t + 8 * (i >> 2) + (i & 3) <= last ? sc[t][i] : kNegInf;
     }
     float mx = kNegInf;
 #pragma unroll
@@ -232,35 +241,49 @@ struct Rows {
   __device__ __forceinline__ void store(T *row, int hh) const {
     const float sum = sum32(l);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that sees no key gives zeros
-    if (!row) return;
+    // a lane and its partner 32 lanes on hold halves of 8 dims: swapped in pairs of
+    // blocks, each lane has 16 bytes in a row
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        *reinterpret_cast<u32x2 *>(row + 4 * hh + 32 * i + 8 * b) =
-            u32x2{Elem<T>::pack(o[i][4 * b] * inv, o[i][4 * b + 1] * inv),
-                  Elem<T>::pack(o[i][4 * b + 2] * inv, o[i][4 * b + 3] * inv)};
+      for (int b = 0; b < 4; b += 2) {
+        uint32_t u[2][2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            u[k][e] = Elem<T>::pack(o[i][4 * (b + k) + 2 * e] * inv, o[i][4 * (b + k) + 2 * e + 1] * inv);
+        const auto x0 = __builtin_amdgcn_permlane32_swap(u[0][0], u[1][0], false, false);
+        const auto x1 = __builtin_amdgcn_permlane32_swap(u[0][1], u[1][1], false, false);
+        if (row)
+          *reinterpret_cast<u32x4 *>(row + 32 * i + 8 * b + 8 * hh) = u32x4{x0[0], x1[0], x0[1], x1[1]};
+      }
   }
 };
 
-// The tile of a work-group: its sequence, rows and keys.
+// The tile of a work-group: its heads, its sequence's rows and keys, its tokens.
 struct Where {
-  int head, qb, lq, kb, lk, q0, past;
+  int group, qb, lq, kb, lk, q0, past;
 };
-template <int kBM>
-__device__ __forceinline__ bool find(const PrefillArgs &a, int slots, int lane, Where &t) {
+__device__ __forceinline__ bool find(const PrefillArgs &a, int tt, int slots, int lane, Where &t) {
   int slot;
-  place(flat_block(), a.h, slots, t.head, slot);
+  place(flat_block(), a.h / a.share, slots, t.group, slot);
   if (slot < 0) return false;  // past the grid's count (last row)
-  const int s = wave_search(a.n_max, slot, lane,
-                            [&](int i) { return cu_at(a.cu_q, i, a.t_max) / kBM + i; });
-  t.qb = cu_at(a.cu_q, s, a.t_max);
-  t.lq = cu_end(a.cu_q, s, t.qb, a.t_max) - t.qb;
-  t.q0 = (slot - (t.qb / kBM + s)) * kBM;
+  int kv[2];
+  const Packed p = locate(
+      a.cu_q, a.n_max, a.t_max, slot, lane, [&](int i, int first) { return first / tt + i; },
+      [&](int i, int(&o)[2]) {
+        o[0] = cu_at(a.cu_k, i, a.tk_max);
+        o[1] = cu_end(a.cu_k, i, o[0], a.tk_max) - o[0];
+      },
+      kv);
+  t.qb = p.b;
+  t.lq = p.n;
+  t.q0 = (slot - (t.qb / tt + p.s)) * tt;
   if (t.q0 < 0 || t.q0 >= t.lq) return false;  // no tile of the sequence has this slot
-  t.kb = cu_at(a.cu_k, s, a.tk_max);
-  t.lk = cu_end(a.cu_k, s, t.kb, a.tk_max) - t.kb;
-  t.past = t.lk - t.lq;  // row r sees keys 0 .. past + r
+  t.kb = kv[0];
+  t.lk = kv[1];
+  t.past = t.lk - t.lq;  // token r sees keys 0 .. past + r
   return true;
 }
 
@@ -279,13 +302,19 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 || D == 128 ? 2 : 1) void 
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, hh = lane >> 5;
   Where t;
-  if (!find<kBM>(a, slots, lane, t)) return;
-  const int kvh = t.head / (a.h / a.hkv);
-  const int r0 = t.q0 + 32 * w;                // the wave's first row
-  const int r = min(r0 + col, t.lq - 1);       // this lane's row (the last one again past the end)
-  const int lim = t.past + r;
-  const int wave_lo = t.past + min(r0, t.lq - 1), wave_hi = t.past + min(r0 + 31, t.lq - 1);
-  const int keys = min(t.past + min(t.q0 + kBM, t.lq), t.lk);  // keys any row of the tile sees
+  const int share = a.share, tt = kBM / share;
+  if (!find(a, tt, slots, lane, t)) return;
+  // one value per wave, which the compiler does not see by itself
+  t = {uniform(t.group), uniform(t.qb), uniform(t.lq), uniform(t.kb), uniform(t.lk), uniform(t.q0),
+       uniform(t.past)};
+  const int kvh = t.group * share / (a.h / a.hkv);
+  // this lane's row; those past the tile's tokens or the sequence's end take the
+  // last token's limit and are not stored
+  const int tok = min(t.q0 + (32 * w + col) / share, t.lq - 1);
+  const int lim = t.past + tok;
+  const int wave_lo = t.past + min(t.q0 + 32 * w / share, t.lq - 1);
+  const int wave_hi = t.past + min(t.q0 + min((32 * w + 31) / share, tt - 1), t.lq - 1);
+  const int keys = min(t.past + min(t.q0 + tt, t.lq), t.lk);  // keys any row of the tile sees
   const int tiles = keys > 0 ? (keys + kBN - 1) / kBN : 0;
 
   const T *kp = static_cast<const T *>(a.k) + (int64_t)t.kb * a.k_row + kvh * D;
@@ -307,7 +336,8 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 || D == 128 ? 2 : 1) void 
     get_k(0, k_a);
     get_v(0, v_a);
   }
-  x.load(static_cast<const T *>(a.q) + (int64_t)(t.qb + r) * a.q_row + t.head * D, hh);
+  x.load(static_cast<const T *>(a.q) + (int64_t)(t.qb + tok) * a.q_row +
+             (t.group * share + (32 * w + col) % share) * D, hh);
   auto score = [&](int j, T *kt) __attribute__((always_inline)) {
     const int k0 = j * kBN;
     if (k0 <= wave_hi)
@@ -382,16 +412,24 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 || D == 128 ? 2 : 1) void 
       }
     }
   }
-  x.store(r0 + col < t.lq
-              ? static_cast<T *>(a.o) + ((int64_t)(t.qb + r0 + col) * a.h + t.head) * D
+  const int row = opaque<true>(32 * w + col);  // not kept along the loop
+  const int token = t.q0 + row / share;
+  x.store(row < tt * share && token < t.lq
+              ? static_cast<T *>(a.o) +
+                    ((int64_t)(t.qb + token) * a.h + t.group * share + row % share) * D
               : nullptr, hh);
 }
 
+// Average tokens per sequence from which heads of 128 take work-groups of eight
+// waves: 4096 tokens 137 us against 140 us with four, 16384 tokens 955 against 968;
+// 32 sequences of 500 on average 177 against 159 us.
+constexpr int kLongPrompt = 2048;
+
 template <typename T, int D, int kBN, int kWaves>
 hipError_t run(const gdn_attn_config *cfg, const PrefillArgs &a, hipStream_t stream) {
-  const int64_t slots = tile_slots(cfg->t_max, cfg->n_max, 32 * kWaves);
+  const int64_t slots = cfg->t_max / (32 * kWaves / a.share) + cfg->n_max;
   dim3 grid;
-  if (!flat_grid(slots * cfg->h, 64 * kWaves, grid)) return hipErrorInvalidValue;
+  if (!flat_grid(slots * (cfg->h / a.share), 64 * kWaves, grid)) return hipErrorInvalidValue;
   hipLaunchKernelGGL((attn_prefill_kernel<T, D, kBN, kWaves>), grid, dim3(64 * kWaves), 0, stream, a,
                      static_cast<int>(slots));
   return hipGetLastError();
@@ -399,13 +437,16 @@ hipError_t run(const gdn_attn_config *cfg, const PrefillArgs &a, hipStream_t str
 
 template <typename T>
 hipError_t run_of(const gdn_attn_config *cfg, const PrefillArgs &a, hipStream_t stream) {
-  return cfg->d == 128 ? run<T, 128, 64, 4>(cfg, a, stream) : run<T, 256, 64, 8>(cfg, a, stream);
+  if (cfg->d == 256) return run<T, 256, 64, 8>(cfg, a, stream);
+  return cfg->t_max / cfg->n_max >= kLongPrompt ? run<T, 128, 64, 8>(cfg, a, stream)
+                                                : run<T, 128, 64, 4>(cfg, a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_attn_prefill(const gdn_attn_config *cfg, PrefillArgs a, hipStream_t stream) {
   if (cfg->t_max == 0) return hipSuccess;
+  a.share = share_of(cfg->h / cfg->hkv);
   return cfg->dtype == GDN_BF16 ? run_of<__bf16>(cfg, a, stream) : run_of<_Float16>(cfg, a, stream);
 }
 

@@ -54,29 +54,65 @@ int page_shift(const gdn_attn_config *cfg) {
   return s;
 }
 
-struct Layout {
-  size_t plan, part_o, part_ml, done_o, done_ml, total;
+// What gdn_attn_prefill needs, and what gdn_attn_paged needs, from offset 0 each (a
+// workspace serves one call at a time).
+struct PrefillLayout {
+  size_t part_o, part_ml, total;
+};
+struct PagedLayout {
+  size_t plan, part_o, part_ml, done_o, done_ml, pre_o, pre_ml, total;
 };
 
-Layout layout_of(const gdn_attn_config *cfg) {
-  const size_t d = static_cast<size_t>(cfg->d);
-  const size_t slots = static_cast<size_t>(gdn::paged_grid(cfg)) * 2 * 16 * gdn::paged_row_tiles(cfg);
-  const size_t rows =
-      cfg->shared_max > 0 ? 2 * static_cast<size_t>(cfg->t_max) * static_cast<size_t>(cfg->h) : 0;
-  Layout l;
+struct Taker {
   size_t at = 0;
-  auto take = [&](size_t bytes) { const size_t here = at; at += align_up(bytes); return here; };
-  l.plan = take(kPlanBytes + (static_cast<size_t>(cfg->n_max) + 1) * 8);
-  l.part_o = take(slots * d * 4);
-  l.part_ml = take(slots * 2 * 4);
-  l.done_o = take(rows * d * 4);
-  l.done_ml = take(rows * 2 * 4);
-  l.total = at;
+  size_t operator()(size_t bytes) {
+    const size_t here = at;
+    at += align_up(bytes);
+    return here;
+  }
+};
+
+PrefillLayout prefill_layout(const gdn_attn_config *cfg, gdn::Keys keys) {
+  const size_t rows = static_cast<size_t>(gdn::tile_part_rows(cfg, gdn::tile_shape(cfg, keys), keys));
+  Taker take;
+  PrefillLayout l;
+  l.part_o = take(rows * cfg->d * 4);
+  l.part_ml = take(rows * 2 * 4);
+  l.total = take.at;
   return l;
 }
 
-gdn_status check_workspace(const Layout &l, const void *ws, size_t bytes) {
-  if (!ws || bytes < l.total || !aligned(ws, kAlign)) return GDN_ERR_WORKSPACE;
+PagedLayout paged_layout(const gdn_attn_config *cfg) {
+  const size_t d = static_cast<size_t>(cfg->d);
+  const size_t slots = static_cast<size_t>(gdn::stream_grid(cfg)) * 2 * 16 * gdn::stream_row_tiles(cfg);
+  const bool shared = cfg->shared_max > 0;
+  const size_t done = shared ? static_cast<size_t>(cfg->t_max) * static_cast<size_t>(cfg->h) : 0;
+  const size_t pre = shared ? static_cast<size_t>(gdn::tile_part_rows(
+                                  cfg, gdn::tile_shape(cfg, gdn::Keys::kShared), gdn::Keys::kShared))
+                            : 0;
+  Taker take;
+  PagedLayout l;
+  l.plan = take(kPlanBytes + (static_cast<size_t>(cfg->n_max) + 1) * 8);
+  l.part_o = take(slots * d * 4);
+  l.part_ml = take(slots * 2 * 4);
+  l.done_o = take(done * d * 4);
+  l.done_ml = take(done * 2 * 4);
+  l.pre_o = take(pre * d * 4);
+  l.pre_ml = take(pre * 2 * 4);
+  l.total = take.at;
+  return l;
+}
+
+size_t workspace_bytes(const gdn_attn_config *cfg) {
+  const size_t prefill = prefill_layout(cfg, gdn::Keys::kRows).total;
+  const size_t paged = gdn::streams(cfg) ? paged_layout(cfg).total
+                                         : prefill_layout(cfg, gdn::Keys::kPages).total;
+  const size_t most = prefill > paged ? prefill : paged;
+  return most > kAlign ? most : kAlign;
+}
+
+gdn_status check_workspace(size_t need, const void *ws, size_t bytes) {
+  if (!ws || bytes < need || !aligned(ws, kAlign)) return GDN_ERR_WORKSPACE;
   return GDN_OK;
 }
 
@@ -95,6 +131,17 @@ float scale_log2(const gdn_attn_config *cfg) {
 
 gdn_status from_hip(hipError_t e) { return e == hipSuccess ? GDN_OK : GDN_ERR_HIP; }
 hipStream_t as_stream(void *s) { return reinterpret_cast<hipStream_t>(s); }
+
+void tile_common(const gdn_attn_config *cfg, gdn::TileArgs &a, char *ws, size_t part_o,
+                 size_t part_ml) {
+  a.t_max = cfg->t_max;
+  a.n_max = cfg->n_max;
+  a.h = cfg->h;
+  a.hkv = cfg->hkv;
+  a.scale_log2 = scale_log2(cfg);
+  a.part_o = reinterpret_cast<float *>(ws + part_o);
+  a.part_ml = reinterpret_cast<float *>(ws + part_ml);
+}
 
 gdn_status front(const gdn_attn_config *cfg, const void *qkv, int64_t qkv_row, const float *q_w,
                  const float *k_w, const float *inv_freq, const int32_t *cu_seqlens,
@@ -141,7 +188,7 @@ gdn_status gdn_attn_workspace_size(const gdn_attn_config *cfg, size_t *bytes) {
   const gdn_status st = check_config(cfg);
   if (st != GDN_OK) return st;
   if (!bytes) return GDN_ERR_INVALID_ARG;
-  *bytes = layout_of(cfg).total;
+  *bytes = workspace_bytes(cfg);
   return GDN_OK;
 }
 
@@ -176,9 +223,10 @@ gdn_status gdn_attn_prefill(const gdn_attn_config *cfg, const void *q, int64_t q
   const gdn_status st = check_config(cfg);
   if (st != GDN_OK) return st;
   if (!q || !k || !v || !cu_q || !o) return GDN_ERR_INVALID_ARG;
-  const gdn_status ws = check_workspace(layout_of(cfg), workspace, ws_bytes);
+  const PrefillLayout l = prefill_layout(cfg, gdn::Keys::kRows);
+  const gdn_status ws = check_workspace(workspace_bytes(cfg), workspace, ws_bytes);
   if (ws != GDN_OK) return ws;
-  gdn::PrefillArgs a;
+  gdn::TileArgs a = {};
   const int64_t kv = static_cast<int64_t>(cfg->hkv) * cfg->d;
   if (!row_of(q_row, static_cast<int64_t>(cfg->h) * cfg->d, a.q_row) ||
       !row_of(k_row, kv, a.k_row) || !row_of(v_row, kv, a.v_row))
@@ -192,13 +240,9 @@ gdn_status gdn_attn_prefill(const gdn_attn_config *cfg, const void *q, int64_t q
   a.cu_q = cu_q;
   a.cu_k = cu_k ? cu_k : cu_q;
   a.o = o;
-  a.t_max = cfg->t_max;
   a.tk_max = cfg->tk_max > 0 ? cfg->tk_max : cfg->t_max;
-  a.n_max = cfg->n_max;
-  a.h = cfg->h;
-  a.hkv = cfg->hkv;
-  a.scale_log2 = scale_log2(cfg);
-  return from_hip(gdn::launch_attn_prefill(cfg, a, as_stream(stream)));
+  tile_common(cfg, a, static_cast<char *>(workspace), l.part_o, l.part_ml);
+  return from_hip(gdn::launch_attn_tiles(cfg, gdn::Keys::kRows, a, as_stream(stream)));
 }
 
 gdn_status gdn_attn_paged(const gdn_attn_config *cfg, const void *q, int64_t q_row,
@@ -211,40 +255,72 @@ gdn_status gdn_attn_paged(const gdn_attn_config *cfg, const void *q, int64_t q_r
   if (!q || !k_pages || !v_pages || !cu_seqlens || !kv_lens || !block_table || !o)
     return GDN_ERR_INVALID_ARG;
   if (cfg->n_pages < 1 || cfg->max_pages < 1) return GDN_ERR_INVALID_ARG;
-  const Layout l = layout_of(cfg);
-  const gdn_status ws = check_workspace(l, workspace, ws_bytes);
+  const gdn_status ws = check_workspace(workspace_bytes(cfg), workspace, ws_bytes);
   if (ws != GDN_OK) return ws;
-  gdn::PagedArgs a;
-  if (!row_of(q_row, static_cast<int64_t>(cfg->h) * cfg->d, a.q_row)) return GDN_ERR_INVALID_ARG;
+  int64_t row;
+  if (!row_of(q_row, static_cast<int64_t>(cfg->h) * cfg->d, row)) return GDN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(o, 16) ||
       !aligned(cu_seqlens, 4) || !aligned(kv_lens, 4) || !aligned(block_table, 4) ||
       !aligned(shared_len, 4))
     return GDN_ERR_INVALID_ARG;
   char *at = static_cast<char *>(workspace);
+  gdn::PagedBatch pg;
+  pg.cu = cu_seqlens;
+  pg.kv_lens = kv_lens;
+  pg.table = block_table;
+  pg.shared_len = shared_len;
+  pg.t_max = cfg->t_max;
+  pg.n_max = cfg->n_max;
+  pg.page_shift = page_shift(cfg);
+  pg.n_pages = cfg->n_pages;
+  pg.max_pages = cfg->max_pages;
+  pg.shared_max = cfg->shared_max;
+  gdn::TileArgs t = {};
+  t.q = q;
+  t.q_row = row;
+  t.k = k_pages;
+  t.v = v_pages;
+  t.cu_q = cu_seqlens;
+  t.pg = pg;
+  t.o = o;
+  if (!gdn::streams(cfg)) {
+    const PrefillLayout l = prefill_layout(cfg, gdn::Keys::kPages);
+    tile_common(cfg, t, at, l.part_o, l.part_ml);
+    return from_hip(gdn::launch_attn_tiles(cfg, gdn::Keys::kPages, t, as_stream(stream)));
+  }
+  const PagedLayout l = paged_layout(cfg);
+  gdn::StreamArgs a = {};
+  if (cfg->shared_max > 0 && shared_len) {
+    tile_common(cfg, t, at, l.pre_o, l.pre_ml);
+    const hipError_t e = gdn::launch_attn_tiles(cfg, gdn::Keys::kShared, t, as_stream(stream));
+    if (e != hipSuccess) return GDN_ERR_HIP;
+    const gdn::TileShape s = gdn::tile_shape(cfg, gdn::Keys::kShared);
+    a.pre_share = s.share;
+    a.pre_tt = s.tt;
+    a.pre_slots = s.slots;
+    a.pre_splits = s.splits;
+    a.pre_rows = 32 * s.waves;
+  } else {
+    a.pre_share = a.pre_tt = 1;  // the prefix is empty: these are divided by, not used
+  }
   a.q = q;
+  a.q_row = row;
   a.k_pages = k_pages;
   a.v_pages = v_pages;
-  a.cu = cu_seqlens;
-  a.kv_lens = kv_lens;
-  a.table = block_table;
-  a.shared_len = shared_len;
+  a.pg = pg;
   a.o = o;
-  a.t_max = cfg->t_max;
-  a.n_max = cfg->n_max;
   a.h = cfg->h;
   a.hkv = cfg->hkv;
-  a.page_shift = page_shift(cfg);
-  a.n_pages = cfg->n_pages;
-  a.max_pages = cfg->max_pages;
-  a.shared_max = cfg->shared_max;
   a.scale_log2 = scale_log2(cfg);
-  a.grid = gdn::paged_grid(cfg);
+  a.grid = gdn::stream_grid(cfg);
   a.plan = reinterpret_cast<int32_t *>(at + l.plan);
   a.part_o = reinterpret_cast<float *>(at + l.part_o);
   a.part_ml = reinterpret_cast<float *>(at + l.part_ml);
   a.done_o = reinterpret_cast<float *>(at + l.done_o);
   a.done_ml = reinterpret_cast<float *>(at + l.done_ml);
-  return from_hip(gdn::launch_attn_paged(cfg, a, as_stream(stream)));
+  a.pre_o = reinterpret_cast<float *>(at + l.pre_o);
+  a.pre_ml = reinterpret_cast<float *>(at + l.pre_ml);
+  return from_hip(gdn::launch_attn_stream(cfg, a, as_stream(stream)));
 }
 
 }  // extern "C"

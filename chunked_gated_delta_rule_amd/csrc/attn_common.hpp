@@ -2,6 +2,7 @@
 // element types, packing, cross-lane steps, and the search of a packed batch.
 #pragma once
 
+#include "attn_launch.hpp"
 #include "gdn_common.hpp"
 
 namespace gdn {
@@ -133,6 +134,65 @@ __device__ __forceinline__ Packed seq_of_row(const int32_t *__restrict__ cu, int
       [&](int s, int(&o)[1]) { o[0] = extra(s); }, v);
   out = v[0];
   return p;
+}
+
+// New tokens and keys of sequence s of a paged batch.
+struct Seq {
+  int bos, n, kv;
+};
+__device__ __forceinline__ int kv_of(const PagedBatch &a, int s) {
+  const int64_t room = (int64_t)a.max_pages << a.page_shift;  // positions the table reaches
+  const int kv = max(a.kv_lens[s], 0);
+  return kv < room ? kv : (int)room;
+}
+__device__ __forceinline__ Seq seq_at(const PagedBatch &a, int s) {
+  Seq q;
+  q.bos = cu_at(a.cu, s, a.t_max);
+  q.n = cu_end(a.cu, s, q.bos, a.t_max) - q.bos;
+  q.kv = kv_of(a, s);
+  return q;
+}
+
+// Start of the 16 rows of one key head that hold position `key` (a multiple of 16)
+// of the sequence with this table row, in rows of the pool.
+__device__ __forceinline__ int64_t pool_row(const PagedBatch &a, const int32_t *__restrict__ row,
+                                            int key, int kh, int hkv) {
+  const int page = min(max(row[key >> a.page_shift], 0), a.n_pages - 1);
+  return (((int64_t)page * hkv + kh) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+}
+
+// The shared prefix as it is used: whole pages, before every new token of the
+// batch; and a sequence with new tokens, whose table leads to it. For a
+// work-group of kThreads; `at` is its LDS.
+struct Prefix {
+  int len, seq;
+};
+template <int kThreads>
+__device__ __forceinline__ Prefix shared_prefix(const PagedBatch &a, int tid,
+                                                int (&at)[kThreads / 64][2]) {
+  if (!a.shared_len || a.shared_max <= 0) return {0, 0};
+  int least = min(max(a.shared_len[0], 0), a.shared_max), first = a.n_max;
+  for (int s = tid; s < a.n_max; s += kThreads) {
+    const Seq q = seq_at(a, s);
+    if (q.n > 0) {
+      least = min(least, q.kv - q.n);
+      first = min(first, s);
+    }
+  }
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    least = min(least, __shfl_xor(least, off, 64));
+    first = min(first, __shfl_xor(first, off, 64));
+  }
+  if (tid % 64 == 0) at[tid / 64][0] = least, at[tid / 64][1] = first;
+  __syncthreads();
+  for (int i = 0; i < kThreads / 64; ++i) {
+    least = min(least, at[i][0]);
+    first = min(first, at[i][1]);
+  }
+  least = uniform(least);
+  first = uniform(first);
+  return {first < a.n_max ? max(least, 0) >> a.page_shift << a.page_shift : 0, min(first, a.n_max - 1)};
 }
 
 }  // namespace gdn

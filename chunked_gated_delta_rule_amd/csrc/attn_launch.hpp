@@ -24,37 +24,66 @@ struct FrontArgs {
 };
 hipError_t launch_attn_front(const gdn_attn_config *cfg, FrontArgs a, hipStream_t stream);
 
-struct PrefillArgs {
-  const void *q, *k, *v;
-  int64_t q_row, k_row, v_row;  // elements
-  const int32_t *cu_q, *cu_k;
+// A batch whose keys and values lie in pages.
+struct PagedBatch {
+  const int32_t *cu, *kv_lens, *table, *shared_len;  // shared_len may be null
+  int t_max, n_max, page_shift, n_pages, max_pages, shared_max;
+};
+
+// Where a tile kernel's keys are: rows of k and v; the pages of each sequence; or
+// the pages that the batch shares, for all its tokens at once.
+enum class Keys { kRows = 0, kPages = 1, kShared = 2 };
+
+struct TileArgs {
+  const void *q, *k, *v;          // k, v: rows, or the page pools
+  int64_t q_row, k_row, v_row;    // elements
+  const int32_t *cu_q, *cu_k;     // cu_k: with rows only
+  PagedBatch pg;                  // with pages only
   void *o;
   int t_max, tk_max, n_max, h, hkv;
-  float scale_log2;  // score scale * log2(e)
-  int share;         // query heads of one key head that a tile's rows share
+  float scale_log2;               // score scale * log2(e)
+  // partial results of keys split over work-groups: [item][split][row]
+  float *part_o, *part_ml;
+  // filled in by the launcher (TileShape)
+  int share, splits, slots;
 };
-hipError_t launch_attn_prefill(const gdn_attn_config *cfg, PrefillArgs a, hipStream_t stream);
 
-struct PagedArgs {
+// How a call is cut into tiles: rows per tile are tokens times `share` query heads
+// of one key head, tt tokens; `slots` token tiles at most, times h / share head
+// groups; each tile's keys in `splits` parts.
+struct TileShape {
+  int waves, share, tt, slots, splits;
+};
+TileShape tile_shape(const gdn_attn_config *cfg, Keys keys);
+// Rows of partial results the shape needs (0 where o is written at once).
+int64_t tile_part_rows(const gdn_attn_config *cfg, const TileShape &s, Keys keys);
+// With more than one split, kRows and kPages are joined into o; the parts of
+// kShared are left to the caller.
+hipError_t launch_attn_tiles(const gdn_attn_config *cfg, Keys keys, TileArgs a, hipStream_t stream);
+
+struct StreamArgs {
   const void *q;
   int64_t q_row;  // elements
   const void *k_pages, *v_pages;
-  const int32_t *cu, *kv_lens, *table, *shared_len;
+  PagedBatch pg;
   void *o;
-  int t_max, n_max, h, hkv;
-  int page_shift, n_pages, max_pages, shared_max;
+  int h, hkv;
   float scale_log2;
   int grid;  // work-groups of the main kernel
-  // workspace: the plan, the partial results of items split over work-groups
-  // (two per work-group), and with a shared prefix the results of items that
-  // one work-group finished (two per row: the prefix's and the sequence's)
+  // workspace: the plan; the partial results of items split over work-groups (two
+  // per work-group); with a shared prefix, the results of items that one
+  // work-group finished (one per row) and the prefix's parts
   int32_t *plan;
   float *part_o, *part_ml, *done_o, *done_ml;
+  const float *pre_o, *pre_ml;
+  int pre_share, pre_tt, pre_slots, pre_splits, pre_rows;
 };
-// Rows (16-row tiles times this) of q that one paged work item takes.
-int paged_row_tiles(const gdn_attn_config *cfg);
-// Work-groups of the paged kernel on the current device.
-int paged_grid(const gdn_attn_config *cfg);
-hipError_t launch_attn_paged(const gdn_attn_config *cfg, PagedArgs a, hipStream_t stream);
+// Rows (16-row tiles times this) of q that one streamed work item takes.
+int stream_row_tiles(const gdn_attn_config *cfg);
+// Work-groups of the streaming kernel on the current device.
+int stream_grid(const gdn_attn_config *cfg);
+// Whether gdn_attn_paged streams the keys past few rows, or tiles many rows.
+bool streams(const gdn_attn_config *cfg);
+hipError_t launch_attn_stream(const gdn_attn_config *cfg, StreamArgs a, hipStream_t stream);
 
 }  // namespace gdn

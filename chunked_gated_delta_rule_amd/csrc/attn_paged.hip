@@ -1,19 +1,18 @@
-// Attention of a few new tokens per sequence to a paged cache (decode, verify),
-// with the pages that the whole batch shares read once.
+// Attention of a few new tokens per sequence to a paged cache (decode, verify).
 //
-// The rows of an item are the new tokens of one sequence times the query heads
-// of one key / value head (of every sequence, for the shared prefix), 16 kRT at
-// a time; an item's keys are cut into units of 128. HBM-bound on the keys and
-// values: each unit is read once per item.
+// The rows of an item are the new tokens of one sequence times the query heads of
+// one key / value head, 16 kRT at a time; an item's keys are cut into units of 128.
+// HBM-bound on the keys and values: each unit is read once per item. Pages that the
+// whole batch shares come before: the tile kernel has taken all rows past them and
+// left partial results, and the items here start behind them.
 //
-//  * Work: all units of the batch in one line (key head, prefix, sequences in
-//    order, row tiles, units), cut into equal runs, one per work-group of a
-//    fixed grid. So lengths need not be known on the host, a single long
-//    sequence fills the device, and a ragged batch is balanced to one unit. A
-//    run covers the end of one item, whole items, and the start of another.
-//    Whole items are written at once; the others leave (maximum, sum, output
-//    sum) in the workspace, at most two per work-group, and the join kernel
-//    adds them up, row by row.
+//  * Work: all units of the batch in one line (key head, sequences in order, row
+//    tiles, units), cut into equal runs, one per work-group of a fixed grid. So
+//    lengths need not be known on the host, a single long sequence fills the
+//    device, and a ragged batch is balanced to one unit. A run covers the end of one
+//    item, whole items, and the start of another. Whole items are written at once;
+//    the others leave (maximum, sum, output sum) in the workspace, at most two per
+//    work-group, and the join kernel adds them up, row by row.
 //  * Each of the four waves takes 32 keys of a unit on its own, with a running
 //    maximum and sum of its own; the waves meet once per item, in LDS. There is
 //    no barrier in the loop over keys.
@@ -33,43 +32,19 @@ namespace {
 
 constexpr int kUnit = 128;  // keys per unit: 32 per wave
 
-// Items of the batch, the same in the main kernel and in the join.
-struct Plan {
-  int prefix;       // shared positions: whole pages, before every new token
-  int tokens;       // packed rows
-  int first;        // a sequence with new tokens (its table leads to the prefix)
-  int per_wg;       // units per work-group
-  int64_t total;    // units
-  int64_t head;     // units per key head
-  int64_t lead;     // of these, the prefix's
-};
-// workspace: the plan, then units before each sequence (int64 [n_max + 1])
+// workspace plan: prefix, units per key head, units per work-group; then the units
+// before each sequence (int64 [n_max + 1])
 constexpr int kPlanInts = 16;
 
 __device__ __forceinline__ int units_of(int keys) { return (keys + kUnit - 1) / kUnit; }
-
-// New tokens and keys of sequence s.
-struct Seq {
-  int bos, n, kv;
-};
-__device__ __forceinline__ Seq seq_at(const PagedArgs &a, int s) {
-  Seq q;
-  q.bos = cu_at(a.cu, s, a.t_max);
-  q.n = cu_end(a.cu, s, q.bos, a.t_max) - q.bos;
-  const int64_t room = (int64_t)a.max_pages << a.page_shift;  // positions the table reaches
-  const int kv = max(a.kv_lens[s], 0);
-  q.kv = kv < room ? kv : (int)room;
-  return q;
-}
 
 template <int kRT>
 __device__ __forceinline__ int row_tiles(int64_t rows) {
   return (int)((rows + 16 * kRT - 1) / (16 * kRT));
 }
 
-// The work of one wave-set on one item's run of units, and what it leaves.
 template <typename T, int D, int kRT>
-__global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_paged_kernel(PagedArgs a) {
+__global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kernel(StreamArgs a) {
   typedef typename Elem<T>::vec8 vec8;
   constexpr int kRows = 16 * kRT;
   constexpr int kDC = D / 128;   // 128-dim blocks
@@ -78,9 +53,9 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_paged_kernel
   __shared__ __attribute__((aligned(16))) float os[4][16][kPad];
   __shared__ float wm[4][kRows], wl[4][kRows];
   __shared__ int64_t scan64[5];
-  __shared__ int scan32[4][3];
+  __shared__ int scan32[4][2], found;
 
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int G = a.h / a.hkv;
   // consecutive runs on one XCD: its L2 then holds the rows that they share
@@ -88,34 +63,12 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_paged_kernel
   if (wg >= a.grid) return;
 
   // ---- the plan: shared prefix, units of every sequence
-  const int tokens = cu_at(a.cu, a.n_max, a.t_max);
-  const int per = (a.n_max + 255) / 256;
-  const int s0 = min(tid * per, a.n_max), s1 = min(s0 + per, a.n_max);
-  int prefix = 0, first = a.n_max;
-  if (a.shared_len && a.shared_max > 0) {
-    int least = min(max(a.shared_len[0], 0), a.shared_max);
-    for (int s = s0; s < s1; ++s) {
-      const Seq q = seq_at(a, s);
-      if (q.n > 0) {
-        least = min(least, q.kv - q.n);
-        first = min(first, s);
-      }
-    }
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      least = min(least, __shfl_xor(least, off, 64));
-      first = min(first, __shfl_xor(first, off, 64));
-    }
-    if (lane == 0) scan32[w][0] = least, scan32[w][1] = first;
-    __syncthreads();
-    for (int i = 0; i < 4; ++i) {
-      least = min(least, scan32[i][0]);
-      first = min(first, scan32[i][1]);
-    }
-    prefix = first < a.n_max ? max(least, 0) >> a.page_shift << a.page_shift : 0;
-  }
+  const PagedBatch &pg = a.pg;
+  const int prefix = shared_prefix<256>(pg, tid, scan32).len;
+  const int per = (pg.n_max + 255) / 256;
+  const int s0 = min(tid * per, pg.n_max), s1 = min(s0 + per, pg.n_max);
   auto units_in = [&](int s) __attribute__((always_inline)) -> int64_t {
-    const Seq q = seq_at(a, s);
+    const Seq q = seq_at(pg, s);
     return q.n > 0 && q.kv > prefix
                ? (int64_t)row_tiles<kRT>((int64_t)q.n * G) * units_of(q.kv - prefix)
                : 0;
@@ -130,13 +83,12 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_paged_kernel
   }
   if (lane == 63) scan64[w] = incl;
   __syncthreads();
-  int64_t before = incl - mine, seqs = 0;
+  int64_t before = incl - mine, per_head = 0;
   for (int i = 0; i < 4; ++i) {
     if (i < w) before += scan64[i];
-    seqs += scan64[i];
+    per_head += scan64[i];
   }
-  const int64_t lead = prefix > 0 ? (int64_t)row_tiles<kRT>((int64_t)tokens * G) * units_of(prefix) : 0;
-  const int64_t per_head = lead + seqs, total = per_head * a.hkv;
+  const int64_t total = per_head * a.hkv;
   const int64_t per_wg = max((total + a.grid - 1) / a.grid, (int64_t)1);
   if (wg == 0) {
     int64_t *starts = reinterpret_cast<int64_t *>(a.plan + kPlanInts);
@@ -148,8 +100,7 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_paged_kernel
     if (tid == 0) {
       a.plan[0] = prefix;
       reinterpret_cast<int64_t *>(a.plan)[1] = per_head;
-      reinterpret_cast<int64_t *>(a.plan)[2] = lead;
-      reinterpret_cast<int64_t *>(a.plan)[3] = per_wg;
+      reinterpret_cast<int64_t *>(a.plan)[2] = per_wg;
     }
   }
   const int64_t u0 = (int64_t)wg * per_wg, u1 = min(u0 + per_wg, total);
@@ -158,41 +109,30 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_paged_kernel
   // ---- the item of u0: the thread whose sequences hold it names it
   int kh = (int)(u0 / per_head);
   int64_t in_head = u0 - kh * per_head;
-  int s = -1;  // -1: the prefix
-  int64_t in_seq = in_head;
-  if (in_head >= lead) {
-    const int64_t x = in_head - lead;
-    if (x >= before && x < before + mine) {
-      int64_t at = before;
-      int i = s0;
-      for (int64_t n = units_in(i); x >= at + n; n = units_in(i)) {
-        at += n;
-        ++i;
-      }
-      scan32[0][2] = i;
-      scan64[4] = x - at;
+  if (in_head >= before && in_head < before + mine) {
+    int64_t at = before;
+    int i = s0;
+    for (int64_t n = units_in(i); in_head >= at + n; n = units_in(i)) {
+      at += n;
+      ++i;
     }
-    __syncthreads();
-    s = scan32[0][2];
-    in_seq = scan64[4];
+    found = i;
+    scan64[4] = in_head - at;
   }
+  __syncthreads();
+  int s = found;
+  int64_t in_seq = scan64[4];
 
   const T *kpool = static_cast<const T *>(a.k_pages), *vpool = static_cast<const T *>(a.v_pages);
   int64_t u = u0;
   while (u < u1) {
     // the item: its rows, its keys, the units of it in this run
-    Seq q{0, tokens, prefix};
-    int key0 = 0, row0 = first;
-    if (s >= 0) {
-      q = seq_at(a, s);
-      key0 = prefix;
-      row0 = s;
-    }
-    const int nu = units_of(q.kv - key0);
+    const Seq q = seq_at(pg, s);
+    const int nu = units_of(q.kv - prefix);
     const int rt = (int)(in_seq / nu), un = (int)(in_seq - (int64_t)rt * nu);
     const int run = (int)min((int64_t)(nu - un), u1 - u);
     const int64_t rows = (int64_t)q.n * G, r0 = (int64_t)rt * kRows;
-    const int32_t *table = a.table + (int64_t)row0 * a.max_pages;
+    const int32_t *table = pg.table + (int64_t)s * pg.max_pages;
 
     __syncthreads();  // the item before may still be read
     for (int i = tid; i < kRows * (D / 8); i += 256) {
@@ -207,9 +147,9 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_paged_kernel
 #pragma unroll
     for (int t = 0; t < kRT; ++t) {
       const int64_t r = r0 + 16 * t + c;
-      lim[t] = s < 0 ? q.kv - 1 : q.kv - q.n + (int)(min(r, rows - 1) / G);
+      lim[t] = q.kv - q.n + (int)(min(r, rows - 1) / G);
     }
-    const int all_see = s < 0 ? q.kv - 1 : q.kv - q.n + (int)(r0 / G);  // every row sees these
+    const int all_see = q.kv - q.n + (int)(r0 / G);  // every row sees these
     __syncthreads();
 
     f32x4 o[kRT][kDC][8];
@@ -224,16 +164,14 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_paged_kernel
         for (int j = 0; j < 8; ++j) o[t][b][j] = zero4();
     }
     for (int i = 0; i < run; ++i) {
-      const int k0 = key0 + (un + i) * kUnit + 32 * w;  // the wave's 32 keys
+      const int k0 = prefix + (un + i) * kUnit + 32 * w;  // the wave's 32 keys
       if (k0 >= q.kv) continue;
       // two tiles of 16 keys, each inside one page
       const T *kt[2], *vt[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const int key = min(k0 + 16 * t, (q.kv - 1) & ~15);
-        const int page = min(max(table[key >> a.page_shift], 0), a.n_pages - 1);
-        const int64_t at = ((((int64_t)page * a.hkv + kh) << a.page_shift) +
-                            (key & ((1 << a.page_shift) - 1))) * D;
+        const int64_t at = pool_row(pg, table, key, kh, a.hkv) * D;
         kt[t] = kpool + at;
         vt[t] = vpool + at;
       }
@@ -364,9 +302,8 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_paged_kernel
         const float inv = ll == 0.f ? 0.f : 1.f / ll;
         float *po, *pm;
         if (whole) {
-          const int64_t at = (s < 0 ? 0 : (int64_t)a.t_max * a.h) + orow;
-          po = a.done_o + at * D;
-          pm = a.done_ml + at * 2;
+          po = a.done_o + orow * D;
+          pm = a.done_ml + orow * 2;
         } else {
           po = a.part_o + (place * kRows + 16 * t + row) * D;
           pm = a.part_ml + (place * kRows + 16 * t + row) * 2;
@@ -399,11 +336,6 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_paged_kernel
     if (in_head == per_head) {
       ++kh;
       in_head = in_seq = 0;
-      s = -1;
-    }
-    if (s < 0) {
-      if (in_head < lead) continue;
-      in_seq = 0;
       s = 0;
       while (units_in(s) == 0) ++s;
     } else if (in_seq == units_in(s)) {
@@ -414,11 +346,11 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_paged_kernel
   }
 }
 
-// Joins what several work-groups, or the prefix and a sequence, left of a row,
+// Joins what several work-groups, the shared prefix's included, left of a row,
 // and writes zeros where a row sees no key. One work-group per (token, query
 // head); rows that the main kernel finished are left alone.
 template <typename T, int D, int kRT>
-__global__ __launch_bounds__(256) void attn_join_kernel(PagedArgs a) {
+__global__ __launch_bounds__(256) void attn_stream_join_kernel(StreamArgs a) {
   constexpr int kRows = 16 * kRT;
   constexpr int kLanes = D / 4;            // threads per partial result
   constexpr int kPar = 256 / kLanes;       // partial results at a time
@@ -427,57 +359,48 @@ __global__ __launch_bounds__(256) void attn_join_kernel(PagedArgs a) {
   const int wg = flat_block();
   const int t = wg / a.h, head = wg % a.h;
   const int tid = threadIdx.x, lane = tid & 63;
-  if (t >= cu_at(a.cu, a.n_max, a.t_max)) return;
+  const PagedBatch &pg = a.pg;
+  if (t >= cu_at(pg.cu, pg.n_max, pg.t_max)) return;
   const int G = a.h / a.hkv, kh = head / G;
   int kv;
-  const Packed p = seq_of_row(
-      a.cu, a.n_max, a.t_max, t, lane, [&](int i) { return seq_at(a, i).kv; }, kv);
-  const int s = p.s;
-  const Seq q{p.b, p.n, kv};
-  if (t < q.bos || t >= q.bos + q.n) return;  // an unsorted cu_seqlens: a row of no sequence
+  const Packed q = seq_of_row(
+      pg.cu, pg.n_max, pg.t_max, t, lane, [&](int i) { return kv_of(pg, i); }, kv);
+  if (t < q.b || t >= q.b + q.n) return;  // an unsorted cu_seqlens: a row of no sequence
   const int prefix = a.plan[0];
   const int64_t per_head = reinterpret_cast<const int64_t *>(a.plan)[1];
-  const int64_t lead = reinterpret_cast<const int64_t *>(a.plan)[2];
-  const int64_t per_wg = reinterpret_cast<const int64_t *>(a.plan)[3];
-  const int64_t start = reinterpret_cast<const int64_t *>(a.plan + kPlanInts)[s];
+  const int64_t per_wg = reinterpret_cast<const int64_t *>(a.plan)[2];
 
-  // the two items of the row: units [lo, hi), and the row's number in its tile
-  int64_t lo[2] = {0, 0}, hi[2] = {0, 0};
-  int in_tile[2] = {0, 0};
-  if (prefix > 0) {
-    const int64_t r = (int64_t)t * G + head % G;
-    const int nu = units_of(prefix);
-    lo[0] = kh * per_head + r / kRows * nu;
-    hi[0] = lo[0] + nu;
-    in_tile[0] = (int)(r % kRows);
+  // the row's item: units [lo, hi) in the work-groups w0 .., and its row of the tile
+  int64_t lo = 0, w0 = 0, parts = 0;
+  int in_tile = 0;
+  if (kv > prefix) {
+    const int64_t start = reinterpret_cast<const int64_t *>(a.plan + kPlanInts)[q.s];
+    const int64_t r = (int64_t)(t - q.b) * G + head % G;
+    const int nu = units_of(kv - prefix);
+    lo = kh * per_head + start + r / kRows * nu;
+    in_tile = (int)(r % kRows);
+    w0 = lo / per_wg;
+    parts = (lo + nu - 1) / per_wg - w0 + 1;
   }
-  if (q.kv > prefix) {
-    const int64_t r = (int64_t)(t - q.bos) * G + head % G;
-    const int nu = units_of(q.kv - prefix);
-    lo[1] = kh * per_head + lead + start + r / kRows * nu;
-    hi[1] = lo[1] + nu;
-    in_tile[1] = (int)(r % kRows);
-  }
-  int64_t w0[2], cnt[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    w0[i] = lo[i] / per_wg;
-    cnt[i] = hi[i] > lo[i] ? (hi[i] - 1) / per_wg - w0[i] + 1 : 0;
-  }
-  if (prefix == 0 && cnt[1] == 1) return;  // the main kernel wrote it
+  if (prefix == 0 && parts == 1) return;  // the main kernel wrote it
   const int64_t orow = (int64_t)t * a.h + head;
-  const int64_t n = cnt[0] + cnt[1];
-  // partial result i of the row: its output sum and its statistics
+  // the prefix's parts of the row come first
+  const int lead = prefix > 0 ? a.pre_splits : 0;
+  const int64_t pre_item =
+      (int64_t)(a.pre_slots - 1 - t / a.pre_tt) * (a.h / a.pre_share) + head / a.pre_share;
+  const int pre_row = t % a.pre_tt * a.pre_share + head % a.pre_share;
+  const int64_t n = lead + parts;
   auto where = [&](int64_t i, const float *&po, const float *&pm) __attribute__((always_inline)) {
-    const int k = i < cnt[0] ? 0 : 1;
-    const int64_t j = i - (k ? cnt[0] : 0);
-    if (cnt[k] == 1) {
-      const int64_t at = (k ? (int64_t)a.t_max * a.h : 0) + orow;
-      po = a.done_o + at * D;
-      pm = a.done_ml + at * 2;
+    if (i < lead) {
+      const int64_t at = (pre_item * a.pre_splits + i) * a.pre_rows + pre_row;
+      po = a.pre_o + at * D;
+      pm = a.pre_ml + at * 2;
+    } else if (parts == 1) {
+      po = a.done_o + orow * D;
+      pm = a.done_ml + orow * 2;
     } else {
-      const int64_t wgi = w0[k] + j;
-      const int64_t at = (wgi * 2 + (lo[k] >= wgi * per_wg ? 1 : 0)) * kRows + in_tile[k];
+      const int64_t wgi = w0 + i - lead;
+      const int64_t at = (wgi * 2 + (lo >= wgi * per_wg ? 1 : 0)) * kRows + in_tile;
       po = a.part_o + at * D;
       pm = a.part_ml + at * 2;
     }
@@ -519,17 +442,17 @@ __global__ __launch_bounds__(256) void attn_join_kernel(PagedArgs a) {
 }
 
 template <typename T, int D, int kRT>
-hipError_t run(const PagedArgs &a, dim3 join, hipStream_t stream) {
-  hipLaunchKernelGGL((attn_paged_kernel<T, D, kRT>), dim3((a.grid + 7) / 8 * 8), dim3(256), 0,
+hipError_t run(const StreamArgs &a, dim3 join, hipStream_t stream) {
+  hipLaunchKernelGGL((attn_stream_kernel<T, D, kRT>), dim3((a.grid + 7) / 8 * 8), dim3(256), 0,
                      stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attn_join_kernel<T, D, kRT>), join, dim3(256), 0, stream, a);
+  hipLaunchKernelGGL((attn_stream_join_kernel<T, D, kRT>), join, dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
 template <typename T>
-hipError_t run_of(const PagedArgs &a, int d, int rt, dim3 join, hipStream_t stream) {
+hipError_t run_of(const StreamArgs &a, int d, int rt, dim3 join, hipStream_t stream) {
   if (d == 128)
     return rt == 1   ? run<T, 128, 1>(a, join, stream)
            : rt == 2 ? run<T, 128, 2>(a, join, stream)
@@ -537,30 +460,34 @@ hipError_t run_of(const PagedArgs &a, int d, int rt, dim3 join, hipStream_t stre
   return rt == 1 ? run<T, 256, 1>(a, join, stream) : run<T, 256, 2>(a, join, stream);
 }
 
+int64_t rows_per_seq(const gdn_attn_config *cfg) {
+  return (int64_t)cfg->t_max * (cfg->h / cfg->hkv) / cfg->n_max;
+}
+
 }  // namespace
 
-// One 16-row tile per item holds a decoding sequence's heads; where the rows of
-// an average sequence, or of the batch on its shared prefix, are more, wider
-// items read the keys fewer times.
-int paged_row_tiles(const gdn_attn_config *cfg) {
-  const int64_t rows = cfg->shared_max > 0
-                           ? (int64_t)cfg->t_max * (cfg->h / cfg->hkv)
-                           : (int64_t)cfg->t_max * (cfg->h / cfg->hkv) / cfg->n_max;
+// Rows of an average sequence (new tokens times query heads per key head) from
+// which its keys are taken in tiles of 128 or 256 rows.
+bool streams(const gdn_attn_config *cfg) { return rows_per_seq(cfg) < 128; }
+
+// One 16-row tile per item holds a decoding sequence's heads; where an average
+// sequence has more rows, wider items read the keys fewer times.
+int stream_row_tiles(const gdn_attn_config *cfg) {
   const int most = cfg->d == 128 ? 4 : 2;
   int rt = 1;
-  while (rt < most && rows > 16 * rt) rt *= 2;
+  while (rt < most && rows_per_seq(cfg) > 16 * rt) rt *= 2;
   return rt;
 }
 
-int paged_grid(const gdn_attn_config *cfg) {
-  return cu_count() * (paged_row_tiles(cfg) * cfg->d <= 256 ? 2 : 1);
+int stream_grid(const gdn_attn_config *cfg) {
+  return cu_count() * (stream_row_tiles(cfg) * cfg->d <= 256 ? 2 : 1);
 }
 
-hipError_t launch_attn_paged(const gdn_attn_config *cfg, PagedArgs a, hipStream_t stream) {
+hipError_t launch_attn_stream(const gdn_attn_config *cfg, StreamArgs a, hipStream_t stream) {
   if (cfg->t_max == 0) return hipSuccess;
   dim3 join;
   if (!flat_grid((int64_t)cfg->t_max * cfg->h, 256, join)) return hipErrorInvalidValue;
-  const int rt = paged_row_tiles(cfg);
+  const int rt = stream_row_tiles(cfg);
   return cfg->dtype == GDN_BF16 ? run_of<__bf16>(a, cfg->d, rt, join, stream)
                                 : run_of<_Float16>(a, cfg->d, rt, join, stream);
 }

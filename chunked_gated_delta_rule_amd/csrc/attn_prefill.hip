@@ -18,6 +18,8 @@
 #include "attn_common.hpp"
 #include "attn_launch.hpp"
 
+#include <type_traits>
+
 namespace gdn {
 
 namespace {
@@ -42,31 +44,27 @@ __device__ __forceinline__ u32x2 tr_read(Lds<T> tile, int at) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(tile + at)));
 }
 
-// A tile's rows are tokens times the query heads that share a key head, as many
-// of those as divide their number and are at most 16 (`share`): tiles then span
-// few tokens, so little is computed beyond the diagonal or past a sequence's end.
-// Tiles of tt tokens have slots: sequence s starts at slot floor(cu[s] / tt) + s,
-// which is distinct for every tile of the batch and grows with s, so a slot's
-// sequence is found by a search and no table is needed.
-constexpr int kMostShare = 16;
-int share_of(int group) {
-  int g = group < kMostShare ? group : kMostShare;
-  while (group % g) --g;
-  return g;
-}
-
-// Head group and tile slot of a work-group. The last (longest) tiles come first.
-// With a multiple of 8 groups, neighbouring groups (which may read the same keys)
-// go to one XCD, whose L2 then holds their keys and values.
-__device__ __forceinline__ void place(int wg, int groups, int slots, int &group, int &slot) {
+// Head group, tile slot and split of a work-group. The last (longest) tiles come
+// first. Unsplit, with a multiple of 8 groups, neighbouring groups (which may read
+// the same keys) go to one XCD, whose L2 then holds their keys and values; the
+// splits are numbered fastest, so that tiles of the same keys share an XCD.
+struct Place {
+  int group, slot, split;
+};
+__device__ __forceinline__ Place place(int wg, int groups, int slots, int splits) {
+  if (splits > 1) {
+    const int i = wg / splits;
+    return {i % groups, slots - 1 - i / groups, wg % splits};
+  }
   if (groups % 8 == 0) {
     const int per = groups / 8, i = wg >> 3;
-    group = (wg & 7) * per + i % per;
-    slot = slots - 1 - i / per;
-  } else {
-    group = wg % groups;
-    slot = slots - 1 - wg / groups;
+    return {(wg & 7) * per + i % per, slots - 1 - i / per, 0};
   }
+  return {wg % groups, slots - 1 - wg / groups, 0};
+}
+// Number of a tile among the partial results.
+__device__ __forceinline__ int64_t item_of(int group, int slot, int groups, int slots) {
+  return (int64_t)(slots - 1 - slot) * groups + group;
 }
 
 template <typename T, int D, int kBN, int kWaves>
@@ -104,22 +102,26 @@ __device__ __forceinline__ void barrier() {
   asm volatile("" ::: "memory");
 }
 
-// Copies kBN rows (those of them that the descriptor's range holds, zeros for the
+// Copies kBN rows (those of them that the descriptors' ranges hold, zeros for the
 // others) straight to LDS: lane l of wave w fills the 16 bytes at kPass i + 1024 w +
-// 16 l with the chunk that belongs there.
-template <typename T, int D, int kBN, int kWaves, bool kV>
-__device__ __forceinline__ void fetch(Lds<T> dst, rsrc_t src, int row_bytes, int lane, int w) {
+// 16 l with the chunk that belongs there. What a wave copies at a time lies in one
+// aligned group of 16 rows: these have one set of swizzles, and lie in one page.
+// rsrc(g, add): the descriptor of rows 16 g .., and what to add to offsets in it.
+template <typename T, int D, int kBN, int kWaves, bool kV, typename F>
+__device__ __forceinline__ void fetch(Lds<T> dst, int row_bytes, int lane, int w, F rsrc) {
   typedef Tile<T, D, kBN, kWaves> L;
-  // rows kRowsPerLoad apart (a multiple of 16) have the same swizzle, so a lane's
-  // places in one copy and the next differ by whole rows
-  static_assert(L::kRowsPerLoad % 16 == 0, "swizzles repeat every 16 rows");
+  static_assert(L::kRowsPerLoad % 16 == 0, "a wave stays in its rows' places of a group");
   const int in = 1024 * w + 16 * lane;
-  const int row = in / L::kRowBytes, ch = in % L::kRowBytes / 16 ^ (kV ? v_swz(row) : k_swz(row));
+  const int row = in / L::kRowBytes & 15;
+  const int ch = in % L::kRowBytes / 16 ^ (kV ? v_swz(row) : k_swz(row));
   const int from = opaque<D == 256>(row * row_bytes + 16 * ch);
 #pragma unroll
-  for (int i = 0; i < L::kLoads; ++i)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (Lds<void>)(dst + L::kPass / 2 * i + 512 * w), 16,
-                                             from + i * L::kRowsPerLoad * row_bytes, 0, 0, 0);
+  for (int i = 0; i < L::kLoads; ++i) {
+    int add = 0;
+    const rsrc_t r = rsrc(i * (L::kRowsPerLoad / 16) + 1024 / L::kRowBytes * w / 16, add);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (Lds<void>)(dst + L::kPass / 2 * i + 512 * w), 16,
+                                             from + add, 0, 0, 0);
+  }
 }
 
 // Running state of a wave's 32 query rows, and its two parts of a step over a
@@ -238,6 +240,18 @@ struct Rows {
     __builtin_amdgcn_sched_group_barrier(kSchedMfma, 4, 1);
   }
 
+  // The running state as it is, for a later join.
+  __device__ __forceinline__ void store_part(float *po, float *pm, int hh) const {
+    const float sum = sum32(l);
+    if (hh == 0) *reinterpret_cast<f32x2 *>(pm) = f32x2{m, sum};
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        *reinterpret_cast<f32x4 *>(po + 32 * i + 8 * b + 4 * hh) =
+            f32x4{o[i][4 * b], o[i][4 * b + 1], o[i][4 * b + 2], o[i][4 * b + 3]};
+  }
+
   __device__ __forceinline__ void store(T *row, int hh) const {
     const float sum = sum32(l);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that sees no key gives zeros
@@ -261,76 +275,118 @@ struct Rows {
   }
 };
 
-// The tile of a work-group: its heads, its sequence's rows and keys, its tokens.
+// The tile of a work-group: its heads and sequence, the sequence's rows and keys, the
+// tile's first token, and the part of its keys.
 struct Where {
-  int group, qb, lq, kb, lk, q0, past;
+  int group, slot, split, s, qb, lq, kb, lk, q0, past;
 };
-__device__ __forceinline__ bool find(const PrefillArgs &a, int tt, int slots, int lane, Where &t) {
-  int slot;
-  place(flat_block(), a.h / a.share, slots, t.group, slot);
-  if (slot < 0) return false;  // past the grid's count (last row)
-  int kv[2];
-  const Packed p = locate(
-      a.cu_q, a.n_max, a.t_max, slot, lane, [&](int i, int first) { return first / tt + i; },
-      [&](int i, int(&o)[2]) {
-        o[0] = cu_at(a.cu_k, i, a.tk_max);
-        o[1] = cu_end(a.cu_k, i, o[0], a.tk_max) - o[0];
-      },
-      kv);
-  t.qb = p.b;
-  t.lq = p.n;
-  t.q0 = (slot - (t.qb / tt + p.s)) * tt;
-  if (t.q0 < 0 || t.q0 >= t.lq) return false;  // no tile of the sequence has this slot
-  t.kb = kv[0];
-  t.lk = kv[1];
-  t.past = t.lk - t.lq;  // token r sees keys 0 .. past + r
-  return true;
+template <Keys kKeys, int kThreads>
+__device__ __forceinline__ bool find(const TileArgs &a, int tt, int tid, Where &t,
+                                     int (&lds)[kThreads / 64][2]) {
+  const Place at = place(flat_block(), a.h / a.share, a.slots, a.splits);
+  t.group = at.group;
+  t.slot = at.slot;
+  t.split = at.split;
+  if (at.slot < 0) return false;  // past the grid's count (last row)
+  if constexpr (kKeys == Keys::kShared) {
+    const Prefix p = shared_prefix<kThreads>(a.pg, tid, lds);
+    t.s = p.seq;
+    t.qb = t.kb = 0;
+    t.lq = cu_at(a.cu_q, a.n_max, a.t_max);
+    t.lk = p.len;
+    t.q0 = at.slot * tt;
+    t.past = t.lk;  // every token sees the whole prefix
+    return t.q0 < t.lq && t.lk > 0;
+  } else {
+    int kv[2];
+    const Packed p = locate(
+        a.cu_q, a.n_max, a.t_max, at.slot, tid & 63, [&](int i, int b) { return b / tt + i; },
+        [&](int i, int(&o)[2]) {
+          if constexpr (kKeys == Keys::kRows) {
+            o[0] = cu_at(a.cu_k, i, a.tk_max);
+            o[1] = cu_end(a.cu_k, i, o[0], a.tk_max) - o[0];
+          } else {
+            o[0] = 0;
+            o[1] = kv_of(a.pg, i);
+          }
+        },
+        kv);
+    t.s = p.s;
+    t.qb = p.b;
+    t.lq = p.n;
+    t.q0 = (at.slot - (t.qb / tt + p.s)) * tt;
+    t.kb = kv[0];
+    t.lk = kv[1];
+    t.past = t.lk - t.lq;                  // token r sees keys 0 .. past + r
+    return t.q0 >= 0 && t.q0 < t.lq;       // else no tile of the sequence has this slot
+  }
 }
 
 // kWaves waves of 32 rows. With four, two work-groups share a CU (D = 128) and
 // overlap by chance. With eight, the two waves of a SIMD (w and w + 4) go through
 // the two parts of a step in opposite order, a barrier after each part: while one
 // runs its score products the other forms weights.
-template <typename T, int D, int kBN, int kWaves>
-__global__ __launch_bounds__(64 * kWaves, kWaves == 8 || D == 128 ? 2 : 1) void attn_prefill_kernel(
-    PrefillArgs a, int slots) {
+template <typename T, int D, int kBN, int kWaves, Keys kKeys, bool kPart>
+__global__ __launch_bounds__(64 * kWaves, kWaves == 8 || D == 128 ? 2 : 1) void attn_tile_kernel(
+    TileArgs a) {
   constexpr int kBM = 32 * kWaves;
   // four arrays of their own, so that a tile in flight is known to be another
   // than the ones being read
   __shared__ __attribute__((aligned(16))) T k_a[kBN * D], v_a[kBN * D], k_b[kBN * D], v_b[kBN * D];
+  __shared__ int scan[kWaves][2];
 
-  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
   const int col = lane & 31, hh = lane >> 5;
   Where t;
   const int share = a.share, tt = kBM / share;
-  if (!find(a, tt, slots, lane, t)) return;
+  if (!find<kKeys, 64 * kWaves>(a, tt, tid, t, scan)) return;
   // one value per wave, which the compiler does not see by itself
-  t = {uniform(t.group), uniform(t.qb), uniform(t.lq), uniform(t.kb), uniform(t.lk), uniform(t.q0),
-       uniform(t.past)};
+  t = {uniform(t.group), uniform(t.slot), uniform(t.split), uniform(t.s), uniform(t.qb),
+       uniform(t.lq), uniform(t.kb), uniform(t.lk), uniform(t.q0), uniform(t.past)};
   const int kvh = t.group * share / (a.h / a.hkv);
   // this lane's row; those past the tile's tokens or the sequence's end take the
   // last token's limit and are not stored
   const int tok = min(t.q0 + (32 * w + col) / share, t.lq - 1);
-  const int lim = t.past + tok;
-  const int wave_lo = t.past + min(t.q0 + 32 * w / share, t.lq - 1);
-  const int wave_hi = t.past + min(t.q0 + min((32 * w + 31) / share, tt - 1), t.lq - 1);
-  const int keys = min(t.past + min(t.q0 + tt, t.lq), t.lk);  // keys any row of the tile sees
-  const int tiles = keys > 0 ? (keys + kBN - 1) / kBN : 0;
+  int lim = t.past + tok, wave_lo = t.past + min(t.q0 + 32 * w / share, t.lq - 1);
+  int wave_hi = t.past + min(t.q0 + min((32 * w + 31) / share, tt - 1), t.lq - 1);
+  int keys = min(t.past + min(t.q0 + tt, t.lq), t.lk);  // keys any row of the tile sees
+  if constexpr (kKeys == Keys::kShared) {
+    lim = wave_lo = wave_hi = t.lk - 1;
+    keys = t.lk;
+  }
+  int tiles = keys > 0 ? (keys + kBN - 1) / kBN : 0, j0 = 0;
+  if constexpr (kPart) {
+    const int per = (tiles + a.splits - 1) / a.splits;
+    j0 = t.split * per;
+    tiles = max(min(per, tiles - j0), 0);
+  }
 
-  const T *kp = static_cast<const T *>(a.k) + (int64_t)t.kb * a.k_row + kvh * D;
-  const T *vp = static_cast<const T *>(a.v) + (int64_t)t.kb * a.v_row + kvh * D;
-  const int k_bytes = (int)a.k_row * 2, v_bytes = (int)a.v_row * 2;
-  // a tile's rows as a range that ends with the sequence's last key
-  auto get_k = [&](int j, T *kt) __attribute__((always_inline)) {
-    const int64_t k0 = (int64_t)j * kBN;
-    fetch<T, D, kBN, kWaves, false>((Lds<T>)kt,
-        make_rsrc(kp + k0 * a.k_row, (min(kBN, t.lk - (int)k0) - 1) * k_bytes + D * 2), k_bytes, lane, w);
+  const int k_bytes = kKeys == Keys::kRows ? (int)a.k_row * 2 : D * 2;
+  const int v_bytes = kKeys == Keys::kRows ? (int)a.v_row * 2 : D * 2;
+  // a tile's rows as ranges that end with the sequence's last key
+  auto get = [&](auto is_v, int j, T *tile) __attribute__((always_inline)) {
+    constexpr bool kV = decltype(is_v)::value;
+    const int k0 = (j0 + j) * kBN;
+    const int row_bytes = kV ? v_bytes : k_bytes;
+    if constexpr (kKeys == Keys::kRows) {
+      const T *p = static_cast<const T *>(kV ? a.v : a.k) +
+                   (int64_t)(t.kb + k0) * (kV ? a.v_row : a.k_row) + kvh * D;
+      const rsrc_t r = make_rsrc(p, (min(kBN, t.lk - k0) - 1) * row_bytes + D * 2);
+      fetch<T, D, kBN, kWaves, kV>((Lds<T>)tile, row_bytes, lane, w, [&](int g, int &add) {
+        add = 16 * g * row_bytes;
+        return r;
+      });
+    } else {
+      const int32_t *table = a.pg.table + (int64_t)t.s * a.pg.max_pages;
+      fetch<T, D, kBN, kWaves, kV>((Lds<T>)tile, row_bytes, lane, w, [&](int g, int &) {
+        const int key = k0 + 16 * g, rows = max(min(16, t.lk - key), 0);
+        const int64_t at = pool_row(a.pg, table, min(key, (t.lk - 1) & ~15), kvh, a.hkv);
+        return make_rsrc(static_cast<const T *>(kV ? a.v : a.k) + at * D, rows * row_bytes);
+      });
+    }
   };
-  auto get_v = [&](int j, T *vt) __attribute__((always_inline)) {
-    const int64_t k0 = (int64_t)j * kBN;
-    fetch<T, D, kBN, kWaves, true>((Lds<T>)vt,
-        make_rsrc(vp + k0 * a.v_row, (min(kBN, t.lk - (int)k0) - 1) * v_bytes + D * 2), v_bytes, lane, w);
-  };
+  auto get_k = [&](int j, T *tile) __attribute__((always_inline)) { get(std::false_type{}, j, tile); };
+  auto get_v = [&](int j, T *tile) __attribute__((always_inline)) { get(std::true_type{}, j, tile); };
   Rows<T, D, kBN> x;
   if (tiles > 0) {
     get_k(0, k_a);
@@ -339,12 +395,12 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 || D == 128 ? 2 : 1) void 
   x.load(static_cast<const T *>(a.q) + (int64_t)(t.qb + tok) * a.q_row +
              (t.group * share + (32 * w + col) % share) * D, hh);
   auto score = [&](int j, T *kt) __attribute__((always_inline)) {
-    const int k0 = j * kBN;
+    const int k0 = (j0 + j) * kBN;
     if (k0 <= wave_hi)
       x.score((Lds<T>)kt, k0, lim, k0 + kBN - 1 > wave_lo, a.scale_log2, lane);
   };
   auto weigh = [&](int j, T *vt) __attribute__((always_inline)) {
-    if (j * kBN <= wave_hi) x.weigh((Lds<T>)vt, a.scale_log2, lane);
+    if ((j0 + j) * kBN <= wave_hi) x.weigh((Lds<T>)vt, a.scale_log2, lane);
   };
   if constexpr (kWaves == 4) {
     for (int j = 0; j < tiles; j += 2) {
@@ -413,41 +469,157 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 || D == 128 ? 2 : 1) void 
     }
   }
   const int row = opaque<true>(32 * w + col);  // not kept along the loop
-  const int token = t.q0 + row / share;
-  x.store(row < tt * share && token < t.lq
-              ? static_cast<T *>(a.o) +
-                    ((int64_t)(t.qb + token) * a.h + t.group * share + row % share) * D
-              : nullptr, hh);
+  if constexpr (kPart) {
+    const int64_t at =
+        (item_of(t.group, t.slot, a.h / share, a.slots) * a.splits + t.split) * kBM + row;
+    x.store_part(a.part_o + at * D, a.part_ml + at * 2, hh);
+  } else {
+    const int token = t.q0 + row / share;
+    x.store(row < tt * share && token < t.lq
+                ? static_cast<T *>(a.o) +
+                      ((int64_t)(t.qb + token) * a.h + t.group * share + row % share) * D
+                : nullptr, hh);
+  }
+}
+
+// Joins the parts of a row's keys: one wave per row.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void attn_tile_join_kernel(TileArgs a, int tt, int bm) {
+  constexpr int kPer = D / 64;  // dims per lane
+  typedef float vec __attribute__((ext_vector_type(kPer)));
+  const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
+  const int64_t i = (int64_t)flat_block() * 4 + w;
+  const int t = (int)(i / a.h), head = (int)(i % a.h);
+  if (t >= cu_at(a.cu_q, a.n_max, a.t_max)) return;
+  int none;
+  const Packed p = seq_of_row(
+      a.cu_q, a.n_max, a.t_max, t, lane, [](int) { return 0; }, none);
+  if (t < p.b || t >= p.b + p.n) return;  // an unsorted cu_seqlens: a row of no sequence
+  const int tile = (t - p.b) / tt;
+  const int64_t item =
+      item_of(head / a.share, p.b / tt + p.s + tile, a.h / a.share, a.slots) * a.splits;
+  const int row = (t - p.b - tile * tt) * a.share + head % a.share;
+  // the splits' statistics, one per lane
+  const float mine = lane < a.splits ? a.part_ml[((item + lane) * bm + row) * 2] : kNegInf;
+  float big = mine;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) big = fmaxf(big, __shfl_xor(big, off, 64));
+  const float f = mine == kNegInf ? 0.f : fast_exp2(mine - big);
+  float l = lane < a.splits ? a.part_ml[((item + lane) * bm + row) * 2 + 1] * f : 0.f;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) l += __shfl_xor(l, off, 64);
+  vec sum = {};
+  for (int k = 0; k < a.splits; k += 4) {  // four loads at a time
+    vec x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      x[e] = *reinterpret_cast<const vec *>(
+          a.part_o + ((item + min(k + e, a.splits - 1)) * bm + row) * D + kPer * lane);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float g = __shfl(f, (k + e) & 63, 64);
+      if (k + e < a.splits) sum += g * x[e];
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<T *>(a.o) + ((int64_t)t * a.h + head) * D);
+#pragma unroll
+  for (int k = 0; k < kPer / 2; ++k)
+    o[kPer / 2 * lane + k] = Elem<T>::pack(sum[2 * k] * inv, sum[2 * k + 1] * inv);
+}
+
+template <typename T, int D, int kWaves, Keys kKeys, bool kPart>
+hipError_t run(const gdn_attn_config *cfg, const TileArgs &a, int tt, hipStream_t stream) {
+  dim3 grid;
+  if (!flat_grid((int64_t)a.slots * (cfg->h / a.share) * a.splits, 64 * kWaves, grid))
+    return hipErrorInvalidValue;
+  dim3 join;
+  if (kPart && kKeys != Keys::kShared && !flat_grid(((int64_t)cfg->t_max * cfg->h + 3) / 4, 256, join))
+    return hipErrorInvalidValue;
+  hipLaunchKernelGGL((attn_tile_kernel<T, D, 64, kWaves, kKeys, kPart>), grid, dim3(64 * kWaves), 0,
+                     stream, a);
+  if (kPart && kKeys != Keys::kShared) {
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((attn_tile_join_kernel<T, D>), join, dim3(256), 0, stream, a, tt, 32 * kWaves);
+  }
+  return hipGetLastError();
+}
+
+template <typename T, int D, int kWaves, Keys kKeys>
+hipError_t run_split(const gdn_attn_config *cfg, const TileArgs &a, int tt, hipStream_t stream) {
+  return a.splits > 1 ? run<T, D, kWaves, kKeys, true>(cfg, a, tt, stream)
+                      : run<T, D, kWaves, kKeys, false>(cfg, a, tt, stream);
+}
+
+template <typename T>
+hipError_t run_of(const gdn_attn_config *cfg, Keys keys, const TileArgs &a, const TileShape &s,
+                  hipStream_t stream) {
+  if (keys == Keys::kShared)
+    return cfg->d == 256 ? run<T, 256, 8, Keys::kShared, true>(cfg, a, s.tt, stream)
+                         : run<T, 128, 4, Keys::kShared, true>(cfg, a, s.tt, stream);
+  if (keys == Keys::kPages)
+    return cfg->d == 256  ? run_split<T, 256, 8, Keys::kPages>(cfg, a, s.tt, stream)
+           : s.waves == 8 ? run_split<T, 128, 8, Keys::kPages>(cfg, a, s.tt, stream)
+                          : run_split<T, 128, 4, Keys::kPages>(cfg, a, s.tt, stream);
+  return cfg->d == 256  ? run_split<T, 256, 8, Keys::kRows>(cfg, a, s.tt, stream)
+         : s.waves == 8 ? run_split<T, 128, 8, Keys::kRows>(cfg, a, s.tt, stream)
+                        : run_split<T, 128, 4, Keys::kRows>(cfg, a, s.tt, stream);
 }
 
 // Average tokens per sequence from which heads of 128 take work-groups of eight
 // waves: 4096 tokens 137 us against 140 us with four, 16384 tokens 955 against 968;
 // 32 sequences of 500 on average 177 against 159 us.
 constexpr int kLongPrompt = 2048;
-
-template <typename T, int D, int kBN, int kWaves>
-hipError_t run(const gdn_attn_config *cfg, const PrefillArgs &a, hipStream_t stream) {
-  const int64_t slots = cfg->t_max / (32 * kWaves / a.share) + cfg->n_max;
-  dim3 grid;
-  if (!flat_grid(slots * (cfg->h / a.share), 64 * kWaves, grid)) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((attn_prefill_kernel<T, D, kBN, kWaves>), grid, dim3(64 * kWaves), 0, stream, a,
-                     static_cast<int>(slots));
-  return hipGetLastError();
-}
-
-template <typename T>
-hipError_t run_of(const gdn_attn_config *cfg, const PrefillArgs &a, hipStream_t stream) {
-  if (cfg->d == 256) return run<T, 256, 64, 8>(cfg, a, stream);
-  return cfg->t_max / cfg->n_max >= kLongPrompt ? run<T, 128, 64, 8>(cfg, a, stream)
-                                                : run<T, 128, 64, 4>(cfg, a, stream);
-}
+// A tile's rows are tokens times the query heads that share a key head, as many
+// of those as divide their number and are at most this many: tiles then span few
+// tokens, so little is computed beyond the diagonal or past a sequence's end (32
+// prompts of 500 tokens on average, two heads per key head: 176 -> 160 us).
+constexpr int kMostShare = 16;
+// A split has at least this many keys of the longest possible sequence, and there
+// are at most 64 (one per lane of the join).
+constexpr int kSplitKeys = 256;
+constexpr int kMostSplits = 64;
 
 }  // namespace
 
-hipError_t launch_attn_prefill(const gdn_attn_config *cfg, PrefillArgs a, hipStream_t stream) {
+// Tiles of tt tokens have slots: sequence s starts at slot floor(cu[s] / tt) + s,
+// which is distinct for every tile of the batch and grows with s, so a slot's
+// sequence is found by a search and no table is needed.
+TileShape tile_shape(const gdn_attn_config *cfg, Keys keys) {
+  TileShape s;
+  const int group = cfg->h / cfg->hkv;
+  s.share = group < kMostShare ? group : kMostShare;
+  while (group % s.share) --s.share;
+  s.waves = cfg->d == 256 || (keys != Keys::kShared && cfg->t_max / cfg->n_max >= kLongPrompt) ? 8 : 4;
+  s.tt = 32 * s.waves / s.share;
+  s.slots = keys == Keys::kShared ? (cfg->t_max + s.tt - 1) / s.tt : cfg->t_max / s.tt + cfg->n_max;
+  // few tiles and many keys: split the keys until the device is full
+  const int64_t room = (int64_t)cfg->max_pages * cfg->page_size;
+  const int64_t longest = keys == Keys::kShared  ? (cfg->shared_max < room ? cfg->shared_max : room)
+                          : keys == Keys::kPages ? room
+                                                 : (cfg->tk_max > 0 ? cfg->tk_max : cfg->t_max) / cfg->n_max;
+  const int64_t tiles = (int64_t)s.slots * (cfg->h / s.share);
+  const int64_t full = cu_count() * (s.waves == 8 ? 1 : 2);
+  int64_t n = tiles > 0 ? full / tiles : 1;
+  if (n > longest / kSplitKeys) n = longest / kSplitKeys;
+  s.splits = n < 1 ? 1 : n > kMostSplits ? kMostSplits : static_cast<int>(n);
+  return s;
+}
+
+int64_t tile_part_rows(const gdn_attn_config *cfg, const TileShape &s, Keys keys) {
+  if (s.splits == 1 && keys != Keys::kShared) return 0;
+  return (int64_t)s.slots * (cfg->h / s.share) * s.splits * 32 * s.waves;
+}
+
+hipError_t launch_attn_tiles(const gdn_attn_config *cfg, Keys keys, TileArgs a, hipStream_t stream) {
   if (cfg->t_max == 0) return hipSuccess;
-  a.share = share_of(cfg->h / cfg->hkv);
-  return cfg->dtype == GDN_BF16 ? run_of<__bf16>(cfg, a, stream) : run_of<_Float16>(cfg, a, stream);
+  const TileShape s = tile_shape(cfg, keys);
+  a.share = s.share;
+  a.splits = s.splits;
+  a.slots = s.slots;
+  return cfg->dtype == GDN_BF16 ? run_of<__bf16>(cfg, keys, a, s, stream)
+                                : run_of<_Float16>(cfg, keys, a, s, stream);
 }
 
 }  // namespace gdn

@@ -166,6 +166,11 @@ PREFILL = [
     ([9, 40, 5], [0, 17, 5], 2, 1, 128),     # rows that see no key
     ([200, 140], [130, 40], 2, 1, 256),      # whole tiles that see no key
     ([260], [260], 16, 1, 128),
+    ([70, 1], [110, 41], 5, 1, 128),          # queries that start inside a tile of keys
+    ([150], [190], 2, 2, 256),
+    ([40], [3000], 8, 2, 128),                # few rows and many keys: split
+    ([3], [2500], 4, 1, 256),
+    ([12, 7], [0, 2100], 6, 2, 128),
 ]
 
 
@@ -196,6 +201,23 @@ def test_prefill(t, new, full, h, hkv, d):
         worst = max(worst, check_attention(o[a], f64(q[a]), f64(k[b]), f64(v[b]), d ** -0.5, t))
     say(f"  off / bound {worst:.3f}")
     assert (o[sum(new):] == MARK).all()
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("T,past,h,hkv,d", [(4500, 0, 2, 1, 128), (2100, 25, 1, 1, 256),
+                                            (1500, 2011, 4, 1, 128)])
+def test_prefill_of_long_prompts_at_sampled_rows(t, T, past, h, hkv, d):
+    """Every 97th row and the last one against the oracle; every row finite, and of
+    the size of a mean of values."""
+    q = normal(1, T, h, d, dtype=t, scale=2.0)
+    k, v = (normal(i, T + past, hkv, d, dtype=t) for i in (2, 3))
+    say(f"prefill {t} {T} of {T + past} h={h} d={d}")
+    o = gdn.causal_attention(q.to(DEV), k.to(DEV), v.to(DEV), on(cu_of([T])),
+                             on(cu_of([T + past])))
+    assert o.isfinite().all() and float(o.abs().max()) <= float(v.abs().max()) * 1.01
+    for r in [*range(0, T, 97), T - 1]:
+        check_attention(o[r:r + 1], f64(q[r:r + 1]), f64(k[:past + r + 1]), f64(v[:past + r + 1]),
+                        d ** -0.5, t)
 
 
 @pytest.mark.parametrize("t", TYPES)
@@ -262,6 +284,11 @@ PAGED = [
     ([3, 3], [330, 200], 8, 1, 128, 16, 197),              # all after the prefix, to the token
     ([1, 6], [900, 500], 4, 1, 256, 32, 490),              # tokens reach into it: fewer pages
     ([1] * 300, [1 + i % 50 for i in range(300)], 2, 1, 128, 16, 0),
+    ([1] * 20, [1100 + 9 * i for i in range(20)], 16, 2, 256, 16, 1000),  # prefix in parts
+    ([60, 45], [700, 300], 8, 1, 128, 16, 0),              # many rows: tiles over the pages
+    ([130, 0, 20], [130, 77, 1500], 8, 2, 256, 64, 0),
+    ([90], [60], 8, 1, 128, 32, 0),
+    ([300, 280], [400, 333], 2, 1, 128, 128, 64),
 ]
 
 

@@ -299,7 +299,7 @@ gdn_status gdn_attn_paged(const gdn_attn_config *cfg, const void *q, int64_t q_r
     a.pre_tt = s.tt;
     a.pre_slots = s.slots;
     a.pre_splits = s.splits;
-    a.pre_rows = 32 * s.waves;
+    a.pre_rows = s.rows;
   } else {
     a.pre_share = a.pre_tt = 1;  // the prefix is empty: these are divided by, not used
   }

@@ -50,9 +50,9 @@ struct TileArgs {
 
 // How a call is cut into tiles: rows per tile are tokens times `share` query heads
 // of one key head, tt tokens; `slots` token tiles at most, times h / share head
-// groups; each tile's keys in `splits` parts.
+// groups; each tile's keys in `splits` parts. `rows` rows (tt * share, rounded up).
 struct TileShape {
-  int waves, share, tt, slots, splits;
+  int waves, rows, share, tt, slots, splits;
 };
 TileShape tile_shape(const gdn_attn_config *cfg, Keys keys);
 // Rows of partial results the shape needs (0 where o is written at once).

@@ -346,118 +346,146 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
   }
 }
 
-// Joins what several work-groups, the shared prefix's included, left of a row,
-// and writes zeros where a row sees no key. One work-group per (token, query
-// head); rows that the main kernel finished are left alone.
+// Joins what several work-groups, the shared prefix's included, left of a row, and
+// writes zeros where a row sees no key. One work-group per token and `per` query
+// heads; rows that the main kernel finished are left alone. The parts' statistics
+// are read first and become weights in LDS, so that the output sums, which are
+// most of the bytes, are read without waiting for anything.
 template <typename T, int D, int kRT>
-__global__ __launch_bounds__(256) void attn_stream_join_kernel(StreamArgs a) {
+__global__ __launch_bounds__(256) void attn_stream_join_kernel(StreamArgs a, int per) {
   constexpr int kRows = 16 * kRT;
-  constexpr int kLanes = D / 4;            // threads per partial result
-  constexpr int kPar = 256 / kLanes;       // partial results at a time
+  constexpr int kLanes = D / 4;            // threads per part
+  constexpr int kPar = 256 / kLanes;       // parts at a time
+  constexpr int kMost = 1024;              // weights held at a time
   __shared__ __attribute__((aligned(16))) float os[kPar][D];
-  __shared__ float ms[4], ls[kPar];
-  const int wg = flat_block();
-  const int t = wg / a.h, head = wg % a.h;
-  const int tid = threadIdx.x, lane = tid & 63;
+  __shared__ float weight[kMost], red[4][2];
+  const int wg = flat_block(), cuts = (a.h + per - 1) / per;
+  const int t = wg / cuts, h0 = wg % cuts * per, h1 = min(h0 + per, a.h);
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const PagedBatch &pg = a.pg;
   if (t >= cu_at(pg.cu, pg.n_max, pg.t_max)) return;
-  const int G = a.h / a.hkv, kh = head / G;
   int kv;
   const Packed q = seq_of_row(
       pg.cu, pg.n_max, pg.t_max, t, lane, [&](int i) { return kv_of(pg, i); }, kv);
   if (t < q.b || t >= q.b + q.n) return;  // an unsorted cu_seqlens: a row of no sequence
+  const int G = a.h / a.hkv;
   const int prefix = a.plan[0];
   const int64_t per_head = reinterpret_cast<const int64_t *>(a.plan)[1];
   const int64_t per_wg = reinterpret_cast<const int64_t *>(a.plan)[2];
+  const int64_t start = reinterpret_cast<const int64_t *>(a.plan + kPlanInts)[q.s];
+  const int lead = prefix > 0 ? a.pre_splits : 0;  // the prefix's parts of a row come first
 
-  // the row's item: units [lo, hi) in the work-groups w0 .., and its row of the tile
-  int64_t lo = 0, w0 = 0, parts = 0;
-  int in_tile = 0;
-  if (kv > prefix) {
-    const int64_t start = reinterpret_cast<const int64_t *>(a.plan + kPlanInts)[q.s];
-    const int64_t r = (int64_t)(t - q.b) * G + head % G;
-    const int nu = units_of(kv - prefix);
-    lo = kh * per_head + start + r / kRows * nu;
-    in_tile = (int)(r % kRows);
-    w0 = lo / per_wg;
-    parts = (lo + nu - 1) / per_wg - w0 + 1;
-  }
-  if (prefix == 0 && parts == 1) return;  // the main kernel wrote it
-  const int64_t orow = (int64_t)t * a.h + head;
-  // the prefix's parts of the row come first
-  const int lead = prefix > 0 ? a.pre_splits : 0;
-  const int64_t pre_item =
-      (int64_t)(a.pre_slots - 1 - t / a.pre_tt) * (a.h / a.pre_share) + head / a.pre_share;
-  const int pre_row = t % a.pre_tt * a.pre_share + head % a.pre_share;
-  const int64_t n = lead + parts;
-  auto where = [&](int64_t i, const float *&po, const float *&pm) __attribute__((always_inline)) {
-    if (i < lead) {
-      const int64_t at = (pre_item * a.pre_splits + i) * a.pre_rows + pre_row;
-      po = a.pre_o + at * D;
-      pm = a.pre_ml + at * 2;
-    } else if (parts == 1) {
-      po = a.done_o + orow * D;
-      pm = a.done_ml + orow * 2;
-    } else {
-      const int64_t wgi = w0 + i - lead;
-      const int64_t at = (wgi * 2 + (lo >= wgi * per_wg ? 1 : 0)) * kRows + in_tile;
-      po = a.part_o + at * D;
-      pm = a.part_ml + at * 2;
+  for (int head = h0; head < h1; ++head) {
+    // the row's item: units [lo, hi) in the work-groups w0 .., and its row of the tile
+    int64_t lo = 0, w0 = 0;
+    int parts = 0, in_tile = 0;
+    if (kv > prefix) {
+      const int64_t r = (int64_t)(t - q.b) * G + head % G;
+      const int nu = units_of(kv - prefix);
+      lo = head / G * per_head + start + r / kRows * nu;
+      in_tile = (int)(r % kRows);
+      w0 = lo / per_wg;
+      parts = (int)((lo + nu - 1) / per_wg - w0 + 1);
     }
-  };
-  float big = kNegInf;
-  for (int64_t i = tid; i < n; i += 256) {
-    const float *po, *pm;
-    where(i, po, pm);
-    big = fmaxf(big, pm[0]);
-  }
+    if (prefix == 0 && parts == 1) continue;  // the main kernel wrote it
+    const int64_t orow = (int64_t)t * a.h + head;
+    const int64_t pre_item =
+        (int64_t)(a.pre_slots - 1 - t / a.pre_tt) * (a.h / a.pre_share) + head / a.pre_share;
+    const int pre_row = t % a.pre_tt * a.pre_share + head % a.pre_share;
+    const int n = lead + parts;
+    // place of a part among the rows of its array
+    auto where = [&](int i, const float *&po, const float *&pm) __attribute__((always_inline)) {
+      if (i < lead) {
+        const int64_t at = (pre_item * a.pre_splits + i) * a.pre_rows + pre_row;
+        po = a.pre_o + at * D;
+        pm = a.pre_ml + at * 2;
+      } else if (parts == 1) {
+        po = a.done_o + orow * D;
+        pm = a.done_ml + orow * 2;
+      } else {
+        const int64_t wgi = w0 + i - lead;
+        const int64_t at = (wgi * 2 + (lo >= wgi * per_wg ? 1 : 0)) * kRows + in_tile;
+        po = a.part_o + at * D;
+        pm = a.part_ml + at * 2;
+      }
+    };
+    float big = kNegInf;
+    for (int i = tid; i < n; i += 256) {
+      const float *po, *pm;
+      where(i, po, pm);
+      big = fmaxf(big, pm[0]);
+    }
 #pragma unroll
-  for (int off = 1; off < 64; off <<= 1) big = fmaxf(big, __shfl_xor(big, off, 64));
-  if (lane == 0) ms[tid >> 6] = big;
-  __syncthreads();
-  big = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3]));
-  f32x4 sum = zero4();
-  float l = 0.f;
-  const int part = tid / kLanes, d4 = 4 * (tid % kLanes);
-  for (int64_t i = part; i < n; i += kPar) {
-    const float *po, *pm;
-    where(i, po, pm);
-    if (pm[0] == kNegInf) continue;
-    const float f = fast_exp2(pm[0] - big);
-    l = fmaf(pm[1], f, l);
-    sum += *reinterpret_cast<const f32x4 *>(po + d4) * f;
-  }
-  *reinterpret_cast<f32x4 *>(&os[part][d4]) = sum;
-  if (tid % kLanes == 0) ls[part] = l;
-  __syncthreads();
-  if (part > 0) return;
+    for (int off = 1; off < 64; off <<= 1) big = fmaxf(big, __shfl_xor(big, off, 64));
+    __syncthreads();  // the head before may still read LDS
+    if (lane == 0) red[w][0] = big;
+    __syncthreads();
+    big = fmaxf(fmaxf(red[0][0], red[1][0]), fmaxf(red[2][0], red[3][0]));
+
+    f32x4 sum = zero4();
+    float l = 0.f;
+    const int part = tid / kLanes, d4 = 4 * (tid % kLanes);
+    for (int base = 0; base < n; base += kMost) {
+      const int m = min(n - base, kMost);
+      if (base) __syncthreads();
+      for (int i = tid; i < m; i += 256) {
+        const float *po, *pm;
+        where(base + i, po, pm);
+        const float f = pm[0] == kNegInf ? 0.f : fast_exp2(pm[0] - big);
+        weight[i] = f;
+        l = fmaf(pm[1], f, l);
+      }
+      __syncthreads();
+      for (int i = part; i < m; i += 4 * kPar) {
+        f32x4 x[4];
+        float f[4];
 #pragma unroll
-  for (int i = 1; i < kPar; ++i) {
-    sum += *reinterpret_cast<const f32x4 *>(&os[i][d4]);
-    l += ls[i];
+        for (int e = 0; e < 4; ++e) {  // four loads at a time
+          const int k = min(i + e * kPar, m - 1);
+          const float *po, *pm;
+          where(base + k, po, pm);
+          x[e] = *reinterpret_cast<const f32x4 *>(po + d4);
+          f[e] = i + e * kPar < m ? weight[k] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (f[e] != 0.f) sum += x[e] * f[e];
+      }
+    }
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) l += __shfl_xor(l, off, 64);
+    if (lane == 0) red[w][1] = l;
+    *reinterpret_cast<f32x4 *>(&os[part][d4]) = sum;
+    __syncthreads();
+    if (part == 0) {
+      l = red[0][1] + red[1][1] + red[2][1] + red[3][1];
+#pragma unroll
+      for (int i = 1; i < kPar; ++i) sum += *reinterpret_cast<const f32x4 *>(&os[i][d4]);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      *reinterpret_cast<u32x2 *>(static_cast<T *>(a.o) + orow * D + d4) =
+          u32x2{Elem<T>::pack(sum[0] * inv, sum[1] * inv),
+                Elem<T>::pack(sum[2] * inv, sum[3] * inv)};
+    }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  *reinterpret_cast<u32x2 *>(static_cast<T *>(a.o) + orow * D + d4) =
-      u32x2{Elem<T>::pack(sum[0] * inv, sum[1] * inv), Elem<T>::pack(sum[2] * inv, sum[3] * inv)};
 }
 
 template <typename T, int D, int kRT>
-hipError_t run(const StreamArgs &a, dim3 join, hipStream_t stream) {
+hipError_t run(const StreamArgs &a, dim3 join, int per, hipStream_t stream) {
   hipLaunchKernelGGL((attn_stream_kernel<T, D, kRT>), dim3((a.grid + 7) / 8 * 8), dim3(256), 0,
                      stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attn_stream_join_kernel<T, D, kRT>), join, dim3(256), 0, stream, a);
+  hipLaunchKernelGGL((attn_stream_join_kernel<T, D, kRT>), join, dim3(256), 0, stream, a, per);
   return hipGetLastError();
 }
 
 template <typename T>
-hipError_t run_of(const StreamArgs &a, int d, int rt, dim3 join, hipStream_t stream) {
+hipError_t run_of(const StreamArgs &a, int d, int rt, dim3 join, int per, hipStream_t stream) {
   if (d == 128)
-    return rt == 1   ? run<T, 128, 1>(a, join, stream)
-           : rt == 2 ? run<T, 128, 2>(a, join, stream)
-                     : run<T, 128, 4>(a, join, stream);
-  return rt == 1 ? run<T, 256, 1>(a, join, stream) : run<T, 256, 2>(a, join, stream);
+    return rt == 1   ? run<T, 128, 1>(a, join, per, stream)
+           : rt == 2 ? run<T, 128, 2>(a, join, per, stream)
+                     : run<T, 128, 4>(a, join, per, stream);
+  return rt == 1 ? run<T, 256, 1>(a, join, per, stream) : run<T, 256, 2>(a, join, per, stream);
 }
 
 int64_t rows_per_seq(const gdn_attn_config *cfg) {
@@ -485,11 +513,16 @@ int stream_grid(const gdn_attn_config *cfg) {
 
 hipError_t launch_attn_stream(const gdn_attn_config *cfg, StreamArgs a, hipStream_t stream) {
   if (cfg->t_max == 0) return hipSuccess;
+  // heads per joining work-group: most rows of a large batch need no join, and finding
+  // a token's sequence costs more than looking at one
+  const int64_t fair = (int64_t)cfg->t_max * cfg->h / (4 * cu_count());
+  const int per = static_cast<int>(fair < 1 ? 1 : fair > cfg->h ? cfg->h : fair);
   dim3 join;
-  if (!flat_grid((int64_t)cfg->t_max * cfg->h, 256, join)) return hipErrorInvalidValue;
+  if (!flat_grid((int64_t)cfg->t_max * ((cfg->h + per - 1) / per), 256, join))
+    return hipErrorInvalidValue;
   const int rt = stream_row_tiles(cfg);
-  return cfg->dtype == GDN_BF16 ? run_of<__bf16>(a, cfg->d, rt, join, stream)
-                                : run_of<_Float16>(a, cfg->d, rt, join, stream);
+  return cfg->dtype == GDN_BF16 ? run_of<__bf16>(a, cfg->d, rt, join, per, stream)
+                                : run_of<_Float16>(a, cfg->d, rt, join, per, stream);
 }
 
 }  // namespace gdn

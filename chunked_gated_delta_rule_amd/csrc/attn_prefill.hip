@@ -24,6 +24,8 @@ namespace gdn {
 
 namespace {
 
+constexpr int kPartRows = 128;  // rows of a tile whose keys are split
+
 // instruction kinds of __builtin_amdgcn_sched_group_barrier
 constexpr int kSchedValu = 0x2, kSchedMfma = 0x8, kSchedLds = 0x100;
 
@@ -110,17 +112,24 @@ __device__ __forceinline__ void barrier() {
 template <typename T, int D, int kBN, int kWaves, bool kV, typename F>
 __device__ __forceinline__ void fetch(Lds<T> dst, int row_bytes, int lane, int w, F rsrc) {
   typedef Tile<T, D, kBN, kWaves> L;
-  static_assert(L::kRowsPerLoad % 16 == 0, "a wave stays in its rows' places of a group");
+  static_assert(L::kRowsPerLoad % 8 == 0, "copies start at even halves of a group");
   const int in = 1024 * w + 16 * lane;
-  const int row = in / L::kRowBytes & 15;
-  const int ch = in % L::kRowBytes / 16 ^ (kV ? v_swz(row) : k_swz(row));
-  const int from = opaque<D == 256>(row * row_bytes + 16 * ch);
+  // a lane's offset in its group, for copies that start in the group's first and
+  // (copies of 8 rows) second half
+  constexpr int kHalves = L::kRowsPerLoad % 16 ? 2 : 1;
+  int from[kHalves];
+#pragma unroll
+  for (int i = 0; i < kHalves; ++i) {
+    const int row = (in / L::kRowBytes + 8 * i) & 15;
+    const int ch = in % L::kRowBytes / 16 ^ (kV ? v_swz(row) : k_swz(row));
+    from[i] = opaque<D == 256>(row * row_bytes + 16 * ch);
+  }
 #pragma unroll
   for (int i = 0; i < L::kLoads; ++i) {
     int add = 0;
-    const rsrc_t r = rsrc(i * (L::kRowsPerLoad / 16) + 1024 / L::kRowBytes * w / 16, add);
+    const rsrc_t r = rsrc((i * L::kRowsPerLoad + 1024 / L::kRowBytes * w) / 16, add);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (Lds<void>)(dst + L::kPass / 2 * i + 512 * w), 16,
-                                             from + add, 0, 0, 0);
+                                             from[i % kHalves] + add, 0, 0, 0);
   }
 }
 
@@ -279,6 +288,11 @@ struct Rows {
 // tile's first token, and the part of its keys.
 struct Where {
   int group, slot, split, s, qb, lq, kb, lk, q0, past;
+  // one value per wave, which the compiler does not see by itself
+  __device__ __forceinline__ Where uniform_() const {
+    return {uniform(group), uniform(slot), uniform(split), uniform(s),  uniform(qb),
+            uniform(lq),    uniform(kb),   uniform(lk),    uniform(q0), uniform(past)};
+  }
 };
 template <Keys kKeys, int kThreads>
 __device__ __forceinline__ bool find(const TileArgs &a, int tt, int tid, Where &t,
@@ -322,14 +336,67 @@ __device__ __forceinline__ bool find(const TileArgs &a, int tt, int tid, Where &
   }
 }
 
-// kWaves waves of 32 rows. With four, two work-groups share a CU (D = 128) and
-// overlap by chance. With eight, the two waves of a SIMD (w and w + 4) go through
-// the two parts of a step in opposite order, a barrier after each part: while one
-// runs its score products the other forms weights.
-template <typename T, int D, int kBN, int kWaves, Keys kKeys, bool kPart>
-__global__ __launch_bounds__(64 * kWaves, kWaves == 8 || D == 128 ? 2 : 1) void attn_tile_kernel(
-    TileArgs a) {
-  constexpr int kBM = 32 * kWaves;
+// What the tile's rows see: keys 0 .. `keys` - 1 some row; lo (hi): the last key that
+// the wave's first (last) row sees, lim this lane's row.
+struct Sight {
+  int tok, lim, lo, hi, keys;
+};
+// rw: the wave's first row of the tile, tt tokens times `share` heads.
+template <Keys kKeys>
+__device__ __forceinline__ Sight sight_of(const Where &t, int rw, int col, int tt, int share) {
+  Sight s;
+  // rows past the tile's tokens or the sequence's end take the last token's limit
+  // and are not stored
+  s.tok = min(t.q0 + (rw + col) / share, t.lq - 1);
+  s.lim = t.past + s.tok;
+  s.lo = t.past + min(t.q0 + rw / share, t.lq - 1);
+  s.hi = t.past + min(t.q0 + min((rw + 31) / share, tt - 1), t.lq - 1);
+  s.keys = min(t.past + min(t.q0 + tt, t.lq), t.lk);
+  if constexpr (kKeys == Keys::kShared) {
+    s.lim = s.lo = s.hi = t.lk - 1;
+    s.keys = t.lk;
+  }
+  return s;
+}
+
+// Copies the kBN keys (values) from k0 on to LDS, as ranges that end with the
+// sequence's last key. kWaves waves take part, of which this is number w.
+template <typename T, int D, int kBN, int kWaves, Keys kKeys, bool kV>
+__device__ __forceinline__ void get(const TileArgs &a, const Where &t, int kvh, int k0, T *tile,
+                                    int lane, int w) {
+  const T *base = static_cast<const T *>(kV ? a.v : a.k);
+  if constexpr (kKeys == Keys::kRows) {
+    const int64_t stride = kV ? a.v_row : a.k_row;
+    const int row_bytes = (int)stride * 2;
+    const rsrc_t r = make_rsrc(base + (t.kb + k0) * stride + kvh * D,
+                               (min(kBN, t.lk - k0) - 1) * row_bytes + D * 2);
+    fetch<T, D, kBN, kWaves, kV>((Lds<T>)tile, row_bytes, lane, w, [&](int g, int &add) {
+      add = 16 * g * row_bytes;
+      return r;
+    });
+  } else {
+    const int32_t *table = a.pg.table + (int64_t)t.s * a.pg.max_pages;
+    fetch<T, D, kBN, kWaves, kV>((Lds<T>)tile, D * 2, lane, w, [&](int g, int &) {
+      const int key = k0 + 16 * g, rows = max(min(16, t.lk - key), 0);
+      const int64_t at = pool_row(a.pg, table, min(key, (t.lk - 1) & ~15), kvh, a.hkv);
+      return make_rsrc(base + at * D, rows * D * 2);
+    });
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ const T *q_row(const TileArgs &a, const Where &t, int tok, int row, int D) {
+  return static_cast<const T *>(a.q) + (int64_t)(t.qb + tok) * a.q_row +
+         (t.group * a.share + row % a.share) * D;
+}
+
+// Whole tiles: kWaves waves of 32 rows. With four, two work-groups share a CU (D =
+// 128) and overlap by chance. With eight, the two waves of a SIMD (w and w + 4) go
+// through the two parts of a step in opposite order, a barrier after each part:
+// while one runs its score products the other forms weights.
+template <typename T, int D, int kWaves, Keys kKeys>
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(TileArgs a) {
+  constexpr int kBM = 32 * kWaves, kBN = 64;
   // four arrays of their own, so that a tile in flight is known to be another
   // than the ones being read
   __shared__ __attribute__((aligned(16))) T k_a[kBN * D], v_a[kBN * D], k_b[kBN * D], v_b[kBN * D];
@@ -340,67 +407,29 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 || D == 128 ? 2 : 1) void 
   Where t;
   const int share = a.share, tt = kBM / share;
   if (!find<kKeys, 64 * kWaves>(a, tt, tid, t, scan)) return;
-  // one value per wave, which the compiler does not see by itself
-  t = {uniform(t.group), uniform(t.slot), uniform(t.split), uniform(t.s), uniform(t.qb),
-       uniform(t.lq), uniform(t.kb), uniform(t.lk), uniform(t.q0), uniform(t.past)};
+  t = t.uniform_();
   const int kvh = t.group * share / (a.h / a.hkv);
-  // this lane's row; those past the tile's tokens or the sequence's end take the
-  // last token's limit and are not stored
-  const int tok = min(t.q0 + (32 * w + col) / share, t.lq - 1);
-  int lim = t.past + tok, wave_lo = t.past + min(t.q0 + 32 * w / share, t.lq - 1);
-  int wave_hi = t.past + min(t.q0 + min((32 * w + 31) / share, tt - 1), t.lq - 1);
-  int keys = min(t.past + min(t.q0 + tt, t.lq), t.lk);  // keys any row of the tile sees
-  if constexpr (kKeys == Keys::kShared) {
-    lim = wave_lo = wave_hi = t.lk - 1;
-    keys = t.lk;
-  }
-  int tiles = keys > 0 ? (keys + kBN - 1) / kBN : 0, j0 = 0;
-  if constexpr (kPart) {
-    const int per = (tiles + a.splits - 1) / a.splits;
-    j0 = t.split * per;
-    tiles = max(min(per, tiles - j0), 0);
-  }
+  const Sight see = sight_of<kKeys>(t, 32 * w, col, tt, share);
+  const int tiles = see.keys > 0 ? (see.keys + kBN - 1) / kBN : 0;
 
-  const int k_bytes = kKeys == Keys::kRows ? (int)a.k_row * 2 : D * 2;
-  const int v_bytes = kKeys == Keys::kRows ? (int)a.v_row * 2 : D * 2;
-  // a tile's rows as ranges that end with the sequence's last key
-  auto get = [&](auto is_v, int j, T *tile) __attribute__((always_inline)) {
-    constexpr bool kV = decltype(is_v)::value;
-    const int k0 = (j0 + j) * kBN;
-    const int row_bytes = kV ? v_bytes : k_bytes;
-    if constexpr (kKeys == Keys::kRows) {
-      const T *p = static_cast<const T *>(kV ? a.v : a.k) +
-                   (int64_t)(t.kb + k0) * (kV ? a.v_row : a.k_row) + kvh * D;
-      const rsrc_t r = make_rsrc(p, (min(kBN, t.lk - k0) - 1) * row_bytes + D * 2);
-      fetch<T, D, kBN, kWaves, kV>((Lds<T>)tile, row_bytes, lane, w, [&](int g, int &add) {
-        add = 16 * g * row_bytes;
-        return r;
-      });
-    } else {
-      const int32_t *table = a.pg.table + (int64_t)t.s * a.pg.max_pages;
-      fetch<T, D, kBN, kWaves, kV>((Lds<T>)tile, row_bytes, lane, w, [&](int g, int &) {
-        const int key = k0 + 16 * g, rows = max(min(16, t.lk - key), 0);
-        const int64_t at = pool_row(a.pg, table, min(key, (t.lk - 1) & ~15), kvh, a.hkv);
-        return make_rsrc(static_cast<const T *>(kV ? a.v : a.k) + at * D, rows * row_bytes);
-      });
-    }
+  auto get_k = [&](int j, T *tile) __attribute__((always_inline)) {
+    get<T, D, kBN, kWaves, kKeys, false>(a, t, kvh, j * kBN, tile, lane, w);
   };
-  auto get_k = [&](int j, T *tile) __attribute__((always_inline)) { get(std::false_type{}, j, tile); };
-  auto get_v = [&](int j, T *tile) __attribute__((always_inline)) { get(std::true_type{}, j, tile); };
+  auto get_v = [&](int j, T *tile) __attribute__((always_inline)) {
+    get<T, D, kBN, kWaves, kKeys, true>(a, t, kvh, j * kBN, tile, lane, w);
+  };
   Rows<T, D, kBN> x;
   if (tiles > 0) {
     get_k(0, k_a);
     get_v(0, v_a);
   }
-  x.load(static_cast<const T *>(a.q) + (int64_t)(t.qb + tok) * a.q_row +
-             (t.group * share + (32 * w + col) % share) * D, hh);
+  x.load(q_row<T>(a, t, see.tok, 32 * w + col, D), hh);
   auto score = [&](int j, T *kt) __attribute__((always_inline)) {
-    const int k0 = (j0 + j) * kBN;
-    if (k0 <= wave_hi)
-      x.score((Lds<T>)kt, k0, lim, k0 + kBN - 1 > wave_lo, a.scale_log2, lane);
+    const int k0 = j * kBN;
+    if (k0 <= see.hi) x.score((Lds<T>)kt, k0, see.lim, k0 + kBN - 1 > see.lo, a.scale_log2, lane);
   };
   auto weigh = [&](int j, T *vt) __attribute__((always_inline)) {
-    if ((j0 + j) * kBN <= wave_hi) x.weigh((Lds<T>)vt, a.scale_log2, lane);
+    if (j * kBN <= see.hi) x.weigh((Lds<T>)vt, a.scale_log2, lane);
   };
   if constexpr (kWaves == 4) {
     for (int j = 0; j < tiles; j += 2) {
@@ -469,17 +498,123 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 || D == 128 ? 2 : 1) void 
     }
   }
   const int row = opaque<true>(32 * w + col);  // not kept along the loop
-  if constexpr (kPart) {
-    const int64_t at =
-        (item_of(t.group, t.slot, a.h / share, a.slots) * a.splits + t.split) * kBM + row;
-    x.store_part(a.part_o + at * D, a.part_ml + at * 2, hh);
-  } else {
-    const int token = t.q0 + row / share;
-    x.store(row < tt * share && token < t.lq
-                ? static_cast<T *>(a.o) +
-                      ((int64_t)(t.qb + token) * a.h + t.group * share + row % share) * D
-                : nullptr, hh);
+  const int token = t.q0 + row / share;
+  x.store(row < tt * share && token < t.lq
+              ? static_cast<T *>(a.o) +
+                    ((int64_t)(t.qb + token) * a.h + t.group * share + row % share) * D
+              : nullptr, hh);
+}
+
+// One part of a tile's keys, its running state left for a join. 128 rows: the more
+// rows and parts, the more partial results are written and read again, so instead of
+// taking 256 rows the eight waves are two sets of four, on the even and the odd tiles
+// of the part, each with its own copies (double buffered), in opposite phase as
+// above. The second set's state is added to the first's through LDS at the end.
+template <typename T, int D, Keys kKeys>
+__global__ __launch_bounds__(512, 2) void attn_part_kernel(TileArgs a) {
+  constexpr int kBM = 128, kBN = D == 256 ? 32 : 64;
+  constexpr int kTile = kBN * D;
+  // [set] [buffer] K and V; at the end, the second set's output sums
+  __shared__ __attribute__((aligned(16))) T k_a[2 * kTile], v_a[2 * kTile], k_b[2 * kTile],
+      v_b[2 * kTile];
+  __shared__ float stat[4][64][2];
+  __shared__ int scan[8][2];
+
+  const int tid = threadIdx.x, lane = tid & 63, set = uniform(tid >> 8), w = uniform(tid >> 6) & 3;
+  const int col = lane & 31, hh = lane >> 5;
+  Where t;
+  const int share = a.share, tt = kBM / share;
+  if (!find<kKeys, 512>(a, tt, tid, t, scan)) return;
+  t = t.uniform_();
+  const int kvh = t.group * share / (a.h / a.hkv);
+  const Sight see = sight_of<kKeys>(t, 32 * w, col, tt, share);
+  const int all = see.keys > 0 ? (see.keys + kBN - 1) / kBN : 0;
+  const int per = (all + a.splits - 1) / a.splits;
+  const int j0 = t.split * per + set, end = min(t.split * per + per, all);
+  const int steps = max((end - t.split * per + 1) / 2, 0);  // of either set
+  // this set's tile of step j, if it has one
+  auto has = [&](int j) { return j0 + 2 * j < end; };
+  auto get_k = [&](int j, T *tile) __attribute__((always_inline)) {
+    if (has(j))
+      get<T, D, kBN, 4, kKeys, false>(a, t, kvh, (j0 + 2 * j) * kBN, tile + set * kTile, lane, w);
+  };
+  auto get_v = [&](int j, T *tile) __attribute__((always_inline)) {
+    if (has(j))
+      get<T, D, kBN, 4, kKeys, true>(a, t, kvh, (j0 + 2 * j) * kBN, tile + set * kTile, lane, w);
+  };
+  Rows<T, D, kBN> x;
+  get_k(0, k_a);
+  get_v(0, v_a);
+  x.load(q_row<T>(a, t, see.tok, 32 * w + col, D), hh);
+  auto score = [&](int j, T *kt) __attribute__((always_inline)) {
+    const int k0 = (j0 + 2 * j) * kBN;
+    if (has(j) && k0 <= see.hi)
+      x.score((Lds<T>)(kt + set * kTile), k0, see.lim, k0 + kBN - 1 > see.lo, a.scale_log2, lane);
+  };
+  auto weigh = [&](int j, T *vt) __attribute__((always_inline)) {
+    if (has(j) && (j0 + 2 * j) * kBN <= see.hi)
+      x.weigh((Lds<T>)(vt + set * kTile), a.scale_log2, lane);
+  };
+  // K (V) of the next step is copied from the end of this step's score (weigh) phase
+  // on, into the place that the step before left; both are waited for before they
+  // are read, one and two phases later
+  auto k_end = [&](int j, T *kt) __attribute__((always_inline)) {
+    wait_lds();
+    get_k(j, kt);
+    barrier();
+  };
+  auto v_end = [&](int j, T *vt) __attribute__((always_inline)) {
+    wait_lds();
+    get_v(j, vt);
+    barrier();
+  };
+  wait_lds();
+  barrier();
+  if (set) barrier();
+  for (int j = 0; j < steps; j += 2) {
+    score(j, k_a);
+    k_end(j + 1, k_b);
+    weigh(j, v_a);
+    v_end(j + 1, v_b);
+    if (j + 1 >= steps) break;
+    score(j + 1, k_b);
+    k_end(j + 2, k_a);
+    weigh(j + 1, v_b);
+    v_end(j + 2, v_a);
   }
+  if (!set) barrier();
+
+  // the second set's state, lane by lane: a lane of both holds the same row and dims
+  const Lds<T> tile = w == 0 ? (Lds<T>)k_a : w == 1 ? (Lds<T>)v_a : w == 2 ? (Lds<T>)k_b : (Lds<T>)v_b;
+  const Lds<f32x4> mine = (Lds<f32x4>)tile;  // 32 rows of D floats
+  if (set) {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        mine[(4 * i + b) * 64 + lane] =
+            f32x4{x.o[i][4 * b], x.o[i][4 * b + 1], x.o[i][4 * b + 2], x.o[i][4 * b + 3]};
+    stat[w][lane][0] = x.m;
+    stat[w][lane][1] = x.l;
+  }
+  __syncthreads();
+  if (set) return;
+  const float m2 = stat[w][lane][0], big = fmaxf(x.m, m2);
+  const float f1 = x.m == kNegInf ? 0.f : fast_exp2(x.m - big);
+  const float f2 = m2 == kNegInf ? 0.f : fast_exp2(m2 - big);
+  x.m = big;
+  x.l = x.l * f1 + stat[w][lane][1] * f2;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const f32x4 y = mine[(4 * i + b) * 64 + lane];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x.o[i][4 * b + e] = x.o[i][4 * b + e] * f1 + y[e] * f2;
+    }
+  const int64_t at = (item_of(t.group, t.slot, a.h / share, a.slots) * a.splits + t.split) * kBM +
+                     32 * w + col;
+  x.store_part(a.part_o + at * D, a.part_ml + at * 2, hh);
 }
 
 // Joins the parts of a row's keys: one wave per row.
@@ -528,43 +663,46 @@ __global__ __launch_bounds__(256) void attn_tile_join_kernel(TileArgs a, int tt,
     o[kPer / 2 * lane + k] = Elem<T>::pack(sum[2 * k] * inv, sum[2 * k + 1] * inv);
 }
 
-template <typename T, int D, int kWaves, Keys kKeys, bool kPart>
-hipError_t run(const gdn_attn_config *cfg, const TileArgs &a, int tt, hipStream_t stream) {
+template <typename T, int D, int kWaves, Keys kKeys>
+hipError_t run_whole(const gdn_attn_config *cfg, const TileArgs &a, hipStream_t stream) {
   dim3 grid;
-  if (!flat_grid((int64_t)a.slots * (cfg->h / a.share) * a.splits, 64 * kWaves, grid))
+  if (!flat_grid((int64_t)a.slots * (cfg->h / a.share), 64 * kWaves, grid))
     return hipErrorInvalidValue;
-  dim3 join;
-  if (kPart && kKeys != Keys::kShared && !flat_grid(((int64_t)cfg->t_max * cfg->h + 3) / 4, 256, join))
-    return hipErrorInvalidValue;
-  hipLaunchKernelGGL((attn_tile_kernel<T, D, 64, kWaves, kKeys, kPart>), grid, dim3(64 * kWaves), 0,
-                     stream, a);
-  if (kPart && kKeys != Keys::kShared) {
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((attn_tile_join_kernel<T, D>), join, dim3(256), 0, stream, a, tt, 32 * kWaves);
-  }
+  hipLaunchKernelGGL((attn_tile_kernel<T, D, kWaves, kKeys>), grid, dim3(64 * kWaves), 0, stream, a);
   return hipGetLastError();
 }
 
-template <typename T, int D, int kWaves, Keys kKeys>
-hipError_t run_split(const gdn_attn_config *cfg, const TileArgs &a, int tt, hipStream_t stream) {
-  return a.splits > 1 ? run<T, D, kWaves, kKeys, true>(cfg, a, tt, stream)
-                      : run<T, D, kWaves, kKeys, false>(cfg, a, tt, stream);
+template <typename T, int D, Keys kKeys>
+hipError_t run_parts(const gdn_attn_config *cfg, const TileArgs &a, int tt, hipStream_t stream) {
+  dim3 grid, join;
+  if (!flat_grid((int64_t)a.slots * (cfg->h / a.share) * a.splits, 512, grid) ||
+      !flat_grid(((int64_t)cfg->t_max * cfg->h + 3) / 4, 256, join))
+    return hipErrorInvalidValue;
+  hipLaunchKernelGGL((attn_part_kernel<T, D, kKeys>), grid, dim3(512), 0, stream, a);
+  if (kKeys == Keys::kShared) return hipGetLastError();  // the caller joins them
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((attn_tile_join_kernel<T, D>), join, dim3(256), 0, stream, a, tt, kPartRows);
+  return hipGetLastError();
 }
 
-template <typename T>
+template <typename T, int D, Keys kKeys>
+hipError_t run_keys(const gdn_attn_config *cfg, const TileArgs &a, const TileShape &s,
+                    hipStream_t stream) {
+  if (s.splits > 1) return run_parts<T, D, kKeys>(cfg, a, s.tt, stream);
+  if constexpr (D == 256)
+    return run_whole<T, D, 8, kKeys>(cfg, a, stream);
+  else
+    return s.waves == 8 ? run_whole<T, D, 8, kKeys>(cfg, a, stream)
+                        : run_whole<T, D, 4, kKeys>(cfg, a, stream);
+}
+
+template <typename T, int D>
 hipError_t run_of(const gdn_attn_config *cfg, Keys keys, const TileArgs &a, const TileShape &s,
                   hipStream_t stream) {
-  if (keys == Keys::kShared)
-    return cfg->d == 256 ? run<T, 256, 8, Keys::kShared, true>(cfg, a, s.tt, stream)
-                         : run<T, 128, 4, Keys::kShared, true>(cfg, a, s.tt, stream);
-  if (keys == Keys::kPages)
-    return cfg->d == 256  ? run_split<T, 256, 8, Keys::kPages>(cfg, a, s.tt, stream)
-           : s.waves == 8 ? run_split<T, 128, 8, Keys::kPages>(cfg, a, s.tt, stream)
-                          : run_split<T, 128, 4, Keys::kPages>(cfg, a, s.tt, stream);
-  return cfg->d == 256  ? run_split<T, 256, 8, Keys::kRows>(cfg, a, s.tt, stream)
-         : s.waves == 8 ? run_split<T, 128, 8, Keys::kRows>(cfg, a, s.tt, stream)
-                        : run_split<T, 128, 4, Keys::kRows>(cfg, a, s.tt, stream);
+  return keys == Keys::kShared  ? run_parts<T, D, Keys::kShared>(cfg, a, s.tt, stream)
+         : keys == Keys::kPages ? run_keys<T, D, Keys::kPages>(cfg, a, s, stream)
+                                : run_keys<T, D, Keys::kRows>(cfg, a, s, stream);
 }
 
 // Average tokens per sequence from which heads of 128 take work-groups of eight
@@ -591,25 +729,32 @@ TileShape tile_shape(const gdn_attn_config *cfg, Keys keys) {
   const int group = cfg->h / cfg->hkv;
   s.share = group < kMostShare ? group : kMostShare;
   while (group % s.share) --s.share;
-  s.waves = cfg->d == 256 || (keys != Keys::kShared && cfg->t_max / cfg->n_max >= kLongPrompt) ? 8 : 4;
-  s.tt = 32 * s.waves / s.share;
-  s.slots = keys == Keys::kShared ? (cfg->t_max + s.tt - 1) / s.tt : cfg->t_max / s.tt + cfg->n_max;
   // few tiles and many keys: split the keys until the device is full
   const int64_t room = (int64_t)cfg->max_pages * cfg->page_size;
   const int64_t longest = keys == Keys::kShared  ? (cfg->shared_max < room ? cfg->shared_max : room)
                           : keys == Keys::kPages ? room
                                                  : (cfg->tk_max > 0 ? cfg->tk_max : cfg->t_max) / cfg->n_max;
-  const int64_t tiles = (int64_t)s.slots * (cfg->h / s.share);
-  const int64_t full = cu_count() * (s.waves == 8 ? 1 : 2);
-  int64_t n = tiles > 0 ? full / tiles : 1;
+  auto cut = [&](int rows) {
+    s.tt = rows / s.share;
+    s.slots = keys == Keys::kShared ? (cfg->t_max + s.tt - 1) / s.tt : cfg->t_max / s.tt + cfg->n_max;
+    return (int64_t)s.slots * (cfg->h / s.share);
+  };
+  s.rows = kPartRows;
+  s.waves = 8;
+  const int64_t tiles = cut(s.rows);
+  int64_t n = tiles > 0 ? cu_count() / tiles : 1;
   if (n > longest / kSplitKeys) n = longest / kSplitKeys;
   s.splits = n < 1 ? 1 : n > kMostSplits ? kMostSplits : static_cast<int>(n);
+  if (s.splits > 1 || keys == Keys::kShared) return s;
+  s.waves = cfg->d == 256 || cfg->t_max / cfg->n_max >= kLongPrompt ? 8 : 4;
+  s.rows = 32 * s.waves;
+  cut(s.rows);
   return s;
 }
 
 int64_t tile_part_rows(const gdn_attn_config *cfg, const TileShape &s, Keys keys) {
   if (s.splits == 1 && keys != Keys::kShared) return 0;
-  return (int64_t)s.slots * (cfg->h / s.share) * s.splits * 32 * s.waves;
+  return (int64_t)s.slots * (cfg->h / s.share) * s.splits * s.rows;
 }
 
 hipError_t launch_attn_tiles(const gdn_attn_config *cfg, Keys keys, TileArgs a, hipStream_t stream) {
@@ -618,8 +763,11 @@ hipError_t launch_attn_tiles(const gdn_attn_config *cfg, Keys keys, TileArgs a, 
   a.share = s.share;
   a.splits = s.splits;
   a.slots = s.slots;
-  return cfg->dtype == GDN_BF16 ? run_of<__bf16>(cfg, keys, a, s, stream)
-                                : run_of<_Float16>(cfg, keys, a, s, stream);
+  if (cfg->dtype == GDN_BF16)
+    return cfg->d == 128 ? run_of<__bf16, 128>(cfg, keys, a, s, stream)
+                         : run_of<__bf16, 256>(cfg, keys, a, s, stream);
+  return cfg->d == 128 ? run_of<_Float16, 128>(cfg, keys, a, s, stream)
+                       : run_of<_Float16, 256>(cfg, keys, a, s, stream);
 }
 
 }  // namespace gdn

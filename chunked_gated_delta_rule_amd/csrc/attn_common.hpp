@@ -74,6 +74,14 @@ __device__ __forceinline__ float sum16x(float x) {
   return h.a + h.b;
 }
 
+// A value the compiler may not see through: what is derived from it is formed
+// anew at each use, where keeping it would cost registers all along the loop.
+template <bool kDo>
+__device__ __forceinline__ int opaque(int x) {
+  if constexpr (kDo) asm volatile("" : "+v"(x));
+  return x;
+}
+
 constexpr float kNegInf = -__builtin_inff();
 
 // Softmax statistics move only when a row's maximum (log2 scale) has grown by
@@ -104,6 +112,10 @@ struct Packed {
 };
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)x);
+  return (int64_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32 | lo;
+}
 
 // The last sequence s of the batch whose key(s, first row of s) is at most x. Each
 // lane of the last level loads what belongs to its sequence, extra(s) included,
@@ -153,11 +165,16 @@ __device__ __forceinline__ Seq seq_at(const PagedBatch &a, int s) {
   return q;
 }
 
-// Start of the 16 rows of one key head that hold position `key` (a multiple of 16)
-// of the sequence with this table row, in rows of the pool.
-__device__ __forceinline__ int64_t pool_row(const PagedBatch &a, const int32_t *__restrict__ row,
-                                            int key, int kh, int hkv) {
-  const int page = min(max(row[key >> a.page_shift], 0), a.n_pages - 1);
+// Page of position `key` of sequence s, as an index into the pool whatever the table
+// says. s and key are uniform: the table is read through the scalar cache (which a
+// plain load, next to stores, would not be).
+__device__ __forceinline__ int page_of(const PagedBatch &a, int s, int key) {
+  typedef __attribute__((address_space(4))) const int32_t *scalar;
+  const scalar row = (scalar)(uintptr_t)(a.table + (int64_t)s * a.max_pages);
+  return min(max(row[key >> a.page_shift], 0), a.n_pages - 1);
+}
+// Row of the pool at which position `key` of a key head lies in its page.
+__device__ __forceinline__ int64_t pool_row(const PagedBatch &a, int page, int key, int kh, int hkv) {
   return (((int64_t)page * hkv + kh) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
 }
 

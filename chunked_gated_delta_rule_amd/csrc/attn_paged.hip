@@ -36,12 +36,24 @@ constexpr int kUnit = 128;  // keys per unit: 32 per wave
 // before each sequence (int64 [n_max + 1])
 constexpr int kPlanInts = 16;
 
+// Rows (tokens times query heads) from which the join takes one wave per row and not
+// four.
+constexpr int kManyRows = 4096;
+
 __device__ __forceinline__ int units_of(int keys) { return (keys + kUnit - 1) / kUnit; }
 
 template <int kRT>
 __device__ __forceinline__ int row_tiles(int64_t rows) {
   return (int)((rows + 16 * kRT - 1) / (16 * kRT));
 }
+
+// A wave's 32 keys of a unit: K fragments of two tiles of 16, and rows of V (keys 4 g
+// + e of tile 0, then of tile 1).
+template <typename T, int D>
+struct Keys32 {
+  typename Elem<T>::vec8 k[2][D / 32];
+  u32x4 v[D / 128][8];
+};
 
 template <typename T, int D, int kRT>
 __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kernel(StreamArgs a) {
@@ -57,13 +69,13 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
 
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int G = a.h / a.hkv;
   // consecutive runs on one XCD: its L2 then holds the rows that they share
   const int wg = (blockIdx.x & 7) * ((a.grid + 7) / 8) + (blockIdx.x >> 3);
   if (wg >= a.grid) return;
 
   // ---- the plan: shared prefix, units of every sequence
-  const PagedBatch &pg = a.pg;
+  PagedBatch pg = a.pg;
+  int G = a.h / a.hkv;
   const int prefix = shared_prefix<256>(pg, tid, scan32).len;
   const int per = (pg.n_max + 255) / 256;
   const int s0 = min(tid * per, pg.n_max), s1 = min(s0 + per, pg.n_max);
@@ -88,6 +100,7 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
     if (i < w) before += scan64[i];
     per_head += scan64[i];
   }
+  per_head = uniform(per_head);
   const int64_t total = per_head * a.hkv;
   const int64_t per_wg = max((total + a.grid - 1) / a.grid, (int64_t)1);
   if (wg == 0) {
@@ -120,19 +133,29 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
     scan64[4] = in_head - at;
   }
   __syncthreads();
-  int s = found;
-  int64_t in_seq = scan64[4];
+  int s = uniform(found);
+  int64_t in_seq = uniform(scan64[4]);
+  // From here on everything but the lanes' data is one value per wave. The compiler
+  // would merge what the branch above derived from these into lane values.
+  G = uniform(G);
+  pg.n_max = uniform(pg.n_max);
+  pg.t_max = uniform(pg.t_max);
+  pg.n_pages = uniform(pg.n_pages);
+  pg.max_pages = uniform(pg.max_pages);
+  pg.page_shift = uniform(pg.page_shift);
 
   const T *kpool = static_cast<const T *>(a.k_pages), *vpool = static_cast<const T *>(a.v_pages);
   int64_t u = u0;
   while (u < u1) {
     // the item: its rows, its keys, the units of it in this run
-    const Seq q = seq_at(pg, s);
+    const int seq = uniform(s), head = uniform(kh);
+    const Seq at = seq_at(pg, seq);
+    const Seq q{uniform(at.bos), uniform(at.n), uniform(at.kv)};
     const int nu = units_of(q.kv - prefix);
-    const int rt = (int)(in_seq / nu), un = (int)(in_seq - (int64_t)rt * nu);
-    const int run = (int)min((int64_t)(nu - un), u1 - u);
+    // (one value per wave each, which the compiler does not see by itself)
+    const int rt = uniform((int)(in_seq / nu)), un = uniform((int)(in_seq - (int64_t)rt * nu));
+    const int run = uniform((int)min((int64_t)(nu - un), u1 - u));
     const int64_t rows = (int64_t)q.n * G, r0 = (int64_t)rt * kRows;
-    const int32_t *table = pg.table + (int64_t)s * pg.max_pages;
 
     __syncthreads();  // the item before may still be read
     for (int i = tid; i < kRows * (D / 8); i += 256) {
@@ -141,7 +164,7 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
       const int tok = (int)(r / G);
       *reinterpret_cast<u32x4 *>(&qs[row][8 * ch]) = *reinterpret_cast<const u32x4 *>(
           static_cast<const T *>(a.q) + (int64_t)(q.bos + tok) * a.q_row +
-          ((int64_t)kh * G + (r - (int64_t)tok * G)) * D + 8 * ch);
+          ((int64_t)head * G + (r - (int64_t)tok * G)) * D + 8 * ch);
     }
     int lim[kRT];  // the last key that this lane's row of each tile sees
 #pragma unroll
@@ -163,68 +186,80 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[t][b][j] = zero4();
     }
-    for (int i = 0; i < run; ++i) {
-      const int k0 = prefix + (un + i) * kUnit + 32 * w;  // the wave's 32 keys
-      if (k0 >= q.kv) continue;
-      // two tiles of 16 keys, each inside one page
-      const T *kt[2], *vt[2];
+    // this wave's 32 keys of unit i of the run, as two tiles of 16, each in one page
+    const int first = prefix + un * kUnit + 32 * w;
+    const int mine_n = min(run, units_of(q.kv - first));  // units in which it has keys
+    auto tile_key = [&](int i, int t) { return min(first + i * kUnit + 16 * t, (q.kv - 1) & ~15); };
+    int pages[2];
+    auto look = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) pages[t] = page_of(pg, seq, tile_key(i, t));
+    };
+    // a tile's rows as a range that ends with the sequence's last key: zeros past it,
+    // where a page may hold anything
+    auto rows_of = [&](const T *pool, int i, int t) __attribute__((always_inline)) {
+      const int left = q.kv - (first + i * kUnit + 16 * t);
+      const T *p = pool + pool_row(pg, pages[t], tile_key(i, t), head, a.hkv) * D;
+      return make_rsrc(p, uniform(max(min(left, 16), 0)) * D * 2);
+    };
+    auto load_k = [&](Keys32<T, D> &x, int i) __attribute__((always_inline)) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const int key = min(k0 + 16 * t, (q.kv - 1) & ~15);
-        const int64_t at = pool_row(pg, table, key, kh, a.hkv) * D;
-        kt[t] = kpool + at;
-        vt[t] = vpool + at;
+        const rsrc_t r = rows_of(kpool, i, t);
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j)
+          x.k[t][j] = __builtin_bit_cast(vec8, buf_load16(r, (c * D + 8 * g + 32 * j) * 2));
       }
-      vec8 kf[2][D / 32];
+    };
+    auto load_v = [&](Keys32<T, D> &x, int i) __attribute__((always_inline)) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < 2; ++t) {
+        const rsrc_t r = rows_of(vpool, i, t);
 #pragma unroll
-        for (int p = 0; p < D / 32; ++p)
-          kf[t][p] = *reinterpret_cast<const vec8 *>(kt[t] + c * D + 32 * p + 8 * g);
-      // keys 4 g + e of tile 0, then of tile 1
-      u32x4 vr[kDC][8];
+        for (int e = 0; e < 4; ++e)
 #pragma unroll
-      for (int b = 0; b < kDC; ++b)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          vr[b][e] = *reinterpret_cast<const u32x4 *>(vt[e >> 2] + (4 * g + (e & 3)) * D + 128 * b +
-                                                      8 * c);
-      if (k0 + 32 > q.kv) {  // rows past the length may hold anything
-#pragma unroll
-        for (int b = 0; b < kDC; ++b)
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (k0 + 16 * (e >> 2) + 4 * g + (e & 3) >= q.kv) vr[b][e] = u32x4{0u, 0u, 0u, 0u};
+          for (int b = 0; b < kDC; ++b)
+            x.v[b][4 * t + e] = buf_load16(r, ((4 * g + e) * D + 128 * b + 8 * c) * 2);
       }
-      vec8 vf[kDC][8];
-#pragma unroll
-      for (int b = 0; b < kDC; ++b)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          u32x4 x;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            x[e] = __builtin_amdgcn_perm(vr[b][2 * e + 1][j >> 1], vr[b][2 * e][j >> 1],
-                                         j & 1 ? 0x07060302u : 0x05040100u);
-          vf[b][j] = __builtin_bit_cast(vec8, x);
-        }
+    };
+    Keys32<T, D> x;
+    if (mine_n > 0) {
+      look(0);
+      load_k(x, 0);
+      load_v(x, 0);
+      if (mine_n > 1) look(1);
+    }
+    // the next keys come while these are weighed, the next values while their scores
+    // are formed, in the registers that are free by then
+    for (int i = 0; i < mine_n; ++i) {
+      const int k0 = first + i * kUnit;
       const bool masked = k0 + 31 > all_see;
+      // q's fragments are read anew for every unit (with one tile of 128 dims they fit
+      // the registers and the compiler keeps them)
+      const int qrow = opaque<(kRT * D > 128)>(c);
+      f32x4 sc[kRT][2];
 #pragma unroll
       for (int t = 0; t < kRT; ++t) {
-        f32x4 sc[2] = {zero4(), zero4()};
+        sc[t][0] = sc[t][1] = zero4();
 #pragma unroll
         for (int p = 0; p < D / 32; ++p) {
-          const vec8 qf = *reinterpret_cast<const vec8 *>(&qs[16 * t + c][32 * p + 8 * g]);
-          sc[0] = mfma(kf[0][p], qf, sc[0]);
-          sc[1] = mfma(kf[1][p], qf, sc[1]);
+          const vec8 qf = *reinterpret_cast<const vec8 *>(&qs[16 * t + qrow][32 * p + 8 * g]);
+          sc[t][0] = mfma(x.k[0][p], qf, sc[t][0]);
+          sc[t][1] = mfma(x.k[1][p], qf, sc[t][1]);
         }
+      }
+      if (i + 1 < mine_n) load_k(x, i + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      vec8 pf[kRT];
+#pragma unroll
+      for (int t = 0; t < kRT; ++t) {
         if (masked) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (k0 + 16 * (e >> 2) + 4 * g + (e & 3) > lim[t]) sc[e >> 2][e & 3] = kNegInf;
+            if (k0 + 16 * (e >> 2) + 4 * g + (e & 3) > lim[t]) sc[t][e >> 2][e & 3] = kNegInf;
         }
-        float mx = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])),
-                         fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3])));
+        float mx = fmaxf(fmaxf(fmaxf(sc[t][0][0], sc[t][0][1]), fmaxf(sc[t][0][2], sc[t][0][3])),
+                         fmaxf(fmaxf(sc[t][1][0], sc[t][1][1]), fmaxf(sc[t][1][2], sc[t][1][3])));
         mx = max32(max16(mx)) * a.scale_log2;
         if (__any(mx > m[t] + kRescaleLog2)) {
           const float mn = fmaxf(m[t], mx);
@@ -240,17 +275,29 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
         u32x4 pw;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float e0 = fast_exp2(fmaf(sc[e >> 1][2 * (e & 1)], a.scale_log2, -ms));
-          const float e1 = fast_exp2(fmaf(sc[e >> 1][2 * (e & 1) + 1], a.scale_log2, -ms));
+          const float e0 = fast_exp2(fmaf(sc[t][e >> 1][2 * (e & 1)], a.scale_log2, -ms));
+          const float e1 = fast_exp2(fmaf(sc[t][e >> 1][2 * (e & 1) + 1], a.scale_log2, -ms));
           l[t] += e0 + e1;
           pw[e] = Elem<T>::pack(e0, e1);
         }
-        const vec8 pf = __builtin_bit_cast(vec8, pw);
-#pragma unroll
-        for (int b = 0; b < kDC; ++b)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[t][b][j] = mfma(vf[b][j], pf, o[t][b][j]);
+        pf[t] = __builtin_bit_cast(vec8, pw);
       }
+#pragma unroll
+      for (int b = 0; b < kDC; ++b)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          u32x4 y;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            y[e] = __builtin_amdgcn_perm(x.v[b][2 * e + 1][j >> 1], x.v[b][2 * e][j >> 1],
+                                         j & 1 ? 0x07060302u : 0x05040100u);
+          const vec8 vf = __builtin_bit_cast(vec8, y);
+#pragma unroll
+          for (int t = 0; t < kRT; ++t) o[t][b][j] = mfma(vf, pf[t], o[t][b][j]);
+        }
+      __builtin_amdgcn_sched_barrier(0);
+      if (i + 1 < mine_n) load_v(x, i + 1);
+      if (i + 2 < mine_n) look(i + 2);
     }
 
     // ---- the four waves meet, one 16-row tile at a time
@@ -298,7 +345,7 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
           ll += wm[i][16 * t + row] == kNegInf ? 0.f
                                                : wl[i][16 * t + row] * fast_exp2(wm[i][16 * t + row] - mm);
         const int tok = (int)(r / G);
-        const int64_t orow = (int64_t)(q.bos + tok) * a.h + (int64_t)kh * G + (r - (int64_t)tok * G);
+        const int64_t orow = (int64_t)(q.bos + tok) * a.h + (int64_t)head * G + (r - (int64_t)tok * G);
         const float inv = ll == 0.f ? 0.f : 1.f / ll;
         float *po, *pm;
         if (whole) {
@@ -337,31 +384,30 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
       ++kh;
       in_head = in_seq = 0;
       s = 0;
-      while (units_in(s) == 0) ++s;
-    } else if (in_seq == units_in(s)) {
+      while (uniform(units_in(s)) == 0) ++s;
+    } else if (in_seq == uniform(units_in(s))) {
       in_seq = 0;
       ++s;
-      while (units_in(s) == 0) ++s;
+      while (uniform(units_in(s)) == 0) ++s;
     }
   }
 }
 
 // Joins what several work-groups, the shared prefix's included, left of a row, and
-// writes zeros where a row sees no key. One work-group per token and `per` query
-// heads; rows that the main kernel finished are left alone. The parts' statistics
-// are read first and become weights in LDS, so that the output sums, which are
-// most of the bytes, are read without waiting for anything.
-template <typename T, int D, int kRT>
-__global__ __launch_bounds__(256) void attn_stream_join_kernel(StreamArgs a, int per) {
+// writes zeros where a row sees no key. kWaves waves per row (token and query head),
+// each on every kWaves-th part; rows that the main kernel finished are left alone.
+// The parts' statistics are read first, a lane each, so that the output sums, which
+// are most of the bytes, are read without waiting for anything.
+template <typename T, int D, int kRT, int kWaves>
+__global__ __launch_bounds__(256) void attn_stream_join_kernel(StreamArgs a) {
   constexpr int kRows = 16 * kRT;
-  constexpr int kLanes = D / 4;            // threads per part
-  constexpr int kPar = 256 / kLanes;       // parts at a time
-  constexpr int kMost = 1024;              // weights held at a time
-  __shared__ __attribute__((aligned(16))) float os[kPar][D];
-  __shared__ float weight[kMost], red[4][2];
-  const int wg = flat_block(), cuts = (a.h + per - 1) / per;
-  const int t = wg / cuts, h0 = wg % cuts * per, h1 = min(h0 + per, a.h);
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  constexpr int kPer = D / 64;  // dims per lane
+  typedef float vec __attribute__((ext_vector_type(kPer)));
+  __shared__ float os[kWaves][64][kPer], stat[kWaves][2];
+  const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
+  const int64_t row = (int64_t)flat_block() * (4 / kWaves) + (kWaves == 1 ? w : 0);
+  const int t = (int)(row / a.h), head = (int)(row % a.h);
+  const int sub = kWaves == 1 ? 0 : w;  // this wave among the row's
   const PagedBatch &pg = a.pg;
   if (t >= cu_at(pg.cu, pg.n_max, pg.t_max)) return;
   int kv;
@@ -373,119 +419,119 @@ __global__ __launch_bounds__(256) void attn_stream_join_kernel(StreamArgs a, int
   const int64_t per_head = reinterpret_cast<const int64_t *>(a.plan)[1];
   const int64_t per_wg = reinterpret_cast<const int64_t *>(a.plan)[2];
   const int64_t start = reinterpret_cast<const int64_t *>(a.plan + kPlanInts)[q.s];
-  const int lead = prefix > 0 ? a.pre_splits : 0;  // the prefix's parts of a row come first
+  const int lead = prefix > 0 ? a.pre_splits : 0;  // the prefix's parts come first
 
-  for (int head = h0; head < h1; ++head) {
-    // the row's item: units [lo, hi) in the work-groups w0 .., and its row of the tile
-    int64_t lo = 0, w0 = 0;
-    int parts = 0, in_tile = 0;
-    if (kv > prefix) {
-      const int64_t r = (int64_t)(t - q.b) * G + head % G;
-      const int nu = units_of(kv - prefix);
-      lo = head / G * per_head + start + r / kRows * nu;
-      in_tile = (int)(r % kRows);
-      w0 = lo / per_wg;
-      parts = (int)((lo + nu - 1) / per_wg - w0 + 1);
+  // the row's item: units [lo, hi) in the work-groups w0 .., and its row of the tile
+  int64_t lo = 0, w0 = 0;
+  int parts = 0, in_tile = 0;
+  if (kv > prefix) {
+    const int64_t r = (int64_t)(t - q.b) * G + head % G;
+    const int nu = units_of(kv - prefix);
+    lo = head / G * per_head + start + r / kRows * nu;
+    in_tile = (int)(r % kRows);
+    w0 = lo / per_wg;
+    parts = (int)((lo + nu - 1) / per_wg - w0 + 1);
+  }
+  if (prefix == 0 && parts == 1) return;  // the main kernel wrote it
+  const int64_t pre_item =
+      (int64_t)(a.pre_slots - 1 - t / a.pre_tt) * (a.h / a.pre_share) + head / a.pre_share;
+  const int pre_row = t % a.pre_tt * a.pre_share + head % a.pre_share;
+  const int n = lead + parts;
+  auto where = [&](int i, const float *&po, const float *&pm) __attribute__((always_inline)) {
+    if (i < lead) {
+      const int64_t at = (pre_item * a.pre_splits + i) * a.pre_rows + pre_row;
+      po = a.pre_o + at * D;
+      pm = a.pre_ml + at * 2;
+    } else if (parts == 1) {
+      po = a.done_o + row * D;
+      pm = a.done_ml + row * 2;
+    } else {
+      const int64_t wgi = w0 + i - lead;
+      const int64_t at = (wgi * 2 + (lo >= wgi * per_wg ? 1 : 0)) * kRows + in_tile;
+      po = a.part_o + at * D;
+      pm = a.part_ml + at * 2;
     }
-    if (prefix == 0 && parts == 1) continue;  // the main kernel wrote it
-    const int64_t orow = (int64_t)t * a.h + head;
-    const int64_t pre_item =
-        (int64_t)(a.pre_slots - 1 - t / a.pre_tt) * (a.h / a.pre_share) + head / a.pre_share;
-    const int pre_row = t % a.pre_tt * a.pre_share + head % a.pre_share;
-    const int n = lead + parts;
-    // place of a part among the rows of its array
-    auto where = [&](int i, const float *&po, const float *&pm) __attribute__((always_inline)) {
-      if (i < lead) {
-        const int64_t at = (pre_item * a.pre_splits + i) * a.pre_rows + pre_row;
-        po = a.pre_o + at * D;
-        pm = a.pre_ml + at * 2;
-      } else if (parts == 1) {
-        po = a.done_o + orow * D;
-        pm = a.done_ml + orow * 2;
-      } else {
-        const int64_t wgi = w0 + i - lead;
-        const int64_t at = (wgi * 2 + (lo >= wgi * per_wg ? 1 : 0)) * kRows + in_tile;
-        po = a.part_o + at * D;
-        pm = a.part_ml + at * 2;
+  };
+  // running state of this wave's parts: sub, sub + kWaves, ..., 64 at a time
+  float big = kNegInf, l = 0.f;
+  vec sum = {};
+  for (int base = sub; base < n; base += 64 * kWaves) {
+    const int mine = base + lane * kWaves, here = min(64, (n - base + kWaves - 1) / kWaves);
+    const float *po, *pm;
+    where(min(mine, n - 1), po, pm);
+    const float m = mine < n ? pm[0] : kNegInf;
+    float top = m;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+    const float now = fmaxf(big, top);
+    const float old = big == kNegInf ? 0.f : fast_exp2(big - now);
+    const float f = m == kNegInf ? 0.f : fast_exp2(m - now);
+    float add = f == 0.f ? 0.f : pm[1] * f;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) add += __shfl_xor(add, off, 64);
+    big = now;
+    l = l * old + add;
+    sum *= old;
+    for (int k = 0; k < here; k += 4) {  // four loads at a time
+      vec x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        where(min(base + (k + e) * kWaves, n - 1), po, pm);
+        x[e] = *reinterpret_cast<const vec *>(po + kPer * lane);
       }
-    };
-    float big = kNegInf;
-    for (int i = tid; i < n; i += 256) {
-      const float *po, *pm;
-      where(i, po, pm);
-      big = fmaxf(big, pm[0]);
-    }
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) big = fmaxf(big, __shfl_xor(big, off, 64));
-    __syncthreads();  // the head before may still read LDS
-    if (lane == 0) red[w][0] = big;
-    __syncthreads();
-    big = fmaxf(fmaxf(red[0][0], red[1][0]), fmaxf(red[2][0], red[3][0]));
-
-    f32x4 sum = zero4();
-    float l = 0.f;
-    const int part = tid / kLanes, d4 = 4 * (tid % kLanes);
-    for (int base = 0; base < n; base += kMost) {
-      const int m = min(n - base, kMost);
-      if (base) __syncthreads();
-      for (int i = tid; i < m; i += 256) {
-        const float *po, *pm;
-        where(base + i, po, pm);
-        const float f = pm[0] == kNegInf ? 0.f : fast_exp2(pm[0] - big);
-        weight[i] = f;
-        l = fmaf(pm[1], f, l);
+      for (int e = 0; e < 4; ++e) {
+        const float g = __shfl(f, (k + e) & 63, 64);
+        if (k + e < here && g != 0.f) sum += g * x[e];
       }
-      __syncthreads();
-      for (int i = part; i < m; i += 4 * kPar) {
-        f32x4 x[4];
-        float f[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {  // four loads at a time
-          const int k = min(i + e * kPar, m - 1);
-          const float *po, *pm;
-          where(base + k, po, pm);
-          x[e] = *reinterpret_cast<const f32x4 *>(po + d4);
-          f[e] = i + e * kPar < m ? weight[k] : 0.f;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (f[e] != 0.f) sum += x[e] * f[e];
-      }
-    }
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) l += __shfl_xor(l, off, 64);
-    if (lane == 0) red[w][1] = l;
-    *reinterpret_cast<f32x4 *>(&os[part][d4]) = sum;
-    __syncthreads();
-    if (part == 0) {
-      l = red[0][1] + red[1][1] + red[2][1] + red[3][1];
-#pragma unroll
-      for (int i = 1; i < kPar; ++i) sum += *reinterpret_cast<const f32x4 *>(&os[i][d4]);
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      *reinterpret_cast<u32x2 *>(static_cast<T *>(a.o) + orow * D + d4) =
-          u32x2{Elem<T>::pack(sum[0] * inv, sum[1] * inv),
-                Elem<T>::pack(sum[2] * inv, sum[3] * inv)};
     }
   }
+  if constexpr (kWaves > 1) {
+    *reinterpret_cast<vec *>(os[sub][lane]) = sum;
+    if (lane == 0) stat[sub][0] = big, stat[sub][1] = l;
+    __syncthreads();
+    if (sub) return;
+    const float mine = big;
+    for (int i = 1; i < kWaves; ++i) big = fmaxf(big, stat[i][0]);
+    const float f = mine == kNegInf ? 0.f : fast_exp2(mine - big);
+    l *= f;
+    sum *= f;
+    for (int i = 1; i < kWaves; ++i) {
+      const float g = stat[i][0] == kNegInf ? 0.f : fast_exp2(stat[i][0] - big);
+      l += stat[i][1] * g;
+      sum += *reinterpret_cast<const vec *>(os[i][lane]) * g;
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<T *>(a.o) + row * D);
+#pragma unroll
+  for (int k = 0; k < kPer / 2; ++k)
+    o[kPer / 2 * lane + k] = Elem<T>::pack(sum[2 * k] * inv, sum[2 * k + 1] * inv);
 }
 
 template <typename T, int D, int kRT>
-hipError_t run(const StreamArgs &a, dim3 join, int per, hipStream_t stream) {
+hipError_t run(const StreamArgs &a, int64_t rows, hipStream_t stream) {
+  const bool wide = rows < kManyRows;
+  dim3 join;
+  if (!flat_grid(wide ? rows : (rows + 3) / 4, 256, join)) return hipErrorInvalidValue;
   hipLaunchKernelGGL((attn_stream_kernel<T, D, kRT>), dim3((a.grid + 7) / 8 * 8), dim3(256), 0,
                      stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attn_stream_join_kernel<T, D, kRT>), join, dim3(256), 0, stream, a, per);
+  if (wide)
+    hipLaunchKernelGGL((attn_stream_join_kernel<T, D, kRT, 4>), join, dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL((attn_stream_join_kernel<T, D, kRT, 1>), join, dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
 template <typename T>
-hipError_t run_of(const StreamArgs &a, int d, int rt, dim3 join, int per, hipStream_t stream) {
+hipError_t run_of(const StreamArgs &a, int d, int rt, int64_t rows, hipStream_t stream) {
   if (d == 128)
-    return rt == 1   ? run<T, 128, 1>(a, join, per, stream)
-           : rt == 2 ? run<T, 128, 2>(a, join, per, stream)
-                     : run<T, 128, 4>(a, join, per, stream);
-  return rt == 1 ? run<T, 256, 1>(a, join, per, stream) : run<T, 256, 2>(a, join, per, stream);
+    return rt == 1   ? run<T, 128, 1>(a, rows, stream)
+           : rt == 2 ? run<T, 128, 2>(a, rows, stream)
+                     : run<T, 128, 4>(a, rows, stream);
+  return rt == 1 ? run<T, 256, 1>(a, rows, stream) : run<T, 256, 2>(a, rows, stream);
 }
 
 int64_t rows_per_seq(const gdn_attn_config *cfg) {
@@ -513,16 +559,10 @@ int stream_grid(const gdn_attn_config *cfg) {
 
 hipError_t launch_attn_stream(const gdn_attn_config *cfg, StreamArgs a, hipStream_t stream) {
   if (cfg->t_max == 0) return hipSuccess;
-  // heads per joining work-group: most rows of a large batch need no join, and finding
-  // a token's sequence costs more than looking at one
-  const int64_t fair = (int64_t)cfg->t_max * cfg->h / (4 * cu_count());
-  const int per = static_cast<int>(fair < 1 ? 1 : fair > cfg->h ? cfg->h : fair);
-  dim3 join;
-  if (!flat_grid((int64_t)cfg->t_max * ((cfg->h + per - 1) / per), 256, join))
-    return hipErrorInvalidValue;
   const int rt = stream_row_tiles(cfg);
-  return cfg->dtype == GDN_BF16 ? run_of<__bf16>(a, cfg->d, rt, join, per, stream)
-                                : run_of<_Float16>(a, cfg->d, rt, join, per, stream);
+  const int64_t rows = (int64_t)cfg->t_max * cfg->h;
+  return cfg->dtype == GDN_BF16 ? run_of<__bf16>(a, cfg->d, rt, rows, stream)
+                                : run_of<_Float16>(a, cfg->d, rt, rows, stream);
 }
 
 }  // namespace gdn

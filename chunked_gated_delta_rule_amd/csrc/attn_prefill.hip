@@ -82,14 +82,6 @@ struct Tile {
 __device__ __forceinline__ int k_swz(int r) { return r & 15; }
 __device__ __forceinline__ int v_swz(int r) { return (r & 3) << 2; }
 
-// A value the compiler may not see through: what is derived from it is formed
-// anew at each use, where keeping it would cost registers all along the loop.
-template <bool kDo>
-__device__ __forceinline__ int opaque(int x) {
-  if constexpr (kDo) asm volatile("" : "+v"(x));
-  return x;
-}
-
 // Waits for this wave's reads of LDS and copies into it (lgkmcnt(0), vmcnt(0)).
 __device__ __forceinline__ void wait_lds() {
   asm volatile("" ::: "memory");
@@ -108,7 +100,7 @@ __device__ __forceinline__ void barrier() {
 // others) straight to LDS: lane l of wave w fills the 16 bytes at kPass i + 1024 w +
 // 16 l with the chunk that belongs there. What a wave copies at a time lies in one
 // aligned group of 16 rows: these have one set of swizzles, and lie in one page.
-// rsrc(g, add): the descriptor of rows 16 g .., and what to add to offsets in it.
+// rsrc(i, add): the descriptor of the wave's i-th group, and what to add to offsets.
 template <typename T, int D, int kBN, int kWaves, bool kV, typename F>
 __device__ __forceinline__ void fetch(Lds<T> dst, int row_bytes, int lane, int w, F rsrc) {
   typedef Tile<T, D, kBN, kWaves> L;
@@ -127,7 +119,7 @@ __device__ __forceinline__ void fetch(Lds<T> dst, int row_bytes, int lane, int w
 #pragma unroll
   for (int i = 0; i < L::kLoads; ++i) {
     int add = 0;
-    const rsrc_t r = rsrc((i * L::kRowsPerLoad + 1024 / L::kRowBytes * w) / 16, add);
+    const rsrc_t r = rsrc(i / kHalves, add);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (Lds<void>)(dst + L::kPass / 2 * i + 512 * w), 16,
                                              from[i % kHalves] + add, 0, 0, 0);
   }
@@ -359,27 +351,45 @@ __device__ __forceinline__ Sight sight_of(const Where &t, int rw, int col, int t
   return s;
 }
 
+// The pages of the groups of 16 keys that a wave copies of a tile. Looked up a phase
+// before the copies, which then start at once.
+template <typename L, Keys kKeys>
+struct Spot {
+  static constexpr int kN = L::kLoads * L::kRowsPerLoad / 16;
+  int page[kN];
+  // first key of the wave's i-th group in the tile
+  static __device__ __forceinline__ int key(int i, int w) {
+    return 16 * ((i * (L::kRowsPerLoad < 16 ? 16 : L::kRowsPerLoad) + 1024 / L::kRowBytes * w) / 16);
+  }
+  __device__ __forceinline__ void look(const TileArgs &a, const Where &t, int k0, int w) {
+    if constexpr (kKeys != Keys::kRows) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) page[i] = page_of(a.pg, t.s, min(k0 + key(i, w), t.lk - 1));
+    }
+  }
+};
+
 // Copies the kBN keys (values) from k0 on to LDS, as ranges that end with the
 // sequence's last key. kWaves waves take part, of which this is number w.
 template <typename T, int D, int kBN, int kWaves, Keys kKeys, bool kV>
-__device__ __forceinline__ void get(const TileArgs &a, const Where &t, int kvh, int k0, T *tile,
-                                    int lane, int w) {
+__device__ __forceinline__ void get(const TileArgs &a, const Where &t,
+                                    const Spot<Tile<T, D, kBN, kWaves>, kKeys> &spot, int kvh, int k0,
+                                    T *tile, int lane, int w) {
   const T *base = static_cast<const T *>(kV ? a.v : a.k);
   if constexpr (kKeys == Keys::kRows) {
     const int64_t stride = kV ? a.v_row : a.k_row;
     const int row_bytes = (int)stride * 2;
     const rsrc_t r = make_rsrc(base + (t.kb + k0) * stride + kvh * D,
                                (min(kBN, t.lk - k0) - 1) * row_bytes + D * 2);
-    fetch<T, D, kBN, kWaves, kV>((Lds<T>)tile, row_bytes, lane, w, [&](int g, int &add) {
-      add = 16 * g * row_bytes;
+    fetch<T, D, kBN, kWaves, kV>((Lds<T>)tile, row_bytes, lane, w, [&](int i, int &add) {
+      add = spot.key(i, w) * row_bytes;
       return r;
     });
   } else {
-    const int32_t *table = a.pg.table + (int64_t)t.s * a.pg.max_pages;
-    fetch<T, D, kBN, kWaves, kV>((Lds<T>)tile, D * 2, lane, w, [&](int g, int &) {
-      const int key = k0 + 16 * g, rows = max(min(16, t.lk - key), 0);
-      const int64_t at = pool_row(a.pg, table, min(key, (t.lk - 1) & ~15), kvh, a.hkv);
-      return make_rsrc(base + at * D, rows * D * 2);
+    fetch<T, D, kBN, kWaves, kV>((Lds<T>)tile, D * 2, lane, w, [&](int i, int &) {
+      const int key = k0 + spot.key(i, w);
+      const T *p = base + pool_row(a.pg, spot.page[i], key, kvh, a.hkv) * D;
+      return make_rsrc(p, max(min(16, t.lk - key), 0) * D * 2);
     });
   }
 }
@@ -412,16 +422,23 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(TileArgs a) {
   const Sight see = sight_of<kKeys>(t, 32 * w, col, tt, share);
   const int tiles = see.keys > 0 ? (see.keys + kBN - 1) / kBN : 0;
 
-  auto get_k = [&](int j, T *tile) __attribute__((always_inline)) {
-    get<T, D, kBN, kWaves, kKeys, false>(a, t, kvh, j * kBN, tile, lane, w);
+  typedef Spot<Tile<T, D, kBN, kWaves>, kKeys> Spots;
+  auto look = [&](int j) __attribute__((always_inline)) {
+    Spots s = {};
+    if (j < tiles) s.look(a, t, j * kBN, w);
+    return s;
   };
-  auto get_v = [&](int j, T *tile) __attribute__((always_inline)) {
-    get<T, D, kBN, kWaves, kKeys, true>(a, t, kvh, j * kBN, tile, lane, w);
+  auto get_k = [&](int j, T *tile, const Spots &s) __attribute__((always_inline)) {
+    if (j < tiles) get<T, D, kBN, kWaves, kKeys, false>(a, t, s, kvh, j * kBN, tile, lane, w);
+  };
+  auto get_v = [&](int j, T *tile, const Spots &s) __attribute__((always_inline)) {
+    if (j < tiles) get<T, D, kBN, kWaves, kKeys, true>(a, t, s, kvh, j * kBN, tile, lane, w);
   };
   Rows<T, D, kBN> x;
-  if (tiles > 0) {
-    get_k(0, k_a);
-    get_v(0, v_a);
+  {
+    const Spots s = look(0);
+    get_k(0, k_a, s);
+    get_v(0, v_a, s);
   }
   x.load(q_row<T>(a, t, see.tok, 32 * w + col, D), hh);
   auto score = [&](int j, T *kt) __attribute__((always_inline)) {
@@ -432,22 +449,21 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(TileArgs a) {
     if (j * kBN <= see.hi) x.weigh((Lds<T>)vt, a.scale_log2, lane);
   };
   if constexpr (kWaves == 4) {
+    Spots s = look(1);
     for (int j = 0; j < tiles; j += 2) {
       wait_lds();
       barrier();  // tile j is there, and the other pair is no longer read
-      if (j + 1 < tiles) {
-        get_k(j + 1, k_b);
-        get_v(j + 1, v_b);
-      }
+      get_k(j + 1, k_b, s);
+      get_v(j + 1, v_b, s);
+      s = look(j + 2);
       score(j, k_a);
       weigh(j, v_a);
       if (j + 1 >= tiles) break;
       wait_lds();
       barrier();
-      if (j + 2 < tiles) {
-        get_k(j + 2, k_a);
-        get_v(j + 2, v_a);
-      }
+      get_k(j + 2, k_a, s);
+      get_v(j + 2, v_a, s);
+      s = look(j + 3);
       score(j + 1, k_b);
       weigh(j + 1, v_b);
     }
@@ -457,43 +473,48 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(TileArgs a) {
     // copied from the end of phase 2 j (its place was last read in 2 j - 1) and
     // first read in 2 j + 2; V of tile j + 1 from the end of 2 j + 1 (last read in
     // 2 j) for 2 j + 3: each has a whole phase, and is waited for at its end.
-    auto k_end = [&](int j, T *kt) __attribute__((always_inline)) {
+    auto k_end = [&](int j, T *kt, const Spots &s) __attribute__((always_inline)) {
       wait_lds();
-      if (j < tiles) get_k(j, kt);
+      get_k(j, kt, s);
       barrier();
     };
-    auto v_end = [&](int j, T *vt) __attribute__((always_inline)) {
+    auto v_end = [&](int j, T *vt, const Spots &s) __attribute__((always_inline)) {
       wait_lds();
-      if (j < tiles) get_v(j, vt);
+      get_v(j, vt, s);
       barrier();
     };
+    Spots s = look(1);
     wait_lds();
     barrier();
     if (w < 4) {
       for (int j = 0; j < tiles; j += 2) {
         score(j, k_a);
-        k_end(j + 1, k_b);
+        k_end(j + 1, k_b, s);
         weigh(j, v_a);
-        v_end(j + 1, v_b);
+        v_end(j + 1, v_b, s);
         if (j + 1 >= tiles) break;
+        s = look(j + 2);
         score(j + 1, k_b);
-        k_end(j + 2, k_a);
+        k_end(j + 2, k_a, s);
         weigh(j + 1, v_b);
-        v_end(j + 2, v_a);
+        v_end(j + 2, v_a, s);
+        s = look(j + 3);
       }
       barrier();
     } else {
-      k_end(1, k_b);
+      k_end(1, k_b, s);
       for (int j = 0; j < tiles; j += 2) {
         score(j, k_a);
-        v_end(j + 1, v_b);
+        v_end(j + 1, v_b, s);
+        s = look(j + 2);
         weigh(j, v_a);
-        k_end(j + 2, k_a);
+        k_end(j + 2, k_a, s);
         if (j + 1 >= tiles) break;
         score(j + 1, k_b);
-        v_end(j + 2, v_a);
+        v_end(j + 2, v_a, s);
+        s = look(j + 3);
         weigh(j + 1, v_b);
-        k_end(j + 3, k_b);
+        k_end(j + 3, k_b, s);
       }
     }
   }
@@ -534,17 +555,26 @@ __global__ __launch_bounds__(512, 2) void attn_part_kernel(TileArgs a) {
   const int steps = max((end - t.split * per + 1) / 2, 0);  // of either set
   // this set's tile of step j, if it has one
   auto has = [&](int j) { return j0 + 2 * j < end; };
-  auto get_k = [&](int j, T *tile) __attribute__((always_inline)) {
-    if (has(j))
-      get<T, D, kBN, 4, kKeys, false>(a, t, kvh, (j0 + 2 * j) * kBN, tile + set * kTile, lane, w);
+  typedef Spot<Tile<T, D, kBN, 4>, kKeys> Spots;
+  auto look = [&](int j) __attribute__((always_inline)) {
+    Spots s = {};
+    if (has(j)) s.look(a, t, (j0 + 2 * j) * kBN, w);
+    return s;
   };
-  auto get_v = [&](int j, T *tile) __attribute__((always_inline)) {
+  auto get_k = [&](int j, T *tile, const Spots &s) __attribute__((always_inline)) {
     if (has(j))
-      get<T, D, kBN, 4, kKeys, true>(a, t, kvh, (j0 + 2 * j) * kBN, tile + set * kTile, lane, w);
+      get<T, D, kBN, 4, kKeys, false>(a, t, s, kvh, (j0 + 2 * j) * kBN, tile + set * kTile, lane, w);
+  };
+  auto get_v = [&](int j, T *tile, const Spots &s) __attribute__((always_inline)) {
+    if (has(j))
+      get<T, D, kBN, 4, kKeys, true>(a, t, s, kvh, (j0 + 2 * j) * kBN, tile + set * kTile, lane, w);
   };
   Rows<T, D, kBN> x;
-  get_k(0, k_a);
-  get_v(0, v_a);
+  {
+    const Spots s = look(0);
+    get_k(0, k_a, s);
+    get_v(0, v_a, s);
+  }
   x.load(q_row<T>(a, t, see.tok, 32 * w + col, D), hh);
   auto score = [&](int j, T *kt) __attribute__((always_inline)) {
     const int k0 = (j0 + 2 * j) * kBN;
@@ -558,29 +588,32 @@ __global__ __launch_bounds__(512, 2) void attn_part_kernel(TileArgs a) {
   // K (V) of the next step is copied from the end of this step's score (weigh) phase
   // on, into the place that the step before left; both are waited for before they
   // are read, one and two phases later
-  auto k_end = [&](int j, T *kt) __attribute__((always_inline)) {
+  auto k_end = [&](int j, T *kt, const Spots &s) __attribute__((always_inline)) {
     wait_lds();
-    get_k(j, kt);
+    get_k(j, kt, s);
     barrier();
   };
-  auto v_end = [&](int j, T *vt) __attribute__((always_inline)) {
+  auto v_end = [&](int j, T *vt, const Spots &s) __attribute__((always_inline)) {
     wait_lds();
-    get_v(j, vt);
+    get_v(j, vt, s);
     barrier();
   };
+  Spots s = look(1);
   wait_lds();
   barrier();
   if (set) barrier();
   for (int j = 0; j < steps; j += 2) {
     score(j, k_a);
-    k_end(j + 1, k_b);
+    k_end(j + 1, k_b, s);
     weigh(j, v_a);
-    v_end(j + 1, v_b);
+    v_end(j + 1, v_b, s);
     if (j + 1 >= steps) break;
+    s = look(j + 2);
     score(j + 1, k_b);
-    k_end(j + 2, k_a);
+    k_end(j + 2, k_a, s);
     weigh(j + 1, v_b);
-    v_end(j + 2, v_a);
+    v_end(j + 2, v_a, s);
+    s = look(j + 3);
   }
   if (!set) barrier();
 
@@ -622,7 +655,7 @@ template <typename T, int D>
 __global__ __launch_bounds__(256) void attn_tile_join_kernel(TileArgs a, int tt, int bm) {
   constexpr int kPer = D / 64;  // dims per lane
   typedef float vec __attribute__((ext_vector_type(kPer)));
-  const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, w = uniform((int)(threadIdx.x >> 6));
   const int64_t i = (int64_t)flat_block() * 4 + w;
   const int t = (int)(i / a.h), head = (int)(i % a.h);
   if (t >= cu_at(a.cu_q, a.n_max, a.t_max)) return;

@@ -5,13 +5,14 @@
 //   x' = x / sqrt(mean(x^2) + eps) * w
 //   (a, b) -> s (a cos t - b sin t, b cos t + a sin t),  t = position * inv_freq[i]
 //
-// HBM-bound: each row is read once and written once. One 256-thread work-group
-// per token; D / 8 lanes own a head, eight channels each, and the work-group
-// walks the heads 2048 / D at a time. The channels of a lane are chosen so that
-// both members of its pairs are its own (half layout: four channels and the
-// four rot_dim / 2 further; interleaved: eight in a row), so the rotation needs
-// no other lane. cos and sin of the token's rot_dim / 2 angles are formed once
-// per work-group, in LDS, while the first heads' loads are in flight.
+// HBM-bound: each row is read once and written once. A 256-thread work-group takes a
+// few tokens; D / 8 lanes own a head's row, eight channels each, and the work-group
+// walks the heads of its tokens 2048 / D at a time, the next rows' loads in flight.
+// The channels of a lane are chosen so that both members of its pairs are its own
+// (half layout: four channels and the four rot_dim / 2 further; interleaved: eight in
+// a row), so the rotation needs no other lane. Sequence, position, cache row, and the
+// cos and sin of the rot_dim / 2 angles of each token are found once per work-group,
+// in LDS, while the first rows' loads are in flight.
 #include "attn_common.hpp"
 #include "attn_launch.hpp"
 
@@ -20,6 +21,7 @@ namespace gdn {
 namespace {
 
 constexpr int kFrontThreads = 256;
+constexpr int kMostTokens = 4;  // per work-group (32768 tokens: 149 us; one: 230; 16: 160)
 
 // How a lane's eight channels are placed: pairs inside the lane (half layout
 // with rot_dim a multiple of 8, or interleaved), or (half layout with any other
@@ -40,12 +42,15 @@ __device__ __forceinline__ void unpack4(const u32x2 &w, float *f) {
 template <typename T, int D, Pairs kPairs, bool kCache>
 __global__ __launch_bounds__(kFrontThreads) void attn_front_kernel(FrontArgs a) {
   constexpr int kLanes = D / 8;                    // lanes per head
-  constexpr int kHeads = kFrontThreads / kLanes;   // heads per pass
-  __shared__ __attribute__((aligned(16))) float cs[D / 2], sn[D / 2];
-  const int t = flat_block();
-  const int tid = threadIdx.x, lane = tid & 63;
+  constexpr int kRows = kFrontThreads / kLanes;    // rows per pass
+  __shared__ __attribute__((aligned(16))) float cs[kMostTokens][D / 2], sn[kMostTokens][D / 2];
+  __shared__ int64_t pos_of[kMostTokens], slot_of[kMostTokens];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int li = tid % kLanes;
-  if (t >= cu_at(a.cu, a.n_max, a.t_max)) return;
+  const int64_t t0 = (int64_t)flat_block() * a.tokens;
+  const int total = cu_at(a.cu, a.n_max, a.t_max);
+  if (t0 >= total) return;
+  const int nt = min(a.tokens, total - (int)t0);
   const int half = a.rot_dim >> 1;
 
   // this lane's channels: c0 .. c0 + 3 and c1 .. c1 + 3
@@ -56,38 +61,41 @@ __global__ __launch_bounds__(kFrontThreads) void attn_front_kernel(FrontArgs a) 
     c0 = turned ? 4 * li : a.rot_dim + 8 * (li - half / 4);
     c1 = turned ? half + 4 * li : c0 + 4;
   }
-  const int heads = a.h + (kCache ? 2 : 1) * a.hkv;
-  const T *row = static_cast<const T *>(a.qkv) + t * a.qkv_row;
+  // rows of the work-group: token by token, its heads in order
   const int first = a.q ? 0 : a.h;
-  int hd = first + tid / kLanes;
+  const int heads = a.h + (kCache ? 2 : 1) * a.hkv - first, rows = nt * heads;
+  const T *base = static_cast<const T *>(a.qkv) + t0 * a.qkv_row;
+  int r = tid / kLanes, tok = r / heads, head = first + r - tok * heads;
   u32x2 x0{0u, 0u}, x1{0u, 0u};
-  auto load = [&](int head) __attribute__((always_inline)) {
-    if (head < heads) {
-      x0 = *reinterpret_cast<const u32x2 *>(row + head * D + c0);
-      x1 = *reinterpret_cast<const u32x2 *>(row + head * D + c1);
+  auto load = [&]() __attribute__((always_inline)) {
+    if (r < rows) {
+      const T *p = base + tok * a.qkv_row + head * D;
+      x0 = *reinterpret_cast<const u32x2 *>(p + c0);
+      x1 = *reinterpret_cast<const u32x2 *>(p + c1);
     }
   };
-  load(hd);
+  load();
 
-  int len = 0;
-  const Packed p = seq_of_row(
-      a.cu, a.n_max, a.t_max, t, lane, [&](int i) { return a.kv_lens ? a.kv_lens[i] : 0; }, len);
-  const int s = p.s;
-  // kv_lens is the caller's: the position is formed in 64 bits
-  const int64_t pos = a.kv_lens ? (int64_t)len - (p.b + p.n - t) : t - p.b;
-  for (int i = tid; i < half; i += kFrontThreads) {
-    const double turns = (double)pos * (double)a.inv_freq[i] * kInvTwoPi;
-    const float f = (float)(turns - __builtin_rint(turns));  // -1/2 .. 1/2
-    cs[i] = a.rot_scale * __builtin_amdgcn_cosf(f);  // cos(2 pi f)
-    sn[i] = a.rot_scale * __builtin_amdgcn_sinf(f);
-  }
-  int64_t slot = -1;  // the token's row in a page pool of one head
-  if constexpr (kCache) {
-    const int64_t col = pos >> a.page_shift;
-    if (pos >= 0 && col < a.max_pages) {
-      const int page = a.table[(int64_t)s * a.max_pages + col];
-      if (page >= 0 && page < a.n_pages)
-        slot = (((int64_t)page * a.hkv) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+  // (a single token: every wave for itself, and no barrier)
+  for (int i = a.tokens > 1 ? w : 0; i < nt; i += kFrontThreads / 64) {
+    const int t = (int)t0 + i;
+    int len = 0;
+    const Packed p = seq_of_row(
+        a.cu, a.n_max, a.t_max, t, lane, [&](int s) { return a.kv_lens ? a.kv_lens[s] : 0; }, len);
+    // kv_lens is the caller's: the position is formed in 64 bits
+    const int64_t pos = a.kv_lens ? (int64_t)len - (p.b + p.n - t) : t - p.b;
+    int64_t slot = -1;  // the token's row in a page pool of one head
+    if constexpr (kCache) {
+      const int64_t col = pos >> a.page_shift;
+      if (pos >= 0 && col < a.max_pages) {
+        const int page = a.table[(int64_t)p.s * a.max_pages + col];
+        if (page >= 0 && page < a.n_pages)
+          slot = (((int64_t)page * a.hkv) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+      }
+    }
+    if (lane == 0) {
+      pos_of[i] = pos;
+      slot_of[i] = slot;
     }
   }
   float wq[8], wk[8];
@@ -97,15 +105,28 @@ __global__ __launch_bounds__(kFrontThreads) void attn_front_kernel(FrontArgs a) 
     wq[j] = a.q_w ? a.q_w[c] : 1.f;
     wk[j] = a.k_w ? a.k_w[c] : 1.f;
   }
+  if (a.tokens > 1) __syncthreads();
+  for (int i = tid; i < nt * half; i += kFrontThreads) {
+    const int k = i / half, j = i - k * half;
+    const double turns = (double)pos_of[k] * (double)a.inv_freq[j] * kInvTwoPi;
+    const float f = (float)(turns - __builtin_rint(turns));  // -1/2 .. 1/2
+    cs[k][j] = a.rot_scale * __builtin_amdgcn_cosf(f);  // cos(2 pi f)
+    sn[k][j] = a.rot_scale * __builtin_amdgcn_sinf(f);
+  }
   __syncthreads();
 
-  for (int base = first; base < heads; base += kHeads) {
-    const bool in = hd < heads;
+  for (int at = 0; at < rows; at += kRows) {
+    const bool in = r < rows;
     const u32x2 y0 = x0, y1 = x1;
-    const int head = hd;
-    hd += kHeads;
-    load(hd);
-    const bool is_q = head < a.h, is_v = head >= a.h + a.hkv;
+    const int hd = head, tk = in ? tok : 0;
+    r += kRows;
+    head += kRows;
+    while (head >= first + heads) {
+      head -= heads;
+      ++tok;
+    }
+    load();
+    const bool is_q = hd < a.h, is_v = hd >= a.h + a.hkv;
     const bool norm = (is_q ? a.q_w : a.k_w) != nullptr && !is_v;
     float x[8];
     unpack4<T>(y0, x);
@@ -115,42 +136,44 @@ __global__ __launch_bounds__(kFrontThreads) void attn_front_kernel(FrontArgs a) 
     for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
     ss = sum16(ss);
     if constexpr (kLanes == 32) ss = sum16x(ss);
-    const float r = norm ? 1.f / sqrtf(ss * (1.f / D) + a.eps) : 1.f;
+    const float rn = norm ? 1.f / sqrtf(ss * (1.f / D) + a.eps) : 1.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] *= r * (is_q ? wq[j] : wk[j]);
+    for (int j = 0; j < 8; ++j) x[j] *= rn * (is_q ? wq[j] : wk[j]);
     if (!is_v) {
+      const float *ct = cs[tk], *st = sn[tk];
       if constexpr (kPairs == Pairs::kHalf) {
         if (turned) {
-          const f32x4 c = *reinterpret_cast<const f32x4 *>(cs + c0);
-          const f32x4 d = *reinterpret_cast<const f32x4 *>(sn + c0);
+          const f32x4 c = *reinterpret_cast<const f32x4 *>(ct + c0);
+          const f32x4 d = *reinterpret_cast<const f32x4 *>(st + c0);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float u = x[j], w = x[j + 4];
-            x[j] = u * c[j] - w * d[j];
-            x[j + 4] = w * c[j] + u * d[j];
+            const float u = x[j], v = x[j + 4];
+            x[j] = u * c[j] - v * d[j];
+            x[j + 4] = v * c[j] + u * d[j];
           }
         }
       } else if constexpr (kPairs == Pairs::kInterleaved) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (c0 + 2 * j < a.rot_dim) {
-            const float c = cs[(c0 >> 1) + j], d = sn[(c0 >> 1) + j];
-            const float u = x[2 * j], w = x[2 * j + 1];
-            x[2 * j] = u * c - w * d;
-            x[2 * j + 1] = w * c + u * d;
+            const float c = ct[(c0 >> 1) + j], d = st[(c0 >> 1) + j];
+            const float u = x[2 * j], v = x[2 * j + 1];
+            x[2 * j] = u * c - v * d;
+            x[2 * j + 1] = v * c + u * d;
           }
         }
       } else {
         if (in) {
           const float *wp = is_q ? a.q_w : a.k_w;
+          const T *row = base + tk * a.qkv_row + hd * D;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const int c = c0 + j;
             if (c < a.rot_dim) {
               const bool low = c < half;
               const int p = low ? c + half : c - half, i = low ? c : p;
-              const float y = static_cast<float>(row[head * D + p]) * r * (wp ? wp[p] : 1.f);
-              x[j] = x[j] * cs[i] + (low ? -y : y) * sn[i];
+              const float y = static_cast<float>(row[p]) * rn * (wp ? wp[p] : 1.f);
+              x[j] = x[j] * ct[i] + (low ? -y : y) * st[i];
             }
           }
         }
@@ -164,13 +187,15 @@ __global__ __launch_bounds__(kFrontThreads) void attn_front_kernel(FrontArgs a) 
       *reinterpret_cast<u32x2 *>(p + c0) = z0;
       *reinterpret_cast<u32x2 *>(p + c1) = z1;
     };
+    const int64_t t = t0 + tk;
     if (is_q) {
-      store(static_cast<T *>(a.q) + ((int64_t)t * a.h + head) * D);
+      store(static_cast<T *>(a.q) + (t * a.h + hd) * D);
       continue;
     }
-    const int kh = head - a.h - (is_v ? a.hkv : 0);
-    if (!is_v && a.k) store(static_cast<T *>(a.k) + ((int64_t)t * a.hkv + kh) * D);
+    const int kh = hd - a.h - (is_v ? a.hkv : 0);
+    if (!is_v && a.k) store(static_cast<T *>(a.k) + (t * a.hkv + kh) * D);
     if constexpr (kCache) {
+      const int64_t slot = slot_of[tk];
       if (slot >= 0)
         store(static_cast<T *>(is_v ? a.v_pages : a.k_pages) +
               (slot + ((int64_t)kh << a.page_shift)) * D);
@@ -205,8 +230,12 @@ void run_of(const FrontArgs &a, int d, bool interleaved, dim3 grid, hipStream_t 
 
 hipError_t launch_attn_front(const gdn_attn_config *cfg, FrontArgs a, hipStream_t stream) {
   if (cfg->t_max == 0) return hipSuccess;
+  // several tokens per work-group once there are enough for every CU's eight
+  const int most = cfg->t_max / (8 * cu_count());
+  a.tokens = most < 1 ? 1 : most > kMostTokens ? kMostTokens : most;
   dim3 grid;
-  if (!flat_grid(cfg->t_max, kFrontThreads, grid)) return hipErrorInvalidValue;
+  if (!flat_grid((cfg->t_max + a.tokens - 1) / a.tokens, kFrontThreads, grid))
+    return hipErrorInvalidValue;
   if (cfg->dtype == GDN_BF16)
     run_of<__bf16>(a, cfg->d, cfg->rot_interleaved != 0, grid, stream);
   else

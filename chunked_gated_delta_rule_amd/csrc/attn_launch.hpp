@@ -21,6 +21,7 @@ struct FrontArgs {
   int rot_dim;
   float eps, rot_scale;
   int page_shift, n_pages, max_pages;
+  int tokens;  // per work-group; set by the launcher
 };
 hipError_t launch_attn_front(const gdn_attn_config *cfg, FrontArgs a, hipStream_t stream);
 

@@ -529,8 +529,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(TileArgs a) {
 // One part of a tile's keys, its running state left for a join. 128 rows: the more
 // rows and parts, the more partial results are written and read again, so instead of
 // taking 256 rows the eight waves are two sets of four, on the even and the odd tiles
-// of the part, each with its own copies (double buffered), in opposite phase as
-// above. The second set's state is added to the first's through LDS at the end.
+// of the part, each with its own copies (double buffered). One barrier per step, the
+// two waves of a SIMD overlap by chance: with a step of 32 keys (D = 256) the phases
+// above cost more in barriers than they gain (39 against 36 us for 1024 rows on 8192
+// keys of two heads). The second set's state is added to the first's through LDS at
+// the end.
 template <typename T, int D, Keys kKeys>
 __global__ __launch_bounds__(512, 2) void attn_part_kernel(TileArgs a) {
   constexpr int kBM = 128, kBN = D == 256 ? 32 : 64;
@@ -585,37 +588,26 @@ __global__ __launch_bounds__(512, 2) void attn_part_kernel(TileArgs a) {
     if (has(j) && (j0 + 2 * j) * kBN <= see.hi)
       x.weigh((Lds<T>)(vt + set * kTile), a.scale_log2, lane);
   };
-  // K (V) of the next step is copied from the end of this step's score (weigh) phase
-  // on, into the place that the step before left; both are waited for before they
-  // are read, one and two phases later
-  auto k_end = [&](int j, T *kt, const Spots &s) __attribute__((always_inline)) {
-    wait_lds();
-    get_k(j, kt, s);
-    barrier();
-  };
-  auto v_end = [&](int j, T *vt, const Spots &s) __attribute__((always_inline)) {
-    wait_lds();
-    get_v(j, vt, s);
-    barrier();
-  };
   Spots s = look(1);
-  wait_lds();
-  barrier();
-  if (set) barrier();
   for (int j = 0; j < steps; j += 2) {
-    score(j, k_a);
-    k_end(j + 1, k_b, s);
-    weigh(j, v_a);
-    v_end(j + 1, v_b, s);
-    if (j + 1 >= steps) break;
+    wait_lds();
+    barrier();
+    get_k(j + 1, k_b, s);
+    get_v(j + 1, v_b, s);
     s = look(j + 2);
-    score(j + 1, k_b);
-    k_end(j + 2, k_a, s);
-    weigh(j + 1, v_b);
-    v_end(j + 2, v_a, s);
+    score(j, k_a);
+    weigh(j, v_a);
+    if (j + 1 >= steps) break;
+    wait_lds();
+    barrier();
+    get_k(j + 2, k_a, s);
+    get_v(j + 2, v_a, s);
     s = look(j + 3);
+    score(j + 1, k_b);
+    weigh(j + 1, v_b);
   }
-  if (!set) barrier();
+  wait_lds();
+  barrier();  // the tiles are no longer read
 
   // the second set's state, lane by lane: a lane of both holds the same row and dims
   const Lds<T> tile = w == 0 ? (Lds<T>)k_a : w == 1 ? (Lds<T>)v_a : w == 2 ? (Lds<T>)k_b : (Lds<T>)v_b;

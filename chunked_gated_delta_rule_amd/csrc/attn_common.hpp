@@ -100,7 +100,7 @@ __device__ __forceinline__ void narrow(int n, int x, int lane, int &lo, int &len
     const int step = (len + 63) / 64;
     const int at = lane * step;
     const bool in = at < len && key(lo + at) <= x;
-    const int skip = (max(__popcll(__ballot(in)), 1) - 1) * step;
+    const int skip = max((int)__popcll(__ballot(in)) - 1, 0) * step;
     lo += skip;
     len = min(step, len - skip);
   }
@@ -130,7 +130,7 @@ __device__ __forceinline__ Packed locate(const int32_t *__restrict__ cu, int n_m
   const int b = cu_at(cu, s, t_max), n = cu_end(cu, s, b, t_max) - b;
   int mine[kExtra];
   extra(s, mine);
-  const int hit = max(__popcll(__ballot(lane < len && key(s, b) <= x)), 1) - 1;
+  const int hit = max((int)__popcll(__ballot(lane < len && key(s, b) <= x)) - 1, 0);
 #pragma unroll
   for (int i = 0; i < kExtra; ++i) out[i] = __builtin_amdgcn_readlane(mine[i], hit);
   return {uniform(lo + hit), __builtin_amdgcn_readlane(b, hit), __builtin_amdgcn_readlane(n, hit)};

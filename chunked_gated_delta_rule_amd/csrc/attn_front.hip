@@ -48,9 +48,6 @@ __global__ __launch_bounds__(kFrontThreads) void attn_front_kernel(FrontArgs a) 
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int li = tid % kLanes;
   const int64_t t0 = (int64_t)flat_block() * a.tokens;
-  const int total = cu_at(a.cu, a.n_max, a.t_max);
-  if (t0 >= total) return;
-  const int nt = min(a.tokens, total - (int)t0);
   const int half = a.rot_dim >> 1;
 
   // this lane's channels: c0 .. c0 + 3 and c1 .. c1 + 3
@@ -61,9 +58,11 @@ __global__ __launch_bounds__(kFrontThreads) void attn_front_kernel(FrontArgs a) 
     c0 = turned ? 4 * li : a.rot_dim + 8 * (li - half / 4);
     c1 = turned ? half + 4 * li : c0 + 4;
   }
-  // rows of the work-group: token by token, its heads in order
+  // rows of the work-group: token by token, its heads in order. The first ones are
+  // asked for before it is known how many tokens there are (qkv has t_max rows)
   const int first = a.q ? 0 : a.h;
-  const int heads = a.h + (kCache ? 2 : 1) * a.hkv - first, rows = nt * heads;
+  const int heads = a.h + (kCache ? 2 : 1) * a.hkv - first;
+  int rows = (int)min((int64_t)a.tokens, a.t_max - t0) * heads;
   const T *base = static_cast<const T *>(a.qkv) + t0 * a.qkv_row;
   int r = tid / kLanes, tok = r / heads, head = first + r - tok * heads;
   u32x2 x0{0u, 0u}, x1{0u, 0u};
@@ -75,6 +74,21 @@ __global__ __launch_bounds__(kFrontThreads) void attn_front_kernel(FrontArgs a) 
     }
   };
   load();
+  const float freq = tid < half ? a.inv_freq[tid] : 0.f;
+  typedef f32x4 weights __attribute__((aligned(4)));
+  f32x4 wq0{1.f, 1.f, 1.f, 1.f}, wq1 = wq0, wk0 = wq0, wk1 = wq0;
+  if (a.q_w) {
+    wq0 = *reinterpret_cast<const weights *>(a.q_w + c0);
+    wq1 = *reinterpret_cast<const weights *>(a.q_w + c1);
+  }
+  if (a.k_w) {
+    wk0 = *reinterpret_cast<const weights *>(a.k_w + c0);
+    wk1 = *reinterpret_cast<const weights *>(a.k_w + c1);
+  }
+  const int total = cu_at(a.cu, a.n_max, a.t_max);
+  if (t0 >= total) return;
+  const int nt = min(a.tokens, total - (int)t0);
+  rows = nt * heads;
 
   // (a single token: every wave for itself, and no barrier)
   for (int i = a.tokens > 1 ? w : 0; i < nt; i += kFrontThreads / 64) {
@@ -98,17 +112,11 @@ __global__ __launch_bounds__(kFrontThreads) void attn_front_kernel(FrontArgs a) 
       slot_of[i] = slot;
     }
   }
-  float wq[8], wk[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int c = j < 4 ? c0 + j : c1 + j - 4;
-    wq[j] = a.q_w ? a.q_w[c] : 1.f;
-    wk[j] = a.k_w ? a.k_w[c] : 1.f;
-  }
   if (a.tokens > 1) __syncthreads();
   for (int i = tid; i < nt * half; i += kFrontThreads) {
     const int k = i / half, j = i - k * half;
-    const double turns = (double)pos_of[k] * (double)a.inv_freq[j] * kInvTwoPi;
+    const float per_pos = k == 0 ? freq : a.inv_freq[j];
+    const double turns = (double)pos_of[k] * (double)per_pos * kInvTwoPi;
     const float f = (float)(turns - __builtin_rint(turns));  // -1/2 .. 1/2
     cs[k][j] = a.rot_scale * __builtin_amdgcn_cosf(f);  // cos(2 pi f)
     sn[k][j] = a.rot_scale * __builtin_amdgcn_sinf(f);
@@ -138,7 +146,10 @@ __global__ __launch_bounds__(kFrontThreads) void attn_front_kernel(FrontArgs a) 
     if constexpr (kLanes == 32) ss = sum16x(ss);
     const float rn = norm ? 1.f / sqrtf(ss * (1.f / D) + a.eps) : 1.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] *= rn * (is_q ? wq[j] : wk[j]);
+    for (int j = 0; j < 4; ++j) {
+      x[j] *= rn * (is_q ? wq0[j] : wk0[j]);
+      x[j + 4] *= rn * (is_q ? wq1[j] : wk1[j]);
+    }
     if (!is_v) {
       const float *ct = cs[tk], *st = sn[tk];
       if constexpr (kPairs == Pairs::kHalf) {

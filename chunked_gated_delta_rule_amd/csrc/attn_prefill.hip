@@ -400,13 +400,15 @@ __device__ __forceinline__ const T *q_row(const TileArgs &a, const Where &t, int
          (t.group * a.share + row % a.share) * D;
 }
 
-// Whole tiles: kWaves waves of 32 rows. With four, two work-groups share a CU (D =
-// 128) and overlap by chance. With eight, the two waves of a SIMD (w and w + 4) go
+// Whole tiles: kWaves waves of 32 rows. With four (D = 128, shorter sequences), three
+// work-groups share a CU and overlap one's start and end with another's products; the
+// keys go 32 at a time, for which the registers suffice (two work-groups and 64 keys:
+// 128 sequences of 128 tokens 97 us against 85). With eight, the two waves of a SIMD (w and w + 4) go
 // through the two parts of a step in opposite order, a barrier after each part:
 // while one runs its score products the other forms weights.
 template <typename T, int D, int kWaves, Keys kKeys>
-__global__ __launch_bounds__(64 * kWaves, 2) void attn_tile_kernel(TileArgs a) {
-  constexpr int kBM = 32 * kWaves, kBN = 64;
+__global__ __launch_bounds__(64 * kWaves, kWaves == 4 ? 3 : 2) void attn_tile_kernel(TileArgs a) {
+  constexpr int kBM = 32 * kWaves, kBN = kWaves == 4 ? 32 : 64;
   // four arrays of their own, so that a tile in flight is known to be another
   // than the ones being read
   __shared__ __attribute__((aligned(16))) T k_a[kBN * D], v_a[kBN * D], k_b[kBN * D], v_b[kBN * D];

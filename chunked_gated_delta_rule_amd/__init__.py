@@ -480,17 +480,18 @@ def gdn_attn_workspace_size(cfg: gdn_attn_config) -> int:
 # A small attention call is bound by the host, so its argument checks are kept to
 # one short function per tensor, with the message put together only on failure.
 
-# torch's raw handle of the current stream of a device (a Stream object for the
-# same question costs more than a kernel launch).
+# torch's raw handle of the current stream of a device, and its current device (the
+# Stream object for the former costs as much as a kernel launch).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _dev(*tensors):
     """Index of the device of the first tensor (None: raw pointers only; below 0: a
     host tensor, which the call refuses after the other checks)."""
     for x in tensors:
-        if isinstance(x, torch.Tensor):
+        if x.__class__ is not int and x is not None:
             return x.get_device()
     return None
 
@@ -501,7 +502,7 @@ def _at(x, name, dtype, elems, dev, last=None):
     if x is None or x.__class__ is int:
         return x
     if x.dtype is dtype and x.get_device() == dev and x.is_contiguous() and \
-            x.numel() >= elems and (last is None or x.shape[-1] == last):
+            x.numel() >= elems and (last is None or x.size(-1) == last):
         return x.data_ptr()
     _need(x, name, elems, dtype, last)
     if x.get_device() != dev:
@@ -516,21 +517,27 @@ def _rows_at(x, name, dtype, tokens, heads, d, dev):
     heads * d]), each token's values in one piece, any distance apart."""
     if x is None or x.__class__ is int:
         return x, 0
-    shape, stride = x.shape, x.stride()
-    if x.dtype is not dtype:
-        raise ValueError(f"{name}: dtype {x.dtype}, {dtype} expected")
-    if len(shape) == 3:
-        ok = shape[1] == heads and shape[2] == d and stride[2] == 1 and \
-            (stride[1] == d or heads == 1)
+    shape = x.shape
+    three = len(shape) == 3
+    if three:
+        ok = shape[1] == heads and shape[2] == d
     else:
-        ok = len(shape) == 2 and shape[1] == heads * d and stride[1] == 1
-    many = shape[0] > 1  # a single row's stride says nothing: torch may report any value
-    if not ok or shape[0] < tokens or (many and stride[0] < heads * d):
-        raise ValueError(f"{name}: {tuple(shape)} with strides {stride}, [{tokens}, {heads}, {d}] "
-                         f"with every token's row in one piece expected")
-    if x.get_device() != dev:
+        ok = len(shape) == 2 and shape[1] == heads * d
+    if ok and x.dtype is dtype and shape[0] >= tokens and x.get_device() == dev:
+        if x.is_contiguous():
+            return x.data_ptr(), 0
+        stride = x.stride()
+        if stride[-1] == 1 and (not three or heads == 1 or stride[1] == d):
+            if shape[0] == 1:  # a single row's stride says nothing: torch may report any value
+                return x.data_ptr(), 0
+            if stride[0] >= heads * d:  # (less: rows that overlap, or one row broadcast)
+                return x.data_ptr(), stride[0]
+    if x.dtype != dtype:
+        raise ValueError(f"{name}: dtype {x.dtype}, {dtype} expected")
+    if ok and shape[0] >= tokens and x.get_device() != dev:
         raise ValueError(f"{name}: on {x.device}, device {dev} expected")
-    return x.data_ptr(), stride[0] if many else 0
+    raise ValueError(f"{name}: {tuple(shape)} with strides {x.stride()}, [{tokens}, {heads}, {d}] "
+                     f"with every token's row in one piece expected")
 
 
 def _ws_at(x, ws_bytes, dev):
@@ -544,23 +551,19 @@ def _ws_at(x, ws_bytes, dev):
     return x.data_ptr(), have if ws_bytes is None else int(ws_bytes)
 
 
-def _attn_call(where, dev, stream, *args):
+def _attn_call(where, dev, stream, args):
     """The call on its tensors' device, on that device's current stream unless
     `stream` is given."""
     fn = getattr(_lib or load_library(), where)
-    if stream is not None:
+    if stream is not None or dev is None:
         stream = _stream(stream)
-    elif dev is None:
-        stream = _stream(None)
-    elif dev >= 0:
-        stream = _raw_stream(dev)
     if dev is not None and dev < 0:
         raise ValueError("device tensor expected")
-    if dev is None or dev == torch.cuda.current_device():
-        st = fn(*args, stream)
+    if dev is None or dev == _current_device():
+        st = fn(*args, _raw_stream(dev) if stream is None else stream)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, stream)
+            st = fn(*args, _raw_stream(dev) if stream is None else stream)
     if st:
         raise GDNError(st, where)
 
@@ -568,48 +571,48 @@ def _attn_call(where, dev, stream, *args):
 def _front_args(cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens, t, dev):
     d = cfg.d
     p, row = _rows_at(qkv, "qkv", t, cfg.t_max, cfg.h + 2 * cfg.hkv, d, dev)
-    f32, i32 = torch.float32, torch.int32
+    f32, i32, n = torch.float32, torch.int32, cfg.n_max
     return (ctypes.byref(cfg), p, row, _at(q_w, "q_w", f32, d, dev), _at(k_w, "k_w", f32, d, dev),
             _at(inv_freq, "inv_freq", f32, cfg.rot_dim // 2, dev),
-            _at(cu_seqlens, "cu_seqlens", i32, cfg.n_max + 1, dev),
-            _at(kv_lens, "kv_lens", i32, cfg.n_max, dev))
+            _at(cu_seqlens, "cu_seqlens", i32, n + 1, dev), _at(kv_lens, "kv_lens", i32, n, dev))
 
 
 def gdn_qk_norm_rope(cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens, q, k, stream=None):
     """RMS norm of every query and key head and rotation by the token's position.
     qkv [t_max, (h + 2 hkv) d] may have any row stride (a multiple of 8)."""
-    dev, t, n = _dev(qkv, q, k), _GDN_DTYPE.get(cfg.dtype), cfg.t_max * cfg.d
+    dev, t, d = _dev(qkv, q, k), _GDN_DTYPE.get(cfg.dtype), cfg.d
+    n = cfg.t_max * d
     _attn_call("gdn_qk_norm_rope", dev, stream,
-               *_front_args(cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens, t, dev),
-               _at(q, "q", t, n * cfg.h, dev, cfg.d), _at(k, "k", t, n * cfg.hkv, dev, cfg.d))
+               _front_args(cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens, t, dev) +
+               (_at(q, "q", t, n * cfg.h, dev, d), _at(k, "k", t, n * cfg.hkv, dev, d)))
 
 
 def gdn_kv_append(cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens, block_table, q, k, k_pages,
                   v_pages, stream=None):
     """gdn_qk_norm_rope that also writes k and v into the pages of the cache; q and
     k may be None."""
-    dev, t, d, cols = _dev(qkv, k_pages), _GDN_DTYPE.get(cfg.dtype), cfg.d, cfg.max_pages
-    n, pool = cfg.t_max * d, cfg.n_pages * cfg.hkv * cfg.page_size * d
+    dev, t, d, cols, hkv = _dev(qkv, k_pages), _GDN_DTYPE.get(cfg.dtype), cfg.d, cfg.max_pages, cfg.hkv
+    n, pool = cfg.t_max * d, cfg.n_pages * hkv * cfg.page_size * d
     _attn_call("gdn_kv_append", dev, stream,
-               *_front_args(cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens, t, dev),
-               _at(block_table, "block_table", torch.int32, cfg.n_max * cols, dev, cols),
-               _at(q, "q", t, n * cfg.h, dev, d), _at(k, "k", t, n * cfg.hkv, dev, d),
-               _at(k_pages, "k_pages", t, pool, dev, d), _at(v_pages, "v_pages", t, pool, dev, d))
+               _front_args(cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens, t, dev) +
+               (_at(block_table, "block_table", torch.int32, cfg.n_max * cols, dev, cols),
+                _at(q, "q", t, n * cfg.h, dev, d), _at(k, "k", t, n * hkv, dev, d),
+                _at(k_pages, "k_pages", t, pool, dev, d), _at(v_pages, "v_pages", t, pool, dev, d)))
 
 
 def gdn_attn_prefill(cfg, q, k, v, cu_q, cu_k, o, workspace, ws_bytes=None, stream=None):
     """Causal attention over packed prompts; q, k, v [tokens, heads, d] may have any
     row stride (a multiple of 8); cu_k None = cu_q."""
-    dev, t = _dev(q, k, v, o), _GDN_DTYPE.get(cfg.dtype)
+    dev, t, i32 = _dev(q, k, v, o), _GDN_DTYPE.get(cfg.dtype), torch.int32
     d, h, hkv, tq, n = cfg.d, cfg.h, cfg.hkv, cfg.t_max, cfg.n_max + 1
     tk = cfg.tk_max or tq
     q, q_row = _rows_at(q, "q", t, tq, h, d, dev)
     k, k_row = _rows_at(k, "k", t, tk, hkv, d, dev)
     v, v_row = _rows_at(v, "v", t, tk, hkv, d, dev)
     ws, ws_bytes = _ws_at(workspace, ws_bytes, dev)
-    _attn_call("gdn_attn_prefill", dev, stream, ctypes.byref(cfg), q, q_row, k, k_row, v, v_row,
-               _at(cu_q, "cu_q", torch.int32, n, dev), _at(cu_k, "cu_k", torch.int32, n, dev),
-               _at(o, "o", t, tq * h * d, dev, d), ws, ws_bytes)
+    _attn_call("gdn_attn_prefill", dev, stream,
+               (ctypes.byref(cfg), q, q_row, k, k_row, v, v_row, _at(cu_q, "cu_q", i32, n, dev),
+                _at(cu_k, "cu_k", i32, n, dev), _at(o, "o", t, tq * h * d, dev, d), ws, ws_bytes))
 
 
 def gdn_attn_paged(cfg, q, k_pages, v_pages, cu_seqlens, kv_lens, block_table, shared_len, o,
@@ -621,12 +624,14 @@ def gdn_attn_paged(cfg, q, k_pages, v_pages, cu_seqlens, kv_lens, block_table, s
     pool = cfg.n_pages * cfg.hkv * cfg.page_size * d
     q, q_row = _rows_at(q, "q", t, tq, h, d, dev)
     ws, ws_bytes = _ws_at(workspace, ws_bytes, dev)
-    _attn_call("gdn_attn_paged", dev, stream, ctypes.byref(cfg), q, q_row,
-               _at(k_pages, "k_pages", t, pool, dev, d), _at(v_pages, "v_pages", t, pool, dev, d),
-               _at(cu_seqlens, "cu_seqlens", i32, n + 1, dev), _at(kv_lens, "kv_lens", i32, n, dev),
-               _at(block_table, "block_table", i32, n * cols, dev, cols),
-               _at(shared_len, "shared_len", i32, 1, dev), _at(o, "o", t, tq * h * d, dev, d), ws,
-               ws_bytes)
+    _attn_call("gdn_attn_paged", dev, stream,
+               (ctypes.byref(cfg), q, q_row, _at(k_pages, "k_pages", t, pool, dev, d),
+                _at(v_pages, "v_pages", t, pool, dev, d),
+                _at(cu_seqlens, "cu_seqlens", i32, n + 1, dev),
+                _at(kv_lens, "kv_lens", i32, n, dev),
+                _at(block_table, "block_table", i32, n * cols, dev, cols),
+                _at(shared_len, "shared_len", i32, 1, dev), _at(o, "o", t, tq * h * d, dev, d), ws,
+                ws_bytes))
 
 
 def rope_inv_freq(rot_dim, base=10000.0, factor=1.0, original_len=None, low_turns=1.0,

@@ -14,7 +14,7 @@ namespace {
 
 constexpr int kMaxHeads = 4096;
 constexpr size_t kAlign = 256;
-constexpr int kPlanBytes = 64;
+constexpr int kPlanBytes = 16;  // per row
 constexpr double kLog2e = 1.4426950408889634;
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
@@ -60,7 +60,7 @@ struct PrefillLayout {
   size_t part_o, part_ml, total;
 };
 struct PagedLayout {
-  size_t plan, part_o, part_ml, done_o, done_ml, pre_o, pre_ml, total;
+  size_t prefix, plan, part_o, part_ml, done_o, done_ml, pre_o, pre_ml, total;
 };
 
 struct Taker {
@@ -92,7 +92,8 @@ PagedLayout paged_layout(const gdn_attn_config *cfg) {
                             : 0;
   Taker take;
   PagedLayout l;
-  l.plan = take(kPlanBytes + (static_cast<size_t>(cfg->n_max) + 1) * 8);
+  l.prefix = take(sizeof(int32_t));
+  l.plan = take(static_cast<size_t>(cfg->t_max) * cfg->h * kPlanBytes);
   l.part_o = take(slots * d * 4);
   l.part_ml = take(slots * 2 * 4);
   l.done_o = take(done * d * 4);
@@ -313,7 +314,8 @@ gdn_status gdn_attn_paged(const gdn_attn_config *cfg, const void *q, int64_t q_r
   a.hkv = cfg->hkv;
   a.scale_log2 = scale_log2(cfg);
   a.grid = gdn::stream_grid(cfg);
-  a.plan = reinterpret_cast<int32_t *>(at + l.plan);
+  a.prefix = reinterpret_cast<int32_t *>(at + l.prefix);
+  a.plan = at + l.plan;
   a.part_o = reinterpret_cast<float *>(at + l.part_o);
   a.part_ml = reinterpret_cast<float *>(at + l.part_ml);
   a.done_o = reinterpret_cast<float *>(at + l.done_o);

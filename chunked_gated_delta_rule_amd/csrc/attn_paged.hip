@@ -32,9 +32,12 @@ namespace {
 
 constexpr int kUnit = 128;  // keys per unit: 32 per wave
 
-// workspace plan: prefix, units per key head, units per work-group; then the units
-// before each sequence (int64 [n_max + 1])
-constexpr int kPlanInts = 16;
+// What the join is told of a row (token and query head): the first work-group with a
+// part of it, how many there are (0: it sees no key; 1: finished by one), and its
+// number in the item's rows. Written by the work-group in whose run the item begins.
+struct RowPlan {
+  int first, parts, in_item, unused;
+};
 
 // Rows (tokens times query heads) from which the join takes one wave per row and not
 // four.
@@ -103,17 +106,15 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
   per_head = uniform(per_head);
   const int64_t total = per_head * a.hkv;
   const int64_t per_wg = max((total + a.grid - 1) / a.grid, (int64_t)1);
+  RowPlan *const plan = reinterpret_cast<RowPlan *>(a.plan);
   if (wg == 0) {
-    int64_t *starts = reinterpret_cast<int64_t *>(a.plan + kPlanInts);
-    int64_t at = before;
+    if (tid == 0) a.prefix[0] = prefix;
+    // rows of sequences without keys belong to no item
     for (int s = s0; s < s1; ++s) {
-      starts[s] = at;
-      at += units_in(s);
-    }
-    if (tid == 0) {
-      a.plan[0] = prefix;
-      reinterpret_cast<int64_t *>(a.plan)[1] = per_head;
-      reinterpret_cast<int64_t *>(a.plan)[2] = per_wg;
+      const Seq q = seq_at(pg, s);
+      if (q.kv <= prefix)
+        for (int64_t i = 0; i < (int64_t)q.n * a.h; ++i)
+          plan[(int64_t)q.bos * a.h + i] = RowPlan{0, 0, 0, 0};
     }
   }
   const int64_t u0 = (int64_t)wg * per_wg, u1 = min(u0 + per_wg, total);
@@ -165,6 +166,13 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
       *reinterpret_cast<u32x4 *>(&qs[row][8 * ch]) = *reinterpret_cast<const u32x4 *>(
           static_cast<const T *>(a.q) + (int64_t)(q.bos + tok) * a.q_row +
           ((int64_t)head * G + (r - (int64_t)tok * G)) * D + 8 * ch);
+    }
+    if (un == 0 && tid < kRows && r0 + tid < rows) {
+      const int64_t r = r0 + tid;
+      const int tok = (int)(r / G);
+      const int parts = (int)((u + nu - 1) / per_wg) - wg + 1;
+      plan[(int64_t)(q.bos + tok) * a.h + (int64_t)head * G + (r - (int64_t)tok * G)] =
+          RowPlan{wg, parts, tid, 0};
     }
     int lim[kRT];  // the last key that this lane's row of each tile sees
 #pragma unroll
@@ -408,31 +416,16 @@ __global__ __launch_bounds__(256) void attn_stream_join_kernel(StreamArgs a) {
   const int64_t row = (int64_t)flat_block() * (4 / kWaves) + (kWaves == 1 ? w : 0);
   const int t = (int)(row / a.h), head = (int)(row % a.h);
   const int sub = kWaves == 1 ? 0 : w;  // this wave among the row's
-  const PagedBatch &pg = a.pg;
-  if (t >= cu_at(pg.cu, pg.n_max, pg.t_max)) return;
-  int kv;
-  const Packed q = seq_of_row(
-      pg.cu, pg.n_max, pg.t_max, t, lane, [&](int i) { return kv_of(pg, i); }, kv);
-  if (t < q.b || t >= q.b + q.n) return;  // an unsorted cu_seqlens: a row of no sequence
-  const int G = a.h / a.hkv;
-  const int prefix = a.plan[0];
-  const int64_t per_head = reinterpret_cast<const int64_t *>(a.plan)[1];
-  const int64_t per_wg = reinterpret_cast<const int64_t *>(a.plan)[2];
-  const int64_t start = reinterpret_cast<const int64_t *>(a.plan + kPlanInts)[q.s];
+  if (t >= a.pg.t_max) return;
+  const RowPlan plan = reinterpret_cast<const RowPlan *>(a.plan)[row];
+  const int prefix = a.prefix[0];
+  if (t >= cu_at(a.pg.cu, a.pg.n_max, a.pg.t_max)) return;
+  // (an unsorted cu_seqlens leaves rows without a plan: whatever it holds is kept in range)
+  const int w0 = min(max(uniform(plan.first), 0), a.grid - 1);
+  const int parts = min(max(uniform(plan.parts), 0), a.grid - w0);
+  const int in_item = uniform(plan.in_item) & (kRows - 1);
   const int lead = prefix > 0 ? a.pre_splits : 0;  // the prefix's parts come first
-
-  // the row's item: units [lo, hi) in the work-groups w0 .., and its row of the tile
-  int64_t lo = 0, w0 = 0;
-  int parts = 0, in_tile = 0;
-  if (kv > prefix) {
-    const int64_t r = (int64_t)(t - q.b) * G + head % G;
-    const int nu = units_of(kv - prefix);
-    lo = head / G * per_head + start + r / kRows * nu;
-    in_tile = (int)(r % kRows);
-    w0 = lo / per_wg;
-    parts = (int)((lo + nu - 1) / per_wg - w0 + 1);
-  }
-  if (prefix == 0 && parts == 1) return;  // the main kernel wrote it
+  if (lead == 0 && parts == 1) return;  // the main kernel wrote it
   const int64_t pre_item =
       (int64_t)(a.pre_slots - 1 - t / a.pre_tt) * (a.h / a.pre_share) + head / a.pre_share;
   const int pre_row = t % a.pre_tt * a.pre_share + head % a.pre_share;
@@ -446,8 +439,8 @@ __global__ __launch_bounds__(256) void attn_stream_join_kernel(StreamArgs a) {
       po = a.done_o + row * D;
       pm = a.done_ml + row * 2;
     } else {
-      const int64_t wgi = w0 + i - lead;
-      const int64_t at = (wgi * 2 + (lo >= wgi * per_wg ? 1 : 0)) * kRows + in_tile;
+      // place 1 of the work-group in which the item begins, place 0 of the others
+      const int64_t at = ((int64_t)(w0 + i - lead) * 2 + (i == lead ? 1 : 0)) * kRows + in_item;
       po = a.part_o + at * D;
       pm = a.part_ml + at * 2;
     }

@@ -43,7 +43,7 @@ gdn_status check_config(const gdn_attn_config *cfg) {
   if (cfg->t_max > GDN_T_MAX_LIMIT || cfg->tk_max > GDN_T_MAX_LIMIT ||
       cfg->n_max > GDN_N_MAX_LIMIT || cfg->h > kMaxHeads ||
       static_cast<int64_t>(cfg->max_pages) * cfg->page_size > (1 << 30) ||
-      static_cast<int64_t>(cfg->t_max) * cfg->h > 0x7fffffffLL)
+      static_cast<int64_t>(cfg->t_max) * cfg->h > 0x7fff0000LL)
     return GDN_ERR_CAPACITY;
   return GDN_OK;
 }

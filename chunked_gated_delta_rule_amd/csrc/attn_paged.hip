@@ -43,11 +43,21 @@ struct RowPlan {
 // four.
 constexpr int kManyRows = 4096;
 
+// a / b for a >= 0, b > 0: mostly both fit 32 bits.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+__device__ __forceinline__ int64_t lane_of(int64_t x, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane((int)x, lane);
+  return (int64_t)__builtin_amdgcn_readlane((int)(x >> 32), lane) << 32 | lo;
+}
+
 __device__ __forceinline__ int units_of(int keys) { return (keys + kUnit - 1) / kUnit; }
 
 template <int kRT>
-__device__ __forceinline__ int row_tiles(int64_t rows) {
-  return (int)((rows + 16 * kRT - 1) / (16 * kRT));
+__device__ __forceinline__ int row_tiles(int rows) {
+  return (int)(((int64_t)rows + 16 * kRT - 1) / (16 * kRT));
 }
 
 // A wave's 32 keys of a unit: K fragments of two tiles of 16, and rows of V (keys 4 g
@@ -80,14 +90,16 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
   PagedBatch pg = a.pg;
   int G = a.h / a.hkv;
   const int prefix = shared_prefix<256>(pg, tid, scan32).len;
-  const int per = (pg.n_max + 255) / 256;
-  const int s0 = min(tid * per, pg.n_max), s1 = min(s0 + per, pg.n_max);
   auto units_in = [&](int s) __attribute__((always_inline)) -> int64_t {
     const Seq q = seq_at(pg, s);
-    return q.n > 0 && q.kv > prefix
-               ? (int64_t)row_tiles<kRT>((int64_t)q.n * G) * units_of(q.kv - prefix)
-               : 0;
+    return q.n > 0 && q.kv > prefix ? (int64_t)row_tiles<kRT>(q.n * G) * units_of(q.kv - prefix) : 0;
   };
+  // up to 64 sequences: one per lane, every wave for itself; more: a stretch of them per
+  // thread
+  const bool few = pg.n_max <= 64;
+  const int per = (pg.n_max + 255) / 256;
+  const int s0 = min(few ? lane : tid * per, pg.n_max);
+  const int s1 = min(s0 + (few ? 1 : per), pg.n_max);
   int64_t mine = 0;
   for (int s = s0; s < s1; ++s) mine += units_in(s);
   int64_t incl = mine;
@@ -96,18 +108,23 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
     const int64_t y = __shfl_up(incl, off, 64);
     if (lane >= off) incl += y;
   }
-  if (lane == 63) scan64[w] = incl;
-  __syncthreads();
-  int64_t before = incl - mine, per_head = 0;
-  for (int i = 0; i < 4; ++i) {
-    if (i < w) before += scan64[i];
-    per_head += scan64[i];
+  int64_t before = incl - mine, per_head;
+  if (few) {
+    per_head = lane_of(incl, 63);
+  } else {
+    if (lane == 63) scan64[w] = incl;
+    __syncthreads();
+    per_head = 0;
+    for (int i = 0; i < 4; ++i) {
+      if (i < w) before += scan64[i];
+      per_head += scan64[i];
+    }
+    per_head = uniform(per_head);
   }
-  per_head = uniform(per_head);
   const int64_t total = per_head * a.hkv;
-  const int64_t per_wg = max((total + a.grid - 1) / a.grid, (int64_t)1);
+  const int64_t per_wg = max(quotient(total + a.grid - 1, a.grid), (int64_t)1);
   RowPlan *const plan = reinterpret_cast<RowPlan *>(a.plan);
-  if (wg == 0) {
+  if (wg == 0 && (!few || w == 0)) {
     if (tid == 0) a.prefix[0] = prefix;
     // rows of sequences without keys belong to no item
     for (int s = s0; s < s1; ++s) {
@@ -120,22 +137,30 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
   const int64_t u0 = (int64_t)wg * per_wg, u1 = min(u0 + per_wg, total);
   if (u0 >= u1) return;
 
-  // ---- the item of u0: the thread whose sequences hold it names it
-  int kh = (int)(u0 / per_head);
+  // ---- the item of u0: the lane or thread whose sequences hold it names it
+  int kh = (int)quotient(u0, per_head);
   int64_t in_head = u0 - kh * per_head;
-  if (in_head >= before && in_head < before + mine) {
-    int64_t at = before;
-    int i = s0;
-    for (int64_t n = units_in(i); in_head >= at + n; n = units_in(i)) {
-      at += n;
-      ++i;
+  const bool here = in_head >= before && in_head < before + mine;
+  int s;
+  int64_t in_seq;
+  if (few) {
+    s = __ffsll((unsigned long long)__ballot(here)) - 1;
+    in_seq = in_head - lane_of(before, s);
+  } else {
+    if (here) {
+      int64_t at = before;
+      int i = s0;
+      for (int64_t n = units_in(i); in_head >= at + n; n = units_in(i)) {
+        at += n;
+        ++i;
+      }
+      found = i;
+      scan64[4] = in_head - at;
     }
-    found = i;
-    scan64[4] = in_head - at;
+    __syncthreads();
+    s = uniform(found);
+    in_seq = uniform(scan64[4]);
   }
-  __syncthreads();
-  int s = uniform(found);
-  int64_t in_seq = uniform(scan64[4]);
   // From here on everything but the lanes' data is one value per wave. The compiler
   // would merge what the branch above derived from these into lane values.
   G = uniform(G);
@@ -154,46 +179,10 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
     const Seq q{uniform(at.bos), uniform(at.n), uniform(at.kv)};
     const int nu = units_of(q.kv - prefix);
     // (one value per wave each, which the compiler does not see by itself)
-    const int rt = uniform((int)(in_seq / nu)), un = uniform((int)(in_seq - (int64_t)rt * nu));
+    const int rt = uniform((int)quotient(in_seq, nu)), un = uniform((int)(in_seq - (int64_t)rt * nu));
     const int run = uniform((int)min((int64_t)(nu - un), u1 - u));
-    const int64_t rows = (int64_t)q.n * G, r0 = (int64_t)rt * kRows;
+    const int rows = q.n * G, r0 = rt * kRows;  // at most t_max * h, which fits
 
-    __syncthreads();  // the item before may still be read
-    for (int i = tid; i < kRows * (D / 8); i += 256) {
-      const int row = i / (D / 8), ch = i % (D / 8);
-      const int64_t r = min(r0 + row, rows - 1);
-      const int tok = (int)(r / G);
-      *reinterpret_cast<u32x4 *>(&qs[row][8 * ch]) = *reinterpret_cast<const u32x4 *>(
-          static_cast<const T *>(a.q) + (int64_t)(q.bos + tok) * a.q_row +
-          ((int64_t)head * G + (r - (int64_t)tok * G)) * D + 8 * ch);
-    }
-    if (un == 0 && tid < kRows && r0 + tid < rows) {
-      const int64_t r = r0 + tid;
-      const int tok = (int)(r / G);
-      const int parts = (int)((u + nu - 1) / per_wg) - wg + 1;
-      plan[(int64_t)(q.bos + tok) * a.h + (int64_t)head * G + (r - (int64_t)tok * G)] =
-          RowPlan{wg, parts, tid, 0};
-    }
-    int lim[kRT];  // the last key that this lane's row of each tile sees
-#pragma unroll
-    for (int t = 0; t < kRT; ++t) {
-      const int64_t r = r0 + 16 * t + c;
-      lim[t] = q.kv - q.n + (int)(min(r, rows - 1) / G);
-    }
-    const int all_see = q.kv - q.n + (int)(r0 / G);  // every row sees these
-    __syncthreads();
-
-    f32x4 o[kRT][kDC][8];
-    float m[kRT], l[kRT];
-#pragma unroll
-    for (int t = 0; t < kRT; ++t) {
-      m[t] = kNegInf;
-      l[t] = 0.f;
-#pragma unroll
-      for (int b = 0; b < kDC; ++b)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[t][b][j] = zero4();
-    }
     // this wave's 32 keys of unit i of the run, as two tiles of 16, each in one page
     const int first = prefix + un * kUnit + 32 * w;
     const int mine_n = min(run, units_of(q.kv - first));  // units in which it has keys
@@ -236,6 +225,38 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
       load_k(x, 0);
       load_v(x, 0);
       if (mine_n > 1) look(1);
+    }
+    // the rows, while the first keys come
+    __syncthreads();  // the item before may still be read
+    for (int i = tid; i < kRows * (D / 8); i += 256) {
+      const int row = i / (D / 8), ch = i % (D / 8);
+      const int r = min(r0 + row, rows - 1), tok = r / G;
+      *reinterpret_cast<u32x4 *>(&qs[row][8 * ch]) = *reinterpret_cast<const u32x4 *>(
+          static_cast<const T *>(a.q) + (int64_t)(q.bos + tok) * a.q_row +
+          (head * G + (r - tok * G)) * D + 8 * ch);
+    }
+    if (un == 0 && tid < kRows && r0 + tid < rows) {
+      const int r = r0 + tid, tok = r / G;
+      const int64_t over = u + nu - u1;  // units of the item past this run
+      const int parts = over > 0 ? (int)quotient(over + per_wg - 1, per_wg) + 1 : 1;
+      plan[(int64_t)(q.bos + tok) * a.h + head * G + (r - tok * G)] = RowPlan{wg, parts, tid, 0};
+    }
+    int lim[kRT];  // the last key that this lane's row of each tile sees
+#pragma unroll
+    for (int t = 0; t < kRT; ++t) lim[t] = q.kv - q.n + min(r0 + 16 * t + c, rows - 1) / G;
+    const int all_see = q.kv - q.n + r0 / G;  // every row sees these
+    __syncthreads();
+
+    f32x4 o[kRT][kDC][8];
+    float m[kRT], l[kRT];
+#pragma unroll
+    for (int t = 0; t < kRT; ++t) {
+      m[t] = kNegInf;
+      l[t] = 0.f;
+#pragma unroll
+      for (int b = 0; b < kDC; ++b)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[t][b][j] = zero4();
     }
     // the next keys come while these are weighed, the next values while their scores
     // are formed, in the registers that are free by then
@@ -343,7 +364,7 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
       __syncthreads();
       // sixteen threads per row, 4 dims each at a time
       const int row = tid >> 4, q4 = 4 * (tid & 15);
-      const int64_t r = r0 + 16 * t + row;
+      const int r = r0 + 16 * t + row;
       if (r < rows) {
         float mm = kNegInf, ll = 0.f;
 #pragma unroll
@@ -352,8 +373,8 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
         for (int i = 0; i < 4; ++i)
           ll += wm[i][16 * t + row] == kNegInf ? 0.f
                                                : wl[i][16 * t + row] * fast_exp2(wm[i][16 * t + row] - mm);
-        const int tok = (int)(r / G);
-        const int64_t orow = (int64_t)(q.bos + tok) * a.h + (int64_t)head * G + (r - (int64_t)tok * G);
+        const int tok = r / G;
+        const int64_t orow = (int64_t)(q.bos + tok) * a.h + head * G + (r - tok * G);
         const float inv = ll == 0.f ? 0.f : 1.f / ll;
         float *po, *pm;
         if (whole) {

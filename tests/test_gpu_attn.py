@@ -63,6 +63,49 @@ def test_norm_rope(t, d, rot, inter):
 
 
 @pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("T,d,rot,inter", [(5000, 128, 128, False), (10001, 128, 34, False),
+                                           (9000, 256, 64, True)])
+def test_norm_rope_and_append_of_many_tokens(t, T, d, rot, inter):
+    """Several tokens per work-group, sequences that begin and end inside one."""
+    h, hkv, page = 2, 1, 32
+    lens = [7, 1, 0, 2, 1500, 3, 1]
+    lens.append(T - sum(lens))
+    n = len(lens)
+    kv = [x + 11 * i for i, x in enumerate(lens)]
+    cu = cu_of(lens)
+    qkv = normal(30, T, 4 * d, dtype=t).to(DEV)
+    w = normal(31, d, dtype=torch.float32).to(DEV)
+    f = gdn.rope_inv_freq(rot).to(DEV)
+    need = [-(-x // page) for x in kv]
+    cols = max(need)
+    table = np.zeros((n, cols), np.int32)
+    at = 0
+    for i, u in enumerate(need):
+        table[i, :u] = range(at, at + u)
+        at += u
+    kp = torch.full((at, hkv, page, d), MARK, dtype=t, device=DEV)
+    vp = kp.clone()
+    say(f"norm_rope / append {t} T={T} d={d} rot={rot}")
+    q, k = gdn.append_paged_kv(qkv, h, on(cu), on(np.array(kv, np.int32)), on(table), kp, vp, w,
+                               None, f, interleaved=inter, output_k=True)
+    x = f64(qkv).reshape(T, 4, d)
+    pos = attention.positions(cu, kv)
+    for got, part, wt in ((q, x[:, :h], f64(w)), (k, x[:, h:h + 1], None)):
+        want, mag = attention.norm_rope(part, wt, pos, f64(f), 1e-6, inter)
+        check_norm_rope(got, want, mag, t)
+    q2, k2 = gdn.qk_norm_rope(qkv, h, hkv, on(cu), w, None, f, on(np.array(kv, np.int32)),
+                              interleaved=inter)
+    assert torch.equal(q, q2) and torch.equal(k, k2)
+    v = qkv.view(T, 4, d)[:, 3:]
+    for i in range(n):
+        for pool, rows in ((kp, k), (vp, v)):
+            have = pool[table[i, 0]:table[i, 0] + need[i]].transpose(1, 2).reshape(-1, hkv, d)
+            old = kv[i] - lens[i]
+            assert torch.equal(have[old:kv[i]], rows[cu[i]:cu[i + 1]])
+            assert (have[:old] == MARK).all() and (have[kv[i]:] == MARK).all()
+
+
+@pytest.mark.parametrize("t", TYPES)
 @pytest.mark.parametrize("qn,kn", [(True, False), (False, True), (False, False)])
 def test_norm_rope_without_norms_and_from_wider_rows(t, qn, kn):
     """Norms are optional each; positions count from 0 without kv_lens; the packed
@@ -171,6 +214,9 @@ PREFILL = [
     ([40], [3000], 8, 2, 128),                # few rows and many keys: split
     ([3], [2500], 4, 1, 256),
     ([12, 7], [0, 2100], 6, 2, 128),
+    ([140], [140], 17, 1, 128),               # a prime number of heads on one key head
+    ([50, 33], [90, 40], 24, 1, 256),
+    ([30], [40], 64, 2, 128),
 ]
 
 
@@ -289,6 +335,10 @@ PAGED = [
     ([130, 0, 20], [130, 77, 1500], 8, 2, 256, 64, 0),
     ([90], [60], 8, 1, 128, 32, 0),
     ([300, 280], [400, 333], 2, 1, 128, 128, 64),
+    ([1] * 100, [200 + i for i in range(100)], 4, 2, 128, 16, 150),   # more sequences than lanes
+    ([1] * 280, [1 + 3 * i for i in range(280)], 16, 4, 128, 32, 0),  # a wave per joined row
+    ([2] * 90, [500 - i for i in range(90)], 24, 2, 256, 16, 300),
+    ([1, 2], [300, 40], 17, 1, 128, 16, 0),
 ]
 
 
@@ -331,6 +381,70 @@ def test_paged_of_one_long_context(t):
                             on(np.array([n], np.int32)), on(c.table))
     k, v = c.rows(0)
     check_attention(o, f64(q), k, v, d ** -0.5, t)
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("T,past,d", [(2100, 333, 128), (700, 900, 256)])
+def test_paged_of_a_long_prompt_at_sampled_rows(t, T, past, d):
+    h, hkv, page = 2, 1, 64
+    c = Cache([T + past], hkv, d, page, t, 33)
+    q = normal(1, T, h, d, dtype=t, scale=2.0)
+    o = gdn.paged_attention(q.to(DEV), c.k.to(DEV), c.v.to(DEV), on(cu_of([T])),
+                            on(np.array([T + past], np.int32)), on(c.table))
+    k, v = c.rows(0)
+    assert o.isfinite().all()
+    for r in [*range(0, T, 131), T - 1]:
+        check_attention(o[r:r + 1], f64(q[r:r + 1]), k[:past + r + 1], v[:past + r + 1], d ** -0.5, t)
+
+
+def test_both_capacity_limits_with_sequences_at_the_end():
+    """t_max = 2^24 rows and n_max = 16384 sequences, the checked ones the last two
+    (byte offsets far past 2^32): front, prefill and paged attention."""
+    t, d, h, hkv = torch.bfloat16, 128, 1, 1
+    T, n, page = gdn.GDN_T_MAX_LIMIT, gdn.GDN_N_MAX_LIMIT, 256
+    tail = [70, 3]
+    cu = np.zeros(n + 1, np.int64)
+    cu[:n - 1] = np.linspace(0, T - sum(tail), n - 1).astype(np.int64)
+    cu[n - 1:] = T - tail[1], T
+    say(f"capacity limits: {T} rows, {n} sequences")
+    x = torch.zeros(T, 3 * d, dtype=t, device=DEV)
+    x[T - sum(tail):] = normal(1, sum(tail), 3 * d, dtype=t).to(DEV)
+    f, w = gdn.rope_inv_freq(d).to(DEV), torch.ones(d, device=DEV)
+    cud = on(cu.astype(np.int32))
+    q, k = gdn.qk_norm_rope(x, h, hkv, cud, w, w, f)
+    xs = f64(x[-sum(tail):]).reshape(-1, 3, d)
+    pos = np.concatenate([np.arange(70.0), np.arange(3.0)])
+    for got, part in ((q, xs[:, :1]), (k, xs[:, 1:2])):
+        want, mag = attention.norm_rope(part, np.ones(d), pos, f64(f), 1e-6)
+        check_norm_rope(got[-sum(tail):], want, mag, t)
+        assert not got[:T - sum(tail)].any()
+    v = x.view(T, 3, d)[:, 2:]
+    o = gdn.causal_attention(q, k, v, cud)
+    for a, b in ((T - 73, T - 3), (T - 3, T)):
+        check_attention(o[a:b], f64(q[a:b]), f64(k[a:b]), f64(v[a:b]), d ** -0.5, t)
+    assert not o[:T - sum(tail)].any()
+    del x, o, v
+    # the paged side: one row per sequence, all tables in a small pool
+    c = Cache([300, 41], hkv, d, page, t, 5)
+    table = np.zeros((n, c.cols), np.int32)
+    table[n - 2:] = c.table
+    kv = np.ones(n, np.int32)
+    kv[n - 2:] = c.lens
+    qq = torch.zeros(n, h, d, dtype=t, device=DEV)
+    qq[n - 2:] = normal(6, 2, h, d, dtype=t).to(DEV)
+    vp = c.v.clone()
+    vp[0, :, 0] = torch.where(vp[0, :, 0].isnan(), torch.zeros_like(vp[0, :, 0]), vp[0, :, 0])
+    kp = c.k.clone()
+    kp[0, :, 0] = torch.where(kp[0, :, 0].isnan(), torch.zeros_like(kp[0, :, 0]), kp[0, :, 0])
+    o = gdn.paged_attention(qq, kp.to(DEV), vp.to(DEV), on(np.arange(n + 1, dtype=np.int32)),
+                            on(kv), on(table))
+    assert torch.equal(o[:n - 2, 0], vp[0, 0, 0].to(DEV).expand(n - 2, d))
+    c.k, c.v = kp, vp
+    for i in range(2):
+        rk, rv = c.rows(i)
+        check_attention(o[n - 2 + i:n - 1 + i], f64(qq[n - 2 + i:n - 1 + i]), rk, rv, d ** -0.5, t)
+    del q, k
+    torch.cuda.empty_cache()
 
 
 def test_paged_indexes_that_name_nothing_stay_inside():

@@ -680,7 +680,8 @@ def qk_norm_rope(qkv, heads, kv_heads, cu_seqlens, q_weight=None, k_weight=None,
                            rot_interleaved=interleaved, rot_scale=rot_scale)
     q = torch.empty((T, heads, d), dtype=qkv.dtype, device=qkv.device)
     k = torch.empty((T, kv_heads, d), dtype=qkv.dtype, device=qkv.device)
-    gdn_qk_norm_rope(cfg, qkv, q_weight, k_weight, inv_freq, cu_seqlens, kv_lens, q, k)
+    if T:
+        gdn_qk_norm_rope(cfg, qkv, q_weight, k_weight, inv_freq, cu_seqlens, kv_lens, q, k)
     return q, k
 
 
@@ -709,8 +710,9 @@ def append_paged_kv(qkv, heads, cu_seqlens, kv_lens, block_table, k_pages, v_pag
                            n_pages=pages, max_pages=block_table.shape[1])
     q = torch.empty((T, heads, d), dtype=qkv.dtype, device=qkv.device)
     k = torch.empty((T, hkv, d), dtype=qkv.dtype, device=qkv.device) if output_k else None
-    gdn_kv_append(cfg, qkv, q_weight, k_weight, inv_freq, cu_seqlens, kv_lens, block_table, q, k,
-                  k_pages, v_pages)
+    if T:
+        gdn_kv_append(cfg, qkv, q_weight, k_weight, inv_freq, cu_seqlens, kv_lens, block_table, q,
+                      k, k_pages, v_pages)
     return (q, k) if output_k else q
 
 
@@ -719,6 +721,15 @@ def _attn_workspace(cfg, device, workspace):
         return workspace
     with torch.cuda.device(device):
         return torch.empty(gdn_attn_workspace_size(cfg), dtype=torch.uint8, device=device)
+
+
+def _scale(scale):
+    """A caller's score scale (None: the default, which a cfg holds as 0)."""
+    if scale is None:
+        return 0.0
+    if not ctypes.c_float(scale).value > 0.0:
+        raise ValueError(f"scale {scale}: a positive number expected")
+    return scale
 
 
 def causal_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, scale=None, workspace=None):
@@ -737,10 +748,12 @@ def causal_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, scale=None, workspa
     T, H, d = q.shape
     if cu_seqlens_k is None and k.shape[0] < T:
         raise ValueError(f"k, v: {k.shape[0]} rows, at least {T} expected")
-    cfg = make_attn_config(T, cu_seqlens.numel() - 1, H, k.shape[1], d, q.dtype, scale or 0.0,
+    cfg = make_attn_config(T, cu_seqlens.numel() - 1, H, k.shape[1], d, q.dtype, _scale(scale),
                            tk_max=k.shape[0])
-    workspace = _attn_workspace(cfg, q.device, workspace)
     o = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+    if T == 0:
+        return o
+    workspace = _attn_workspace(cfg, q.device, workspace)
     gdn_attn_prefill(cfg, q, k, v, cu_seqlens, cu_seqlens_k, o, workspace)
     return o
 
@@ -758,10 +771,12 @@ def paged_attention(q, k_pages, v_pages, cu_seqlens, kv_lens, block_table, share
         raise ValueError(f"q [T, heads, {d}] expected: {tuple(q.shape)}")
     cols = block_table.shape[1]
     cfg = make_attn_config(q.shape[0], cu_seqlens.numel() - 1, q.shape[1], hkv, d, q.dtype,
-                           scale or 0.0, page_size=size, n_pages=pages, max_pages=cols,
+                           _scale(scale), page_size=size, n_pages=pages, max_pages=cols,
                            shared_max=0 if shared_len is None else cols * size)
-    workspace = _attn_workspace(cfg, q.device, workspace)
     o = torch.empty((q.shape[0], q.shape[1], d), dtype=q.dtype, device=q.device)
+    if q.shape[0] == 0:
+        return o
+    workspace = _attn_workspace(cfg, q.device, workspace)
     gdn_attn_paged(cfg, q, k_pages, v_pages, cu_seqlens, kv_lens, block_table, shared_len, o,
                    workspace)
     return o

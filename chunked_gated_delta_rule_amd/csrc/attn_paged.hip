@@ -370,9 +370,10 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
 #pragma unroll
         for (int i = 0; i < 4; ++i) mm = fmaxf(mm, wm[i][16 * t + row]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          ll += wm[i][16 * t + row] == kNegInf ? 0.f
-                                               : wl[i][16 * t + row] * fast_exp2(wm[i][16 * t + row] - mm);
+        for (int i = 0; i < 4; ++i) {
+          const float mi = wm[i][16 * t + row];
+          ll += wl[i][16 * t + row] * (mi == kNegInf ? 0.f : fast_exp2(mi - mm));
+        }
         const int tok = r / G;
         const int64_t orow = (int64_t)(q.bos + tok) * a.h + head * G + (r - tok * G);
         const float inv = ll == 0.f ? 0.f : 1.f / ll;
@@ -480,7 +481,7 @@ __global__ __launch_bounds__(256) void attn_stream_join_kernel(StreamArgs a) {
     const float now = fmaxf(big, top);
     const float old = big == kNegInf ? 0.f : fast_exp2(big - now);
     const float f = m == kNegInf ? 0.f : fast_exp2(m - now);
-    float add = f == 0.f ? 0.f : pm[1] * f;
+    float add = pm[1] * f;  // (a sum that is NaN stays, also beside a maximum of -inf)
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) add += __shfl_xor(add, off, 64);
     big = now;
@@ -496,7 +497,7 @@ __global__ __launch_bounds__(256) void attn_stream_join_kernel(StreamArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float g = __shfl(f, (k + e) & 63, 64);
-        if (k + e < here && g != 0.f) sum += g * x[e];
+        if (k + e < here) sum += g * x[e];
       }
     }
   }

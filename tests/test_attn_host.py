@@ -189,6 +189,30 @@ def test_binding_refuses_tensors_that_do_not_fit():
                             pages, pages)
 
 
+@pytest.mark.parametrize("scale", [0.0, -1.0, float("nan"), 1e-60])
+def test_high_level_calls_refuse_a_scale_that_is_not_positive(scale):
+    t = torch.bfloat16
+    q, cu = torch.zeros(4, 2, 128, dtype=t), torch.zeros(2, dtype=torch.int32)
+    pages, table = torch.zeros(3, 2, 16, 128, dtype=t), torch.zeros(1, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="scale"):
+        gdn.causal_attention(q, q, q, cu, scale=scale)
+    with pytest.raises(ValueError, match="scale"):
+        gdn.paged_attention(q, pages, pages, cu, cu[:1], table, scale=scale)
+
+
+def test_high_level_calls_of_no_tokens_give_empty_results():
+    t = torch.float16
+    cu = torch.zeros(3, dtype=torch.int32)
+    pages, table = torch.zeros(3, 2, 16, 128, dtype=t), torch.zeros(2, 2, dtype=torch.int32)
+    qkv, q = torch.zeros(0, 8 * 128, dtype=t), torch.zeros(0, 4, 128, dtype=t)
+    a, b = gdn.qk_norm_rope(qkv, 4, 2, cu)
+    assert a.shape == (0, 4, 128) and b.shape == (0, 2, 128) and a.dtype == t
+    a, b = gdn.append_paged_kv(qkv, 4, cu, cu[:2], table, pages, pages.clone(), output_k=True)
+    assert a.shape == (0, 4, 128) and b.shape == (0, 2, 128)
+    assert gdn.causal_attention(q, q[:, :2], q[:, :2], cu).shape == (0, 4, 128)
+    assert gdn.paged_attention(q, pages, pages, cu, cu[:2], table).shape == (0, 4, 128)
+
+
 def test_binding_struct_matches_the_header(tmp_path):
     import shutil
     cc = shutil.which("gcc") or shutil.which("cc")

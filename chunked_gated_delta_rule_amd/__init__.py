@@ -759,20 +759,22 @@ def causal_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, scale=None, workspa
 
 
 def paged_attention(q, k_pages, v_pages, cu_seqlens, kv_lens, block_table, shared_len=None,
-                    scale=None, workspace=None):
+                    scale=None, workspace=None, shared_max=None):
     """Allocate the output with torch and run gdn_attn_paged on the current stream.
 
     q [T, heads, d]: the new tokens of every sequence (one each when decoding),
     whose keys and values the cache already holds; shared_len: int32 [1] on the
-    device, positions that lie in the same pages for the whole batch (read once
-    for all). Returns o [T, heads, d]."""
+    device, positions that lie in the same pages for the whole batch (at most
+    shared_max, by default the table's capacity; read once for all where that saves
+    more than it costs). Returns o [T, heads, d]."""
     pages, hkv, size, d = _pages(k_pages, v_pages, block_table)
     if q.dim() != 3 or q.shape[2] != d:
         raise ValueError(f"q [T, heads, {d}] expected: {tuple(q.shape)}")
     cols = block_table.shape[1]
     cfg = make_attn_config(q.shape[0], cu_seqlens.numel() - 1, q.shape[1], hkv, d, q.dtype,
                            _scale(scale), page_size=size, n_pages=pages, max_pages=cols,
-                           shared_max=0 if shared_len is None else cols * size)
+                           shared_max=0 if shared_len is None else
+                           cols * size if shared_max is None else shared_max)
     o = torch.empty((q.shape[0], q.shape[1], d), dtype=q.dtype, device=q.device)
     if q.shape[0] == 0:
         return o

@@ -85,7 +85,7 @@ PrefillLayout prefill_layout(const gdn_attn_config *cfg, gdn::Keys keys) {
 PagedLayout paged_layout(const gdn_attn_config *cfg) {
   const size_t d = static_cast<size_t>(cfg->d);
   const size_t slots = static_cast<size_t>(gdn::stream_grid(cfg)) * 2 * 16 * gdn::stream_row_tiles(cfg);
-  const bool shared = cfg->shared_max > 0;
+  const bool shared = gdn::shares(cfg);
   const size_t done = shared ? static_cast<size_t>(cfg->t_max) * static_cast<size_t>(cfg->h) : 0;
   const size_t pre = shared ? static_cast<size_t>(gdn::tile_part_rows(
                                   cfg, gdn::tile_shape(cfg, gdn::Keys::kShared), gdn::Keys::kShared))
@@ -269,7 +269,7 @@ gdn_status gdn_attn_paged(const gdn_attn_config *cfg, const void *q, int64_t q_r
   pg.cu = cu_seqlens;
   pg.kv_lens = kv_lens;
   pg.table = block_table;
-  pg.shared_len = shared_len;
+  pg.shared_len = gdn::shares(cfg) ? shared_len : nullptr;
   pg.t_max = cfg->t_max;
   pg.n_max = cfg->n_max;
   pg.page_shift = page_shift(cfg);
@@ -291,7 +291,7 @@ gdn_status gdn_attn_paged(const gdn_attn_config *cfg, const void *q, int64_t q_r
   }
   const PagedLayout l = paged_layout(cfg);
   gdn::StreamArgs a = {};
-  if (cfg->shared_max > 0 && shared_len) {
+  if (pg.shared_len) {
     tile_common(cfg, t, at, l.pre_o, l.pre_ml);
     const hipError_t e = gdn::launch_attn_tiles(cfg, gdn::Keys::kShared, t, as_stream(stream));
     if (e != hipSuccess) return GDN_ERR_HIP;

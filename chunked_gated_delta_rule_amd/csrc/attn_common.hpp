@@ -148,6 +148,68 @@ __device__ __forceinline__ Packed seq_of_row(const int32_t *__restrict__ cu, int
   return p;
 }
 
+// A sequence of a batch of at most kMostTiled whose tiles of tt tokens are numbered
+// without gaps: index, first row, rows, number of its first tile, what extra(s) gave,
+// and the tiles of the batch.
+struct Tiled {
+  int s, b, n, at, extra[2], total;
+};
+constexpr int kMostTiled = 256;
+// The first sequence with chosen(its first row, rows, first tile, tiles of the batch),
+// by one wave: kPer neighbouring sequences a lane (n_max <= 64 kPer), all loads in one
+// round trip. False if there is none.
+template <int kPer, typename F, typename G>
+__device__ __forceinline__ bool tiled_by(const int32_t *__restrict__ cu, int n_max, int t_max, int tt,
+                                      int lane, F chosen, G extra, Tiled &out) {
+  Tiled mine[kPer], pick = {};
+  int tiles = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    Tiled &p = mine[j];
+    p.s = min(lane * kPer + j, n_max - 1);
+    p.b = cu_at(cu, p.s, t_max);
+    p.n = cu_end(cu, p.s, p.b, t_max) - p.b;
+    extra(p.s, p.extra);
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    if (lane * kPer + j >= n_max) mine[j].n = 0;
+    tiles += (mine[j].n + tt - 1) / tt;
+  }
+  int end = tiles;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int y = __shfl_up(end, off, 64);
+    if (lane >= off) end += y;
+  }
+  const int total = __builtin_amdgcn_readlane(end, 63);
+  int at = end - tiles;
+  bool found = false;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    mine[j].at = at;
+    if (!found && mine[j].n > 0 && chosen(mine[j].b, mine[j].n, at, total)) {
+      found = true;
+      pick = mine[j];
+    }
+    at += (mine[j].n + tt - 1) / tt;
+  }
+  const unsigned long long who = __ballot(found);
+  if (who == 0) return false;
+  const int hit = __ffsll(who) - 1;
+  auto of = [&](int x) { return __builtin_amdgcn_readlane(x, hit); };
+  out = {of(pick.s), of(pick.b), of(pick.n), of(pick.at), {of(pick.extra[0]), of(pick.extra[1])},
+         total};
+  return true;
+}
+
+template <typename F, typename G>
+__device__ __forceinline__ bool tiled(const int32_t *__restrict__ cu, int n_max, int t_max, int tt,
+                                      int lane, F chosen, G extra, Tiled &out) {
+  return n_max <= 64 ? tiled_by<1>(cu, n_max, t_max, tt, lane, chosen, extra, out)
+                     : tiled_by<kMostTiled / 64>(cu, n_max, t_max, tt, lane, chosen, extra, out);
+}
+
 // New tokens and keys of sequence s of a paged batch.
 struct Seq {
   int bos, n, kv;

@@ -84,6 +84,8 @@ struct StreamArgs {
 int stream_row_tiles(const gdn_attn_config *cfg);
 // Work-groups of the streaming kernel on the current device.
 int stream_grid(const gdn_attn_config *cfg);
+// Whether gdn_attn_paged reads a shared prefix once for the whole batch.
+bool shares(const gdn_attn_config *cfg);
 // Whether gdn_attn_paged streams the keys past few rows, or tiles many rows.
 bool streams(const gdn_attn_config *cfg);
 hipError_t launch_attn_stream(const gdn_attn_config *cfg, StreamArgs a, hipStream_t stream);

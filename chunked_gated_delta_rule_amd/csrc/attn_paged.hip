@@ -555,12 +555,29 @@ int64_t rows_per_seq(const gdn_attn_config *cfg) {
 
 }  // namespace
 
-// Rows of an average sequence (new tokens times query heads per key head) from
-// which its keys are taken in tiles of 128 or 256 rows.
-bool streams(const gdn_attn_config *cfg) { return rows_per_seq(cfg) < 128; }
+// Whether the prefix is worth a pass of its own: two launches more and a longer join
+// (about 12 us) against reads of it by every sequence, of which most hit a cache. Even
+// at 128 MiB of the latter (8 sequences on 16384 shared positions, 32 on 4096, 128 on
+// 1024: 29 / 28 / 36 us against 30 / 25 / 29), ahead at 512 MiB (128 on 4096: 44
+// against 57; with 4 times the heads and a quarter of the sequences 36 against 53).
+bool shares(const gdn_attn_config *cfg) {
+  constexpr double kWorth = 256.0 * (1 << 20);
+  const double room = (double)cfg->max_pages * cfg->page_size;
+  const double shared = cfg->shared_max < room ? cfg->shared_max : room;
+  return shared * cfg->n_max * cfg->hkv * cfg->d * 4 >= kWorth;
+}
+
+// Rows of an average sequence (new tokens times query heads per key head) up to which
+// its keys are streamed; with more, they are taken in tiles of 128 rows. With 32 rows
+// both take as long (16 sequences on 2500 keys 44 us against 46, 64 on 1250: 91 against
+// 86), with 64 the tiles are ahead (53 against 48, 116 against 90), except where only
+// streamed items can leave the prefix to its own pass (64 sequences behind 8192 shared
+// positions: 85 against 100; with 96 rows 124 against 102).
+bool streams(const gdn_attn_config *cfg) { return rows_per_seq(cfg) <= (shares(cfg) ? 64 : 32); }
 
 // One 16-row tile per item holds a decoding sequence's heads; where an average
-// sequence has more rows, wider items read the keys fewer times.
+// sequence has more rows, wider items read the keys fewer times (32 rows on 2500 keys,
+// 32 sequences: 84 us against 107; 64 rows: 107 against 199).
 int stream_row_tiles(const gdn_attn_config *cfg) {
   const int most = cfg->d == 128 ? 4 : 2;
   int rt = 1;

@@ -286,7 +286,7 @@ struct Where {
             uniform(lq),    uniform(kb),   uniform(lk),    uniform(q0), uniform(past)};
   }
 };
-template <Keys kKeys, int kThreads>
+template <Keys kKeys, bool kSplit, int kThreads>
 __device__ __forceinline__ bool find(const TileArgs &a, int tt, int tid, Where &t,
                                      int (&lds)[kThreads / 64][2]) {
   const Place at = place(flat_block(), a.h / a.share, a.slots, a.splits);
@@ -304,25 +304,46 @@ __device__ __forceinline__ bool find(const TileArgs &a, int tt, int tid, Where &
     t.past = t.lk;  // every token sees the whole prefix
     return t.q0 < t.lq && t.lk > 0;
   } else {
-    int kv[2];
-    const Packed p = locate(
-        a.cu_q, a.n_max, a.t_max, at.slot, tid & 63, [&](int i, int b) { return b / tt + i; },
-        [&](int i, int(&o)[2]) {
-          if constexpr (kKeys == Keys::kRows) {
-            o[0] = cu_at(a.cu_k, i, a.tk_max);
-            o[1] = cu_end(a.cu_k, i, o[0], a.tk_max) - o[0];
-          } else {
-            o[0] = 0;
-            o[1] = kv_of(a.pg, i);
-          }
-        },
-        kv);
-    t.s = p.s;
-    t.qb = p.b;
-    t.lq = p.n;
-    t.q0 = (at.slot - (t.qb / tt + p.s)) * tt;
-    t.kb = kv[0];
-    t.lk = kv[1];
+    auto keys = [&](int i, int(&o)[2]) {
+      if constexpr (kKeys == Keys::kRows) {
+        o[0] = cu_at(a.cu_k, i, a.tk_max);
+        o[1] = cu_end(a.cu_k, i, o[0], a.tk_max) - o[0];
+      } else {
+        o[0] = 0;
+        o[1] = kv_of(a.pg, i);
+      }
+    };
+    if constexpr (kSplit) {
+      // the batch's tiles, last one first, then the slots that are left over
+      const int over = a.slots - at.slot;
+      Tiled p;
+      if (!tiled(
+              a.cu_q, a.n_max, a.t_max, tt, tid & 63,
+              [&](int, int n, int first, int total) {
+                const int x = min(total, a.slots) - over;
+                return x >= first && x < first + (n + tt - 1) / tt;
+              },
+              keys, p))
+        return false;
+      t.slot = min(p.total, a.slots) - over;
+      t.s = p.s;
+      t.qb = p.b;
+      t.lq = p.n;
+      t.q0 = (t.slot - p.at) * tt;
+      t.kb = p.extra[0];
+      t.lk = p.extra[1];
+    } else {
+      int kv[2];
+      const Packed p = locate(
+          a.cu_q, a.n_max, a.t_max, at.slot, tid & 63, [&](int i, int b) { return b / tt + i; },
+          keys, kv);
+      t.s = p.s;
+      t.qb = p.b;
+      t.lq = p.n;
+      t.q0 = (at.slot - (t.qb / tt + p.s)) * tt;
+      t.kb = kv[0];
+      t.lk = kv[1];
+    }
     t.past = t.lk - t.lq;                  // token r sees keys 0 .. past + r
     return t.q0 >= 0 && t.q0 < t.lq;       // else no tile of the sequence has this slot
   }
@@ -348,6 +369,7 @@ __device__ __forceinline__ Sight sight_of(const Where &t, int rw, int col, int t
     s.lim = s.lo = s.hi = t.lk - 1;
     s.keys = t.lk;
   }
+  if (t.q0 + rw / share >= t.lq) s.hi = -1;  // none of the wave's rows is the sequence's
   return s;
 }
 
@@ -418,7 +440,7 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 4 ? 3 : 2) void attn_tile_ke
   const int col = lane & 31, hh = lane >> 5;
   Where t;
   const int share = a.share, tt = kBM / share;
-  if (!find<kKeys, 64 * kWaves>(a, tt, tid, t, scan)) return;
+  if (!find<kKeys, false, 64 * kWaves>(a, tt, tid, t, scan)) return;
   t = t.uniform_();
   const int kvh = t.group * share / (a.h / a.hkv);
   const Sight see = sight_of<kKeys>(t, 32 * w, col, tt, share);
@@ -550,7 +572,7 @@ __global__ __launch_bounds__(512, 2) void attn_part_kernel(TileArgs a) {
   const int col = lane & 31, hh = lane >> 5;
   Where t;
   const int share = a.share, tt = kBM / share;
-  if (!find<kKeys, 512>(a, tt, tid, t, scan)) return;
+  if (!find<kKeys, true, 512>(a, tt, tid, t, scan)) return;
   t = t.uniform_();
   const int kvh = t.group * share / (a.h / a.hkv);
   const Sight see = sight_of<kKeys>(t, 32 * w, col, tt, share);
@@ -653,13 +675,15 @@ __global__ __launch_bounds__(256) void attn_tile_join_kernel(TileArgs a, int tt,
   const int64_t i = (int64_t)flat_block() * 4 + w;
   const int t = (int)(i / a.h), head = (int)(i % a.h);
   if (t >= cu_at(a.cu_q, a.n_max, a.t_max)) return;
-  int none;
-  const Packed p = seq_of_row(
-      a.cu_q, a.n_max, a.t_max, t, lane, [](int) { return 0; }, none);
-  if (t < p.b || t >= p.b + p.n) return;  // an unsorted cu_seqlens: a row of no sequence
-  const int tile = (t - p.b) / tt;
-  const int64_t item =
-      item_of(head / a.share, p.b / tt + p.s + tile, a.h / a.share, a.slots) * a.splits;
+  Tiled p;
+  if (!tiled(
+          a.cu_q, a.n_max, a.t_max, tt, lane,
+          [&](int b, int n, int, int) { return t >= b && t < b + n; },
+          [](int, int(&o)[2]) { o[0] = o[1] = 0; }, p))
+    return;  // an unsorted cu_seqlens: a row of no sequence
+  const int tile = (t - p.b) / tt, slot = p.at + tile;
+  if (slot >= a.slots) return;  // or sequences that overlap
+  const int64_t item = item_of(head / a.share, slot, a.h / a.share, a.slots) * a.splits;
   const int row = (t - p.b - tile * tt) * a.share + head % a.share;
   // the splits' statistics, one per lane
   const float mine = lane < a.splits ? a.part_ml[((item + lane) * bm + row) * 2] : kNegInf;
@@ -745,18 +769,24 @@ constexpr int kMostShare = 16;
 // are at most 64 (one per lane of the join).
 constexpr int kSplitKeys = 256;
 constexpr int kMostSplits = 64;
+// Tiles that fill the device between half and once are split in two: one prompt of 1200
+// tokens with heads of 256 (150 tiles) 66 -> 50 us, of 2000 with heads of 128 (250) 58
+// -> 50. A batch may be uneven and have more tiles than counted, so with several
+// sequences only from this many keys on: 16 of 64 tokens on 2500 keys 140 -> 95 us; but
+// 16 of 1 to 130 tokens on 1300 keys would go from 57 to 71, on 700 from 34 to 58.
+constexpr int kTwoKeys = 2048;
 
 }  // namespace
 
-// Tiles of tt tokens have slots: sequence s starts at slot floor(cu[s] / tt) + s,
-// which is distinct for every tile of the batch and grows with s, so a slot's
-// sequence is found by a search and no table is needed.
+// Tiles of tt tokens have slots. Whole: sequence s starts at slot floor(cu[s] / tt) +
+// s, which is distinct for every tile of the batch and grows with s, so a slot's
+// sequence is found by a search and no table is needed. With split keys, where a
+// work-group without a tile costs a CU its turn, the tiles are numbered without gaps.
 TileShape tile_shape(const gdn_attn_config *cfg, Keys keys) {
   TileShape s;
   const int group = cfg->h / cfg->hkv;
   s.share = group < kMostShare ? group : kMostShare;
   while (group % s.share) --s.share;
-  // few tiles and many keys: split the keys until the device is full
   const int64_t room = (int64_t)cfg->max_pages * cfg->page_size;
   const int64_t longest = keys == Keys::kShared  ? (cfg->shared_max < room ? cfg->shared_max : room)
                           : keys == Keys::kPages ? room
@@ -764,14 +794,21 @@ TileShape tile_shape(const gdn_attn_config *cfg, Keys keys) {
   auto cut = [&](int rows) {
     s.tt = rows / s.share;
     s.slots = keys == Keys::kShared ? (cfg->t_max + s.tt - 1) / s.tt : cfg->t_max / s.tt + cfg->n_max;
-    return (int64_t)s.slots * (cfg->h / s.share);
   };
+  // few tiles (of a batch of equal sequences) and many keys: split the keys until the
+  // device is full
   s.rows = kPartRows;
   s.waves = 8;
-  const int64_t tiles = cut(s.rows);
+  cut(s.rows);
+  const int64_t tiles =
+      (keys == Keys::kShared ? s.slots
+                             : (int64_t)cfg->n_max * ((cfg->t_max / cfg->n_max + s.tt - 1) / s.tt)) *
+      (cfg->h / s.share);
   int64_t n = tiles > 0 ? cu_count() / tiles : 1;
+  if (n == 1 && (cfg->n_max == 1 || longest >= kTwoKeys)) n = 2;
   if (n > longest / kSplitKeys) n = longest / kSplitKeys;
   s.splits = n < 1 ? 1 : n > kMostSplits ? kMostSplits : static_cast<int>(n);
+  if (keys != Keys::kShared && cfg->n_max > kMostTiled) s.splits = 1;
   if (s.splits > 1 || keys == Keys::kShared) return s;
   s.waves = cfg->d == 256 || cfg->t_max / cfg->n_max >= kLongPrompt ? 8 : 4;
   s.rows = 32 * s.waves;

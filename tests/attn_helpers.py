@@ -119,3 +119,15 @@ class Cache:
         from oracle import attention
         return (attention.gather(f64(self.k), self.table[s], self.lens[s]),
                 attention.gather(f64(self.v), self.table[s], self.lens[s]))
+
+
+def shared_cols(n, hkv, d, page):
+    """Table columns with which n sequences of a batch are worth a pass of its own over
+    a shared prefix as long as the table (256 MiB of keys and values read by them all)."""
+    return -(-(1 << 28) // (4 * n * hkv * d * page))
+
+
+def widened(table, cols):
+    """The table with columns that name no page up to `cols`."""
+    pad = np.full((table.shape[0], max(cols - table.shape[1], 0)), -1, np.int32)
+    return np.concatenate([table, pad], 1)

@@ -63,9 +63,13 @@ def test_rows_times_heads_are_counted_in_32_bits():
 
 
 def test_workspace_depends_on_the_prefix_capacity():
-    a, b = gdn.gdn_attn_workspace_size(cfg()), gdn.gdn_attn_workspace_size(cfg(shared_max=100))
+    c = dict(max_pages=1 << 14)
+    a = gdn.gdn_attn_workspace_size(cfg(**c))
+    assert a > 0 and a % 256 == 0
+    # a prefix of at most 100 positions is not worth a pass of its own
+    assert gdn.gdn_attn_workspace_size(cfg(shared_max=100, **c)) == a
     rows = 64 * 8 * 2
-    assert 0 < a < b and a % 256 == 0 and b - a >= rows * 128 * 4
+    assert gdn.gdn_attn_workspace_size(cfg(shared_max=1 << 18, **c)) - a >= rows * 128 * 4
 
 
 FRONT = dict(qkv=P, q_w=P, k_w=P, inv_freq=P, cu_seqlens=P, kv_lens=P, q=P, k=P)
@@ -127,7 +131,7 @@ PAGED = dict(q=P, k_pages=P, v_pages=P, cu_seqlens=P, kv_lens=P, block_table=P, 
     (dict(k_pages=P + 8), INVALID), (dict(v_pages=P + 8), INVALID), (dict(o=P + 2), INVALID),
     (dict(shared_len=P + 2), INVALID), (dict(kv_lens=P + 2), INVALID),
     (dict(workspace=None), WORKSPACE), (dict(workspace=P + 64), WORKSPACE),
-    (dict(ws_bytes=256), WORKSPACE),
+    (dict(ws_bytes=255), WORKSPACE),
 ])
 def test_paged_refusals(change, status):
     refused(status, gdn.gdn_attn_paged, cfg(), **{**PAGED, **change})

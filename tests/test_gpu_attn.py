@@ -8,7 +8,7 @@ import torch
 
 import chunked_gated_delta_rule_amd as gdn
 from attn_helpers import (DEV, TYPES, Cache, check_attention, check_norm_rope, cu_of, f64, normal,
-                          on)
+                          on, shared_cols, widened)
 from oracle import attention
 
 pytestmark = pytest.mark.gpu
@@ -217,6 +217,7 @@ PREFILL = [
     ([140], [140], 17, 1, 128),               # a prime number of heads on one key head
     ([50, 33], [90, 40], 24, 1, 256),
     ([30], [40], 64, 2, 128),
+    ([i % 4 for i in range(100)], [520 + 5 * i for i in range(100)], 1, 1, 128),  # parts, many sequences
 ]
 
 
@@ -339,6 +340,8 @@ PAGED = [
     ([1] * 280, [1 + 3 * i for i in range(280)], 16, 4, 128, 32, 0),  # a wave per joined row
     ([2] * 90, [500 - i for i in range(90)], 24, 2, 256, 16, 300),
     ([1, 2], [300, 40], 17, 1, 128, 16, 0),
+    ([16 + i % 3 for i in range(70)], [600 + 7 * i for i in range(70)], 8, 1, 128, 64, 0),
+    ([40] * 10, [900 + 31 * i for i in range(10)], 4, 1, 256, 32, 0),  # tiles with parts and without
 ]
 
 
@@ -351,20 +354,22 @@ def test_paged(t, new, full, h, hkv, d, page, shared):
     q = _poisoned(normal(1, T, h, d, dtype=t, scale=2.0), cu, T)
     say(f"paged {t} n={len(new)} tokens={sum(new)} keys={sum(full)} h={h} hkv={hkv} d={d} "
         f"page={page} shared={shared}")
-    cfg = gdn.make_attn_config(T, n, h, hkv, d, t, page_size=page, n_pages=c.n_pages,
-                               max_pages=c.cols, shared_max=shared)
-    o = torch.full((T, h, d), MARK, dtype=t, device=DEV)
-    sh = on(np.array([shared], np.int32)) if shared else None
-    args = (q.to(DEV), c.k.to(DEV), c.v.to(DEV), on(cu), on(np.array(c.lens, np.int32)),
-            on(c.table))
-    gdn.gdn_attn_paged(cfg, *args, sh, o, workspace(cfg))
-    worst = 0.0
-    for s in range(len(new)):
-        a = slice(cu[s], cu[s + 1])
-        k, v = c.rows(s)
-        worst = max(worst, check_attention(o[a], f64(q[a]), k, v, d ** -0.5, t))
-    say(f"  off / bound {worst:.3f}")
-    assert (o[sum(new):] == MARK).all()
+    # a prefix, with a capacity that is too small for a pass of its own and with a larger one
+    for cols in [c.cols] + ([shared_cols(n, hkv, d, page)] if shared else []):
+        cfg = gdn.make_attn_config(T, n, h, hkv, d, t, page_size=page, n_pages=c.n_pages,
+                                   max_pages=cols, shared_max=cols * page if shared else 0)
+        o = torch.full((T, h, d), MARK, dtype=t, device=DEV)
+        sh = on(np.array([shared], np.int32)) if shared else None
+        args = (q.to(DEV), c.k.to(DEV), c.v.to(DEV), on(cu), on(np.array(c.lens, np.int32)),
+                on(widened(c.table, cols)))
+        gdn.gdn_attn_paged(cfg, *args, sh, o, workspace(cfg))
+        worst = 0.0
+        for s in range(len(new)):
+            a = slice(cu[s], cu[s + 1])
+            k, v = c.rows(s)
+            worst = max(worst, check_attention(o[a], f64(q[a]), k, v, d ** -0.5, t))
+        say(f"  off / bound {worst:.3f}")
+        assert (o[sum(new):] == MARK).all()
     # the same bits again, with another workspace's content
     o2 = torch.full_like(o, MARK)
     gdn.gdn_attn_paged(cfg, *args, sh, o2, torch.zeros_like(workspace(cfg)))
@@ -381,6 +386,37 @@ def test_paged_of_one_long_context(t):
                             on(np.array([n], np.int32)), on(c.table))
     k, v = c.rows(0)
     check_attention(o, f64(q), k, v, d ** -0.5, t)
+
+
+@pytest.mark.parametrize("new,full,h,hkv,d,page,shared", [
+    ([1, 1], [9000, 700], 8, 2, 128, 16, 0),                 # keys in parts, four waves per row
+    ([1] * 300, [100 + 3 * i for i in range(300)], 16, 4, 128, 32, 0),  # and one wave per row
+    ([1, 2, 1], [900, 950, 1200], 16, 2, 256, 16, 700),      # beside a shared prefix
+    ([200, 40], [500, 40], 8, 2, 128, 16, 0),                # tiles over the pages
+    ([140], [4000], 4, 2, 256, 64, 0),                       # with their keys in parts
+])
+def test_paged_keeps_what_is_not_finite_in_its_rows(new, full, h, hkv, d, page, shared):
+    """NaN in a query row, or +inf in a cached value, comes out of the rows that read it
+    and of no other sequence's."""
+    t = torch.bfloat16
+    c = Cache(full, hkv, d, page, t, 3, shared)
+    q = normal(1, sum(new), h, d, dtype=t)
+    q[0, 0] = float("nan")
+    last = len(new) - 1
+    at = full[last] - 1 - new[last] // 2  # the last sequence's, behind the prefix
+    c.v[c.table[last, at // page], :, at % page] = float("inf")
+    args = [x.to(DEV) for x in (q, c.k, c.v)]
+    sh = torch.tensor([shared], dtype=torch.int32, device=DEV) if shared else None
+    cu = cu_of(new)
+    say(f"paged, values that are not finite {new[:4]} {full[:4]} d={d} shared={shared}")
+    table = widened(c.table, shared_cols(len(new), hkv, d, page)) if shared else c.table
+    o = gdn.paged_attention(*args, on(cu), on(np.array(full, np.int32)), on(table), sh)
+    assert o[0, 0].isnan().all()
+    b = int(cu[last]) if last else 0
+    if last:
+        assert o[:b].flatten(0, 1)[1:].isfinite().all()
+    reads = full[last] - new[last] + np.arange(new[last]) >= at
+    assert not o[b:][torch.from_numpy(reads).to(DEV)].isfinite().any()
 
 
 @pytest.mark.parametrize("t", TYPES)
@@ -453,16 +489,19 @@ def test_paged_indexes_that_name_nothing_stay_inside():
     t, h, hkv, d, page = torch.bfloat16, 4, 1, 128, 16
     n, T, pages = 5, 12, 3
     kp, vp = normal(1, pages, hkv, page, d).to(DEV), normal(2, pages, hkv, page, d).to(DEV)
-    table = on(np.array([[0, 1], [-5, 9], [2_000_000_000, 1], [1, -2_000_000_000], [2, 2]], np.int32))
-    cfg = gdn.make_attn_config(T, n, h, hkv, d, t, page_size=page, n_pages=pages, max_pages=2,
-                               shared_max=64)
+    table = np.array([[0, 1], [-5, 9], [2_000_000_000, 1], [1, -2_000_000_000], [2, 2]], np.int32)
     buf = torch.full((T + 8, h, d), MARK, dtype=t, device=DEV)
     q, sh = normal(3, T, h, d).to(DEV), on(np.array([1 << 30], np.int32))
-    for cu in ([0, 2, 3, 9, 10, 12], [0, 9, 4, 4, 20, 11], [5, 3, -7, 12, 1, 40]):
-        for kv in ([32, 31, 20, 2_000_000_000, 0], [-4, 1000, 32, 32, 32]):
-            gdn.gdn_attn_paged(cfg, q, kp, vp, on(np.array(cu, np.int32)),
-                               on(np.array(kv, np.int32)), table, sh, buf[4:4 + T], workspace(cfg))
-            assert (buf[:4] == MARK).all() and (buf[4 + T:] == MARK).all()
+    for cols in (2, shared_cols(n, hkv, d, page)):
+        cfg = gdn.make_attn_config(T, n, h, hkv, d, t, page_size=page, n_pages=pages, max_pages=cols,
+                                   shared_max=64 if cols == 2 else 1 << 30)
+        wide = on(widened(table, cols))
+        for cu in ([0, 2, 3, 9, 10, 12], [0, 9, 4, 4, 20, 11], [5, 3, -7, 12, 1, 40]):
+            for kv in ([32, 31, 20, 2_000_000_000, 0], [-4, 1000, 32, 32, 32]):
+                gdn.gdn_attn_paged(cfg, q, kp, vp, on(np.array(cu, np.int32)),
+                                   on(np.array(kv, np.int32)), wide, sh, buf[4:4 + T],
+                                   workspace(cfg))
+                assert (buf[:4] == MARK).all() and (buf[4 + T:] == MARK).all()
 
 
 def test_prefill_and_front_with_malformed_cu_seqlens_stay_inside():
@@ -537,7 +576,8 @@ def test_prompt_then_steps(t, d, page, rot, inter):
         cu = cu_of(new)
         kv = [kv[s] + new[s] for s in range(2)]
         q, _ = front(normal(50 + i, sum(new), width, dtype=t).to(DEV), cu, kv)
-        o = gdn.paged_attention(q, kp, vp, on(cu), on(np.array(kv, np.int32)), on(table), shared)
+        wide = widened(table, shared_cols(2, hkv, d, page))
+        o = gdn.paged_attention(q, kp, vp, on(cu), on(np.array(kv, np.int32)), on(wide), shared)
         for s in range(2):
             a = slice(cu[s], cu[s + 1])
             check_attention(o[a], f64(q[a]), np.concatenate(history[s][0]),
@@ -549,12 +589,12 @@ def test_a_captured_decode_step_replays_with_other_lengths():
     are read on the device, so one capture serves every step."""
     t, h, hkv, d, page, n = torch.bfloat16, 8, 2, 128, 16, 6
     rng = np.random.Generator(np.random.PCG64(3))
-    cols = 40
+    cols, most = 40, shared_cols(n, hkv, d, page)
     pages = n * cols
-    table = on(rng.permutation(pages).reshape(n, cols).astype(np.int32))
+    table = on(widened(rng.permutation(pages).reshape(n, cols).astype(np.int32), most))
     kp, vp = normal(1, pages, hkv, page, d).to(DEV), normal(2, pages, hkv, page, d).to(DEV)
     cfg = gdn.make_attn_config(2 * n, n, h, hkv, d, t, rot_dim=128, page_size=page, n_pages=pages,
-                               max_pages=cols, shared_max=200)
+                               max_pages=most, shared_max=most * page)
     x = torch.zeros(2 * n, (h + 2 * hkv) * d, dtype=t, device=DEV)
     cu, kv = on(cu_of([1] * n)), on(np.full(n, 5, np.int32))
     sh = on(np.array([0], np.int32))

@@ -148,67 +148,139 @@ __device__ __forceinline__ Packed seq_of_row(const int32_t *__restrict__ cu, int
   return p;
 }
 
-// A sequence of a batch of at most kMostTiled whose tiles of tt tokens are numbered
-// without gaps: index, first row, rows, number of its first tile, what extra(s) gave,
-// and the tiles of the batch.
+// A sequence of a batch of at most kMostTiled: index, first row, rows, and what extra(s)
+// gave; its rows are cut into tiles of tt tokens.
 struct Tiled {
-  int s, b, n, at, extra[2], total;
+  int s, b, n, extra[2];
 };
 constexpr int kMostTiled = 256;
-// The first sequence with chosen(its first row, rows, first tile, tiles of the batch),
-// by one wave: kPer neighbouring sequences a lane (n_max <= 64 kPer), all loads in one
-// round trip. False if there is none.
-template <int kPer, typename F, typename G>
-__device__ __forceinline__ bool tiled_by(const int32_t *__restrict__ cu, int n_max, int t_max, int tt,
-                                      int lane, F chosen, G extra, Tiled &out) {
-  Tiled mine[kPer], pick = {};
-  int tiles = 0;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    Tiled &p = mine[j];
-    p.s = min(lane * kPer + j, n_max - 1);
-    p.b = cu_at(cu, p.s, t_max);
-    p.n = cu_end(cu, p.s, p.b, t_max) - p.b;
-    extra(p.s, p.extra);
-  }
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    if (lane * kPer + j >= n_max) mine[j].n = 0;
-    tiles += (mine[j].n + tt - 1) / tt;
-  }
-  int end = tiles;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int y = __shfl_up(end, off, 64);
-    if (lane >= off) end += y;
-  }
-  const int total = __builtin_amdgcn_readlane(end, 63);
-  int at = end - tiles;
-  bool found = false;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    mine[j].at = at;
-    if (!found && mine[j].n > 0 && chosen(mine[j].b, mine[j].n, at, total)) {
-      found = true;
-      pick = mine[j];
-    }
-    at += (mine[j].n + tt - 1) / tt;
-  }
-  const unsigned long long who = __ballot(found);
-  if (who == 0) return false;
-  const int hit = __ffsll(who) - 1;
-  auto of = [&](int x) { return __builtin_amdgcn_readlane(x, hit); };
-  out = {of(pick.s), of(pick.b), of(pick.n), of(pick.at), {of(pick.extra[0]), of(pick.extra[1])},
-         total};
-  return true;
-}
 
-template <typename F, typename G>
-__device__ __forceinline__ bool tiled(const int32_t *__restrict__ cu, int n_max, int t_max, int tt,
-                                      int lane, F chosen, G extra, Tiled &out) {
-  return n_max <= 64 ? tiled_by<1>(cu, n_max, t_max, tt, lane, chosen, extra, out)
-                     : tiled_by<kMostTiled / 64>(cu, n_max, t_max, tt, lane, chosen, extra, out);
-}
+// The batch in a wave, kPer (1 or 4) neighbouring sequences a lane, for n_max <= 64 kPer;
+// all loads in one round trip. Sequences past n_max have no rows.
+template <int kPer>
+struct TiledBatch {
+  Tiled seq[kPer];
+  int tiles[kPer];
+
+  template <typename G>
+  __device__ __forceinline__ TiledBatch(const int32_t *__restrict__ cu, int n_max, int t_max, int tt,
+                                        int lane, G extra) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      Tiled &p = seq[j];
+      p.s = min(lane * kPer + j, n_max - 1);
+      p.b = cu_at(cu, p.s, t_max);
+      p.n = cu_end(cu, p.s, p.b, t_max) - p.b;
+      extra(p.s, p.extra);
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (lane * kPer + j >= n_max) seq[j].n = 0;
+      tiles[j] = (seq[j].n + tt - 1) / tt;
+    }
+  }
+  // The sequence for which a lane has found[j], in all lanes (false: none has; the
+  // lowest lane's if several have, which an unsorted cu_seqlens can cause).
+  __device__ __forceinline__ bool pick(const bool (&found)[kPer], Tiled &out) const {
+    int v[5] = {seq[0].s, seq[0].b, seq[0].n, seq[0].extra[0], seq[0].extra[1]};
+    bool any = found[0];
+#pragma unroll
+    for (int j = 1; j < kPer; ++j) {
+      const bool take = found[j] && !any;
+      v[0] = take ? seq[j].s : v[0];
+      v[1] = take ? seq[j].b : v[1];
+      v[2] = take ? seq[j].n : v[2];
+      v[3] = take ? seq[j].extra[0] : v[3];
+      v[4] = take ? seq[j].extra[1] : v[4];
+      any = any || found[j];
+    }
+    const unsigned long long who = __ballot(any);
+    if (who == 0) return false;
+    const int hit = __ffsll(who) - 1;
+    auto of = [&](int x) { return __builtin_amdgcn_readlane(x, hit); };
+    out.s = of(v[0]);
+    out.b = of(v[1]);
+    out.n = of(v[2]);
+    out.extra[0] = of(v[3]);
+    out.extra[1] = of(v[4]);
+    return true;
+  }
+  // Tiles numbered sequence by sequence without gaps: chosen(sequence, its first tile,
+  // tiles of the batch) names one sequence; at and total are its values.
+  template <typename F>
+  __device__ __forceinline__ bool in_order(int lane, F chosen, Tiled &out, int &at, int &total) const {
+    int mine = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) mine += tiles[j];
+    int end = mine;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int y = __shfl_up(end, off, 64);
+      if (lane >= off) end += y;
+    }
+    total = __builtin_amdgcn_readlane(end, 63);
+    int first = end - mine, which = 0;
+    bool found[kPer], any = false;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      found[j] = !any && seq[j].n > 0 && chosen(seq[j], first, total);
+      if (found[j]) which = first;
+      any = any || found[j];
+      first += tiles[j];
+    }
+    if (!pick(found, out)) return false;
+    at = __builtin_amdgcn_readlane(which, __ffsll(__ballot(any)) - 1);
+    return true;
+  }
+  // f over the wave's values: rows of 16 lanes (shifts by 1, 2, 4, 8), then the rows.
+  template <typename F>
+  static __device__ __forceinline__ int all(int v, F f) {
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true));
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true));
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true));
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true));
+    return f(f(__builtin_amdgcn_readlane(v, 15), __builtin_amdgcn_readlane(v, 31)),
+             f(__builtin_amdgcn_readlane(v, 47), __builtin_amdgcn_readlane(v, 63)));
+  }
+  // Tiles of the sequences that have at least x.
+  __device__ __forceinline__ int from(int x) const {
+    int v = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) v += tiles[j] >= x ? tiles[j] : 0;
+    return all(v, [](int a, int b) { return a + b; });
+  }
+  // Tile number r with the longest sequence first and the last tile of each first:
+  // tile is its index in the sequence. False: there are fewer tiles.
+  __device__ __forceinline__ bool longest_first(int lane, int r, Tiled &out, int &tile) const {
+    int most = tiles[0];
+#pragma unroll
+    for (int j = 1; j < kPer; ++j) most = max(most, tiles[j]);
+    most = all(most, [](int a, int b) { return max(a, b); });
+    // the sequence has x tiles: the largest x with more than r tiles in sequences that
+    // have at least x
+    int x = 0, before = 0;
+    for (int bit = 1 << (31 - __builtin_clz(most | 1)); bit > 0; bit >>= 1) {
+      const int c = from(x | bit);
+      if (c > r)
+        x |= bit;
+      else
+        before = c;  // (once all bits are tried: the tiles of sequences with more than x)
+    }
+    if (x == 0) return false;
+    const int in = r - before, which = in / x;
+    tile = x - 1 - (in - which * x);
+    bool found[kPer];
+    int seen = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const unsigned long long equal = __ballot(tiles[j] == x);
+      const int rank = seen + (int)__popcll(equal & ((1ull << lane) - 1));
+      found[j] = tiles[j] == x && rank == which;
+      seen += (int)__popcll(equal);
+    }
+    return pick(found, out);
+  }
+};
 
 // New tokens and keys of sequence s of a paged batch.
 struct Seq {

@@ -313,37 +313,53 @@ __device__ __forceinline__ bool find(const TileArgs &a, int tt, int tid, Where &
         o[1] = kv_of(a.pg, i);
       }
     };
+    const int lane = tid & 63, over = a.slots - at.slot;
+    Tiled p;
     if constexpr (kSplit) {
       // the batch's tiles, last one first, then the slots that are left over
-      const int over = a.slots - at.slot;
-      Tiled p;
-      if (!tiled(
-              a.cu_q, a.n_max, a.t_max, tt, tid & 63,
-              [&](int, int n, int first, int total) {
-                const int x = min(total, a.slots) - over;
-                return x >= first && x < first + (n + tt - 1) / tt;
-              },
-              keys, p))
+      int first, total;
+      auto in = [&](const auto &batch) {
+        return batch.in_order(
+            lane,
+            [&](const Tiled &x, int first, int total) {
+              const int i = min(total, a.slots) - over;
+              return i >= first && i < first + (x.n + tt - 1) / tt;
+            },
+            p, first, total);
+      };
+      if (!(a.n_max <= 64 ? in(TiledBatch<1>(a.cu_q, a.n_max, a.t_max, tt, lane, keys))
+                          : in(TiledBatch<4>(a.cu_q, a.n_max, a.t_max, tt, lane, keys))))
         return false;
-      t.slot = min(p.total, a.slots) - over;
-      t.s = p.s;
-      t.qb = p.b;
-      t.lq = p.n;
-      t.q0 = (t.slot - p.at) * tt;
-      t.kb = p.extra[0];
-      t.lk = p.extra[1];
+      t.slot = min(total, a.slots) - over;
+      t.q0 = (t.slot - first) * tt;
+    } else if (a.n_max == 1) {
+      p.s = 0;
+      p.b = cu_at(a.cu_q, 0, a.t_max);
+      p.n = cu_end(a.cu_q, 0, p.b, a.t_max) - p.b;
+      keys(0, p.extra);
+      t.q0 = ((p.n + tt - 1) / tt - over) * tt;
+    } else if (a.n_max <= kMostTiled) {
+      int tile;
+      if (!(a.n_max <= 64 ? TiledBatch<1>(a.cu_q, a.n_max, a.t_max, tt, lane, keys)
+                                .longest_first(lane, over - 1, p, tile)
+                          : TiledBatch<4>(a.cu_q, a.n_max, a.t_max, tt, lane, keys)
+                                .longest_first(lane, over - 1, p, tile)))
+        return false;
+      t.q0 = tile * tt;
     } else {
-      int kv[2];
-      const Packed p = locate(
-          a.cu_q, a.n_max, a.t_max, at.slot, tid & 63, [&](int i, int b) { return b / tt + i; },
-          keys, kv);
-      t.s = p.s;
-      t.qb = p.b;
-      t.lq = p.n;
-      t.q0 = (at.slot - (t.qb / tt + p.s)) * tt;
-      t.kb = kv[0];
-      t.lk = kv[1];
+      const Packed q = locate(
+          a.cu_q, a.n_max, a.t_max, at.slot, lane, [&](int i, int b) { return b / tt + i; }, keys,
+          p.extra);
+      p.s = q.s;
+      p.b = q.b;
+      p.n = q.n;
+      t.q0 = (at.slot - (p.b / tt + p.s)) * tt;
     }
+    t.s = p.s;
+    t.qb = p.b;
+    t.lq = p.n;
+    t.kb = p.extra[0];
+    t.lk = p.extra[1];
     t.past = t.lk - t.lq;                  // token r sees keys 0 .. past + r
     return t.q0 >= 0 && t.q0 < t.lq;       // else no tile of the sequence has this slot
   }
@@ -676,12 +692,16 @@ __global__ __launch_bounds__(256) void attn_tile_join_kernel(TileArgs a, int tt,
   const int t = (int)(i / a.h), head = (int)(i % a.h);
   if (t >= cu_at(a.cu_q, a.n_max, a.t_max)) return;
   Tiled p;
-  if (!tiled(
-          a.cu_q, a.n_max, a.t_max, tt, lane,
-          [&](int b, int n, int, int) { return t >= b && t < b + n; },
-          [](int, int(&o)[2]) { o[0] = o[1] = 0; }, p))
+  int first, total;
+  auto none = [](int, int(&o)[2]) { o[0] = o[1] = 0; };
+  auto in = [&](const auto &batch) {
+    return batch.in_order(
+        lane, [&](const Tiled &x, int, int) { return t >= x.b && t < x.b + x.n; }, p, first, total);
+  };
+  if (!(a.n_max <= 64 ? in(TiledBatch<1>(a.cu_q, a.n_max, a.t_max, tt, lane, none))
+                      : in(TiledBatch<4>(a.cu_q, a.n_max, a.t_max, tt, lane, none))))
     return;  // an unsorted cu_seqlens: a row of no sequence
-  const int tile = (t - p.b) / tt, slot = p.at + tile;
+  const int tile = (t - p.b) / tt, slot = first + tile;
   if (slot >= a.slots) return;  // or sequences that overlap
   const int64_t item = item_of(head / a.share, slot, a.h / a.share, a.slots) * a.splits;
   const int row = (t - p.b - tile * tt) * a.share + head % a.share;
@@ -778,10 +798,13 @@ constexpr int kTwoKeys = 2048;
 
 }  // namespace
 
-// Tiles of tt tokens have slots. Whole: sequence s starts at slot floor(cu[s] / tt) +
-// s, which is distinct for every tile of the batch and grows with s, so a slot's
-// sequence is found by a search and no table is needed. With split keys, where a
-// work-group without a tile costs a CU its turn, the tiles are numbered without gaps.
+// Tiles of tt tokens have slots, t_max / tt + n_max at most; no table is needed to find
+// a slot's tile. Up to kMostTiled sequences a wave counts the batch's tiles, the longest
+// sequence's first (split: in order, the last first) and the slots left over last: where
+// they lie between the tiles, a work-group without one costs a CU its turn (16
+// sequences of 128 tokens on 2500 keys 165 us against 144, 64 of 32 on 1250: 130 against
+// 96). Beyond, sequence s starts at slot floor(cu[s] / tt) + s, which is distinct for
+// every tile of the batch and grows with s, and is found by a search.
 TileShape tile_shape(const gdn_attn_config *cfg, Keys keys) {
   TileShape s;
   const int group = cfg->h / cfg->hkv;

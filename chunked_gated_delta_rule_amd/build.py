@@ -1,8 +1,8 @@
 """Build libgdn.so (the gfx950 HIP kernels and the C ABI) in-tree with hipcc.
 
 Run ``python -m chunked_gated_delta_rule_amd.build`` (or call ``build()``).
-The library is always rebuilt; the object files of the four kernel sources
-are compiled in parallel.
+The library is always rebuilt; the object files of the sources are compiled
+in parallel.
 """
 
 from __future__ import annotations

@@ -1,20 +1,30 @@
-// Causal attention over packed prompts (grouped heads, queries the last tokens
-// of their keys), forward:  o_r = sum_{c <= lim(r)} softmax_c(scale q_r . k_c) v_c.
+// Causal attention over packed prompts (grouped heads, queries the last tokens of their
+// keys) and over the pages of a cache, forward:
+//   o_r = sum_{c <= lim(r)} softmax_c(scale q_r . k_c) v_c.
 //
-// One pass over the keys per query tile with a running maximum and sum per row.
-// A 256-thread work-group (four waves) owns 128 query rows of one head, 32 per
-// wave, and walks the keys 64 at a time; K and V tiles go through LDS, double
-// buffered, and are shared by the four waves. Everything else stays in the
-// wave's registers: scores are formed transposed, S^T = K Q^T, so a lane's
-// column is one query row and the softmax statistics are per lane (one
-// exchange between the two half-waves per tile), and the C layout of S^T is,
-// with the keys taken in the order the accumulator holds them, the B operand
-// of O^T += V^T P^T. V^T comes from the row-major tile with transposing LDS
-// reads. So the scores and weights never touch LDS.
+// One pass over the keys per tile of query rows, with a running maximum and sum per row
+// (the maximum moves only when it has grown by 2^8, so the output sums are rarely
+// rescaled). A tile's rows are tokens times the query heads that share a key head, 32
+// rows per wave; the tiles of K and V go straight to LDS (16-byte copies that pass no
+// register), double buffered, and are shared by the waves. Everything else stays in the
+// wave's registers: scores are formed transposed, S^T = K Q^T, so a lane's column is
+// one query row and the statistics are per lane (one exchange between the half-waves
+// per tile), and the C layout of S^T is, with the keys taken in the order the
+// accumulator holds them, the B operand of O^T += V^T P^T. V^T comes from the row-major
+// tile by transposing LDS reads. So scores and weights never touch LDS.
 //
-// LDS rows are swizzled by 16-byte chunk (chunk ^ (row & 15)): the 32 rows a
-// K fragment reads at one chunk, and the rows a transposing read spans, fall
-// into different banks.
+// LDS rows are swizzled by 16-byte chunk: the 32 rows that a K fragment reads at one
+// chunk, and the rows that a transposing read spans, fall into different banks (no
+// conflict is counted).
+//
+// Rounding to 16 bits: the weights, for their product with V (relative 2^-9 or 2^-12 of
+// weights that are at most 2^8 times the largest), and the output, once. Sums are fp32.
+//
+// Bound by the matrix instructions and the exponentials between them; long prompts come
+// near what a large matrix product reaches: one of 4096 tokens, 32 heads of 128 134 us
+// (1.03 PFLOP/s; a product of 8192^3 1.26), one of 16384, 16 heads of 256 1.86 ms (1.18
+// PFLOP/s). Short ones wait for their first keys and for each other's copies: 32 of 58
+// to 1203 tokens 142 us, where bytes and products would each take 78.
 #include "attn_common.hpp"
 #include "attn_launch.hpp"
 
@@ -441,9 +451,10 @@ __device__ __forceinline__ const T *q_row(const TileArgs &a, const Where &t, int
 // Whole tiles: kWaves waves of 32 rows. With four (D = 128, shorter sequences), three
 // work-groups share a CU and overlap one's start and end with another's products; the
 // keys go 32 at a time, for which the registers suffice (two work-groups and 64 keys:
-// 128 sequences of 128 tokens 97 us against 85). With eight, the two waves of a SIMD (w and w + 4) go
-// through the two parts of a step in opposite order, a barrier after each part:
-// while one runs its score products the other forms weights.
+// 128 sequences of 128 tokens 97 us against 85). With eight, the two waves of a SIMD (w
+// and w + 4) go through the two parts of a step in opposite order, a barrier after each
+// part: while one runs its score products the other forms weights (16384 tokens, 16
+// heads of 256: 2658 us with four waves, 2130 with eight, when this was built; now 1859).
 template <typename T, int D, int kWaves, Keys kKeys>
 __global__ __launch_bounds__(64 * kWaves, kWaves == 4 ? 3 : 2) void attn_tile_kernel(TileArgs a) {
   constexpr int kBM = 32 * kWaves, kBN = kWaves == 4 ? 32 : 64;

@@ -415,9 +415,13 @@ typedef struct {
   int32_t tk_max;          /* rows of k and v in gdn_attn_prefill; 0 selects t_max */
   int32_t shared_max;      /* largest *shared_len (gdn_attn_paged); 0: no shared prefix */
 } gdn_attn_config;
+/* Limits (GDN_ERR_CAPACITY past them): t_max and tk_max <= GDN_T_MAX_LIMIT, n_max <=
+ * GDN_N_MAX_LIMIT, h <= 4096, t_max * h <= 0x7fff0000, max_pages * page_size <= 2^30. */
 
 /* Bytes of workspace gdn_attn_prefill and gdn_attn_paged need for `cfg` on the
  * current device (its compute units bound the number of partial results).
+ * How a call is cut depends on the capacities, so a smaller cfg can need more
+ * than a larger one: size a workspace for each cfg it serves.
  * Nothing in a workspace has to start at any value; calls that overlap in
  * time need workspaces of their own. */
 gdn_status gdn_attn_workspace_size(const gdn_attn_config *cfg, size_t *bytes);
@@ -464,7 +468,8 @@ gdn_status gdn_kv_append(const gdn_attn_config *cfg, const void *qkv, int64_t qk
  *   o (device) [t_max, h, d], dense: valid rows written
  *   workspace (device) >= gdn_attn_workspace_size bytes, 256-byte aligned.
  * A value that is not finite in k or v reaches at most the rows of its own
- * sequence. */
+ * sequence (in v, also those whose weight for it is 0). A row whose every score
+ * is -inf gives zeros, like one that sees no key. */
 gdn_status gdn_attn_prefill(const gdn_attn_config *cfg, const void *q, int64_t q_row,
                             const void *k, int64_t k_row, const void *v, int64_t v_row,
                             const int32_t *cu_q, const int32_t *cu_k, void *o, void *workspace,
@@ -476,12 +481,18 @@ gdn_status gdn_attn_prefill(const gdn_attn_config *cfg, const void *q, int64_t q
  *   q (device) [t_max, h, d], q_row as above
  *   shared_len (device, nullable = 0) int32 [1]: a promise that the batch's
  *            sequences have their first *shared_len positions in the same
- *            pages (equal leading block_table entries). Those pages are then
- *            read once for the whole batch, as whole pages and as far as all
- *            the sequences' new tokens come after them. At most
- *            cfg->shared_max (a larger value counts as that).
+ *            pages (equal leading block_table entries). Where cfg's
+ *            capacities make that worth its launches (a few new tokens per
+ *            sequence, and 256 MiB or more that n_max sequences would read of
+ *            shared_max positions), those pages are read once for the whole
+ *            batch, as whole pages and as far as all the sequences' new tokens
+ *            come after them. At most cfg->shared_max (a larger value counts
+ *            as that).
  *   o (device) [t_max, h, d], dense
- * A block_table entry that names no page reads page 0 or n_pages - 1. */
+ * A block_table entry that names no page reads page 0 or n_pages - 1. A value
+ * that is not finite in a query row, or in a key or value that rows read, comes
+ * out of those rows; one in a value also of the sequence's earlier rows, whose
+ * weight for it is 0. */
 gdn_status gdn_attn_paged(const gdn_attn_config *cfg, const void *q, int64_t q_row,
                           const void *k_pages, const void *v_pages, const int32_t *cu_seqlens,
                           const int32_t *kv_lens, const int32_t *block_table,

@@ -217,6 +217,7 @@ PREFILL = [
     ([140], [140], 17, 1, 128),               # a prime number of heads on one key head
     ([50, 33], [90, 40], 24, 1, 256),
     ([30], [40], 64, 2, 128),
+    ([2], [9], 4096, 1, 128),                 # the most heads
     ([i % 4 for i in range(100)], [520 + 5 * i for i in range(100)], 1, 1, 128),  # parts, many sequences
 ]
 
@@ -342,6 +343,10 @@ PAGED = [
     ([1, 2], [300, 40], 17, 1, 128, 16, 0),
     ([16 + i % 3 for i in range(70)], [600 + 7 * i for i in range(70)], 8, 1, 128, 64, 0),
     ([40] * 10, [900 + 31 * i for i in range(10)], 4, 1, 256, 32, 0),  # tiles with parts and without
+    ([4] * 9, [700 + 90 * i for i in range(9)], 8, 1, 128, 16, 0),     # two row tiles per item
+    ([8] * 9, [900 + 40 * i for i in range(9)], 8, 1, 128, 16, 400),   # four, behind a prefix
+    ([8] * 9, [900 + 40 * i for i in range(9)], 16, 2, 256, 64, 400),  # and items of two row tiles
+    ([1, 1], [90, 3], 2048, 1, 128, 16, 0),                            # very many heads
 ]
 
 
@@ -481,6 +486,38 @@ def test_both_capacity_limits_with_sequences_at_the_end():
         check_attention(o[n - 2 + i:n - 1 + i], f64(qq[n - 2 + i:n - 1 + i]), rk, rv, d ** -0.5, t)
     del q, k
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_prefill_of_rows_as_far_apart_as_they_may_be(d):
+    """k and v rows 2^24 elements apart: a tile's last offset is just below 2^31 bytes."""
+    t, T, far = torch.bfloat16, 100, 1 << 24
+    q, k, v = (normal(i, T, 1, d, dtype=t) for i in (1, 2, 3))
+    say(f"rows 2^24 apart d={d}")
+    buf = torch.zeros((T - 1) * far + 2 * d, dtype=t, device=DEV)
+    kd, vd = (buf[at:].as_strided((T, 1, d), (far, d, 1)) for at in (0, d))
+    kd.copy_(k.to(DEV)), vd.copy_(v.to(DEV))
+    o = gdn.causal_attention(q.to(DEV), kd, vd, on(cu_of([T])))
+    check_attention(o, f64(q), f64(k), f64(v), d ** -0.5, t)
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_batches_without_tokens_write_nothing(d):
+    t, h, hkv, page, n, T = torch.float16, 4, 2, 16, 3, 9
+    kp = torch.full((5, hkv, page, d), MARK, dtype=t, device=DEV)
+    vp, cu = kp.clone(), on(np.zeros(n + 1, np.int32))
+    kv, table = on(np.full(n, 20, np.int32)), on(np.zeros((n, 2), np.int32))
+    x = normal(1, T, (h + 2 * hkv) * d, dtype=t).to(DEV)
+    cfg = gdn.make_attn_config(T, n, h, hkv, d, t, page_size=page, n_pages=5, max_pages=2)
+    q, o = (torch.full((T, h, d), MARK, dtype=t, device=DEV) for _ in range(2))
+    k = torch.full((T, hkv, d), MARK, dtype=t, device=DEV)
+    gdn.gdn_qk_norm_rope(cfg, x, None, None, None, cu, None, q, k)
+    gdn.gdn_kv_append(cfg, x, None, None, None, cu, kv, table, q, k, kp, vp)
+    gdn.gdn_attn_prefill(cfg, q, k, k, cu, None, o, workspace(cfg))
+    gdn.gdn_attn_paged(cfg, q, kp, vp, cu, kv, table, None, o, workspace(cfg))
+    for y in (q, k, o, kp, vp):
+        assert (y == MARK).all()
 
 
 def test_paged_indexes_that_name_nothing_stay_inside():
@@ -629,6 +666,45 @@ def test_a_captured_decode_step_replays_with_other_lengths():
         torch.cuda.synchronize()
         assert torch.equal(o, o2) and torch.equal(q, q2), i
         assert torch.equal(kp, k2) and torch.equal(vp, v2), i
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_two_graphs_that_share_a_workspace(d):
+    """Split prefill, a prompt over pages and a decode step, captured apart with one
+    workspace and replayed in turn: nothing in it outlives a call."""
+    t, h, hkv, page = torch.bfloat16, 8, 2, 32
+    c = Cache([1500, 260], hkv, d, page, t, 90)
+    kp, vp, table = c.k.to(DEV), c.v.to(DEV), on(c.table)
+    kv, tail = on(np.array(c.lens, np.int32)), on(cu_of([1, 1]))
+    q = normal(91, 300, h, d, dtype=t).to(DEV)
+    k, v = (normal(92 + i, 1900, hkv, d, dtype=t).to(DEV) for i in range(2))
+    cu, cuk = on(cu_of([100, 200])), on(cu_of([900, 1000]))
+    cfgs = [gdn.make_attn_config(300, 2, h, hkv, d, t, tk_max=1900),
+            gdn.make_attn_config(300, 2, h, hkv, d, t, page_size=page, n_pages=c.n_pages,
+                                 max_pages=c.cols),
+            gdn.make_attn_config(2, 2, h, hkv, d, t, page_size=page, n_pages=c.n_pages,
+                                 max_pages=c.cols)]
+    calls = [lambda o, ws: gdn.gdn_attn_prefill(cfgs[0], q, k, v, cu, cuk, o, ws),
+             lambda o, ws: gdn.gdn_attn_paged(cfgs[1], q, kp, vp, cu, kv, table, None, o, ws),
+             lambda o, ws: gdn.gdn_attn_paged(cfgs[2], q[:2], kp, vp, tail, kv, table, None, o[:2], ws)]
+    want = []
+    for cfg, call in zip(cfgs, calls):
+        want.append(torch.zeros_like(q))
+        call(want[-1], workspace(cfg))
+    ws = torch.empty(max(gdn.gdn_attn_workspace_size(x) for x in cfgs), dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for call in calls:
+        outs.append(torch.zeros_like(q))
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call(outs[-1], ws)
+    for i in range(4):
+        for j in (0, 2, 1) if i % 2 else (1, 0, 2):
+            outs[j].zero_()
+            graphs[j].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, outs)), i
 
 
 def test_two_streams_with_their_own_workspaces():

@@ -176,14 +176,16 @@ struct Rows {
       for (int t = 0; t < kT; ++t)
         sc[t] = mfma32(*(Lds<const vec8>)(kt + at + 32 * t * D), q[i], sc[t]);
     }
-    // order: eight fragments ahead, then products and reads in turn
-    __builtin_amdgcn_sched_group_barrier(kSchedLds, 8, 0);
+    // order: some fragments ahead (with heads of 256 as many as the registers leave), then
+    // products and reads in turn
+    constexpr int kAhead = D == 128 ? 8 : 4;
+    __builtin_amdgcn_sched_group_barrier(kSchedLds, kAhead, 0);
 #pragma unroll
-    for (int i = 0; i < D / 16 * kT / 2 - 4; ++i) {
+    for (int i = 0; i < (D / 16 * kT - kAhead) / 2; ++i) {
       __builtin_amdgcn_sched_group_barrier(kSchedMfma, 2, 0);
       __builtin_amdgcn_sched_group_barrier(kSchedLds, 2, 0);
     }
-    __builtin_amdgcn_sched_group_barrier(kSchedMfma, 8, 0);
+    __builtin_amdgcn_sched_group_barrier(kSchedMfma, kAhead, 0);
     if (masked) {
       const int last = opaque<true>(lim - k0 - 4 * hh);
 #pragma unroll
@@ -239,16 +241,17 @@ struct Rows {
       }
     }
     // order: the first keys' fragments and weights, then under each product the
-    // reads of a later one and a part of the next weights
-    __builtin_amdgcn_sched_group_barrier(kSchedLds, 8, 1);
-    __builtin_amdgcn_sched_group_barrier(kSchedValu, 28, 1);
+    // reads of a later one and (heads of 128) a part of the next weights
+    constexpr int kAhead = D == 128 ? 4 : 2;
+    __builtin_amdgcn_sched_group_barrier(kSchedLds, 2 * kAhead, 1);
+    if (D == 128) __builtin_amdgcn_sched_group_barrier(kSchedValu, 28, 1);
 #pragma unroll
-    for (int i = 0; i < D / 32 * 2 * kT - 4; ++i) {
+    for (int i = 0; i < D / 32 * 2 * kT - kAhead; ++i) {
       __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 1);
       __builtin_amdgcn_sched_group_barrier(kSchedLds, 2, 1);
-      __builtin_amdgcn_sched_group_barrier(kSchedValu, D == 128 ? 7 : 4, 1);
+      if (D == 128) __builtin_amdgcn_sched_group_barrier(kSchedValu, 7, 1);
     }
-    __builtin_amdgcn_sched_group_barrier(kSchedMfma, 4, 1);
+    __builtin_amdgcn_sched_group_barrier(kSchedMfma, kAhead, 1);
   }
 
   // The running state as it is, for a later join.
@@ -457,7 +460,7 @@ __device__ __forceinline__ const T *q_row(const TileArgs &a, const Where &t, int
 // heads of 256: 2658 us with four waves, 2130 with eight, when this was built; now 1859).
 template <typename T, int D, int kWaves, Keys kKeys>
 __global__ __launch_bounds__(64 * kWaves, kWaves == 4 ? 3 : 2) void attn_tile_kernel(TileArgs a) {
-  constexpr int kBM = 32 * kWaves, kBN = kWaves == 4 ? 32 : 64;
+  constexpr int kBM = 32 * kWaves, kBN = kWaves == 4 || D == 256 ? 32 : 64;
   // four arrays of their own, so that a tile in flight is known to be another
   // than the ones being read
   __shared__ __attribute__((aligned(16))) T k_a[kBN * D], v_a[kBN * D], k_b[kBN * D], v_b[kBN * D];

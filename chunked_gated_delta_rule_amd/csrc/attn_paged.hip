@@ -8,7 +8,7 @@
 // HBM-bound on the keys and values, each read once per item: 256 sequences of about 2500
 // keys (2.7 GB) 465 us, 5.8 TB/s, where a large copy reaches 5.0 and a large sum, which
 // only reads, 4.0. Few keys are bound by latency: one token on 1000 keys 13 us, of which the
-// main kernel 8.7. 128 tokens behind 8192 shared positions 70 us: the prefix 37, the
+// main kernel 8.7. 128 tokens behind 8192 shared positions 70 us: the prefix 35, the
 // sequences' own 250 keys 25, the join 9.
 //
 //  * Work: all units of the batch in one line (key head, sequences in order, row

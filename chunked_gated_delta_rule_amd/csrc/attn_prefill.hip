@@ -21,10 +21,10 @@
 // weights that are at most 2^8 times the largest), and the output, once. Sums are fp32.
 //
 // Bound by the matrix instructions and the exponentials between them; long prompts come
-// near what a large matrix product reaches: one of 4096 tokens, 32 heads of 128 134 us
-// (1.03 PFLOP/s; a product of 8192^3 1.26), one of 16384, 16 heads of 256 1.86 ms (1.18
+// near what a large matrix product reaches: one of 4096 tokens, 32 heads of 128 132 us
+// (1.04 PFLOP/s; a product of 8192^3 1.26), one of 16384, 16 heads of 256 1.85 ms (1.19
 // PFLOP/s). Short ones wait for their first keys and for each other's copies: 32 of 58
-// to 1203 tokens 142 us, where bytes and products would each take 78.
+// to 1203 tokens 143 us, where bytes and products would each take 78.
 #include "attn_common.hpp"
 #include "attn_launch.hpp"
 
@@ -457,7 +457,7 @@ __device__ __forceinline__ const T *q_row(const TileArgs &a, const Where &t, int
 // 128 sequences of 128 tokens 97 us against 85). With eight, the two waves of a SIMD (w
 // and w + 4) go through the two parts of a step in opposite order, a barrier after each
 // part: while one runs its score products the other forms weights (16384 tokens, 16
-// heads of 256: 2658 us with four waves, 2130 with eight, when this was built; now 1859).
+// heads of 256: 2658 us with four waves, 2130 with eight, when this was built; now 1848).
 template <typename T, int D, int kWaves, Keys kKeys>
 __global__ __launch_bounds__(64 * kWaves, kWaves == 4 ? 3 : 2) void attn_tile_kernel(TileArgs a) {
   constexpr int kBM = 32 * kWaves, kBN = kWaves == 4 || D == 256 ? 32 : 64;

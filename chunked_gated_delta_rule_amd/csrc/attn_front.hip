@@ -5,11 +5,12 @@
 //   x' = x / sqrt(mean(x^2) + eps) * w
 //   (a, b) -> s (a cos t - b sin t, b cos t + a sin t),  t = position * inv_freq[i]
 //
-// HBM-bound: each row is read once and written once (8192 tokens of 40 heads of 128: 40
-// us, 4.1 TB/s, and 33 where the last-level cache still holds the rows; 32768 tokens of 20
-// heads of 256 into pages: 135 us, 5.0 TB/s, as a large copy). 512 or fewer tokens take 6 us, most of it latency. A 256-thread work-group takes a
-// few tokens; D / 8 lanes own a head's row, eight channels each, and the work-group
-// walks the heads of its tokens 2048 / D at a time, the next rows' loads in flight.
+// HBM-bound: each row is read once and written once (8192 tokens of 40 heads of 128: 39
+// us, 4.3 TB/s, and 32 where the last-level cache still holds the rows; 32768 tokens of 20
+// heads of 256 into pages: 130 us, 5.2 TB/s; a large copy reaches 5.0). 512 or fewer
+// tokens take 6 us, most of it latency. A 256-thread work-group takes one or two
+// tokens; D / 8 lanes own a head's row, eight channels each, and the work-group walks
+// the heads of its tokens 2048 / D at a time, the next rows' loads in flight.
 // The channels of a lane are chosen so that both members of its pairs are its own
 // (half layout: four channels and the four rot_dim / 2 further; interleaved: eight in
 // a row), so the rotation needs no other lane. Sequence, position, cache row, and the
@@ -23,9 +24,13 @@ namespace gdn {
 namespace {
 
 constexpr int kFrontThreads = 256;
-// Tokens per work-group at most (32768 tokens of 20 heads of 256: 137 us; with one 147,
-// with eight 144).
-constexpr int kMostTokens = 4;
+// Tokens per work-group at most (32768 tokens of 20 heads of 256 from HBM 132 us, 8192 of
+// 48 of 128 into pages 44; with one 142 and 43, four 136 and 49).
+constexpr int kMostTokens = 2;
+// Bytes written from which stores go past the caches, which then could not hold them for
+// the reader anyway: 132 -> 129 us at 335 MB, and with the attention that follows 16
+// prompts of 2048 tokens 722 -> 715; 16 of 512 (84 MB) would go from 106 to 111.
+constexpr int64_t kPastCache = 256 << 20;
 
 // How a lane's eight channels are placed: pairs inside the lane (half layout
 // with rot_dim a multiple of 8, or interleaved), or (half layout with any other
@@ -199,8 +204,16 @@ __global__ __launch_bounds__(kFrontThreads) void attn_front_kernel(FrontArgs a) 
     const u32x2 z0 = is_v ? y0 : u32x2{Elem<T>::pack(x[0], x[1]), Elem<T>::pack(x[2], x[3])};
     const u32x2 z1 = is_v ? y1 : u32x2{Elem<T>::pack(x[4], x[5]), Elem<T>::pack(x[6], x[7])};
     auto store = [&](T *p) __attribute__((always_inline)) {
-      *reinterpret_cast<u32x2 *>(p + c0) = z0;
-      *reinterpret_cast<u32x2 *>(p + c1) = z1;
+      u32x2 *const p0 = reinterpret_cast<u32x2 *>(p + c0), *const p1 = reinterpret_cast<u32x2 *>(p + c1);
+      if (a.past_cache) {
+        asm volatile("" ::: "memory");  // (the compiler would make one pair of the two)
+        __builtin_nontemporal_store(z0, p0);
+        __builtin_nontemporal_store(z1, p1);
+        asm volatile("" ::: "memory");
+      } else {
+        *p0 = z0;
+        *p1 = z1;
+      }
     };
     const int64_t t = t0 + tk;
     if (is_q) {
@@ -248,6 +261,8 @@ hipError_t launch_attn_front(const gdn_attn_config *cfg, FrontArgs a, hipStream_
   // several tokens per work-group once there are enough for every CU's eight
   const int most = cfg->t_max / (8 * cu_count());
   a.tokens = most < 1 ? 1 : most > kMostTokens ? kMostTokens : most;
+  const int64_t heads = (a.q ? cfg->h : 0) + (a.k ? cfg->hkv : 0) + (a.k_pages ? 2 * cfg->hkv : 0);
+  a.past_cache = heads * cfg->t_max * cfg->d * 2 > kPastCache;
   dim3 grid;
   if (!flat_grid((cfg->t_max + a.tokens - 1) / a.tokens, kFrontThreads, grid))
     return hipErrorInvalidValue;

@@ -21,7 +21,10 @@ struct FrontArgs {
   int rot_dim;
   float eps, rot_scale;
   int page_shift, n_pages, max_pages;
-  int tokens;  // per work-group; set by the launcher
+  // set by the launcher: tokens per work-group, and whether the outputs are too large for
+  // any cache
+  int tokens;
+  bool past_cache;
 };
 hipError_t launch_attn_front(const gdn_attn_config *cfg, FrontArgs a, hipStream_t stream);
 

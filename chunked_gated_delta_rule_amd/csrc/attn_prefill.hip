@@ -458,6 +458,8 @@ __device__ __forceinline__ const T *q_row(const TileArgs &a, const Where &t, int
 // and w + 4) go through the two parts of a step in opposite order, a barrier after each
 // part: while one runs its score products the other forms weights (16384 tokens, 16
 // heads of 256: 2658 us with four waves, 2130 with eight, when this was built; now 1848).
+// Their steps have 64 keys, or 32 with heads of 256, which leaves registers to read
+// fragments ahead (1836 -> 1820).
 template <typename T, int D, int kWaves, Keys kKeys>
 __global__ __launch_bounds__(64 * kWaves, kWaves == 4 ? 3 : 2) void attn_tile_kernel(TileArgs a) {
   constexpr int kBM = 32 * kWaves, kBN = kWaves == 4 || D == 256 ? 32 : 64;

@@ -180,6 +180,34 @@ def test_append(t, d, page, inter, rot):
     assert torch.equal(bits(kp3), bits(kp)) and torch.equal(bits(vp3), bits(vp))
 
 
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("d,rot,inter", [(128, 128, False), (128, 34, False), (256, 64, True)])
+def test_a_large_append_equals_its_halves(t, d, rot, inter):
+    """More than 256 MiB written in one call (outputs past the caches), against the same
+    sequence appended in two, which are small enough for them."""
+    h, hkv, page = 2, 1, 256
+    T = (280 << 20) // ((h + 3 * hkv) * d * 2) // 2 * 2
+    x = torch.randn(T, (h + 2 * hkv) * d, device=DEV).to(t)
+    w, f = normal(31, d, dtype=torch.float32).to(DEV), gdn.rope_inv_freq(rot).to(DEV)
+    pages = -(-T // page)
+    table = torch.randperm(pages, device=DEV).to(torch.int32)[None]
+    kp = torch.full((pages, hkv, page, d), MARK, dtype=t, device=DEV)
+    vp, k2, v2 = kp.clone(), kp.clone(), kp.clone()
+    say(f"large append {t} T={T} d={d}")
+
+    def append(rows, end, kp, vp):
+        n = rows.shape[0]
+        return gdn.append_paged_kv(rows, h, on(cu_of([n])), on(np.array([end], np.int32)), table, kp,
+                                   vp, w, w, f, interleaved=inter, output_k=True)
+
+    q, k = append(x, T, kp, vp)
+    parts = [append(x[:T // 2], T // 2, k2, v2), append(x[T // 2:], T, k2, v2)]
+    assert torch.equal(q, torch.cat([y[0] for y in parts]))
+    assert torch.equal(k, torch.cat([y[1] for y in parts]))
+    assert torch.equal(kp, k2) and torch.equal(vp, v2)
+    torch.cuda.empty_cache()
+
+
 def test_append_skips_rows_without_a_page():
     """Entries that name no page, columns past the table and negative positions."""
     t, d, page, hkv = torch.bfloat16, 128, 16, 1

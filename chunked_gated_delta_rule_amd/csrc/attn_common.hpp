@@ -84,6 +84,10 @@ __device__ __forceinline__ int opaque(int x) {
 
 constexpr float kNegInf = -__builtin_inff();
 
+// Bytes from which what a pass reads or writes once goes past the caches: what the last
+// level holds.
+constexpr int64_t kPastCache = 256 << 20;
+
 // Softmax statistics move only when a row's maximum (log2 scale) has grown by
 // more than this: the weights then stay below 2^8, exact enough in 16 bits and
 // in the fp32 sums, and the output sums are rescaled a few times per row only.
@@ -248,6 +252,15 @@ struct TiledBatch {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) v += tiles[j] >= x ? tiles[j] : 0;
     return all(v, [](int a, int b) { return a + b; });
+  }
+  // Whether every sequence has one tile at most and the keys that extra[1] counts, of
+  // `bytes` each, are more than the caches hold.
+  __device__ __forceinline__ bool past_cache(int bytes) const {
+    int v = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) v += tiles[j] > 0 ? seq[j].extra[1] >> 8 : 0;
+    const int64_t keys = (int64_t)all(v, [](int a, int b) { return a + b; }) << 8;
+    return from(2) == 0 && keys * bytes > kPastCache;
   }
   // Tile number r with the longest sequence first and the last tile of each first:
   // tile is its index in the sequence. False: there are fewer tiles.

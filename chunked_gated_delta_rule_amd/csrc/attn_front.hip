@@ -27,10 +27,6 @@ constexpr int kFrontThreads = 256;
 // Tokens per work-group at most (32768 tokens of 20 heads of 256 from HBM 132 us, 8192 of
 // 48 of 128 into pages 44; with one 142 and 43, four 136 and 49).
 constexpr int kMostTokens = 2;
-// Bytes written from which stores go past the caches, which then could not hold them for
-// the reader anyway: 132 -> 129 us at 335 MB, and with the attention that follows 16
-// prompts of 2048 tokens 722 -> 715; 16 of 512 (84 MB) would go from 106 to 111.
-constexpr int64_t kPastCache = 256 << 20;
 
 // How a lane's eight channels are placed: pairs inside the lane (half layout
 // with rot_dim a multiple of 8, or interleaved), or (half layout with any other
@@ -261,6 +257,9 @@ hipError_t launch_attn_front(const gdn_attn_config *cfg, FrontArgs a, hipStream_
   // several tokens per work-group once there are enough for every CU's eight
   const int most = cfg->t_max / (8 * cu_count());
   a.tokens = most < 1 ? 1 : most > kMostTokens ? kMostTokens : most;
+  // outputs that the caches could not hold for their reader are stored past them: 132 ->
+  // 129 us at 335 MB, and with the attention that follows 16 prompts of 2048 tokens 722 ->
+  // 715; 16 of 512 (84 MB) would go from 106 to 111
   const int64_t heads = (a.q ? cfg->h : 0) + (a.k ? cfg->hkv : 0) + (a.k_pages ? 2 * cfg->hkv : 0);
   a.past_cache = heads * cfg->t_max * cfg->d * 2 > kPastCache;
   dim3 grid;

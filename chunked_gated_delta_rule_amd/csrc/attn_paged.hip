@@ -6,7 +6,7 @@
 // taken all rows past them and left partial results, and the items start behind them.
 //
 // HBM-bound on the keys and values, each read once per item: 256 sequences of about 2500
-// keys (2.7 GB) 465 us, 5.8 TB/s, where a large copy reaches 5.0 and a large sum, which
+// keys (2.7 GB) 441 us, 6.1 TB/s, where a large copy reaches 5.0 and a large sum, which
 // only reads, 4.0. Few keys are bound by latency: one token on 1000 keys 13 us, of which the
 // main kernel 8.7. 128 tokens behind 8192 shared positions 70 us: the prefix 35, the
 // sequences' own 250 keys 25, the join 9.
@@ -30,6 +30,8 @@
 //    lane are the ones its scores hold, so weights never leave the lane.
 #include "attn_common.hpp"
 #include "attn_launch.hpp"
+
+#include <type_traits>
 
 namespace gdn {
 
@@ -60,6 +62,15 @@ __device__ __forceinline__ int64_t lane_of(int64_t x, int lane) {
 }
 
 __device__ __forceinline__ int units_of(int keys) { return (keys + kUnit - 1) / kUnit; }
+
+// Keys and values are read past the caches where those could not hold them (kPastCache):
+// 256 sequences of 2500 keys 471 -> 441 us, 128 of 1250 with two heads of 256 80 -> 75; but
+// 32 of 2200 (240 MB) would take 58 -> 53 from HBM and 48 -> 52 where the last call left them
+// in the cache, 64 of 190 (50 MB) 25 -> 29.
+template <bool kPast>
+__device__ __forceinline__ u32x4 load16(rsrc_t r, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, kPast ? 2 : 0);  // 2: not temporal
+}
 
 template <int kRT>
 __device__ __forceinline__ int row_tiles(int rows) {
@@ -177,256 +188,263 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
   pg.page_shift = uniform(pg.page_shift);
 
   const T *kpool = static_cast<const T *>(a.k_pages), *vpool = static_cast<const T *>(a.v_pages);
-  int64_t u = u0;
-  while (u < u1) {
-    // the item: its rows, its keys, the units of it in this run
-    const int seq = uniform(s), head = uniform(kh);
-    const Seq at = seq_at(pg, seq);
-    const Seq q{uniform(at.bos), uniform(at.n), uniform(at.kv)};
-    const int nu = units_of(q.kv - prefix);
-    // (one value per wave each, which the compiler does not see by itself)
-    const int rt = uniform((int)quotient(in_seq, nu)), un = uniform((int)(in_seq - (int64_t)rt * nu));
-    const int run = uniform((int)min((int64_t)(nu - un), u1 - u));
-    const int rows = q.n * G, r0 = rt * kRows;  // at most t_max * h, which fits
+  auto walk = [&](auto past) __attribute__((always_inline)) {
+    int64_t u = u0;
+    while (u < u1) {
+      // the item: its rows, its keys, the units of it in this run
+      const int seq = uniform(s), head = uniform(kh);
+      const Seq at = seq_at(pg, seq);
+      const Seq q{uniform(at.bos), uniform(at.n), uniform(at.kv)};
+      const int nu = units_of(q.kv - prefix);
+      // (one value per wave each, which the compiler does not see by itself)
+      const int rt = uniform((int)quotient(in_seq, nu)), un = uniform((int)(in_seq - (int64_t)rt * nu));
+      const int run = uniform((int)min((int64_t)(nu - un), u1 - u));
+      const int rows = q.n * G, r0 = rt * kRows;  // at most t_max * h, which fits
 
-    // this wave's 32 keys of unit i of the run, as two tiles of 16, each in one page
-    const int first = prefix + un * kUnit + 32 * w;
-    const int mine_n = min(run, units_of(q.kv - first));  // units in which it has keys
-    auto tile_key = [&](int i, int t) { return min(first + i * kUnit + 16 * t, (q.kv - 1) & ~15); };
-    int pages[2];
-    auto look = [&](int i) __attribute__((always_inline)) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t) pages[t] = page_of(pg, seq, tile_key(i, t));
-    };
-    // a tile's rows as a range that ends with the sequence's last key: zeros past it,
-    // where a page may hold anything
-    auto rows_of = [&](const T *pool, int i, int t) __attribute__((always_inline)) {
-      const int left = q.kv - (first + i * kUnit + 16 * t);
-      const T *p = pool + pool_row(pg, pages[t], tile_key(i, t), head, a.hkv) * D;
-      return make_rsrc(p, uniform(max(min(left, 16), 0)) * D * 2);
-    };
-    auto load_k = [&](Keys32<T, D> &x, int i) __attribute__((always_inline)) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const rsrc_t r = rows_of(kpool, i, t);
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j)
-          x.k[t][j] = __builtin_bit_cast(vec8, buf_load16(r, (c * D + 8 * g + 32 * j) * 2));
-      }
-    };
-    auto load_v = [&](Keys32<T, D> &x, int i) __attribute__((always_inline)) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const rsrc_t r = rows_of(vpool, i, t);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-          for (int b = 0; b < kDC; ++b)
-            x.v[b][4 * t + e] = buf_load16(r, ((4 * g + e) * D + 128 * b + 8 * c) * 2);
-      }
-    };
-    Keys32<T, D> x;
-    if (mine_n > 0) {
-      look(0);
-      load_k(x, 0);
-      load_v(x, 0);
-      if (mine_n > 1) look(1);
-    }
-    // the rows, while the first keys come
-    __syncthreads();  // the item before may still be read
-    for (int i = tid; i < kRows * (D / 8); i += 256) {
-      const int row = i / (D / 8), ch = i % (D / 8);
-      const int r = min(r0 + row, rows - 1), tok = r / G;
-      *reinterpret_cast<u32x4 *>(&qs[row][8 * ch]) = *reinterpret_cast<const u32x4 *>(
-          static_cast<const T *>(a.q) + (int64_t)(q.bos + tok) * a.q_row +
-          (head * G + (r - tok * G)) * D + 8 * ch);
-    }
-    if (un == 0 && tid < kRows && r0 + tid < rows) {
-      const int r = r0 + tid, tok = r / G;
-      const int64_t over = u + nu - u1;  // units of the item past this run
-      const int parts = over > 0 ? (int)quotient(over + per_wg - 1, per_wg) + 1 : 1;
-      plan[(int64_t)(q.bos + tok) * a.h + head * G + (r - tok * G)] = RowPlan{wg, parts, tid, 0};
-    }
-    int lim[kRT];  // the last key that this lane's row of each tile sees
-#pragma unroll
-    for (int t = 0; t < kRT; ++t) lim[t] = q.kv - q.n + min(r0 + 16 * t + c, rows - 1) / G;
-    const int all_see = q.kv - q.n + r0 / G;  // every row sees these
-    __syncthreads();
-
-    f32x4 o[kRT][kDC][8];
-    float m[kRT], l[kRT];
-#pragma unroll
-    for (int t = 0; t < kRT; ++t) {
-      m[t] = kNegInf;
-      l[t] = 0.f;
-#pragma unroll
-      for (int b = 0; b < kDC; ++b)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[t][b][j] = zero4();
-    }
-    // the next keys come while these are weighed, the next values while their scores
-    // are formed, in the registers that are free by then
-    for (int i = 0; i < mine_n; ++i) {
-      const int k0 = first + i * kUnit;
-      const bool masked = k0 + 31 > all_see;
-      // q's fragments are read anew for every unit (with one tile of 128 dims they fit
-      // the registers and the compiler keeps them)
-      const int qrow = opaque<(kRT * D > 128)>(c);
-      f32x4 sc[kRT][2];
-#pragma unroll
-      for (int t = 0; t < kRT; ++t) {
-        sc[t][0] = sc[t][1] = zero4();
-#pragma unroll
-        for (int p = 0; p < D / 32; ++p) {
-          const vec8 qf = *reinterpret_cast<const vec8 *>(&qs[16 * t + qrow][32 * p + 8 * g]);
-          sc[t][0] = mfma(x.k[0][p], qf, sc[t][0]);
-          sc[t][1] = mfma(x.k[1][p], qf, sc[t][1]);
+      // this wave's 32 keys of unit i of the run, as two tiles of 16, each in one page
+      const int first = prefix + un * kUnit + 32 * w;
+      const int mine_n = min(run, units_of(q.kv - first));  // units in which it has keys
+      auto tile_key = [&](int i, int t) { return min(first + i * kUnit + 16 * t, (q.kv - 1) & ~15); };
+      int pages[2];
+      auto look = [&](int i) __attribute__((always_inline)) {
+  #pragma unroll
+        for (int t = 0; t < 2; ++t) pages[t] = page_of(pg, seq, tile_key(i, t));
+      };
+      // a tile's rows as a range that ends with the sequence's last key: zeros past it,
+      // where a page may hold anything
+      auto rows_of = [&](const T *pool, int i, int t) __attribute__((always_inline)) {
+        const int left = q.kv - (first + i * kUnit + 16 * t);
+        const T *p = pool + pool_row(pg, pages[t], tile_key(i, t), head, a.hkv) * D;
+        return make_rsrc(p, uniform(max(min(left, 16), 0)) * D * 2);
+      };
+      auto load_k = [&](Keys32<T, D> &x, int i) __attribute__((always_inline)) {
+  #pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const rsrc_t r = rows_of(kpool, i, t);
+  #pragma unroll
+          for (int j = 0; j < D / 32; ++j)
+            x.k[t][j] = __builtin_bit_cast(
+                vec8, load16<decltype(past)::value>(r, (c * D + 8 * g + 32 * j) * 2));
         }
-      }
-      if (i + 1 < mine_n) load_k(x, i + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      vec8 pf[kRT];
-#pragma unroll
-      for (int t = 0; t < kRT; ++t) {
-        if (masked) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (k0 + 16 * (e >> 2) + 4 * g + (e & 3) > lim[t]) sc[t][e >> 2][e & 3] = kNegInf;
-        }
-        float mx = fmaxf(fmaxf(fmaxf(sc[t][0][0], sc[t][0][1]), fmaxf(sc[t][0][2], sc[t][0][3])),
-                         fmaxf(fmaxf(sc[t][1][0], sc[t][1][1]), fmaxf(sc[t][1][2], sc[t][1][3])));
-        mx = max32(max16(mx)) * a.scale_log2;
-        if (__any(mx > m[t] + kRescaleLog2)) {
-          const float mn = fmaxf(m[t], mx);
-          const float al = mn == kNegInf ? 1.f : fast_exp2(m[t] - mn);
-          m[t] = mn;
-          l[t] *= al;
-#pragma unroll
-          for (int b = 0; b < kDC; ++b)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[t][b][j] *= al;
-        }
-        const float ms = m[t] == kNegInf ? 0.f : m[t];
-        u32x4 pw;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float e0 = fast_exp2(fmaf(sc[t][e >> 1][2 * (e & 1)], a.scale_log2, -ms));
-          const float e1 = fast_exp2(fmaf(sc[t][e >> 1][2 * (e & 1) + 1], a.scale_log2, -ms));
-          l[t] += e0 + e1;
-          pw[e] = Elem<T>::pack(e0, e1);
-        }
-        pf[t] = __builtin_bit_cast(vec8, pw);
-      }
-#pragma unroll
-      for (int b = 0; b < kDC; ++b)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          u32x4 y;
-#pragma unroll
+      };
+      auto load_v = [&](Keys32<T, D> &x, int i) __attribute__((always_inline)) {
+  #pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const rsrc_t r = rows_of(vpool, i, t);
+  #pragma unroll
           for (int e = 0; e < 4; ++e)
-            y[e] = __builtin_amdgcn_perm(x.v[b][2 * e + 1][j >> 1], x.v[b][2 * e][j >> 1],
-                                         j & 1 ? 0x07060302u : 0x05040100u);
-          const vec8 vf = __builtin_bit_cast(vec8, y);
-#pragma unroll
-          for (int t = 0; t < kRT; ++t) o[t][b][j] = mfma(vf, pf[t], o[t][b][j]);
+  #pragma unroll
+            for (int b = 0; b < kDC; ++b)
+              x.v[b][4 * t + e] = load16<decltype(past)::value>(r, ((4 * g + e) * D + 128 * b + 8 * c) * 2);
         }
-      __builtin_amdgcn_sched_barrier(0);
-      if (i + 1 < mine_n) load_v(x, i + 1);
-      if (i + 2 < mine_n) look(i + 2);
-    }
+      };
+      Keys32<T, D> x;
+      if (mine_n > 0) {
+        look(0);
+        load_k(x, 0);
+        load_v(x, 0);
+        if (mine_n > 1) look(1);
+      }
+      // the rows, while the first keys come
+      __syncthreads();  // the item before may still be read
+      for (int i = tid; i < kRows * (D / 8); i += 256) {
+        const int row = i / (D / 8), ch = i % (D / 8);
+        const int r = min(r0 + row, rows - 1), tok = r / G;
+        *reinterpret_cast<u32x4 *>(&qs[row][8 * ch]) = *reinterpret_cast<const u32x4 *>(
+            static_cast<const T *>(a.q) + (int64_t)(q.bos + tok) * a.q_row +
+            (head * G + (r - tok * G)) * D + 8 * ch);
+      }
+      if (un == 0 && tid < kRows && r0 + tid < rows) {
+        const int r = r0 + tid, tok = r / G;
+        const int64_t over = u + nu - u1;  // units of the item past this run
+        const int parts = over > 0 ? (int)quotient(over + per_wg - 1, per_wg) + 1 : 1;
+        plan[(int64_t)(q.bos + tok) * a.h + head * G + (r - tok * G)] = RowPlan{wg, parts, tid, 0};
+      }
+      int lim[kRT];  // the last key that this lane's row of each tile sees
+  #pragma unroll
+      for (int t = 0; t < kRT; ++t) lim[t] = q.kv - q.n + min(r0 + 16 * t + c, rows - 1) / G;
+      const int all_see = q.kv - q.n + r0 / G;  // every row sees these
+      __syncthreads();
 
-    // ---- the four waves meet, one 16-row tile at a time
-#pragma unroll
-    for (int t = 0; t < kRT; ++t) {
-      l[t] = sum32(sum16x(l[t]));
-      if (g == 0) {
-        wm[w][16 * t + c] = m[t];
-        wl[w][16 * t + c] = l[t];
+      f32x4 o[kRT][kDC][8];
+      float m[kRT], l[kRT];
+  #pragma unroll
+      for (int t = 0; t < kRT; ++t) {
+        m[t] = kNegInf;
+        l[t] = 0.f;
+  #pragma unroll
+        for (int b = 0; b < kDC; ++b)
+  #pragma unroll
+          for (int j = 0; j < 8; ++j) o[t][b][j] = zero4();
+      }
+      // the next keys come while these are weighed, the next values while their scores
+      // are formed, in the registers that are free by then
+      for (int i = 0; i < mine_n; ++i) {
+        const int k0 = first + i * kUnit;
+        const bool masked = k0 + 31 > all_see;
+        // q's fragments are read anew for every unit (with one tile of 128 dims they fit
+        // the registers and the compiler keeps them)
+        const int qrow = opaque<(kRT * D > 128)>(c);
+        f32x4 sc[kRT][2];
+  #pragma unroll
+        for (int t = 0; t < kRT; ++t) {
+          sc[t][0] = sc[t][1] = zero4();
+  #pragma unroll
+          for (int p = 0; p < D / 32; ++p) {
+            const vec8 qf = *reinterpret_cast<const vec8 *>(&qs[16 * t + qrow][32 * p + 8 * g]);
+            sc[t][0] = mfma(x.k[0][p], qf, sc[t][0]);
+            sc[t][1] = mfma(x.k[1][p], qf, sc[t][1]);
+          }
+        }
+        if (i + 1 < mine_n) load_k(x, i + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        vec8 pf[kRT];
+  #pragma unroll
+        for (int t = 0; t < kRT; ++t) {
+          if (masked) {
+  #pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (k0 + 16 * (e >> 2) + 4 * g + (e & 3) > lim[t]) sc[t][e >> 2][e & 3] = kNegInf;
+          }
+          float mx = fmaxf(fmaxf(fmaxf(sc[t][0][0], sc[t][0][1]), fmaxf(sc[t][0][2], sc[t][0][3])),
+                           fmaxf(fmaxf(sc[t][1][0], sc[t][1][1]), fmaxf(sc[t][1][2], sc[t][1][3])));
+          mx = max32(max16(mx)) * a.scale_log2;
+          if (__any(mx > m[t] + kRescaleLog2)) {
+            const float mn = fmaxf(m[t], mx);
+            const float al = mn == kNegInf ? 1.f : fast_exp2(m[t] - mn);
+            m[t] = mn;
+            l[t] *= al;
+  #pragma unroll
+            for (int b = 0; b < kDC; ++b)
+  #pragma unroll
+              for (int j = 0; j < 8; ++j) o[t][b][j] *= al;
+          }
+          const float ms = m[t] == kNegInf ? 0.f : m[t];
+          u32x4 pw;
+  #pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float e0 = fast_exp2(fmaf(sc[t][e >> 1][2 * (e & 1)], a.scale_log2, -ms));
+            const float e1 = fast_exp2(fmaf(sc[t][e >> 1][2 * (e & 1) + 1], a.scale_log2, -ms));
+            l[t] += e0 + e1;
+            pw[e] = Elem<T>::pack(e0, e1);
+          }
+          pf[t] = __builtin_bit_cast(vec8, pw);
+        }
+  #pragma unroll
+        for (int b = 0; b < kDC; ++b)
+  #pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            u32x4 y;
+  #pragma unroll
+            for (int e = 0; e < 4; ++e)
+              y[e] = __builtin_amdgcn_perm(x.v[b][2 * e + 1][j >> 1], x.v[b][2 * e][j >> 1],
+                                           j & 1 ? 0x07060302u : 0x05040100u);
+            const vec8 vf = __builtin_bit_cast(vec8, y);
+  #pragma unroll
+            for (int t = 0; t < kRT; ++t) o[t][b][j] = mfma(vf, pf[t], o[t][b][j]);
+          }
+        __builtin_amdgcn_sched_barrier(0);
+        if (i + 1 < mine_n) load_v(x, i + 1);
+        if (i + 2 < mine_n) look(i + 2);
+      }
+
+      // ---- the four waves meet, one 16-row tile at a time
+  #pragma unroll
+      for (int t = 0; t < kRT; ++t) {
+        l[t] = sum32(sum16x(l[t]));
+        if (g == 0) {
+          wm[w][16 * t + c] = m[t];
+          wl[w][16 * t + c] = l[t];
+        }
+      }
+      const bool from_start = un == 0, to_end = un + run == nu;
+      const bool whole = from_start && to_end;
+      // whole and alone: the output; whole beside a prefix: the row's place; else
+      // this work-group's place 0 (the item began before it) or 1 (it goes on)
+      const bool last = whole && prefix == 0;
+      const int64_t place = (int64_t)wg * 2 + (from_start ? 1 : 0);
+  #pragma unroll
+      for (int t = 0; t < kRT; ++t) {
+        __syncthreads();
+        float big = kNegInf;
+  #pragma unroll
+        for (int i = 0; i < 4; ++i) big = fmaxf(big, wm[i][16 * t + c]);
+        const float f = m[t] == kNegInf ? 0.f : fast_exp2(m[t] - big);
+  #pragma unroll
+        for (int b = 0; b < kDC; ++b)
+  #pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float *p = &os[w][c][128 * b + 32 * g + 8 * i];
+            const auto &x = o[t][b];
+            *reinterpret_cast<f32x4 *>(p) = f32x4{x[0][i] * f, x[1][i] * f, x[2][i] * f, x[3][i] * f};
+            *reinterpret_cast<f32x4 *>(p + 4) =
+                f32x4{x[4][i] * f, x[5][i] * f, x[6][i] * f, x[7][i] * f};
+          }
+        __syncthreads();
+        // sixteen threads per row, 4 dims each at a time
+        const int row = tid >> 4, q4 = 4 * (tid & 15);
+        const int r = r0 + 16 * t + row;
+        if (r < rows) {
+          float mm = kNegInf, ll = 0.f;
+  #pragma unroll
+          for (int i = 0; i < 4; ++i) mm = fmaxf(mm, wm[i][16 * t + row]);
+  #pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float mi = wm[i][16 * t + row];
+            ll += wl[i][16 * t + row] * (mi == kNegInf ? 0.f : fast_exp2(mi - mm));
+          }
+          const int tok = r / G;
+          const int64_t orow = (int64_t)(q.bos + tok) * a.h + head * G + (r - tok * G);
+          const float inv = ll == 0.f ? 0.f : 1.f / ll;
+          float *po, *pm;
+          if (whole) {
+            po = a.done_o + orow * D;
+            pm = a.done_ml + orow * 2;
+          } else {
+            po = a.part_o + (place * kRows + 16 * t + row) * D;
+            pm = a.part_ml + (place * kRows + 16 * t + row) * 2;
+          }
+          if (!last && (tid & 15) == 0) {
+            pm[0] = mm;
+            pm[1] = ll;
+          }
+  #pragma unroll
+          for (int b = 0; b < D / 64; ++b) {
+            f32x4 sum = zero4();
+  #pragma unroll
+            for (int i = 0; i < 4; ++i)
+              sum += *reinterpret_cast<const f32x4 *>(&os[i][row][64 * b + q4]);
+            if (last)
+              *reinterpret_cast<u32x2 *>(static_cast<T *>(a.o) + orow * D + 64 * b + q4) =
+                  u32x2{Elem<T>::pack(sum[0] * inv, sum[1] * inv),
+                        Elem<T>::pack(sum[2] * inv, sum[3] * inv)};
+            else
+              *reinterpret_cast<f32x4 *>(po + 64 * b + q4) = sum;
+          }
+        }
+      }
+
+      // ---- the next item
+      u += run;
+      in_seq += run;
+      in_head += run;
+      if (u >= u1) break;
+      if (in_head == per_head) {
+        ++kh;
+        in_head = in_seq = 0;
+        s = 0;
+        while (uniform(units_in(s)) == 0) ++s;
+      } else if (in_seq == uniform(units_in(s))) {
+        in_seq = 0;
+        ++s;
+        while (uniform(units_in(s)) == 0) ++s;
       }
     }
-    const bool from_start = un == 0, to_end = un + run == nu;
-    const bool whole = from_start && to_end;
-    // whole and alone: the output; whole beside a prefix: the row's place; else
-    // this work-group's place 0 (the item began before it) or 1 (it goes on)
-    const bool last = whole && prefix == 0;
-    const int64_t place = (int64_t)wg * 2 + (from_start ? 1 : 0);
-#pragma unroll
-    for (int t = 0; t < kRT; ++t) {
-      __syncthreads();
-      float big = kNegInf;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) big = fmaxf(big, wm[i][16 * t + c]);
-      const float f = m[t] == kNegInf ? 0.f : fast_exp2(m[t] - big);
-#pragma unroll
-      for (int b = 0; b < kDC; ++b)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float *p = &os[w][c][128 * b + 32 * g + 8 * i];
-          const auto &x = o[t][b];
-          *reinterpret_cast<f32x4 *>(p) = f32x4{x[0][i] * f, x[1][i] * f, x[2][i] * f, x[3][i] * f};
-          *reinterpret_cast<f32x4 *>(p + 4) =
-              f32x4{x[4][i] * f, x[5][i] * f, x[6][i] * f, x[7][i] * f};
-        }
-      __syncthreads();
-      // sixteen threads per row, 4 dims each at a time
-      const int row = tid >> 4, q4 = 4 * (tid & 15);
-      const int r = r0 + 16 * t + row;
-      if (r < rows) {
-        float mm = kNegInf, ll = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mm = fmaxf(mm, wm[i][16 * t + row]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float mi = wm[i][16 * t + row];
-          ll += wl[i][16 * t + row] * (mi == kNegInf ? 0.f : fast_exp2(mi - mm));
-        }
-        const int tok = r / G;
-        const int64_t orow = (int64_t)(q.bos + tok) * a.h + head * G + (r - tok * G);
-        const float inv = ll == 0.f ? 0.f : 1.f / ll;
-        float *po, *pm;
-        if (whole) {
-          po = a.done_o + orow * D;
-          pm = a.done_ml + orow * 2;
-        } else {
-          po = a.part_o + (place * kRows + 16 * t + row) * D;
-          pm = a.part_ml + (place * kRows + 16 * t + row) * 2;
-        }
-        if (!last && (tid & 15) == 0) {
-          pm[0] = mm;
-          pm[1] = ll;
-        }
-#pragma unroll
-        for (int b = 0; b < D / 64; ++b) {
-          f32x4 sum = zero4();
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            sum += *reinterpret_cast<const f32x4 *>(&os[i][row][64 * b + q4]);
-          if (last)
-            *reinterpret_cast<u32x2 *>(static_cast<T *>(a.o) + orow * D + 64 * b + q4) =
-                u32x2{Elem<T>::pack(sum[0] * inv, sum[1] * inv),
-                      Elem<T>::pack(sum[2] * inv, sum[3] * inv)};
-          else
-            *reinterpret_cast<f32x4 *>(po + 64 * b + q4) = sum;
-        }
-      }
-    }
-
-    // ---- the next item
-    u += run;
-    in_seq += run;
-    in_head += run;
-    if (u >= u1) break;
-    if (in_head == per_head) {
-      ++kh;
-      in_head = in_seq = 0;
-      s = 0;
-      while (uniform(units_in(s)) == 0) ++s;
-    } else if (in_seq == uniform(units_in(s))) {
-      in_seq = 0;
-      ++s;
-      while (uniform(units_in(s)) == 0) ++s;
-    }
-  }
+  };
+  if (total > kPastCache / (kUnit * D * 4))
+    walk(std::true_type{});
+  else
+    walk(std::false_type{});
 }
 
 // Joins what several work-groups, the shared prefix's included, left of a row, and

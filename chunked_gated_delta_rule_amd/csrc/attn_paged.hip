@@ -6,7 +6,7 @@
 // taken all rows past them and left partial results, and the items start behind them.
 //
 // HBM-bound on the keys and values, each read once per item: 256 sequences of about 2500
-// keys (2.7 GB) 441 us, 6.1 TB/s, where a large copy reaches 5.0 and a large sum, which
+// keys (2.7 GB) 422 us, 6.4 TB/s, where a large copy reaches 5.0 and a large sum, which
 // only reads, 4.0. Few keys are bound by latency: one token on 1000 keys 13 us, of which the
 // main kernel 8.7. 128 tokens behind 8192 shared positions 70 us: the prefix 35, the
 // sequences' own 250 keys 25, the join 9.

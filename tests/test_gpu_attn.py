@@ -452,6 +452,22 @@ def test_paged_keeps_what_is_not_finite_in_its_rows(new, full, h, hkv, d, page, 
     assert not o[b:][torch.from_numpy(reads).to(DEV)].isfinite().any()
 
 
+@pytest.mark.parametrize("d,hkv", [(128, 8), (256, 4)])
+def test_paged_of_more_keys_than_the_caches_hold(d, hkv):
+    """66000 keys of 4096 bytes, read past the caches: a streamed row and tiles in parts."""
+    t, h, T, lens = torch.bfloat16, 4 * hkv, 20, [66000, 300]
+    c = Cache(lens, hkv, d, 256, t, 17)
+    kp, vp, table, kv = c.k.to(DEV), c.v.to(DEV), on(c.table), on(np.array(lens, np.int32))
+    q = normal(5, T + 1, h, d, dtype=t)
+    for new in ([1, 1], [T, 1]):
+        say(f"more keys than the caches hold d={d} new={new}")
+        cu = cu_of(new)
+        o = gdn.paged_attention(q[:sum(new)].to(DEV), kp, vp, on(cu), kv, table)
+        for s in range(2):
+            a = slice(cu[s], cu[s + 1])
+            check_attention(o[a], f64(q[a]), *c.rows(s), d ** -0.5, t)
+
+
 @pytest.mark.parametrize("t", TYPES)
 @pytest.mark.parametrize("T,past,d", [(2100, 333, 128), (700, 900, 256)])
 def test_paged_of_a_long_prompt_at_sampled_rows(t, T, past, d):

@@ -454,7 +454,8 @@ def chunk_gated_delta_rule(q, k, v, g, beta, cu_seqlens, initial_state=None,
     return o, hT
 
 
-# ---- softmax-attention layers of a hybrid stack (include/gdn.h, last section)
+# ---- softmax-attention layers of a hybrid stack (include/gdn.h, last section). Forward
+# only, like the calls above: results carry no gradient.
 
 def make_attn_config(t_max, n_max, h, hkv, d=128, dtype=GDN_BF16, scale=0.0, eps=1e-6, rot_dim=0,
                      rot_interleaved=False, rot_scale=0.0, page_size=16, n_pages=0, max_pages=0,
@@ -672,8 +673,9 @@ def qk_norm_rope(qkv, heads, kv_heads, cu_seqlens, q_weight=None, k_weight=None,
     """Allocate outputs with torch and run gdn_qk_norm_rope on the current stream.
 
     qkv [T, (heads + 2 kv_heads) d] bf16 or fp16; weights fp32 [d] or None (no
-    norm); inv_freq fp32 [rot_dim / 2] or None (no rotation). Returns (q [T,
-    heads, d], k [T, kv_heads, d]); v is qkv's last kv_heads d columns."""
+    norm); inv_freq fp32 [rot_dim / 2] or None (no rotation); rot_scale a factor
+    on cos and sin (0 counts as 1). Returns (q [T, heads, d], k [T, kv_heads,
+    d]); v is qkv's last kv_heads d columns."""
     T, d = _packed_qkv(qkv, heads, kv_heads)
     cfg = make_attn_config(T, cu_seqlens.numel() - 1, heads, kv_heads, d, qkv.dtype, eps=eps,
                            rot_dim=0 if inv_freq is None else 2 * inv_freq.numel(),
@@ -737,8 +739,8 @@ def causal_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, scale=None, workspa
 
     q [T, heads, d], k and v [Tk, kv_heads, d], bf16 or fp16, rows of any stride;
     the queries are the last tokens of their keys (cu_seqlens_k None: the same
-    tokens). Returns o [T, heads, d]; rows behind the last sequence are not
-    written."""
+    tokens); scale: of the scores, positive (None: 1 / sqrt(d)). Returns o [T,
+    heads, d]; rows behind the last sequence are not written."""
     if q.dim() != 3 or k.dim() != 3 or v.shape != k.shape or k.shape[2] != q.shape[2] or \
             not q.dtype == k.dtype == v.dtype:
         raise ValueError(f"q [T, heads, d] and k, v [Tk, kv_heads, d] of one dtype expected: "

@@ -93,6 +93,18 @@ constexpr int64_t kPastCache = 256 << 20;
 // in the fp32 sums, and the output sums are rescaled a few times per row only.
 constexpr float kRescaleLog2 = 8.f;
 
+// A weight's exponent, score * scale - m, is one fused step, so it contains the rounding of
+// m = max * scale, up to 2^-24 |m|: a factor common to the row, which cancels. Past a maximum
+// of this size the factor could leave the 16-bit types (past 2^32, fp32 as well: keys held
+// off with the type's lowest value). The score and the maximum are then rounded alike
+// before they are subtracted, which leaves 0 for equal ones.
+constexpr float kFarLog2 = 1 << 20;
+__device__ __forceinline__ float far_exponent(float score, float scale_log2, float m) {
+  float s = score * scale_log2;
+  asm("" : "+v"(s));  // (the two would be fused after all)
+  return s - m;
+}
+
 // Narrows [0, n) to at most 64 indexes that hold the last s with key(s) <= x, for
 // a non-decreasing key with key(0) <= x, by one wave: 64 probes per level (n <=
 // 16384: at most two levels). [lo, lo + len) stays inside [0, n) for any key.

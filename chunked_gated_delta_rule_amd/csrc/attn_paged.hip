@@ -268,10 +268,12 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
 
       f32x4 o[kRT][kDC][8];
       float m[kRT], l[kRT];
+      int far[kRT];  // whether some row's maximum is past kFarLog2
   #pragma unroll
       for (int t = 0; t < kRT; ++t) {
         m[t] = kNegInf;
         l[t] = 0.f;
+        far[t] = 0;
   #pragma unroll
         for (int b = 0; b < kDC; ++b)
   #pragma unroll
@@ -318,13 +320,21 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
             for (int b = 0; b < kDC; ++b)
   #pragma unroll
               for (int j = 0; j < 8; ++j) o[t][b][j] *= al;
+            far[t] = __any(m[t] != kNegInf && fabsf(m[t]) > kFarLog2);
           }
-          const float ms = m[t] == kNegInf ? 0.f : m[t];
+          float ms = m[t] == kNegInf ? 0.f : m[t], scale = a.scale_log2;
+          if (far[t]) {
+  #pragma unroll
+            for (int e = 0; e < 8; ++e)
+              sc[t][e >> 2][e & 3] = far_exponent(sc[t][e >> 2][e & 3], scale, ms);
+            ms = 0.f;
+            scale = 1.f;
+          }
           u32x4 pw;
   #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float e0 = fast_exp2(fmaf(sc[t][e >> 1][2 * (e & 1)], a.scale_log2, -ms));
-            const float e1 = fast_exp2(fmaf(sc[t][e >> 1][2 * (e & 1) + 1], a.scale_log2, -ms));
+            const float e0 = fast_exp2(fmaf(sc[t][e >> 1][2 * (e & 1)], scale, -ms));
+            const float e1 = fast_exp2(fmaf(sc[t][e >> 1][2 * (e & 1) + 1], scale, -ms));
             l[t] += e0 + e1;
             pw[e] = Elem<T>::pack(e0, e1);
           }

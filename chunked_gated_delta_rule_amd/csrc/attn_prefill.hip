@@ -146,8 +146,12 @@ struct Rows {
   f32x16 o[D / 32];
   f32x16 sc[kT];
   float m, l;  // maximum (log2 scale) and this lane's part of the sum
+  // weights are 2^(sc * mul - sub): with the scale and the maximum, or with 1 and 0 where some
+  // row's maximum is far (past kFarLog2) and score() leaves the exponents themselves in sc
+  float mul, sub;
+  int far;
 
-  __device__ __forceinline__ void load(const T *row, int hh) {
+  __device__ __forceinline__ void load(const T *row, int hh, float scale_log2) {
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
       q[i] = *reinterpret_cast<const vec8 *>(row + 8 * hh + 16 * i);
@@ -157,7 +161,14 @@ struct Rows {
       for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
     m = kNegInf;
     l = 0.f;
+    mul = scale_log2;
+    sub = 0.f;
+    far = 0;
   }
+
+  // (not seen through: the compiler would copy the rest of the step for either answer,
+  // which costs the part kernel its registers)
+  __device__ __forceinline__ bool is_far() const { return uniform(opaque<true>(far)); }
 
   // Scores of the tile, and the running maximum.
   __device__ __forceinline__ void score(Lds<T> kt, int k0, int lim, bool masked, float scale_log2,
@@ -210,12 +221,28 @@ struct Rows {
       for (int i = 0; i < D / 32; ++i)
 #pragma unroll
         for (int k = 0; k < 16; ++k) o[i][k] *= al;
+      const float ms = m == kNegInf ? 0.f : m;
+      far = __any(fabsf(ms) > kFarLog2);
+      mul = far ? 1.f : scale_log2;
+      sub = far ? 0.f : ms;
+    }
+    if (is_far()) {
+      const float ms = m == kNegInf ? 0.f : m;
+#pragma unroll
+      for (int t = 0; t < kT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sc[t][i] = far_exponent(sc[t][i], scale_log2, ms);
     }
   }
 
   // Weights of the tile, and their products with its values.
   __device__ __forceinline__ void weigh(Lds<T> vt, float scale_log2, int lane) {
-    const float ms = m == kNegInf ? 0.f : m;
+    float by = mul, ms = sub;
+    if constexpr (D == 256) {  // (no register left to keep them: 16384 tokens 1900 us against 1805)
+      const bool f = is_far();
+      by = f ? 1.f : scale_log2;
+      ms = f || m == kNegInf ? 0.f : m;
+    }
     // lane's part of a transposing read: row 4 hh + (s16 >> 2) (+ 8), columns 32 i +
     // 16 gb + 4 (s16 & 3)
     const int hh = lane >> 5, s16 = lane & 15, gb = (lane >> 4) & 1, r0 = 4 * hh + (s16 >> 2);
@@ -228,8 +255,8 @@ struct Rows {
       uint32_t wd[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float e0 = fast_exp2(fmaf(sc[b >> 1][8 * (b & 1) + 2 * i], scale_log2, -ms));
-        const float e1 = fast_exp2(fmaf(sc[b >> 1][8 * (b & 1) + 2 * i + 1], scale_log2, -ms));
+        const float e0 = fast_exp2(fmaf(sc[b >> 1][8 * (b & 1) + 2 * i], by, -ms));
+        const float e1 = fast_exp2(fmaf(sc[b >> 1][8 * (b & 1) + 2 * i + 1], by, -ms));
         l += e0 + e1;
         wd[i] = Elem<T>::pack(e0, e1);
       }
@@ -501,7 +528,7 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 4 ? 3 : 2) void attn_tile_ke
     get_k(0, k_a, s);
     get_v(0, v_a, s);
   }
-  x.load(q_row<T>(a, t, see.tok, 32 * w + col, D), hh);
+  x.load(q_row<T>(a, t, see.tok, 32 * w + col, D), hh, a.scale_log2);
   auto score = [&](int j, T *kt) __attribute__((always_inline)) {
     const int k0 = j * kBN;
     if (k0 <= see.hi) x.score((Lds<T>)kt, k0, see.lim, k0 + kBN - 1 > see.lo, a.scale_log2, lane);
@@ -642,7 +669,7 @@ __global__ __launch_bounds__(512, 2) void attn_part_kernel(TileArgs a) {
       get_k(0, k_a, s);
       get_v(0, v_a, s);
     }
-    x.load(q_row<T>(a, t, see.tok, 32 * w + col, D), hh);
+    x.load(q_row<T>(a, t, see.tok, 32 * w + col, D), hh, a.scale_log2);
     auto score = [&](int j, T *kt) __attribute__((always_inline)) {
       const int k0 = (j0 + 2 * j) * kBN;
       if (has(j) && k0 <= see.hi)

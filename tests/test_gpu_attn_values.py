@@ -1,0 +1,85 @@
+"""Softmax attention at the ends of its types' ranges, against the fp64 oracle. Every way
+that keys and values are read takes each case. Bounds: attn_helpers.py, except where one
+is stated."""
+
+import numpy as np
+import pytest
+import torch
+
+import chunked_gated_delta_rule_amd as gdn
+from attn_helpers import DEV, cu_of, f64, half_step, normal, on, shared_cols, widened
+from oracle import attention
+
+pytestmark = pytest.mark.gpu
+
+# new tokens, keys, query and key heads; pages (0: packed rows); sequences behind a shared
+# prefix (0: one sequence)
+WAYS = {
+    "rows": (150, 150, 4, 2, 0, 0),           # whole tiles
+    "row parts": (20, 700, 2, 1, 0, 0),       # tiles with their keys in parts, joined
+    "stream": (1, 30, 4, 1, 16, 0),           # one wave's keys
+    "stream parts": (2, 900, 4, 2, 16, 0),    # work-groups joined
+    "pages": (80, 300, 4, 1, 32, 0),          # tiles over the pages
+    "page parts": (80, 1500, 4, 1, 64, 0),
+    "prefix": (2, 400, 4, 1, 16, 3),          # a prefix of 64 read once, joined with the streams
+}
+
+
+def through(way, q, k, v, scale):
+    """o of one sequence's rows (of the last sequence behind a prefix)."""
+    _, _, _, _, page, n = WAYS[way]
+    T, Tk, (hkv, d) = len(q), len(k), k.shape[1:]
+    if not page:
+        return gdn.causal_attention(q.to(DEV), k.to(DEV), v.to(DEV), on(cu_of([T])),
+                                    on(cu_of([Tk])), scale=scale)
+    pages = -(-Tk // page)
+    pool = [torch.nn.functional.pad(x, (0, 0, 0, 0, 0, pages * page - Tk))
+            .view(pages, page, hkv, d).transpose(1, 2).contiguous().to(DEV) for x in (k, v)]
+    table = np.arange(pages, dtype=np.int32)[None]
+    if not n:
+        return gdn.paged_attention(q.to(DEV), *pool, on(cu_of([T])), on(np.array([Tk], np.int32)),
+                                   on(table), scale=scale)
+    table = widened(table.repeat(n, 0), shared_cols(n, hkv, d, page))
+    o = gdn.paged_attention(q.repeat(n, 1, 1).to(DEV), *pool, on(cu_of([T] * n)),
+                            on(np.full(n, Tk, np.int32)), on(table),
+                            on(np.array([64], np.int32)), scale=scale)
+    assert all(torch.equal(o[:T], o[T * i:T * (i + 1)]) for i in range(n))
+    return o[-T:]
+
+
+def zeros(way, d, t):
+    T, Tk, h, hkv, _, _ = WAYS[way]
+    return torch.zeros(T, h, d, dtype=t), torch.zeros(Tk, hkv, d, dtype=t)
+
+
+# values of q and of k in the first dims (so many of them), and the scale
+FAR = [("lowest", torch.bfloat16, 1.0, torch.finfo(torch.bfloat16).min, 1, None),
+       ("highest", torch.bfloat16, 1.0, torch.finfo(torch.bfloat16).max, 1, None),
+       ("large", torch.bfloat16, 48640.0, 48640.0, 1, None),
+       ("large and low", torch.bfloat16, 48640.0, -48640.0, 128, None),
+       ("fp16 lowest", torch.float16, 65504.0, -65504.0, 128, None),
+       ("fp16 highest", torch.float16, 65504.0, 65504.0, 128, None),
+       ("fp16, one dim", torch.float16, 65504.0, 65504.0, 1, 0.75),
+       ("a large scale", torch.float16, 3.0, 5.0, 1, 1e9)]
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("name,t,a,b,dims,scale", FAR)
+def test_equal_scores_of_any_size_weigh_the_same(way, d, name, t, a, b, dims, scale):
+    """The first 30 keys of a sequence have one score, far past where fp32 holds a score's
+    fraction, the others 0 (so the former are masked, or mask). Keys of the same bits
+    have scores of the same bits: they weigh exactly the same, whatever the size, and no
+    term of the bound goes by it."""
+    q, k = zeros(way, d, t)
+    q[..., :dims] = a
+    k[:30, :, :dims] = b
+    v = normal(4, *k.shape, dtype=t)
+    print(f"equal scores {name} {way} d={d}", flush=True)
+    got = f64(through(way, q, k, v, scale))
+    o, mag, total = attention.attend(f64(q), f64(k), f64(v), d ** -0.5 if scale is None else scale)
+    u = half_step(t)
+    bound = 1.01 * (u * np.abs(o) + (u + 2.0 ** -18) * mag) + 2.0 ** -25
+    off = np.abs(got - o)
+    print(f"  off / bound {np.max(off / bound):.3f}", flush=True)
+    assert np.all(off <= bound), np.max(off / bound)

@@ -18,11 +18,16 @@ __device__ __forceinline__ f32x16 mfma32(f16x8 a, f16x8 b, f32x16 c) {
 
 // The two 16-bit element types: the MFMA operand vector, the rounding of a
 // pair (to nearest even), and the value of the low and high half of a word.
+// kWeightLog2: softmax weights, and with them their sum, are formed 2^kWeightLog2 times
+// larger. fp16 has few exponents below 1: weights from 2^-21 of the row's largest on are
+// then normal numbers, and smaller ones off by 2^-32 of it at most (2^-14 and 2^-25
+// without). The largest can be 2^kRescaleLog2 times that, which fp16 still holds.
 template <typename T>
 struct Elem;
 template <>
 struct Elem<__bf16> {
   typedef bf16x8 vec8;
+  static constexpr float kWeightLog2 = 0.f;
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
   }
@@ -32,6 +37,7 @@ struct Elem<__bf16> {
 template <>
 struct Elem<_Float16> {
   typedef f16x8 vec8;
+  static constexpr float kWeightLog2 = 7.f;
   static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack_f16(a, b); }
   static __device__ __forceinline__ float lo(uint32_t w) {
     return static_cast<float>(__builtin_bit_cast(f16x2, w)[0]);

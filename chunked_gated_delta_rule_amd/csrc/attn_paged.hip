@@ -330,6 +330,7 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
             ms = 0.f;
             scale = 1.f;
           }
+          ms -= Elem<T>::kWeightLog2;
           u32x4 pw;
   #pragma unroll
           for (int e = 0; e < 4; ++e) {

@@ -17,8 +17,9 @@
 // chunk, and the rows that a transposing read spans, fall into different banks (no
 // conflict is counted).
 //
-// Rounding to 16 bits: the weights, for their product with V (relative 2^-9 or 2^-12 of
-// weights that are at most 2^8 times the largest), and the output, once. Sums are fp32.
+// Rounding to 16 bits: the weights, for their product with V (by half a step, 2^-8 or 2^-11
+// of the weight; fp16 ones below 2^-21 of the row's largest by 2^-32 of that), and the
+// output, once. Sums are fp32.
 //
 // Bound by the matrix instructions and the exponentials between them; long prompts come
 // near what a large matrix product reaches: one of 4096 tokens, 32 heads of 128 132 us
@@ -146,8 +147,8 @@ struct Rows {
   f32x16 o[D / 32];
   f32x16 sc[kT];
   float m, l;  // maximum (log2 scale) and this lane's part of the sum
-  // weights are 2^(sc * mul - sub): with the scale and the maximum, or with 1 and 0 where some
-  // row's maximum is far (past kFarLog2) and score() leaves the exponents themselves in sc
+  // weights are 2^(sc * mul - sub): with the scale and the maximum (less kWeightLog2), or with
+  // 1 and 0 where some row's maximum is far (past kFarLog2) and score() leaves exponents in sc
   float mul, sub;
   int far;
 
@@ -162,7 +163,7 @@ struct Rows {
     m = kNegInf;
     l = 0.f;
     mul = scale_log2;
-    sub = 0.f;
+    sub = -Elem<T>::kWeightLog2;
     far = 0;
   }
 
@@ -224,7 +225,7 @@ struct Rows {
       const float ms = m == kNegInf ? 0.f : m;
       far = __any(fabsf(ms) > kFarLog2);
       mul = far ? 1.f : scale_log2;
-      sub = far ? 0.f : ms;
+      sub = (far ? 0.f : ms) - Elem<T>::kWeightLog2;
     }
     if (is_far()) {
       const float ms = m == kNegInf ? 0.f : m;
@@ -241,7 +242,7 @@ struct Rows {
     if constexpr (D == 256) {  // (no register left to keep them: 16384 tokens 1900 us against 1805)
       const bool f = is_far();
       by = f ? 1.f : scale_log2;
-      ms = f || m == kNegInf ? 0.f : m;
+      ms = (f || m == kNegInf ? 0.f : m) - Elem<T>::kWeightLog2;
     }
     // lane's part of a transposing read: row 4 hh + (s16 >> 2) (+ 8), columns 32 i +
     // 16 gb + 4 (s16 & 3)

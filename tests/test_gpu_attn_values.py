@@ -1,6 +1,6 @@
-"""Softmax attention at the ends of its types' ranges, against the fp64 oracle. Every way
-that keys and values are read takes each case. Bounds: attn_helpers.py, except where one
-is stated."""
+"""Softmax attention at the ends of its types' ranges, against the fp64 oracle: weights
+far below the largest, scores past the whole numbers of fp32. Every way that keys and
+values are read takes each case. Bounds: attn_helpers.py, except where one is stated."""
 
 import numpy as np
 import pytest
@@ -50,6 +50,32 @@ def through(way, q, k, v, scale):
 def zeros(way, d, t):
     T, Tk, h, hkv, _, _ = WAYS[way]
     return torch.zeros(T, h, d, dtype=t), torch.zeros(Tk, hkv, d, dtype=t)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("nats", [12.0, 16.0, 17.5, 20.0])
+def test_a_tail_of_weights_far_below_the_largest(way, d, nats):
+    """One key of great weight and a value of zero before many of little weight: the
+    output is the tail's. fp16 weights are formed 2^7 times larger than the row's largest
+    would have them, so a weight is off by half a step or, below the normal numbers, by
+    2^-25 2^-7 of the largest. The scores are exact products of one dim (e: their one
+    rounding with the scale, 2^-24 nats twice)."""
+    t = torch.float16
+    q, k = zeros(way, d, t)
+    q[..., 0] = 1.0
+    k[0, :, 0] = nats
+    v = (1000.0 * (1.0 + 0.25 * normal(3, *k.shape, dtype=torch.float32))).to(t)
+    v[0] = 0
+    print(f"tail {way} d={d} nats={nats}", flush=True)
+    got = f64(through(way, q, k, v, 1.0))
+    o, mag, total = attention.attend(f64(q), f64(k), f64(v), 1.0)
+    u, e = half_step(t), nats * 2.0 ** -23
+    bound = 1.01 * (u * np.abs(o) + (u + 2 * e + 2.0 ** -18) * mag) + 2.0 ** -25 + \
+        len(k) * 2.0 ** -32 * np.abs(f64(v)).max() / total[..., None]
+    off = np.abs(got - o)
+    print(f"  off / bound {np.max(off / bound):.3f}", flush=True)
+    assert np.all(off <= bound), np.max(off / bound)
 
 
 # values of q and of k in the first dims (so many of them), and the scale

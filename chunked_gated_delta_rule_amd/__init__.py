@@ -740,7 +740,8 @@ def causal_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, scale=None, workspa
     q [T, heads, d], k and v [Tk, kv_heads, d], bf16 or fp16, rows of any stride;
     the queries are the last tokens of their keys (cu_seqlens_k None: the same
     tokens); scale: of the scores, positive (None: 1 / sqrt(d)). Returns o [T,
-    heads, d]; rows behind the last sequence are not written."""
+    heads, d]; rows that see no key are zeros (k and v may have no row at all), rows
+    behind the last sequence are not written."""
     if q.dim() != 3 or k.dim() != 3 or v.shape != k.shape or k.shape[2] != q.shape[2] or \
             not q.dtype == k.dtype == v.dtype:
         raise ValueError(f"q [T, heads, d] and k, v [Tk, kv_heads, d] of one dtype expected: "
@@ -750,6 +751,8 @@ def causal_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, scale=None, workspa
     T, H, d = q.shape
     if cu_seqlens_k is None and k.shape[0] < T:
         raise ValueError(f"k, v: {k.shape[0]} rows, at least {T} expected")
+    if k.shape[0] == 0:  # a row that no sequence has (tk_max = 0 would stand for T rows)
+        k = v = k.new_zeros((1, *k.shape[1:]))
     cfg = make_attn_config(T, cu_seqlens.numel() - 1, H, k.shape[1], d, q.dtype, _scale(scale),
                            tk_max=k.shape[0])
     o = torch.empty((T, H, d), dtype=q.dtype, device=q.device)

@@ -109,3 +109,24 @@ def test_equal_scores_of_any_size_weigh_the_same(way, d, name, t, a, b, dims, sc
     off = np.abs(got - o)
     print(f"  off / bound {np.max(off / bound):.3f}", flush=True)
     assert np.all(off <= bound), np.max(off / bound)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("lens", [[5], [3, 0, 40]])
+def test_prompts_without_any_key_row_give_zeros(lens, d):
+    """Rows that see no key give zeros, also where the batch has no key at all; the same
+    call from a captured graph."""
+    t, T = torch.bfloat16, sum(lens)
+    q = normal(1, T, 4, d, dtype=t).to(DEV)
+    k = torch.zeros(0, 2, d, dtype=t, device=DEV)
+    cu, cuk = on(cu_of(lens)), on(cu_of([0] * len(lens)))
+    o = gdn.causal_attention(q, k, k.clone(), cu, cuk)
+    assert o.shape == q.shape and not o.any()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = gdn.causal_attention(q, k, k, cu, cuk)
+    for _ in range(3):
+        o.fill_(1.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert not o.any()

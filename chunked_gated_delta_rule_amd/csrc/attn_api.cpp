@@ -92,7 +92,7 @@ PagedLayout paged_layout(const gdn_attn_config *cfg) {
                             : 0;
   Taker take;
   PagedLayout l;
-  l.prefix = take(sizeof(int32_t));
+  l.prefix = take(2 * sizeof(int32_t));
   l.plan = take(static_cast<size_t>(cfg->t_max) * cfg->h * kPlanBytes);
   l.part_o = take(slots * d * 4);
   l.part_ml = take(slots * 2 * 4);

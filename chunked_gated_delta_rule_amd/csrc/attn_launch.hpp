@@ -74,9 +74,10 @@ struct StreamArgs {
   int h, hkv;
   float scale_log2;
   int grid;  // work-groups of the main kernel
-  // workspace: the prefix's length; 16 bytes per row for the join; the partial results of
-  // items split over work-groups (two per work-group); with a shared prefix, the results
-  // of items that one work-group finished (one per row) and the prefix's parts
+  // workspace: the prefix's length, and (for tests) whether the keys behind it are read past
+  // the caches; 16 bytes per row for the join; the partial results of items split over
+  // work-groups (two per work-group); with a shared prefix, the results of items that one
+  // work-group finished (one per row) and the prefix's parts
   int32_t *prefix;
   void *plan;
   float *part_o, *part_ml, *done_o, *done_ml;

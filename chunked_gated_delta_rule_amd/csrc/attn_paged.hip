@@ -63,10 +63,13 @@ __device__ __forceinline__ int64_t lane_of(int64_t x, int lane) {
 
 __device__ __forceinline__ int units_of(int keys) { return (keys + kUnit - 1) / kUnit; }
 
-// Keys and values are read past the caches where those could not hold them (kPastCache):
+// Keys and values that are read once, by the one row tile of each item's heads, are read
+// past the caches where those could not hold them (kPastCache):
 // 256 sequences of 2500 keys 471 -> 441 us, 128 of 1250 with two heads of 256 80 -> 75; but
 // 32 of 2200 (240 MB) would take 58 -> 53 from HBM and 48 -> 52 where the last call left them
-// in the cache, 64 of 190 (50 MB) 25 -> 29.
+// in the cache, 64 of 190 (50 MB) 25 -> 29. A batch in which some item has several row tiles
+// leaves its keys in the caches for the next of them (400 new tokens on 4000 keys beside 63
+// sequences of 500: 109 us, past the caches 146).
 template <bool kPast>
 __device__ __forceinline__ u32x4 load16(rsrc_t r, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, kPast ? 2 : 0);  // 2: not temporal
@@ -95,7 +98,7 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
   __shared__ __attribute__((aligned(16))) float os[4][16][kPad];
   __shared__ float wm[4][kRows], wl[4][kRows];
   __shared__ int64_t scan64[5];
-  __shared__ int scan32[4][2], found;
+  __shared__ int scan32[4][2], again[4], found;
 
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
@@ -118,7 +121,13 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
   const int s0 = min(few ? lane : tid * per, pg.n_max);
   const int s1 = min(s0 + (few ? 1 : per), pg.n_max);
   int64_t mine = 0;
-  for (int s = s0; s < s1; ++s) mine += units_in(s);
+  bool twice = false;  // keys that more than one row tile reads
+  for (int s = s0; s < s1; ++s) {
+    const int64_t u = units_in(s);
+    mine += u;
+    twice = twice || (u > 0 && row_tiles<kRT>(seq_at(pg, s).n * G) > 1);
+  }
+  twice = __any(twice);
   int64_t incl = mine;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
@@ -129,20 +138,22 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
   if (few) {
     per_head = lane_of(incl, 63);
   } else {
-    if (lane == 63) scan64[w] = incl;
+    if (lane == 63) scan64[w] = incl, again[w] = twice;
     __syncthreads();
     per_head = 0;
     for (int i = 0; i < 4; ++i) {
       if (i < w) before += scan64[i];
       per_head += scan64[i];
+      twice = twice || again[i];
     }
     per_head = uniform(per_head);
   }
   const int64_t total = per_head * a.hkv;
   const int64_t per_wg = max(quotient(total + a.grid - 1, a.grid), (int64_t)1);
+  const bool past = uniform(total > kPastCache / (kUnit * D * 4) && !twice);
   RowPlan *const plan = reinterpret_cast<RowPlan *>(a.plan);
   if (wg == 0 && (!few || w == 0)) {
-    if (tid == 0) a.prefix[0] = prefix;
+    if (tid == 0) a.prefix[0] = prefix, a.prefix[1] = past;
     // rows of sequences without keys belong to no item
     for (int s = s0; s < s1; ++s) {
       const Seq q = seq_at(pg, s);
@@ -452,7 +463,7 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
       }
     }
   };
-  if (total > kPastCache / (kUnit * D * 4))
+  if (past)
     walk(std::true_type{});
   else
     walk(std::false_type{});

@@ -118,3 +118,28 @@ def test_prompts_over_pages(t, lens, past, h, hkv, d, page, waves, split, how, s
     o = gdn.paged_attention(*args)
     check_rows(o, q, cu, functools.lru_cache(None)(c.rows), lens, full, t, step)
     assert torch.equal(o, gdn.paged_attention(*args))
+
+
+@pytest.mark.parametrize("new,full,h,hkv,d,past", [
+    ([1] * 70, [4400] * 70, 4, 2, 128, True),                # 315 MB, each key read by one row tile
+    ([1] * 70, [2100] * 70, 4, 2, 128, False),               # 151 MB
+    ([300] + [1] * 49, [9000] + [500] * 49, 8, 2, 256, False),   # 69 MB, a part of it by 38 tiles: 759
+    ([150] + [1] * 69, [3000] + [300] * 69, 16, 8, 128, False),  # 97 MB, by 19: 348; more than 64 sequences
+    ([60] + [1] * 69, [100] + [2100] * 69, 8, 4, 128, False),    # 298 MB, little of it by several
+])
+def test_streamed_keys_go_past_the_caches_only_if_read_once(new, full, h, hkv, d, past):
+    """Not temporal loads are for keys that the caches could not hold and one row tile
+    reads; the choice is left behind the prefix's length in the workspace."""
+    t, page, n = torch.bfloat16, 16, len(new)
+    need = -(-max(full) // page)
+    table = np.arange(n * need, dtype=np.int32).reshape(n, need) % 64  # pages shared: any keys do
+    cfg = gdn.make_attn_config(sum(new), n, h, hkv, d, t, page_size=page, n_pages=64, max_pages=need)
+    assert attn_shapes.streams(cfg) and not attn_shapes.shares(cfg)
+    q = torch.ones(sum(new), h, d, dtype=t, device=DEV)
+    kp, vp = (normal(i, 64, hkv, page, d, dtype=t).to(DEV) for i in (2, 3))
+    ws = torch.full((gdn.gdn_attn_workspace_size(cfg),), 0x55, dtype=torch.uint8, device=DEV)
+    o = torch.empty_like(q)
+    gdn.gdn_attn_paged(cfg, q, kp, vp, on(cu_of(new)), on(np.array(full, np.int32)), on(table), None,
+                       o, ws)
+    assert o.isfinite().all()
+    assert ws[:8].view(torch.int32).tolist() == [0, int(past)]

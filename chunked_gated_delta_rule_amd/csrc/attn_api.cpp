@@ -5,6 +5,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -28,6 +29,7 @@ gdn_status check_config(const gdn_attn_config *cfg) {
   if (!std::isfinite(cfg->scale) || !std::isfinite(cfg->rot_scale) || !std::isfinite(cfg->eps) ||
       cfg->eps < 0.f)
     return GDN_ERR_INVALID_ARG;
+  if (cfg->scale * kLog2e > FLT_MAX) return GDN_ERR_INVALID_ARG;  // scale_log2, in fp32
   if (cfg->rot_dim < 0 || cfg->rot_dim > cfg->d || cfg->rot_dim % 2 != 0)
     return GDN_ERR_INVALID_ARG;
   if (cfg->rot_interleaved != 0 && cfg->rot_interleaved != 1) return GDN_ERR_INVALID_ARG;

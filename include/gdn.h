@@ -404,7 +404,7 @@ typedef struct {
   int32_t h, hkv;          /* query heads; key / value heads, h a multiple of hkv */
   int32_t d;               /* head dim: 128 or 256 */
   gdn_dtype dtype;         /* GDN_BF16 or GDN_F16 */
-  float scale;             /* score scale; <= 0 selects 1 / sqrt(d) */
+  float scale;             /* score scale, finite (times log2(e) too); <= 0 selects 1 / sqrt(d) */
   float eps;               /* RMS norm: added to the mean square; finite, >= 0 */
   int32_t rot_dim;         /* leading dims of each head that are rotated: even, 0 .. d */
   int32_t rot_interleaved; /* 0: dims (i, i + rot_dim / 2) form pair i; 1: (2 i, 2 i + 1) */

@@ -239,3 +239,14 @@ def test_binding_struct_matches_the_header(tmp_path):
     assert int(got.pop("size")) == ctypes.sizeof(gdn.gdn_attn_config)
     for n in names:
         assert int(got[n]) == getattr(gdn.gdn_attn_config, n).offset, n
+
+
+@pytest.mark.parametrize("scale,status", [(3e38, INVALID), (2.4e38, INVALID), (2.3e38, OK), (1e-44, OK)])
+def test_a_scale_that_leaves_fp32_with_the_exponents_base_is_refused(scale, status):
+    """Kernels take scale * log2(e) in fp32: finite up to 2^128 / log2(e) = 2.3586e38."""
+    out = ctypes.c_size_t(0)
+    lib = gdn.load_library()
+    assert lib.gdn_attn_workspace_size(ctypes.byref(cfg(scale=scale)), ctypes.byref(out)) == status
+    if status != OK:
+        refused(status, gdn.gdn_attn_prefill, cfg(scale=scale), **PREFILL)
+        refused(status, gdn.gdn_attn_paged, cfg(scale=scale), **PAGED)

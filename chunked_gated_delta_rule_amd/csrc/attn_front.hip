@@ -19,6 +19,9 @@
 #include "attn_common.hpp"
 #include "attn_launch.hpp"
 
+#include <cfloat>
+#include <type_traits>
+
 namespace gdn {
 
 namespace {
@@ -33,6 +36,10 @@ constexpr int kMostTokens = 2;
 // rot_dim) eight channels in a row whose partners are read one by one.
 enum class Pairs { kHalf = 0, kInterleaved = 1, kHalfOdd = 2 };
 
+// The least sum of squares that is taken as it is, and the factors for values whose sum is
+// not fp32's (bf16 only): 2^128 2^-96 and 2^-126 2^96 have squares that are.
+constexpr float kSmall = 0x1p-100f, kDown = 0x1p-96f, kUp = 0x1p96f;
+
 // 1 / (2 pi), for angles counted in turns.
 constexpr double kInvTwoPi = 0.15915494309189533577;
 
@@ -44,8 +51,10 @@ __device__ __forceinline__ void unpack4(const u32x2 &w, float *f) {
   f[3] = Elem<T>::hi(w[1]);
 }
 
+// At least six waves per SIMD: the odd layout would take 82 registers, which leaves five (8192
+// tokens of 40 heads of 128, rot_dim 34: 64 us against 58).
 template <typename T, int D, Pairs kPairs, bool kCache>
-__global__ __launch_bounds__(kFrontThreads) void attn_front_kernel(FrontArgs a) {
+__global__ __launch_bounds__(kFrontThreads, 6) void attn_front_kernel(FrontArgs a) {
   constexpr int kLanes = D / 8;                    // lanes per head
   constexpr int kRows = kFrontThreads / kLanes;    // rows per pass
   __shared__ __attribute__((aligned(16))) float cs[kMostTokens][D / 2], sn[kMostTokens][D / 2];
@@ -149,7 +158,25 @@ __global__ __launch_bounds__(kFrontThreads) void attn_front_kernel(FrontArgs a) 
     for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
     ss = sum16(ss);
     if constexpr (kLanes == 32) ss = sum16x(ss);
-    const float rn = norm ? 1.f / sqrtf(ss * (1.f / D) + a.eps) : 1.f;
+    float rn = norm ? 1.f / sqrtf(ss * (1.f / D) + a.eps) : 1.f;
+    float by = 1.f;
+    if constexpr (std::is_same_v<T, __bf16>) {
+      // values whose squares leave fp32 (past about 2^60), or vanish in it with nothing
+      // added to them, are brought to the middle of its range first
+      const bool large = ss > FLT_MAX, small = ss < kSmall && a.eps < kSmall;
+      if (__any(norm && (large || small))) {
+        if (norm && (large || small)) by = large ? kDown : kUp;
+        ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          x[j] *= by;
+          ss = fmaf(x[j], x[j], ss);
+        }
+        ss = sum16(ss);
+        if constexpr (kLanes == 32) ss = sum16x(ss);
+        if (norm) rn = 1.f / sqrtf(ss * (1.f / D) + a.eps * by * by);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       x[j] *= rn * (is_q ? wq0[j] : wk0[j]);
@@ -188,7 +215,7 @@ __global__ __launch_bounds__(kFrontThreads) void attn_front_kernel(FrontArgs a) 
             if (c < a.rot_dim) {
               const bool low = c < half;
               const int p = low ? c + half : c - half, i = low ? c : p;
-              const float y = static_cast<float>(row[p]) * rn * (wp ? wp[p] : 1.f);
+              const float y = static_cast<float>(row[p]) * by * rn * (wp ? wp[p] : 1.f);
               x[j] = x[j] * ct[i] + (low ? -y : y) * st[i];
             }
           }

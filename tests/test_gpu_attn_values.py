@@ -7,7 +7,8 @@ import pytest
 import torch
 
 import chunked_gated_delta_rule_amd as gdn
-from attn_helpers import DEV, cu_of, f64, half_step, normal, on, shared_cols, widened
+from attn_helpers import (DEV, check_norm_rope, cu_of, f64, half_step, normal, on, shared_cols,
+                          widened)
 from oracle import attention
 
 pytestmark = pytest.mark.gpu
@@ -130,3 +131,29 @@ def test_prompts_without_any_key_row_give_zeros(lens, d):
         graph.replay()
         torch.cuda.synchronize()
         assert not o.any()
+
+
+# sizes of a head's values: their squares, or the sum of them, leave fp32, or are below its
+# smallest normal number
+SIZES = [2.0 ** 60, 2.0 ** 62, 1.9e19, 2.0 ** 90, 2.0 ** 120, 2.0 ** -52, 2.0 ** -64, 1e-25, 2.0 ** -100]
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-38, 1e-6])
+@pytest.mark.parametrize("d,rot,inter", [(128, 128, False), (128, 34, False), (256, 64, True)])
+def test_norm_of_values_whose_squares_leave_fp32(d, rot, inter, eps):
+    """The norm divides by the root mean square, which is of the values' own size."""
+    t, h, hkv = torch.bfloat16, 4, 2
+    T = len(SIZES)
+    x = normal(7, T, h + 2 * hkv, d, dtype=torch.float32)
+    x[:, 1:] *= torch.tensor(SIZES)[:, None, None]  # the first head as it is
+    qkv = x.to(t).flatten(1)
+    assert qkv.isfinite().all()
+    w, f = 1.0 + 0.3 * normal(8, d, dtype=torch.float32), gdn.rope_inv_freq(rot)
+    print(f"norm of large and small values d={d} rot={rot} eps={eps}", flush=True)
+    q, k = gdn.qk_norm_rope(qkv.to(DEV), h, hkv, on(cu_of([T])), w.to(DEV), w.to(DEV), f.to(DEV),
+                            eps=eps, interleaved=inter)
+    y = f64(qkv).reshape(T, h + 2 * hkv, d)
+    for got, part in ((q, y[:, :h]), (k, y[:, h:h + hkv])):
+        want, mag = attention.norm_rope(part, f64(w), np.arange(T), f64(f), np.float64(np.float32(eps)),
+                                        inter)
+        check_norm_rope(got, want, mag, t)

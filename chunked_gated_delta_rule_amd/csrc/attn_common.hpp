@@ -47,6 +47,18 @@ struct Elem<_Float16> {
   }
 };
 
+// An output is a mean of values. The weights' roundings can take it past fp16's largest
+// value, by 2^-11 of that at most, where a mean of finite values is not: the largest then.
+constexpr float kPastF16 = 65520.f;  // from here on fp16 rounds to infinity
+__device__ __forceinline__ float mean_f16(float x) {
+  return fabsf(x) < 65600.f ? fminf(fmaxf(x, -65504.f), 65504.f) : x;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack_mean(float a, float b) {
+  if constexpr (__is_same(T, _Float16)) return Elem<T>::pack(mean_f16(a), mean_f16(b));
+  return Elem<T>::pack(a, b);
+}
+
 // Maximum and sum over lanes l and l ^ 32 (l ^ 16), in both: the swap of half
 // (quarter) waves leaves the lower ones' values in one register and the upper
 // ones' in the other.

@@ -438,8 +438,8 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
               sum += *reinterpret_cast<const f32x4 *>(&os[i][row][64 * b + q4]);
             if (last)
               *reinterpret_cast<u32x2 *>(static_cast<T *>(a.o) + orow * D + 64 * b + q4) =
-                  u32x2{Elem<T>::pack(sum[0] * inv, sum[1] * inv),
-                        Elem<T>::pack(sum[2] * inv, sum[3] * inv)};
+                  u32x2{pack_mean<T>(sum[0] * inv, sum[1] * inv),
+                        pack_mean<T>(sum[2] * inv, sum[3] * inv)};
             else
               *reinterpret_cast<f32x4 *>(po + 64 * b + q4) = sum;
           }
@@ -567,7 +567,7 @@ __global__ __launch_bounds__(256) void attn_stream_join_kernel(StreamArgs a) {
   uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<T *>(a.o) + row * D);
 #pragma unroll
   for (int k = 0; k < kPer / 2; ++k)
-    o[kPer / 2 * lane + k] = Elem<T>::pack(sum[2 * k] * inv, sum[2 * k + 1] * inv);
+    o[kPer / 2 * lane + k] = pack_mean<T>(sum[2 * k] * inv, sum[2 * k + 1] * inv);
 }
 
 template <typename T, int D, int kRT>

@@ -295,9 +295,23 @@ struct Rows {
             f32x4{o[i][4 * b], o[i][4 * b + 1], o[i][4 * b + 2], o[i][4 * b + 3]};
   }
 
-  __device__ __forceinline__ void store(T *row, int hh) const {
+  __device__ __forceinline__ void store(T *row, int hh) {
     const float sum = sum32(l);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that sees no key gives zeros
+    float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that sees no key gives zeros
+    if constexpr (std::is_same_v<T, _Float16>) {
+      float most = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) most = fmaxf(most, fabsf(o[i][k]));
+      if (__any(most * inv >= kPastF16)) {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[i][k] = mean_f16(o[i][k] * inv);
+        inv = 1.f;
+      }
+    }
     // a lane and its partner 32 lanes on hold halves of 8 dims: swapped in pairs of
     // blocks, each lane has 16 bytes in a row
 #pragma unroll
@@ -789,7 +803,7 @@ __global__ __launch_bounds__(256) void attn_tile_join_kernel(TileArgs a, int tt,
   uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<T *>(a.o) + ((int64_t)t * a.h + head) * D);
 #pragma unroll
   for (int k = 0; k < kPer / 2; ++k)
-    o[kPer / 2 * lane + k] = Elem<T>::pack(sum[2 * k] * inv, sum[2 * k + 1] * inv);
+    o[kPer / 2 * lane + k] = pack_mean<T>(sum[2 * k] * inv, sum[2 * k + 1] * inv);
 }
 
 template <typename T, int D, int kWaves, Keys kKeys>

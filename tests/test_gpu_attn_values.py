@@ -157,3 +157,23 @@ def test_norm_of_values_whose_squares_leave_fp32(d, rot, inter, eps):
         want, mag = attention.norm_rope(part, f64(w), np.arange(T), f64(f), np.float64(np.float32(eps)),
                                         inter)
         check_norm_rope(got, want, mag, t)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_a_mean_of_the_largest_fp16_values_is_finite(way, d, sign):
+    """Every value is the type's largest, and so is their mean. The weights of all keys but
+    the first are just above the middle between two fp16 numbers: rounded, they are up
+    to half a step larger than what the sum holds."""
+    t = torch.float16
+    q, k = zeros(way, d, t)
+    q[..., 0] = 1.0
+    k[1:, :, 0] = -0.67236328125  # weight 0.510501, in fp16 0.510742
+    v = torch.full_like(k, sign * torch.finfo(t).max)
+    print(f"largest values {way} d={d}", flush=True)
+    got = f64(through(way, q, k, v, 1.0))
+    bound = 1.01 * (2 * half_step(t) + 2.0 ** -18) * torch.finfo(t).max
+    assert np.all(np.abs(got - f64(v)[0, 0, 0]) <= bound)
+    v[0] = float("inf")
+    assert not through(way, q, k, v, 1.0).isfinite().any()

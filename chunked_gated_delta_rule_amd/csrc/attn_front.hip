@@ -7,7 +7,7 @@
 //
 // HBM-bound: each row is read once and written once (8192 tokens of 40 heads of 128: 36
 // us, 4.6 TB/s, and 32 where the last-level cache still holds the rows; 32768 tokens of 20
-// heads of 256 into pages: 126 us, 5.3 TB/s; a large copy reaches 5.0). 512 or fewer
+// heads of 256 into pages: 127 us, 5.3 TB/s; a large copy reaches 5.0). 512 or fewer
 // tokens take 6 us, most of it latency. A 256-thread work-group takes one or two
 // tokens; D / 8 lanes own a head's row, eight channels each, and the work-group walks
 // the heads of its tokens 2048 / D at a time, the next rows' loads in flight.

@@ -22,10 +22,13 @@
 // output, once. Sums are fp32.
 //
 // Bound by the matrix instructions and the exponentials between them; long prompts come
-// near what a large matrix product reaches: one of 4096 tokens, 32 heads of 128 132 us
-// (1.04 PFLOP/s; a product of 8192^3 1.26), one of 16384, 16 heads of 256 1.85 ms (1.19
-// PFLOP/s). Short ones wait for their first keys and for each other's copies: 32 of 58
-// to 1203 tokens 143 us, where bytes and products would each take 78.
+// near what a large matrix product reaches: one of 4096 tokens, 32 heads of 128 137 us
+// (1.00 PFLOP/s; a product of 8192^3 1.26), one of 16384, 16 heads of 256 1.90 ms (1.16
+// PFLOP/s). Boxes differ (133 to 147 us, 1.85 to 1.92 ms), and back to back the card lowers
+// its clock (162 us after twenty of the former). Short ones wait for their first keys and
+// for each other's copies: 32 of 58 to 1203 tokens 146 us, where bytes and products would
+// each take 78. A single prompt of some thousand tokens with few heads is uneven work: its
+// tiles see very different numbers of keys (4000 tokens, 16 heads of 128: 99 us against 52).
 #include "attn_common.hpp"
 #include "attn_launch.hpp"
 
@@ -504,7 +507,7 @@ __device__ __forceinline__ const T *q_row(const TileArgs &a, const Where &t, int
 // 128 sequences of 128 tokens 97 us against 85). With eight, the two waves of a SIMD (w
 // and w + 4) go through the two parts of a step in opposite order, a barrier after each
 // part: while one runs its score products the other forms weights (16384 tokens, 16
-// heads of 256: 2658 us with four waves, 2130 with eight, when this was built; now 1848).
+// heads of 256: 2658 us with four waves, 2130 with eight, when this was built; now 1900).
 // Their steps have 64 keys, or 32 with heads of 256, which leaves registers to read
 // fragments ahead (1836 -> 1820).
 template <typename T, int D, int kWaves, Keys kKeys>
@@ -857,8 +860,9 @@ constexpr int kLongPrompt = 2048;
 // tokens, so little is computed beyond the diagonal or past a sequence's end (32
 // prompts of 500 tokens on average, two heads per key head: 176 -> 160 us).
 constexpr int kMostShare = 16;
-// A split has at least this many keys of the longest possible sequence, and there
-// are at most 64 (one per lane of the join).
+// A split has at least this many keys of the longest sequence that pages or the prefix can
+// hold, or, of packed rows, of an average one, and there are at most 64 (one per lane of
+// the join).
 constexpr int kSplitKeys = 256;
 constexpr int kMostSplits = 64;
 // Tiles that fill the device between half and once are split in two: one prompt of 1200

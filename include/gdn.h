@@ -394,9 +394,13 @@ gdn_status gdn_recurrent_fwd_timed(const gdn_config *cfg, const void *q, const v
  *    lies in page block_table[s][p / page_size], row p % page_size. Rows of a
  *    page past a sequence's length may hold anything, NaN included.
  *  - Types: q, k, v, qkv, the pages and o share cfg->dtype (GDN_BF16 or
- *    GDN_F16). Scores, softmax statistics and output sums are fp32; softmax
- *    weights are rounded to the 16-bit type for their product with v, and the
- *    output is rounded once.
+ *    GDN_F16). Scores, softmax statistics and output sums are fp32 (a score past
+ *    fp32 is infinite); softmax weights are rounded to the 16-bit type for their
+ *    product with v (fp16: by 2^-11 of the weight, or 2^-32 of the row's largest
+ *    where that is more), and the output is rounded once.
+ *  - How a call is cut, and so its time, goes by cfg's capacities and not by the
+ *    lengths on the device: give a decode step a cfg without room for prompts,
+ *    and shared_max no more than the prefix can have.
  * ------------------------------------------------------------------------- */
 typedef struct {
   int32_t t_max;           /* token capacity (rows of q, qkv, o; query tokens) */
@@ -410,8 +414,8 @@ typedef struct {
   int32_t rot_interleaved; /* 0: dims (i, i + rot_dim / 2) form pair i; 1: (2 i, 2 i + 1) */
   float rot_scale;         /* factor on cos and sin (long-context scaling); 0 selects 1 */
   int32_t page_size;       /* tokens per page: 16, 32, 64, 128 or 256 */
-  int32_t n_pages;         /* pages of k_pages and v_pages */
-  int32_t max_pages;       /* columns of block_table */
+  int32_t n_pages;         /* pages of k_pages and v_pages; calls with a cache: at least 1 */
+  int32_t max_pages;       /* columns of block_table; likewise */
   int32_t tk_max;          /* rows of k and v in gdn_attn_prefill; 0 selects t_max */
   int32_t shared_max;      /* largest *shared_len (gdn_attn_paged); 0: no shared prefix */
 } gdn_attn_config;
@@ -477,7 +481,9 @@ gdn_status gdn_attn_prefill(const gdn_attn_config *cfg, const void *q, int64_t q
 
 /* Attention of each sequence's n new tokens (one when decoding, a few when
  * verifying, any number) to its cache, which already holds them: token i sees
- * positions 0 .. kv_lens - n + i. A row that sees no key gives zeros.
+ * positions 0 .. kv_lens - n + i. A row that sees no key gives zeros. One way of
+ * reading the keys serves the whole batch, by its average of tokens: prompt chunks
+ * and decoding sequences take less time in calls of their own.
  *   q (device) [t_max, h, d], q_row as above
  *   shared_len (device, nullable = 0) int32 [1]: a promise that the batch's
  *            sequences have their first *shared_len positions in the same

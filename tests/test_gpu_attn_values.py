@@ -23,6 +23,8 @@ WAYS = {
     "pages": (80, 300, 4, 1, 32, 0),          # tiles over the pages
     "page parts": (80, 1500, 4, 1, 64, 0),
     "prefix": (2, 400, 4, 1, 16, 3),          # a prefix of 64 read once, joined with the streams
+    "wide stream": (6, 500, 4, 1, 16, 0),     # items of two row tiles
+    "wide prefix": (10, 400, 4, 1, 16, 3),    # and of four (heads of 128)
 }
 
 
@@ -110,6 +112,34 @@ def test_equal_scores_of_any_size_weigh_the_same(way, d, name, t, a, b, dims, sc
     off = np.abs(got - o)
     print(f"  off / bound {np.max(off / bound):.3f}", flush=True)
     assert np.all(off <= bound), np.max(off / bound)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("t,a", [(torch.bfloat16, torch.finfo(torch.bfloat16).min),
+                                 (torch.float16, 65504.0)])
+def test_rows_of_far_and_of_ordinary_scores_in_one_tile(way, d, t, a):
+    """Every other head's queries have far scores with the first 30 keys; the heads
+    between are ordinary, and keep the usual bound. (fp16: the scale makes them far.)"""
+    q, k = zeros(way, d, t)
+    scale = 1.0 if t == torch.bfloat16 else 0.75
+    q[:, 1::2] = normal(5, *q[:, 1::2].shape, dtype=t)
+    k[:] = normal(6, *k.shape, dtype=t)
+    q[..., 0] = 0
+    q[:, ::2, 0] = 1.0 if t == torch.bfloat16 else a
+    k[..., 0] = 0
+    k[:30, :, 0] = a
+    v = normal(4, *k.shape, dtype=t)
+    print(f"far and ordinary {way} d={d} {t}", flush=True)
+    got = through(way, q, k, v, scale / d ** 0.5)
+    g, u = f64(got), half_step(t)
+    o, mag, total = attention.attend(f64(q), f64(k), f64(v), scale / d ** 0.5)
+    e = np.zeros(g.shape)  # the far heads' scores are exact, the others' sums are not
+    e[:, 1::2] = d * 2.0 ** -24 * scale / d ** 0.5 * float(
+        (q[:, 1::2].double().abs().amax((0, 1)) * k.double().abs().amax((0, 1)))[1:].sum())
+    bound = 1.01 * (u * np.abs(o) + (u + 2 * e + 2.0 ** -18) * mag) + 2.0 ** -25 + \
+        len(k) * 2.0 ** -32 * np.abs(f64(v)).max() / total[..., None]
+    assert np.all(np.abs(g - o) <= bound)
 
 
 @pytest.mark.parametrize("d", [128, 256])

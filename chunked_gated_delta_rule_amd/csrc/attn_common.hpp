@@ -107,8 +107,9 @@ constexpr float kNegInf = -__builtin_inff();
 constexpr int64_t kPastCache = 256 << 20;
 
 // Softmax statistics move only when a row's maximum (log2 scale) has grown by
-// more than this: the weights then stay below 2^8, exact enough in 16 bits and
-// in the fp32 sums, and the output sums are rescaled a few times per row only.
+// more than this: the weights then stay below 2^8 (fp16, formed larger: 2^15), in the
+// range of 16 bits and of the fp32 sums, and the output sums are rescaled a few times
+// per row only.
 constexpr float kRescaleLog2 = 8.f;
 
 // A weight's exponent, score * scale - m, is one fused step, so it contains the rounding of

@@ -34,7 +34,9 @@ __all__ = [
     "GDN_T_MAX_LIMIT", "GDN_N_MAX_LIMIT", "gdn_chunk_fwd_noalloc", "GDN_NOALLOC_SCRATCH_BYTES",
     "gdn_attn_config", "make_attn_config", "gdn_attn_workspace_size", "gdn_qk_norm_rope",
     "gdn_kv_append", "gdn_attn_prefill", "gdn_attn_paged", "rope_inv_freq", "qk_norm_rope",
-    "append_paged_kv", "causal_attention", "paged_attention",
+    "append_paged_kv", "causal_attention", "paged_attention", "gdn_qk_norm_rope_axes",
+    "gdn_kv_append_axes", "gdn_kv_append8", "gdn_attn_paged8", "gdn_attn_paged8_workspace_size",
+    "rope_pair_axis", "GDN_AXES_LIMIT",
 ]
 
 GDN_BF16 = 0
@@ -46,6 +48,7 @@ GDN_FOUR_TILE_MIN_TOKENS = 384  # include/gdn.h
 GDN_T_MAX_LIMIT = 1 << 24  # include/gdn.h
 GDN_N_MAX_LIMIT = 16384  # include/gdn.h
 GDN_NOALLOC_SCRATCH_BYTES = 256 << 20  # include/gdn.h
+GDN_AXES_LIMIT = 16  # include/gdn.h
 _STATUS = {0: "GDN_OK", 1: "GDN_ERR_INVALID_ARG", 2: "GDN_ERR_UNSUPPORTED",
            3: "GDN_ERR_CAPACITY", 4: "GDN_ERR_WORKSPACE", 5: "GDN_ERR_HIP"}
 EXPORTED_SYMBOLS = ("gdn_nt_max", "gdn_workspace_layout", "gdn_workspace_size",
@@ -54,7 +57,9 @@ EXPORTED_SYMBOLS = ("gdn_nt_max", "gdn_workspace_layout", "gdn_workspace_size",
                     "gdn_chunk_fwd_timed", "gdn_front_conv_silu_l2_timed", "gdn_chunk_fwd_conv",
                     "gdn_chunk_fwd_conv_timed", "gdn_recurrent_fwd", "gdn_recurrent_fwd_timed",
                     "gdn_chunk_fwd_noalloc", "gdn_attn_workspace_size", "gdn_qk_norm_rope",
-                    "gdn_kv_append", "gdn_attn_prefill", "gdn_attn_paged")
+                    "gdn_kv_append", "gdn_attn_prefill", "gdn_attn_paged",
+                    "gdn_qk_norm_rope_axes", "gdn_kv_append_axes", "gdn_kv_append8",
+                    "gdn_attn_paged8", "gdn_attn_paged8_workspace_size")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libgdn.so")
@@ -128,8 +133,17 @@ def load_library():
     lib.gdn_kv_append.argtypes = [acfg, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.gdn_attn_prefill.argtypes = [acfg, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, sz, vp]
     lib.gdn_attn_paged.argtypes = [acfg, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.gdn_qk_norm_rope_axes.argtypes = [acfg, vp, i64, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp]
+    lib.gdn_kv_append_axes.argtypes = [acfg, vp, i64, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp,
+                                       vp, vp]
+    lib.gdn_kv_append8.argtypes = [acfg, vp, i64, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp,
+                                   vp, vp, vp]
+    lib.gdn_attn_paged8_workspace_size.argtypes = [acfg, ctypes.POINTER(sz)]
+    lib.gdn_attn_paged8.argtypes = [acfg, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     for name in ("gdn_attn_workspace_size", "gdn_qk_norm_rope", "gdn_kv_append",
-                 "gdn_attn_prefill", "gdn_attn_paged"):
+                 "gdn_attn_prefill", "gdn_attn_paged", "gdn_qk_norm_rope_axes",
+                 "gdn_kv_append_axes", "gdn_kv_append8", "gdn_attn_paged8",
+                 "gdn_attn_paged8_workspace_size"):
         getattr(lib, name).restype = ctypes.c_int
     for name in ("gdn_workspace_size", "gdn_workspace_layout", "gdn_build_chunk_indices", "gdn_front_conv_silu_l2",
                  "gdn_chunk_fwd_intra", "gdn_chunk_fwd_inter", "gdn_chunk_fwd",
@@ -601,6 +615,79 @@ def gdn_kv_append(cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens, block_table
                 _at(k_pages, "k_pages", t, pool, dev, d), _at(v_pages, "v_pages", t, pool, dev, d)))
 
 
+def _axes_args(cfg, positions, pair_axis, dev):
+    """positions [n_axes, t_max] (one column per token) and pair_axis [rot_dim / 2]."""
+    if positions is None and pair_axis is None:
+        return None, None, 0
+    for x, name in ((positions, "positions"), (pair_axis, "pair_axis")):
+        if not isinstance(x, torch.Tensor):
+            raise ValueError(f"{name}: int32 tensor expected (positions and pair_axis go together)")
+    if positions.dim() != 2 or positions.shape[1] != cfg.t_max:
+        raise ValueError(f"positions: {tuple(positions.shape)}, [axes, {cfg.t_max}] expected")
+    return (_at(positions, "positions", torch.int32, positions.shape[0] * cfg.t_max, dev),
+            _at(pair_axis, "pair_axis", torch.int32, cfg.rot_dim // 2, dev), positions.shape[0])
+
+
+def gdn_qk_norm_rope_axes(cfg, qkv, q_w, k_w, inv_freq, positions, pair_axis, cu_seqlens, q, k,
+                          stream=None):
+    """gdn_qk_norm_rope with positions of several axes: int32 positions [n_axes, t_max] and
+    pair_axis [rot_dim / 2], the axis that turns each pair."""
+    dev, t, d = _dev(qkv, q, k), _GDN_DTYPE.get(cfg.dtype), cfg.d
+    n = cfg.t_max * d
+    front = _front_args(cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, None, t, dev)
+    _attn_call("gdn_qk_norm_rope_axes", dev, stream,
+               front[:6] + _axes_args(cfg, positions, pair_axis, dev) +
+               (front[6], _at(q, "q", t, n * cfg.h, dev, d), _at(k, "k", t, n * cfg.hkv, dev, d)))
+
+
+def gdn_kv_append_axes(cfg, qkv, q_w, k_w, inv_freq, positions, pair_axis, cu_seqlens, kv_lens,
+                       block_table, q, k, k_pages, v_pages, stream=None):
+    """gdn_kv_append with positions of several axes (gdn_qk_norm_rope_axes)."""
+    dev, t, d, cols, hkv = _dev(qkv, k_pages), _GDN_DTYPE.get(cfg.dtype), cfg.d, cfg.max_pages, cfg.hkv
+    n, pool = cfg.t_max * d, cfg.n_pages * hkv * cfg.page_size * d
+    front = _front_args(cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens, t, dev)
+    _attn_call("gdn_kv_append_axes", dev, stream,
+               front[:6] + _axes_args(cfg, positions, pair_axis, dev) + front[6:] +
+               (_at(block_table, "block_table", torch.int32, cfg.n_max * cols, dev, cols),
+                _at(q, "q", t, n * cfg.h, dev, d), _at(k, "k", t, n * hkv, dev, d),
+                _at(k_pages, "k_pages", t, pool, dev, d), _at(v_pages, "v_pages", t, pool, dev, d)))
+
+
+# What 8-bit pages and their scales may be: the float8 types, or their bytes.
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+_SCALES = (torch.float8_e8m0fnu, torch.uint8)
+
+
+def _bytes_at(x, name, types, elems, dev, last):
+    if x.__class__ is int or x is None:
+        return x
+    if x.dtype not in types:
+        raise ValueError(f"{name}: dtype {x.dtype}, {types[0]} or {types[1]} expected")
+    return _at(x, name, x.dtype, elems, dev, last)
+
+
+def _cache8_args(cfg, k_pages, v_pages, k_scales, v_scales, dev):
+    rows, d, blocks = cfg.n_pages * cfg.hkv * cfg.page_size, cfg.d, cfg.page_size // 16
+    return (_bytes_at(k_pages, "k_pages", _CODES, rows * d, dev, d),
+            _bytes_at(v_pages, "v_pages", _CODES, rows * d, dev, d),
+            _bytes_at(k_scales, "k_scales", _SCALES, rows // 16, dev, blocks),
+            _bytes_at(v_scales, "v_scales", _SCALES, rows // 16, dev, blocks))
+
+
+def gdn_kv_append8(cfg, qkv, q_w, k_w, inv_freq, positions, pair_axis, cu_seqlens, kv_lens,
+                   block_table, q, k, k_pages, v_pages, k_scales, v_scales, stream=None):
+    """gdn_kv_append into 8-bit pages: e4m3 codes [n_pages, hkv, page_size, d] and scales (e8m0)
+    [n_pages, hkv, page_size / 16]; positions and pair_axis may be None (one axis)."""
+    dev, t, d, cols, hkv = _dev(qkv, k_pages), _GDN_DTYPE.get(cfg.dtype), cfg.d, cfg.max_pages, cfg.hkv
+    n = cfg.t_max * d
+    front = _front_args(cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens, t, dev)
+    _attn_call("gdn_kv_append8", dev, stream,
+               front[:6] + _axes_args(cfg, positions, pair_axis, dev) + front[6:] +
+               (_at(block_table, "block_table", torch.int32, cfg.n_max * cols, dev, cols),
+                _at(q, "q", t, n * cfg.h, dev, d), _at(k, "k", t, n * hkv, dev, d)) +
+               _cache8_args(cfg, k_pages, v_pages, k_scales, v_scales, dev))
+
+
 def gdn_attn_prefill(cfg, q, k, v, cu_q, cu_k, o, workspace, ws_bytes=None, stream=None):
     """Causal attention over packed prompts; q, k, v [tokens, heads, d] may have any
     row stride (a multiple of 8); cu_k None = cu_q."""
@@ -633,6 +720,52 @@ def gdn_attn_paged(cfg, q, k_pages, v_pages, cu_seqlens, kv_lens, block_table, s
                 _at(block_table, "block_table", i32, n * cols, dev, cols),
                 _at(shared_len, "shared_len", i32, 1, dev), _at(o, "o", t, tq * h * d, dev, d), ws,
                 ws_bytes))
+
+
+def gdn_attn_paged8_workspace_size(cfg: gdn_attn_config) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().gdn_attn_paged8_workspace_size(ctypes.byref(cfg), ctypes.byref(out)),
+           "gdn_attn_paged8_workspace_size")
+    return int(out.value)
+
+
+def gdn_attn_paged8(cfg, q, k_pages, v_pages, k_scales, v_scales, cu_seqlens, kv_lens, block_table,
+                    shared_len, o, workspace, ws_bytes=None, stream=None):
+    """gdn_attn_paged over 8-bit pages and their scales (gdn_kv_append8)."""
+    dev, t, i32 = _dev(q, k_pages, v_pages, o), _GDN_DTYPE.get(cfg.dtype), torch.int32
+    d, h, tq, n, cols = cfg.d, cfg.h, cfg.t_max, cfg.n_max, cfg.max_pages
+    q, q_row = _rows_at(q, "q", t, tq, h, d, dev)
+    ws, ws_bytes = _ws_at(workspace, ws_bytes, dev)
+    _attn_call("gdn_attn_paged8", dev, stream,
+               (ctypes.byref(cfg), q, q_row) +
+               _cache8_args(cfg, k_pages, v_pages, k_scales, v_scales, dev) +
+               (_at(cu_seqlens, "cu_seqlens", i32, n + 1, dev),
+                _at(kv_lens, "kv_lens", i32, n, dev),
+                _at(block_table, "block_table", i32, n * cols, dev, cols),
+                _at(shared_len, "shared_len", i32, 1, dev), _at(o, "o", t, tq * h * d, dev, d), ws,
+                ws_bytes))
+
+
+def rope_pair_axis(sections, interleaved=False, device=None):
+    """The axis of each pair of channels, int32 [sum(sections)]: the first sections[0] pairs are
+    turned by axis 0, the next sections[1] by axis 1, and so on. interleaved: the axes take
+    turns along the pairs instead, an axis dropping out once it has its share (time, height,
+    width, time, ...).
+    """
+    left = [int(x) for x in sections]
+    if not left or min(left) < 0:
+        raise ValueError(f"sections {sections}: pairs of every axis expected")
+    out = []
+    if interleaved:
+        while any(left):
+            for a, n in enumerate(left):
+                if n:
+                    out.append(a)
+                    left[a] -= 1
+    else:
+        for a, n in enumerate(left):
+            out += [a] * n
+    return torch.tensor(out, dtype=torch.int32, device=device)
 
 
 def rope_inv_freq(rot_dim, base=10000.0, factor=1.0, original_len=None, low_turns=1.0,
@@ -669,21 +802,30 @@ def _packed_qkv(qkv, heads, kv_heads):
 
 
 def qk_norm_rope(qkv, heads, kv_heads, cu_seqlens, q_weight=None, k_weight=None, inv_freq=None,
-                 kv_lens=None, eps=1e-6, interleaved=False, rot_scale=1.0):
+                 kv_lens=None, eps=1e-6, interleaved=False, rot_scale=1.0, positions=None,
+                 pair_axis=None):
     """Allocate outputs with torch and run gdn_qk_norm_rope on the current stream.
 
     qkv [T, (heads + 2 kv_heads) d] bf16 or fp16; weights fp32 [d] or None (no
     norm); inv_freq fp32 [rot_dim / 2] or None (no rotation); rot_scale a factor
-    on cos and sin (0 counts as 1). Returns (q [T, heads, d], k [T, kv_heads,
-    d]); v is qkv's last kv_heads d columns."""
+    on cos and sin (0 counts as 1). positions (int32 [axes, T]) with pair_axis
+    (rope_pair_axis): positions of several axes, in the place of kv_lens. Returns
+    (q [T, heads, d], k [T, kv_heads, d]); v is qkv's last kv_heads d columns."""
+    if positions is not None and kv_lens is not None:
+        raise ValueError("positions say where the tokens are: kv_lens must be None")
     T, d = _packed_qkv(qkv, heads, kv_heads)
     cfg = make_attn_config(T, cu_seqlens.numel() - 1, heads, kv_heads, d, qkv.dtype, eps=eps,
                            rot_dim=0 if inv_freq is None else 2 * inv_freq.numel(),
                            rot_interleaved=interleaved, rot_scale=rot_scale)
     q = torch.empty((T, heads, d), dtype=qkv.dtype, device=qkv.device)
     k = torch.empty((T, kv_heads, d), dtype=qkv.dtype, device=qkv.device)
-    if T:
+    if not T:
+        return q, k
+    if positions is None and pair_axis is None:
         gdn_qk_norm_rope(cfg, qkv, q_weight, k_weight, inv_freq, cu_seqlens, kv_lens, q, k)
+    else:
+        gdn_qk_norm_rope_axes(cfg, qkv, q_weight, k_weight, inv_freq, positions, pair_axis,
+                              cu_seqlens, q, k)
     return q, k
 
 
@@ -697,11 +839,14 @@ def _pages(k_pages, v_pages, block_table):
 
 def append_paged_kv(qkv, heads, cu_seqlens, kv_lens, block_table, k_pages, v_pages, q_weight=None,
                     k_weight=None, inv_freq=None, eps=1e-6, interleaved=False, rot_scale=1.0,
-                    output_k=False):
+                    output_k=False, k_scales=None, v_scales=None, positions=None, pair_axis=None):
     """Run gdn_kv_append on the current stream: q and k normed and rotated, k and v
     written into the cache pages of their positions (kv_lens: tokens of each
-    sequence in all, these included). Returns q [T, heads, d], or (q, k) with
-    output_k."""
+    sequence in all, these included). positions (int32 [axes, T]) with pair_axis
+    (rope_pair_axis): rotation by positions of several axes. k_scales, v_scales
+    (float8_e8m0fnu or uint8 [pages, kv_heads, page_size / 16]): the pages hold 8-bit
+    numbers (float8_e4m3fn or uint8; gdn_kv_append8). Returns q [T, heads, d], or (q, k)
+    with output_k."""
     pages, hkv, size, d = _pages(k_pages, v_pages, block_table)
     T, dq = _packed_qkv(qkv, heads, hkv)
     if dq != d:
@@ -712,17 +857,31 @@ def append_paged_kv(qkv, heads, cu_seqlens, kv_lens, block_table, k_pages, v_pag
                            n_pages=pages, max_pages=block_table.shape[1])
     q = torch.empty((T, heads, d), dtype=qkv.dtype, device=qkv.device)
     k = torch.empty((T, hkv, d), dtype=qkv.dtype, device=qkv.device) if output_k else None
-    if T:
-        gdn_kv_append(cfg, qkv, q_weight, k_weight, inv_freq, cu_seqlens, kv_lens, block_table, q,
-                      k, k_pages, v_pages)
+    if T == 0:
+        return (q, k) if output_k else q
+    front = (cfg, qkv, q_weight, k_weight, inv_freq)
+    axes = (positions, pair_axis)
+    cache = (cu_seqlens, kv_lens, block_table, q, k, k_pages, v_pages)
+    if k_scales is not None or v_scales is not None:
+        _both_scales(k_scales, v_scales)
+        gdn_kv_append8(*front, *axes, *cache, k_scales, v_scales)
+    elif axes != (None, None):
+        gdn_kv_append_axes(*front, *axes, *cache)
+    else:
+        gdn_kv_append(*front, *cache)
     return (q, k) if output_k else q
 
 
-def _attn_workspace(cfg, device, workspace):
+def _both_scales(k_scales, v_scales):
+    if k_scales is None or v_scales is None:
+        raise ValueError("k_scales and v_scales go together")
+
+
+def _attn_workspace(cfg, device, workspace, size=gdn_attn_workspace_size):
     if workspace is not None:
         return workspace
     with torch.cuda.device(device):
-        return torch.empty(gdn_attn_workspace_size(cfg), dtype=torch.uint8, device=device)
+        return torch.empty(size(cfg), dtype=torch.uint8, device=device)
 
 
 def _scale(scale):
@@ -764,14 +923,16 @@ def causal_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, scale=None, workspa
 
 
 def paged_attention(q, k_pages, v_pages, cu_seqlens, kv_lens, block_table, shared_len=None,
-                    scale=None, workspace=None, shared_max=None):
+                    scale=None, workspace=None, shared_max=None, k_scales=None, v_scales=None):
     """Allocate the output with torch and run gdn_attn_paged on the current stream.
 
     q [T, heads, d]: the new tokens of every sequence (one each when decoding),
     whose keys and values the cache already holds; shared_len: int32 [1] on the
     device, positions that lie in the same pages for the whole batch (at most
     shared_max, by default the table's capacity; read once for all where that saves
-    more than it costs). Returns o [T, heads, d]."""
+    more than it costs). k_scales, v_scales: the pages hold 8-bit numbers
+    (gdn_attn_paged8; a workspace is then of gdn_attn_paged8_workspace_size bytes).
+    Returns o [T, heads, d]."""
     pages, hkv, size, d = _pages(k_pages, v_pages, block_table)
     if q.dim() != 3 or q.shape[2] != d:
         raise ValueError(f"q [T, heads, {d}] expected: {tuple(q.shape)}")
@@ -782,6 +943,12 @@ def paged_attention(q, k_pages, v_pages, cu_seqlens, kv_lens, block_table, share
                            cols * size if shared_max is None else shared_max)
     o = torch.empty((q.shape[0], q.shape[1], d), dtype=q.dtype, device=q.device)
     if q.shape[0] == 0:
+        return o
+    if k_scales is not None or v_scales is not None:
+        _both_scales(k_scales, v_scales)
+        workspace = _attn_workspace(cfg, q.device, workspace, gdn_attn_paged8_workspace_size)
+        gdn_attn_paged8(cfg, q, k_pages, v_pages, k_scales, v_scales, cu_seqlens, kv_lens,
+                        block_table, shared_len, o, workspace)
         return o
     workspace = _attn_workspace(cfg, q.device, workspace)
     gdn_attn_paged(cfg, q, k_pages, v_pages, cu_seqlens, kv_lens, block_table, shared_len, o,

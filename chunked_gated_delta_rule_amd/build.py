@@ -17,7 +17,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgdn.so")
 SOURCES = ["chunk_index.hip", "front.hip", "intra.hip", "inter.hip", "recurrent.hip", "noalloc.hip",
-           "attn_front.hip", "attn_prefill.hip", "attn_paged.hip", "attn_api.cpp",
+           "attn_front.hip", "attn_append8.hip", "attn_prefill.hip", "attn_paged.hip", "attn_api.cpp",
            "gdn_api.cpp"]
 ARCH = "gfx950"
 

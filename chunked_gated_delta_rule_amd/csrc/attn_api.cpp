@@ -106,12 +106,15 @@ PagedLayout paged_layout(const gdn_attn_config *cfg) {
   return l;
 }
 
-size_t workspace_bytes(const gdn_attn_config *cfg) {
-  const size_t prefill = prefill_layout(cfg, gdn::Keys::kRows).total;
+size_t paged_bytes(const gdn_attn_config *cfg) {
   const size_t paged = gdn::streams(cfg) ? paged_layout(cfg).total
                                          : prefill_layout(cfg, gdn::Keys::kPages).total;
-  const size_t most = prefill > paged ? prefill : paged;
-  return most > kAlign ? most : kAlign;
+  return paged > kAlign ? paged : kAlign;
+}
+
+size_t workspace_bytes(const gdn_attn_config *cfg) {
+  const size_t prefill = prefill_layout(cfg, gdn::Keys::kRows).total, paged = paged_bytes(cfg);
+  return prefill > paged ? prefill : paged;
 }
 
 gdn_status check_workspace(size_t need, const void *ws, size_t bytes) {
@@ -146,30 +149,48 @@ void tile_common(const gdn_attn_config *cfg, gdn::TileArgs &a, char *ws, size_t 
   a.part_ml = reinterpret_cast<float *>(ws + part_ml);
 }
 
+// Positions of several axes (null: none).
+struct Axes {
+  const int32_t *positions, *pair_axis;
+  int32_t n_axes;
+};
+// A cache that k and v are written to (null pages: none; null scales: 16-bit).
+struct Cache {
+  const int32_t *kv_lens, *block_table;
+  void *k_pages, *v_pages;
+  uint8_t *k_scales, *v_scales;
+};
+
 gdn_status front(const gdn_attn_config *cfg, const void *qkv, int64_t qkv_row, const float *q_w,
-                 const float *k_w, const float *inv_freq, const int32_t *cu_seqlens,
-                 const int32_t *kv_lens, const int32_t *block_table, void *q, void *k,
-                 void *k_pages, void *v_pages, void *stream) {
+                 const float *k_w, const float *inv_freq, const Axes &axes,
+                 const int32_t *cu_seqlens, const Cache &cache, void *q, void *k, void *stream) {
   if (!qkv || !cu_seqlens || (inv_freq != nullptr) != (cfg->rot_dim > 0))
     return GDN_ERR_INVALID_ARG;
+  if (cache.k_pages && (cfg->n_pages < 1 || cfg->max_pages < 1)) return GDN_ERR_INVALID_ARG;
   gdn::FrontArgs a;
   if (!row_of(qkv_row, (static_cast<int64_t>(cfg->h) + 2 * cfg->hkv) * cfg->d, a.qkv_row))
     return GDN_ERR_INVALID_ARG;
-  if (!aligned(qkv, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(k_pages, 16) ||
-      !aligned(v_pages, 16) || !aligned(q_w, 4) || !aligned(k_w, 4) || !aligned(inv_freq, 4) ||
-      !aligned(cu_seqlens, 4) || !aligned(kv_lens, 4) || !aligned(block_table, 4))
+  if (!aligned(qkv, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(cache.k_pages, 16) ||
+      !aligned(cache.v_pages, 16) || !aligned(q_w, 4) || !aligned(k_w, 4) || !aligned(inv_freq, 4) ||
+      !aligned(cu_seqlens, 4) || !aligned(cache.kv_lens, 4) || !aligned(cache.block_table, 4) ||
+      !aligned(axes.positions, 4) || !aligned(axes.pair_axis, 4))
     return GDN_ERR_INVALID_ARG;
   a.qkv = qkv;
   a.q_w = q_w;
   a.k_w = k_w;
   a.inv_freq = inv_freq;
   a.cu = cu_seqlens;
-  a.kv_lens = kv_lens;
-  a.table = block_table;
+  a.kv_lens = cache.kv_lens;
+  a.table = cache.block_table;
+  a.positions = axes.positions;
+  a.pair_axis = axes.pair_axis;
+  a.n_axes = axes.n_axes;
   a.q = q;
   a.k = k;
-  a.k_pages = k_pages;
-  a.v_pages = v_pages;
+  a.k_pages = cache.k_pages;
+  a.v_pages = cache.v_pages;
+  a.k_scales = cache.k_scales;
+  a.v_scales = cache.v_scales;
   a.t_max = cfg->t_max;
   a.n_max = cfg->n_max;
   a.h = cfg->h;
@@ -180,7 +201,94 @@ gdn_status front(const gdn_attn_config *cfg, const void *qkv, int64_t qkv_row, c
   a.page_shift = page_shift(cfg);
   a.n_pages = cfg->n_pages;
   a.max_pages = cfg->max_pages;
-  return from_hip(gdn::launch_attn_front(cfg, a, as_stream(stream)));
+  return from_hip(a.k_scales ? gdn::launch_attn_append8(cfg, a, as_stream(stream))
+                             : gdn::launch_attn_front(cfg, a, as_stream(stream)));
+}
+
+// Axes as a call that needs them takes them.
+bool check_axes(const gdn_attn_config *cfg, const Axes &x) {
+  return x.positions && x.pair_axis && x.n_axes >= 1 && x.n_axes <= GDN_AXES_LIMIT && cfg->rot_dim > 0;
+}
+
+gdn_status paged(const gdn_attn_config *cfg, const void *q, int64_t q_row, const void *k_pages,
+                 const void *v_pages, const uint8_t *k_scales, const uint8_t *v_scales,
+                 const int32_t *cu_seqlens, const int32_t *kv_lens, const int32_t *block_table,
+                 const int32_t *shared_len, void *o, void *workspace, size_t need, size_t ws_bytes,
+                 void *stream) {
+  if (!q || !k_pages || !v_pages || !cu_seqlens || !kv_lens || !block_table || !o)
+    return GDN_ERR_INVALID_ARG;
+  if (cfg->n_pages < 1 || cfg->max_pages < 1) return GDN_ERR_INVALID_ARG;
+  const gdn_status ws = check_workspace(need, workspace, ws_bytes);
+  if (ws != GDN_OK) return ws;
+  int64_t row;
+  if (!row_of(q_row, static_cast<int64_t>(cfg->h) * cfg->d, row)) return GDN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(o, 16) ||
+      !aligned(cu_seqlens, 4) || !aligned(kv_lens, 4) || !aligned(block_table, 4) ||
+      !aligned(shared_len, 4))
+    return GDN_ERR_INVALID_ARG;
+  char *at = static_cast<char *>(workspace);
+  gdn::PagedBatch pg;
+  pg.cu = cu_seqlens;
+  pg.kv_lens = kv_lens;
+  pg.table = block_table;
+  pg.shared_len = gdn::shares(cfg) ? shared_len : nullptr;
+  pg.t_max = cfg->t_max;
+  pg.n_max = cfg->n_max;
+  pg.page_shift = page_shift(cfg);
+  pg.n_pages = cfg->n_pages;
+  pg.max_pages = cfg->max_pages;
+  pg.shared_max = cfg->shared_max;
+  gdn::TileArgs t = {};
+  t.q = q;
+  t.q_row = row;
+  t.k = k_pages;
+  t.v = v_pages;
+  t.k_scales = k_scales;
+  t.v_scales = v_scales;
+  t.cu_q = cu_seqlens;
+  t.pg = pg;
+  t.o = o;
+  if (!gdn::streams(cfg)) {
+    const PrefillLayout l = prefill_layout(cfg, gdn::Keys::kPages);
+    tile_common(cfg, t, at, l.part_o, l.part_ml);
+    return from_hip(gdn::launch_attn_tiles(cfg, gdn::Keys::kPages, t, as_stream(stream)));
+  }
+  const PagedLayout l = paged_layout(cfg);
+  gdn::StreamArgs a = {};
+  if (pg.shared_len) {
+    tile_common(cfg, t, at, l.pre_o, l.pre_ml);
+    const hipError_t e = gdn::launch_attn_tiles(cfg, gdn::Keys::kShared, t, as_stream(stream));
+    if (e != hipSuccess) return GDN_ERR_HIP;
+    const gdn::TileShape s = gdn::tile_shape(cfg, gdn::Keys::kShared);
+    a.pre_share = s.share;
+    a.pre_tt = s.tt;
+    a.pre_slots = s.slots;
+    a.pre_splits = s.splits;
+    a.pre_rows = s.rows;
+  } else {
+    a.pre_share = a.pre_tt = 1;  // the prefix is empty: these are divided by, not used
+  }
+  a.q = q;
+  a.q_row = row;
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.pg = pg;
+  a.o = o;
+  a.h = cfg->h;
+  a.hkv = cfg->hkv;
+  a.scale_log2 = scale_log2(cfg);
+  a.grid = gdn::stream_grid(cfg);
+  a.prefix = reinterpret_cast<int32_t *>(at + l.prefix);
+  a.plan = at + l.plan;
+  a.part_o = reinterpret_cast<float *>(at + l.part_o);
+  a.part_ml = reinterpret_cast<float *>(at + l.part_ml);
+  a.done_o = reinterpret_cast<float *>(at + l.done_o);
+  a.done_ml = reinterpret_cast<float *>(at + l.done_ml);
+  a.pre_o = reinterpret_cast<float *>(at + l.pre_o);
+  a.pre_ml = reinterpret_cast<float *>(at + l.pre_ml);
+  return from_hip(gdn::launch_attn_stream(cfg, a, as_stream(stream)));
 }
 
 }  // namespace
@@ -202,8 +310,18 @@ gdn_status gdn_qk_norm_rope(const gdn_attn_config *cfg, const void *qkv, int64_t
   const gdn_status st = check_config(cfg);
   if (st != GDN_OK) return st;
   if (!q || !k) return GDN_ERR_INVALID_ARG;
-  return front(cfg, qkv, qkv_row, q_w, k_w, inv_freq, cu_seqlens, kv_lens, nullptr, q, k, nullptr,
-               nullptr, stream);
+  return front(cfg, qkv, qkv_row, q_w, k_w, inv_freq, {}, cu_seqlens, {kv_lens}, q, k, stream);
+}
+
+gdn_status gdn_qk_norm_rope_axes(const gdn_attn_config *cfg, const void *qkv, int64_t qkv_row,
+                                 const float *q_w, const float *k_w, const float *inv_freq,
+                                 const int32_t *positions, const int32_t *pair_axis, int32_t n_axes,
+                                 const int32_t *cu_seqlens, void *q, void *k, void *stream) {
+  const gdn_status st = check_config(cfg);
+  if (st != GDN_OK) return st;
+  const Axes axes = {positions, pair_axis, n_axes};
+  if (!q || !k || !check_axes(cfg, axes)) return GDN_ERR_INVALID_ARG;
+  return front(cfg, qkv, qkv_row, q_w, k_w, inv_freq, axes, cu_seqlens, {}, q, k, stream);
 }
 
 gdn_status gdn_kv_append(const gdn_attn_config *cfg, const void *qkv, int64_t qkv_row,
@@ -214,9 +332,40 @@ gdn_status gdn_kv_append(const gdn_attn_config *cfg, const void *qkv, int64_t qk
   const gdn_status st = check_config(cfg);
   if (st != GDN_OK) return st;
   if (!kv_lens || !block_table || !k_pages || !v_pages) return GDN_ERR_INVALID_ARG;
-  if (cfg->n_pages < 1 || cfg->max_pages < 1) return GDN_ERR_INVALID_ARG;
-  return front(cfg, qkv, qkv_row, q_w, k_w, inv_freq, cu_seqlens, kv_lens, block_table, q, k,
-               k_pages, v_pages, stream);
+  return front(cfg, qkv, qkv_row, q_w, k_w, inv_freq, {}, cu_seqlens,
+               {kv_lens, block_table, k_pages, v_pages}, q, k, stream);
+}
+
+gdn_status gdn_kv_append_axes(const gdn_attn_config *cfg, const void *qkv, int64_t qkv_row,
+                              const float *q_w, const float *k_w, const float *inv_freq,
+                              const int32_t *positions, const int32_t *pair_axis, int32_t n_axes,
+                              const int32_t *cu_seqlens, const int32_t *kv_lens,
+                              const int32_t *block_table, void *q, void *k, void *k_pages,
+                              void *v_pages, void *stream) {
+  const gdn_status st = check_config(cfg);
+  if (st != GDN_OK) return st;
+  const Axes axes = {positions, pair_axis, n_axes};
+  if (!kv_lens || !block_table || !k_pages || !v_pages || !check_axes(cfg, axes))
+    return GDN_ERR_INVALID_ARG;
+  return front(cfg, qkv, qkv_row, q_w, k_w, inv_freq, axes, cu_seqlens,
+               {kv_lens, block_table, k_pages, v_pages}, q, k, stream);
+}
+
+gdn_status gdn_kv_append8(const gdn_attn_config *cfg, const void *qkv, int64_t qkv_row,
+                          const float *q_w, const float *k_w, const float *inv_freq,
+                          const int32_t *positions, const int32_t *pair_axis, int32_t n_axes,
+                          const int32_t *cu_seqlens, const int32_t *kv_lens,
+                          const int32_t *block_table, void *q, void *k, void *k_pages, void *v_pages,
+                          uint8_t *k_scales, uint8_t *v_scales, void *stream) {
+  const gdn_status st = check_config(cfg);
+  if (st != GDN_OK) return st;
+  const Axes axes = {positions, pair_axis, n_axes};
+  if (!kv_lens || !block_table || !k_pages || !v_pages || !k_scales || !v_scales)
+    return GDN_ERR_INVALID_ARG;
+  const bool none = !positions && !pair_axis && n_axes == 0;
+  if (!none && !check_axes(cfg, axes)) return GDN_ERR_INVALID_ARG;
+  return front(cfg, qkv, qkv_row, q_w, k_w, inv_freq, axes, cu_seqlens,
+               {kv_lens, block_table, k_pages, v_pages, k_scales, v_scales}, q, k, stream);
 }
 
 gdn_status gdn_attn_prefill(const gdn_attn_config *cfg, const void *q, int64_t q_row,
@@ -255,76 +404,29 @@ gdn_status gdn_attn_paged(const gdn_attn_config *cfg, const void *q, int64_t q_r
                           void *stream) {
   const gdn_status st = check_config(cfg);
   if (st != GDN_OK) return st;
-  if (!q || !k_pages || !v_pages || !cu_seqlens || !kv_lens || !block_table || !o)
-    return GDN_ERR_INVALID_ARG;
-  if (cfg->n_pages < 1 || cfg->max_pages < 1) return GDN_ERR_INVALID_ARG;
-  const gdn_status ws = check_workspace(workspace_bytes(cfg), workspace, ws_bytes);
-  if (ws != GDN_OK) return ws;
-  int64_t row;
-  if (!row_of(q_row, static_cast<int64_t>(cfg->h) * cfg->d, row)) return GDN_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(o, 16) ||
-      !aligned(cu_seqlens, 4) || !aligned(kv_lens, 4) || !aligned(block_table, 4) ||
-      !aligned(shared_len, 4))
-    return GDN_ERR_INVALID_ARG;
-  char *at = static_cast<char *>(workspace);
-  gdn::PagedBatch pg;
-  pg.cu = cu_seqlens;
-  pg.kv_lens = kv_lens;
-  pg.table = block_table;
-  pg.shared_len = gdn::shares(cfg) ? shared_len : nullptr;
-  pg.t_max = cfg->t_max;
-  pg.n_max = cfg->n_max;
-  pg.page_shift = page_shift(cfg);
-  pg.n_pages = cfg->n_pages;
-  pg.max_pages = cfg->max_pages;
-  pg.shared_max = cfg->shared_max;
-  gdn::TileArgs t = {};
-  t.q = q;
-  t.q_row = row;
-  t.k = k_pages;
-  t.v = v_pages;
-  t.cu_q = cu_seqlens;
-  t.pg = pg;
-  t.o = o;
-  if (!gdn::streams(cfg)) {
-    const PrefillLayout l = prefill_layout(cfg, gdn::Keys::kPages);
-    tile_common(cfg, t, at, l.part_o, l.part_ml);
-    return from_hip(gdn::launch_attn_tiles(cfg, gdn::Keys::kPages, t, as_stream(stream)));
-  }
-  const PagedLayout l = paged_layout(cfg);
-  gdn::StreamArgs a = {};
-  if (pg.shared_len) {
-    tile_common(cfg, t, at, l.pre_o, l.pre_ml);
-    const hipError_t e = gdn::launch_attn_tiles(cfg, gdn::Keys::kShared, t, as_stream(stream));
-    if (e != hipSuccess) return GDN_ERR_HIP;
-    const gdn::TileShape s = gdn::tile_shape(cfg, gdn::Keys::kShared);
-    a.pre_share = s.share;
-    a.pre_tt = s.tt;
-    a.pre_slots = s.slots;
-    a.pre_splits = s.splits;
-    a.pre_rows = s.rows;
-  } else {
-    a.pre_share = a.pre_tt = 1;  // the prefix is empty: these are divided by, not used
-  }
-  a.q = q;
-  a.q_row = row;
-  a.k_pages = k_pages;
-  a.v_pages = v_pages;
-  a.pg = pg;
-  a.o = o;
-  a.h = cfg->h;
-  a.hkv = cfg->hkv;
-  a.scale_log2 = scale_log2(cfg);
-  a.grid = gdn::stream_grid(cfg);
-  a.prefix = reinterpret_cast<int32_t *>(at + l.prefix);
-  a.plan = at + l.plan;
-  a.part_o = reinterpret_cast<float *>(at + l.part_o);
-  a.part_ml = reinterpret_cast<float *>(at + l.part_ml);
-  a.done_o = reinterpret_cast<float *>(at + l.done_o);
-  a.done_ml = reinterpret_cast<float *>(at + l.done_ml);
-  a.pre_o = reinterpret_cast<float *>(at + l.pre_o);
-  a.pre_ml = reinterpret_cast<float *>(at + l.pre_ml);
-  return from_hip(gdn::launch_attn_stream(cfg, a, as_stream(stream)));
+  return paged(cfg, q, q_row, k_pages, v_pages, nullptr, nullptr, cu_seqlens, kv_lens, block_table,
+               shared_len, o, workspace, workspace_bytes(cfg), ws_bytes, stream);
+}
+
+gdn_status gdn_attn_paged8_workspace_size(const gdn_attn_config *cfg, size_t *bytes) {
+  const gdn_status st = check_config(cfg);
+  if (st != GDN_OK) return st;
+  if (!bytes) return GDN_ERR_INVALID_ARG;
+  *bytes = paged_bytes(cfg);
+  return GDN_OK;
+}
+
+gdn_status gdn_attn_paged8(const gdn_attn_config *cfg, const void *q, int64_t q_row,
+                           const void *k_pages, const void *v_pages, const uint8_t *k_scales,
+                           const uint8_t *v_scales, const int32_t *cu_seqlens,
+                           const int32_t *kv_lens, const int32_t *block_table,
+                           const int32_t *shared_len, void *o, void *workspace, size_t ws_bytes,
+                           void *stream) {
+  const gdn_status st = check_config(cfg);
+  if (st != GDN_OK) return st;
+  if (!k_scales || !v_scales) return GDN_ERR_INVALID_ARG;
+  return paged(cfg, q, q_row, k_pages, v_pages, k_scales, v_scales, cu_seqlens, kv_lens, block_table,
+               shared_len, o, workspace, paged_bytes(cfg), ws_bytes, stream);
 }
 
 }  // extern "C"

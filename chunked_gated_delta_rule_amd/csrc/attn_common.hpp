@@ -390,4 +390,31 @@ __device__ __forceinline__ Prefix shared_prefix(const PagedBatch &a, int tid,
   return {first < a.n_max ? max(least, 0) >> a.page_shift << a.page_shift : 0, min(first, a.n_max - 1)};
 }
 
+// ---- an 8-bit cache: e4m3 codes, one exponent byte for 16 positions of a page and key head
+
+// Codes per 16-byte word pair and their values: two codes of a word (the lower or the upper)
+// times 2^(e - 127), in the 16-bit type; the conversion takes the scale's exponent, so this
+// is exact as far as the type reaches.
+template <typename T, bool kUpper>
+__device__ __forceinline__ uint32_t values2(uint32_t codes, float scale) {
+  if constexpr (__is_same(T, _Float16))
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, scale, kUpper));
+  else
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, kUpper));
+}
+// Eight codes in a row.
+template <typename T>
+__device__ __forceinline__ u32x4 values8(uint32_t lo, uint32_t hi, float scale) {
+  return u32x4{values2<T, false>(lo, scale), values2<T, true>(lo, scale),
+               values2<T, false>(hi, scale), values2<T, true>(hi, scale)};
+}
+// A scale as the conversions take it (0 stands for 2^-127, 255 for NaN).
+__device__ __forceinline__ float scale_of(uint32_t e) { return __uint_as_float(e << 23); }
+
+// Number of the scale of position `key` of a key head, in a pool of scales.
+__device__ __forceinline__ int64_t scale_at(const PagedBatch &a, int page, int key, int kh, int hkv) {
+  const int shift = a.page_shift - 4;
+  return (((int64_t)page * hkv + kh) << shift) + ((key >> 4) & ((1 << shift) - 1));
+}
+
 }  // namespace gdn

@@ -1,6 +1,7 @@
 // Front of a softmax-attention layer: RMS norm of every query and key head,
-// rotation by the token's position, and (gdn_kv_append) the write of k and v
-// into the pages of the cache, in one pass over the packed q | k | v rows.
+// rotation by the token's position (or, of a position of several axes, by the one that
+// turns the pair), and (gdn_kv_append) the write of k and v into the pages of the cache,
+// in one pass over the packed q | k | v rows.
 //
 //   x' = x / sqrt(mean(x^2) + eps) * w
 //   (a, b) -> s (a cos t - b sin t, b cos t + a sin t),  t = position * inv_freq[i]
@@ -18,9 +19,7 @@
 // in LDS, while the first rows' loads are in flight.
 #include "attn_common.hpp"
 #include "attn_launch.hpp"
-
-#include <cfloat>
-#include <type_traits>
+#include "attn_row.hpp"
 
 namespace gdn {
 
@@ -31,47 +30,24 @@ constexpr int kFrontThreads = 256;
 // 48 of 128 into pages 44; with one 142 and 43, four 136 and 49).
 constexpr int kMostTokens = 2;
 
-// How a lane's eight channels are placed: pairs inside the lane (half layout
-// with rot_dim a multiple of 8, or interleaved), or (half layout with any other
-// rot_dim) eight channels in a row whose partners are read one by one.
-enum class Pairs { kHalf = 0, kInterleaved = 1, kHalfOdd = 2 };
-
-// The least sum of squares that is taken as it is, and the factors for values whose sum is
-// not fp32's (bf16 only): 2^128 2^-96 and 2^-126 2^96 have squares that are.
-constexpr float kSmall = 0x1p-100f, kDown = 0x1p-96f, kUp = 0x1p96f;
-
-// 1 / (2 pi), for angles counted in turns.
-constexpr double kInvTwoPi = 0.15915494309189533577;
-
-template <typename T>
-__device__ __forceinline__ void unpack4(const u32x2 &w, float *f) {
-  f[0] = Elem<T>::lo(w[0]);
-  f[1] = Elem<T>::hi(w[0]);
-  f[2] = Elem<T>::lo(w[1]);
-  f[3] = Elem<T>::hi(w[1]);
-}
-
 // At least six waves per SIMD: the odd layout would take 82 registers, which leaves five (8192
 // tokens of 40 heads of 128, rot_dim 34: 64 us against 58).
-template <typename T, int D, Pairs kPairs, bool kCache>
+//
+// kAxes: positions of several axes come with the tokens, one axis for each pair of channels.
+// They and the pairs' axes are asked for with the first rows, and without a cache no sequence
+// is searched for.
+template <typename T, int D, Pairs kPairs, bool kCache, bool kAxes>
 __global__ __launch_bounds__(kFrontThreads, 6) void attn_front_kernel(FrontArgs a) {
   constexpr int kLanes = D / 8;                    // lanes per head
   constexpr int kRows = kFrontThreads / kLanes;    // rows per pass
   __shared__ __attribute__((aligned(16))) float cs[kMostTokens][D / 2], sn[kMostTokens][D / 2];
   __shared__ int64_t pos_of[kMostTokens], slot_of[kMostTokens];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int li = tid % kLanes;
   const int64_t t0 = (int64_t)flat_block() * a.tokens;
   const int half = a.rot_dim >> 1;
 
-  // this lane's channels: c0 .. c0 + 3 and c1 .. c1 + 3
-  int c0 = 8 * li, c1 = c0 + 4;
-  bool turned = c0 < a.rot_dim;
-  if constexpr (kPairs == Pairs::kHalf) {
-    turned = li < half / 4;
-    c0 = turned ? 4 * li : a.rot_dim + 8 * (li - half / 4);
-    c1 = turned ? half + 4 * li : c0 + 4;
-  }
+  const Channels<kPairs> ch(tid % kLanes, a.rot_dim);
+  const int c0 = ch.c0, c1 = ch.c1;
   // rows of the work-group: token by token, its heads in order. The first ones are
   // asked for before it is known how many tokens there are (qkv has t_max rows)
   const int first = a.q ? 0 : a.h;
@@ -89,6 +65,13 @@ __global__ __launch_bounds__(kFrontThreads, 6) void attn_front_kernel(FrontArgs 
   };
   load();
   const float freq = tid < half ? a.inv_freq[tid] : 0.f;
+  int place = 0;  // where the token of this thread's first angle lies along the pair's axis
+  if constexpr (kAxes) {
+    static_assert(kMostTokens * (D / 2) <= kFrontThreads, "one angle per thread");
+    const int k = half > 0 ? tid / half : 0, j = tid - k * half;
+    if (half > 0 && k < a.tokens && t0 + k < a.t_max)
+      place = a.positions[min(max(a.pair_axis[j], 0), a.n_axes - 1) * (int64_t)a.t_max + t0 + k];
+  }
   typedef f32x4 weights __attribute__((aligned(4)));
   f32x4 wq0{1.f, 1.f, 1.f, 1.f}, wq1 = wq0, wk0 = wq0, wk1 = wq0;
   if (a.q_w) {
@@ -105,35 +88,36 @@ __global__ __launch_bounds__(kFrontThreads, 6) void attn_front_kernel(FrontArgs 
   rows = nt * heads;
 
   // (a single token: every wave for itself, and no barrier)
-  for (int i = a.tokens > 1 ? w : 0; i < nt; i += kFrontThreads / 64) {
-    const int t = (int)t0 + i;
-    int len = 0;
-    const Packed p = seq_of_row(
-        a.cu, a.n_max, a.t_max, t, lane, [&](int s) { return a.kv_lens ? a.kv_lens[s] : 0; }, len);
-    // kv_lens is the caller's: the position is formed in 64 bits
-    const int64_t pos = a.kv_lens ? (int64_t)len - (p.b + p.n - t) : t - p.b;
-    int64_t slot = -1;  // the token's row in a page pool of one head
-    if constexpr (kCache) {
-      const int64_t col = pos >> a.page_shift;
-      if (pos >= 0 && col < a.max_pages) {
-        const int page = a.table[(int64_t)p.s * a.max_pages + col];
-        if (page >= 0 && page < a.n_pages)
-          slot = (((int64_t)page * a.hkv) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+  if constexpr (kCache || !kAxes) {
+    for (int i = a.tokens > 1 ? w : 0; i < nt; i += kFrontThreads / 64) {
+      const int t = (int)t0 + i;
+      int len = 0;
+      const Packed p = seq_of_row(
+          a.cu, a.n_max, a.t_max, t, lane, [&](int s) { return a.kv_lens ? a.kv_lens[s] : 0; }, len);
+      // kv_lens is the caller's: the position is formed in 64 bits
+      const int64_t pos = a.kv_lens ? (int64_t)len - (p.b + p.n - t) : t - p.b;
+      int64_t slot = -1;  // the token's row in a page pool of one head
+      if constexpr (kCache) {
+        const int64_t col = pos >> a.page_shift;
+        if (pos >= 0 && col < a.max_pages) {
+          const int page = a.table[(int64_t)p.s * a.max_pages + col];
+          if (page >= 0 && page < a.n_pages)
+            slot = (((int64_t)page * a.hkv) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+        }
       }
-    }
-    if (lane == 0) {
-      pos_of[i] = pos;
-      slot_of[i] = slot;
+      if (lane == 0) {
+        pos_of[i] = pos;
+        slot_of[i] = slot;
+      }
     }
   }
   if (a.tokens > 1) __syncthreads();
   for (int i = tid; i < nt * half; i += kFrontThreads) {
     const int k = i / half, j = i - k * half;
     const float per_pos = k == 0 ? freq : a.inv_freq[j];
-    const double turns = (double)pos_of[k] * (double)per_pos * kInvTwoPi;
-    const float f = (float)(turns - __builtin_rint(turns));  // -1/2 .. 1/2
-    cs[k][j] = a.rot_scale * __builtin_amdgcn_cosf(f);  // cos(2 pi f)
-    sn[k][j] = a.rot_scale * __builtin_amdgcn_sinf(f);
+    const f32x2 turn = turn_of(kAxes ? (double)place : (double)pos_of[k], per_pos, a.rot_scale);
+    cs[k][j] = turn[0];
+    sn[k][j] = turn[1];
   }
   __syncthreads();
 
@@ -153,75 +137,17 @@ __global__ __launch_bounds__(kFrontThreads, 6) void attn_front_kernel(FrontArgs 
     float x[8];
     unpack4<T>(y0, x);
     unpack4<T>(y1, x + 4);
-    float ss = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-    ss = sum16(ss);
-    if constexpr (kLanes == 32) ss = sum16x(ss);
-    float rn = norm ? 1.f / sqrtf(ss * (1.f / D) + a.eps) : 1.f;
-    float by = 1.f;
-    if constexpr (std::is_same_v<T, __bf16>) {
-      // values whose squares leave fp32 (past about 2^60), or vanish in it with nothing
-      // added to them, are brought to the middle of its range first
-      const bool large = ss > FLT_MAX, small = ss < kSmall && a.eps < kSmall;
-      if (__any(norm && (large || small))) {
-        if (norm && (large || small)) by = large ? kDown : kUp;
-        ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          x[j] *= by;
-          ss = fmaf(x[j], x[j], ss);
-        }
-        ss = sum16(ss);
-        if constexpr (kLanes == 32) ss = sum16x(ss);
-        if (norm) rn = 1.f / sqrtf(ss * (1.f / D) + a.eps * by * by);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[j] *= rn * (is_q ? wq0[j] : wk0[j]);
-      x[j + 4] *= rn * (is_q ? wq1[j] : wk1[j]);
-    }
-    if (!is_v) {
-      const float *ct = cs[tk], *st = sn[tk];
-      if constexpr (kPairs == Pairs::kHalf) {
-        if (turned) {
-          const f32x4 c = *reinterpret_cast<const f32x4 *>(ct + c0);
-          const f32x4 d = *reinterpret_cast<const f32x4 *>(st + c0);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float u = x[j], v = x[j + 4];
-            x[j] = u * c[j] - v * d[j];
-            x[j + 4] = v * c[j] + u * d[j];
-          }
-        }
-      } else if constexpr (kPairs == Pairs::kInterleaved) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (c0 + 2 * j < a.rot_dim) {
-            const float c = ct[(c0 >> 1) + j], d = st[(c0 >> 1) + j];
-            const float u = x[2 * j], v = x[2 * j + 1];
-            x[2 * j] = u * c - v * d;
-            x[2 * j + 1] = v * c + u * d;
-          }
-        }
-      } else {
-        if (in) {
-          const float *wp = is_q ? a.q_w : a.k_w;
-          const T *row = base + tk * a.qkv_row + hd * D;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int c = c0 + j;
-            if (c < a.rot_dim) {
-              const bool low = c < half;
-              const int p = low ? c + half : c - half, i = low ? c : p;
-              const float y = static_cast<float>(row[p]) * by * rn * (wp ? wp[p] : 1.f);
-              x[j] = x[j] * ct[i] + (low ? -y : y) * st[i];
-            }
-          }
-        }
-      }
-    }
+    norm_rope_row<T, D, kPairs>(
+        x, ch, norm, !is_v, in, a.eps, a.rot_dim,
+        [&](int j) __attribute__((always_inline)) {
+          return j < 4 ? (is_q ? wq0[j & 3] : wk0[j & 3]) : (is_q ? wq1[j & 3] : wk1[j & 3]);
+        },
+        [&](const float *&ct, const float *&st) __attribute__((always_inline)) {
+          ct = cs[tk];
+          st = sn[tk];
+        },
+        [&]() __attribute__((always_inline)) { return base + tk * a.qkv_row + hd * D; },
+        [&]() __attribute__((always_inline)) { return is_q ? a.q_w : a.k_w; });
     if (!in) continue;
     // v is copied as it is, bit for bit
     const u32x2 z0 = is_v ? y0 : u32x2{Elem<T>::pack(x[0], x[1]), Elem<T>::pack(x[2], x[3])};
@@ -254,27 +180,28 @@ __global__ __launch_bounds__(kFrontThreads, 6) void attn_front_kernel(FrontArgs 
   }
 }
 
-template <typename T, int D, bool kCache>
+template <typename T, int D, bool kCache, bool kAxes>
 void run(const FrontArgs &a, bool interleaved, dim3 grid, hipStream_t stream) {
   const dim3 block(kFrontThreads);
   if (interleaved)
-    hipLaunchKernelGGL((attn_front_kernel<T, D, Pairs::kInterleaved, kCache>), grid, block, 0,
+    hipLaunchKernelGGL((attn_front_kernel<T, D, Pairs::kInterleaved, kCache, kAxes>), grid, block, 0,
                        stream, a);
   else if (a.rot_dim % 8 == 0)
-    hipLaunchKernelGGL((attn_front_kernel<T, D, Pairs::kHalf, kCache>), grid, block, 0, stream, a);
-  else
-    hipLaunchKernelGGL((attn_front_kernel<T, D, Pairs::kHalfOdd, kCache>), grid, block, 0, stream,
+    hipLaunchKernelGGL((attn_front_kernel<T, D, Pairs::kHalf, kCache, kAxes>), grid, block, 0, stream,
                        a);
+  else
+    hipLaunchKernelGGL((attn_front_kernel<T, D, Pairs::kHalfOdd, kCache, kAxes>), grid, block, 0,
+                       stream, a);
 }
 
-template <typename T>
-void run_of(const FrontArgs &a, int d, bool interleaved, dim3 grid, hipStream_t stream) {
-  if (d == 128)
-    a.k_pages ? run<T, 128, true>(a, interleaved, grid, stream)
-              : run<T, 128, false>(a, interleaved, grid, stream);
+template <typename T, int D>
+void run_of(const FrontArgs &a, bool interleaved, dim3 grid, hipStream_t stream) {
+  if (a.positions)
+    a.k_pages ? run<T, D, true, true>(a, interleaved, grid, stream)
+              : run<T, D, false, true>(a, interleaved, grid, stream);
   else
-    a.k_pages ? run<T, 256, true>(a, interleaved, grid, stream)
-              : run<T, 256, false>(a, interleaved, grid, stream);
+    a.k_pages ? run<T, D, true, false>(a, interleaved, grid, stream)
+              : run<T, D, false, false>(a, interleaved, grid, stream);
 }
 
 }  // namespace
@@ -292,10 +219,13 @@ hipError_t launch_attn_front(const gdn_attn_config *cfg, FrontArgs a, hipStream_
   dim3 grid;
   if (!flat_grid((cfg->t_max + a.tokens - 1) / a.tokens, kFrontThreads, grid))
     return hipErrorInvalidValue;
+  const bool interleaved = cfg->rot_interleaved != 0;
   if (cfg->dtype == GDN_BF16)
-    run_of<__bf16>(a, cfg->d, cfg->rot_interleaved != 0, grid, stream);
+    cfg->d == 128 ? run_of<__bf16, 128>(a, interleaved, grid, stream)
+                  : run_of<__bf16, 256>(a, interleaved, grid, stream);
   else
-    run_of<_Float16>(a, cfg->d, cfg->rot_interleaved != 0, grid, stream);
+    cfg->d == 128 ? run_of<_Float16, 128>(a, interleaved, grid, stream)
+                  : run_of<_Float16, 256>(a, interleaved, grid, stream);
   return hipGetLastError();
 }
 

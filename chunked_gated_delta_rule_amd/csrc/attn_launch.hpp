@@ -16,7 +16,12 @@ struct FrontArgs {
   int64_t qkv_row;  // elements
   const float *q_w, *k_w, *inv_freq;
   const int32_t *cu, *kv_lens, *table;
+  // positions of several axes [n_axes][t_max] (null: the place in the sequence), and the
+  // axis of each pair
+  const int32_t *positions, *pair_axis;
+  int n_axes;
   void *q, *k, *k_pages, *v_pages;  // k_pages null: no cache
+  uint8_t *k_scales, *v_scales;     // of an 8-bit cache
   int t_max, n_max, h, hkv;
   int rot_dim;
   float eps, rot_scale;
@@ -27,6 +32,8 @@ struct FrontArgs {
   bool past_cache;
 };
 hipError_t launch_attn_front(const gdn_attn_config *cfg, FrontArgs a, hipStream_t stream);
+// The same into an 8-bit cache.
+hipError_t launch_attn_append8(const gdn_attn_config *cfg, FrontArgs a, hipStream_t stream);
 
 // A batch whose keys and values lie in pages.
 struct PagedBatch {
@@ -40,6 +47,7 @@ enum class Keys { kRows = 0, kPages = 1, kShared = 2 };
 
 struct TileArgs {
   const void *q, *k, *v;          // k, v: rows, or the page pools
+  const uint8_t *k_scales, *v_scales;  // not null: the pools hold 8-bit codes
   int64_t q_row, k_row, v_row;    // elements
   const int32_t *cu_q, *cu_k;     // cu_k: with rows only
   PagedBatch pg;                  // with pages only
@@ -69,6 +77,7 @@ struct StreamArgs {
   const void *q;
   int64_t q_row;  // elements
   const void *k_pages, *v_pages;
+  const uint8_t *k_scales, *v_scales;  // not null: the pages hold 8-bit codes
   PagedBatch pg;
   void *o;
   int h, hkv;

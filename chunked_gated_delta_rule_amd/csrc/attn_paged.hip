@@ -74,6 +74,10 @@ template <bool kPast>
 __device__ __forceinline__ u32x4 load16(rsrc_t r, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, kPast ? 2 : 0);  // 2: not temporal
 }
+template <bool kPast>
+__device__ __forceinline__ u32x2 load8(rsrc_t r, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, kPast ? 2 : 0);
+}
 
 template <int kRT>
 __device__ __forceinline__ int row_tiles(int rows) {
@@ -82,13 +86,34 @@ __device__ __forceinline__ int row_tiles(int rows) {
 
 // A wave's 32 keys of a unit: K fragments of two tiles of 16, and rows of V (keys 4 g
 // + e of tile 0, then of tile 1).
-template <typename T, int D>
+template <typename T, int D, bool k8>
 struct Keys32 {
   typename Elem<T>::vec8 k[2][D / 32];
   u32x4 v[D / 128][8];
 };
+// The same in codes of an 8-bit cache, with each tile's scales. A lane's 16 bytes of a key are
+// the fragments of two steps (dims 64 j + 16 g .., eight each); its part of a row of V
+// is D / 16 dims in a row, from D / 16 * c on.
+template <typename T, int D>
+struct Keys32<T, D, true> {
+  u32x4 k[2][D / 64];
+  uint32_t v[8][D / 64];
+  uint32_t k_scale[2], v_scale[2];
+};
 
-template <typename T, int D, int kRT>
+// The 4 x 4 bytes of four words the other way round: word i of the result has byte i of
+// each.
+__device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, uint32_t d,
+                                           uint32_t (&out)[4]) {
+  const uint32_t ab0 = __builtin_amdgcn_perm(b, a, 0x05010400u), ab2 = __builtin_amdgcn_perm(b, a, 0x07030602u);
+  const uint32_t cd0 = __builtin_amdgcn_perm(d, c, 0x05010400u), cd2 = __builtin_amdgcn_perm(d, c, 0x07030602u);
+  out[0] = __builtin_amdgcn_perm(cd0, ab0, 0x05040100u);
+  out[1] = __builtin_amdgcn_perm(cd0, ab0, 0x07060302u);
+  out[2] = __builtin_amdgcn_perm(cd2, ab2, 0x05040100u);
+  out[3] = __builtin_amdgcn_perm(cd2, ab2, 0x07060302u);
+}
+
+template <typename T, int D, int kRT, bool k8>
 __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kernel(StreamArgs a) {
   typedef typename Elem<T>::vec8 vec8;
   constexpr int kRows = 16 * kRT;
@@ -150,7 +175,7 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
   }
   const int64_t total = per_head * a.hkv;
   const int64_t per_wg = max(quotient(total + a.grid - 1, a.grid), (int64_t)1);
-  const bool past = uniform(total > kPastCache / (kUnit * D * 4) && !twice);
+  const bool past = uniform(total > kPastCache / (kUnit * D * (k8 ? 2 : 4)) && !twice);
   RowPlan *const plan = reinterpret_cast<RowPlan *>(a.plan);
   if (wg == 0 && (!few || w == 0)) {
     if (tid == 0) a.prefix[0] = prefix, a.prefix[1] = past;
@@ -198,7 +223,8 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
   pg.max_pages = uniform(pg.max_pages);
   pg.page_shift = uniform(pg.page_shift);
 
-  const T *kpool = static_cast<const T *>(a.k_pages), *vpool = static_cast<const T *>(a.v_pages);
+  typedef std::conditional_t<k8, uint8_t, T> Held;  // what the pages hold
+  const Held *kpool = static_cast<const Held *>(a.k_pages), *vpool = static_cast<const Held *>(a.v_pages);
   auto walk = [&](auto past) __attribute__((always_inline)) {
     int64_t u = u0;
     while (u < u1) {
@@ -223,33 +249,58 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
       };
       // a tile's rows as a range that ends with the sequence's last key: zeros past it,
       // where a page may hold anything
-      auto rows_of = [&](const T *pool, int i, int t) __attribute__((always_inline)) {
+      auto rows_of = [&](const Held *pool, int i, int t) __attribute__((always_inline)) {
         const int left = q.kv - (first + i * kUnit + 16 * t);
-        const T *p = pool + pool_row(pg, pages[t], tile_key(i, t), head, a.hkv) * D;
-        return make_rsrc(p, uniform(max(min(left, 16), 0)) * D * 2);
+        const Held *p = pool + pool_row(pg, pages[t], tile_key(i, t), head, a.hkv) * D;
+        return make_rsrc(p, uniform(max(min(left, 16), 0)) * D * (int)sizeof(Held));
       };
-      auto load_k = [&](Keys32<T, D> &x, int i) __attribute__((always_inline)) {
+      typedef Keys32<T, D, k8> Unit;
+      auto load_k = [&](Unit &x, int i) __attribute__((always_inline)) {
   #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const rsrc_t r = rows_of(kpool, i, t);
+          if constexpr (k8) {
+            x.k_scale[t] = a.k_scales[scale_at(pg, pages[t], tile_key(i, t), head, a.hkv)];
   #pragma unroll
-          for (int j = 0; j < D / 32; ++j)
-            x.k[t][j] = __builtin_bit_cast(
-                vec8, load16<decltype(past)::value>(r, (c * D + 8 * g + 32 * j) * 2));
+            for (int j = 0; j < D / 64; ++j)
+              x.k[t][j] = load16<decltype(past)::value>(r, c * D + 16 * g + 64 * j);
+          } else {
+  #pragma unroll
+            for (int j = 0; j < D / 32; ++j)
+              x.k[t][j] = __builtin_bit_cast(
+                  vec8, load16<decltype(past)::value>(r, (c * D + 8 * g + 32 * j) * 2));
+          }
         }
       };
-      auto load_v = [&](Keys32<T, D> &x, int i) __attribute__((always_inline)) {
+      auto load_v = [&](Unit &x, int i) __attribute__((always_inline)) {
   #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const rsrc_t r = rows_of(vpool, i, t);
+          if constexpr (k8) {
+            x.v_scale[t] = a.v_scales[scale_at(pg, pages[t], tile_key(i, t), head, a.hkv)];
   #pragma unroll
-          for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (D == 128) {
+                const u32x2 y = load8<decltype(past)::value>(r, (4 * g + e) * D + 8 * c);
+                x.v[4 * t + e][0] = y[0];
+                x.v[4 * t + e][1] = y[1];
+              } else {
+                const u32x4 y = load16<decltype(past)::value>(r, (4 * g + e) * D + 16 * c);
   #pragma unroll
-            for (int b = 0; b < kDC; ++b)
-              x.v[b][4 * t + e] = load16<decltype(past)::value>(r, ((4 * g + e) * D + 128 * b + 8 * c) * 2);
+                for (int k = 0; k < 4; ++k) x.v[4 * t + e][k] = y[k];
+              }
+            }
+          } else {
+  #pragma unroll
+            for (int e = 0; e < 4; ++e)
+  #pragma unroll
+              for (int b = 0; b < kDC; ++b)
+                x.v[b][4 * t + e] =
+                    load16<decltype(past)::value>(r, ((4 * g + e) * D + 128 * b + 8 * c) * 2);
+          }
         }
       };
-      Keys32<T, D> x;
+      Unit x;
       if (mine_n > 0) {
         look(0);
         load_k(x, 0);
@@ -304,9 +355,20 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
           sc[t][0] = sc[t][1] = zero4();
   #pragma unroll
           for (int p = 0; p < D / 32; ++p) {
-            const vec8 qf = *reinterpret_cast<const vec8 *>(&qs[16 * t + qrow][32 * p + 8 * g]);
-            sc[t][0] = mfma(x.k[0][p], qf, sc[t][0]);
-            sc[t][1] = mfma(x.k[1][p], qf, sc[t][1]);
+            if constexpr (k8) {
+              const vec8 qf = *reinterpret_cast<const vec8 *>(
+                  &qs[16 * t + qrow][64 * (p >> 1) + 16 * g + 8 * (p & 1)]);
+  #pragma unroll
+              for (int k = 0; k < 2; ++k)
+                sc[t][k] = mfma(__builtin_bit_cast(vec8, values8<T>(x.k[k][p >> 1][2 * (p & 1)],
+                                                                    x.k[k][p >> 1][2 * (p & 1) + 1],
+                                                                    scale_of(x.k_scale[k]))),
+                                qf, sc[t][k]);
+            } else {
+              const vec8 qf = *reinterpret_cast<const vec8 *>(&qs[16 * t + qrow][32 * p + 8 * g]);
+              sc[t][0] = mfma(x.k[0][p], qf, sc[t][0]);
+              sc[t][1] = mfma(x.k[1][p], qf, sc[t][1]);
+            }
           }
         }
         if (i + 1 < mine_n) load_k(x, i + 1);
@@ -352,6 +414,25 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
           }
           pf[t] = __builtin_bit_cast(vec8, pw);
         }
+        if constexpr (k8) {
+          // four dims at a time: the bytes of a word, of the lane's eight keys
+  #pragma unroll
+          for (int k = 0; k < D / 64; ++k) {
+            uint32_t lo[4], hi[4];
+            transpose4(x.v[0][k], x.v[1][k], x.v[2][k], x.v[3][k], lo);
+            transpose4(x.v[4][k], x.v[5][k], x.v[6][k], x.v[7][k], hi);
+  #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float s0 = scale_of(x.v_scale[0]), s1 = scale_of(x.v_scale[1]);
+              const vec8 vf = __builtin_bit_cast(
+                  vec8, u32x4{values2<T, false>(lo[j], s0), values2<T, true>(lo[j], s0),
+                              values2<T, false>(hi[j], s1), values2<T, true>(hi[j], s1)});
+              const int b = k >> 1, at = 4 * (k & 1) + j;
+  #pragma unroll
+              for (int t = 0; t < kRT; ++t) o[t][b][at] = mfma(vf, pf[t], o[t][b][at]);
+            }
+          }
+        } else
   #pragma unroll
         for (int b = 0; b < kDC; ++b)
   #pragma unroll
@@ -396,7 +477,8 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
         for (int b = 0; b < kDC; ++b)
   #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float *p = &os[w][c][128 * b + 32 * g + 8 * i];
+            // (codes: a lane's dims of V are D / 16 in a row)
+            float *p = &os[w][c][k8 ? D / 4 * g + D / 16 * i + 8 * b : 128 * b + 32 * g + 8 * i];
             const auto &x = o[t][b];
             *reinterpret_cast<f32x4 *>(p) = f32x4{x[0][i] * f, x[1][i] * f, x[2][i] * f, x[3][i] * f};
             *reinterpret_cast<f32x4 *>(p + 4) =
@@ -575,8 +657,11 @@ hipError_t run(const StreamArgs &a, int64_t rows, hipStream_t stream) {
   const bool wide = rows < kManyRows;
   dim3 join;
   if (!flat_grid(wide ? rows : (rows + 3) / 4, 256, join)) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((attn_stream_kernel<T, D, kRT>), dim3((a.grid + 7) / 8 * 8), dim3(256), 0,
-                     stream, a);
+  const dim3 grid((a.grid + 7) / 8 * 8);
+  if (a.k_scales)
+    hipLaunchKernelGGL((attn_stream_kernel<T, D, kRT, true>), grid, dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL((attn_stream_kernel<T, D, kRT, false>), grid, dim3(256), 0, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (wide)

@@ -347,8 +347,9 @@ struct Where {
             uniform(past_cache)};
   }
 };
-template <int D, Keys kKeys, bool kSplit, int kThreads>
-__device__ __forceinline__ bool find(const TileArgs &a, int tt, int tid, Where &t,
+// key_bytes: of a key and its value, of one key head.
+template <Keys kKeys, bool kSplit, int kThreads>
+__device__ __forceinline__ bool find(const TileArgs &a, int tt, int key_bytes, int tid, Where &t,
                                      int (&lds)[kThreads / 64][2]) {
   const Place at = place(flat_block(), a.h / a.share, a.slots, a.splits);
   t.group = at.group;
@@ -381,7 +382,7 @@ __device__ __forceinline__ bool find(const TileArgs &a, int tt, int tid, Where &
       // the batch's tiles, last one first, then the slots that are left over
       int first, total;
       auto in = [&](const auto &batch) {
-        if constexpr (kKeys == Keys::kPages) t.past_cache = batch.past_cache(a.hkv * D * 4);
+        if constexpr (kKeys == Keys::kPages) t.past_cache = batch.past_cache(a.hkv * key_bytes);
         return batch.in_order(
             lane,
             [&](const Tiled &x, int first, int total) {
@@ -495,6 +496,113 @@ __device__ __forceinline__ void get(const TileArgs &a, const Where &t,
   }
 }
 
+// Tiles of an 8-bit cache: the codes of a tile to come wait in registers (ask), and are
+// written to LDS as 16-bit values (put) once its place is free, each by one wave for all.
+// A lane's 16 codes are 16 dims of a row in a group of 16 keys, which lies in one page and
+// has one scale.
+template <typename T, int D, int kBN, int kWaves>
+struct Codes {
+  static constexpr int kPass = 1024 * kWaves;  // bytes the waves load at a time
+  static constexpr int kN = kBN * D / kPass;
+  static_assert(kN > 0 && kBN * D % kPass == 0 && 16 * D % 1024 == 0, "whole loads, in one group each");
+  u32x4 x[kN];
+  uint32_t scale[kN];
+
+  // the wave's i-th load: its first byte in the tile, and the group that holds it
+  static __device__ __forceinline__ int from(int i, int w) { return kPass * i + 1024 * w; }
+  static __device__ __forceinline__ int group(int i, int w) { return from(i, w) / D & ~15; }
+
+  struct Pages {
+    int page[kN];
+    __device__ __forceinline__ void look(const TileArgs &a, const Where &t, int k0, int w) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) page[i] = page_of(a.pg, t.s, min(k0 + group(i, w), t.lk - 1));
+    }
+  };
+  // kPast: past the caches
+  template <bool kPast>
+  __device__ __forceinline__ void ask(const void *pool, const uint8_t *scales, const TileArgs &a,
+                                      const Where &t, const Pages &at, int kvh, int k0, int lane, int w) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int key = k0 + group(i, w), last = min(key, t.lk - 1);
+      const uint8_t *p =
+          static_cast<const uint8_t *>(pool) + pool_row(a.pg, at.page[i], key, kvh, a.hkv) * D;
+      // a range that ends with the sequence's last key: zeros past it
+      const rsrc_t r = make_rsrc(p, max(min(16, t.lk - key), 0) * D);
+      x[i] = __builtin_amdgcn_raw_buffer_load_b128(
+          r, (from(i, w) - group(i, w) * D) + 16 * lane, 0, kPast ? 2 : 0);
+      scale[i] = scales[scale_at(a.pg, at.page[i], last, kvh, a.hkv)];
+    }
+  }
+  template <bool kV>
+  __device__ __forceinline__ void put(Lds<T> tile, int lane, int w) const {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int at = from(i, w) + 16 * lane, row = at / D, ch = at % D / 8;
+      const int swz = kV ? v_swz(row) : k_swz(row);
+      const float s = scale_of(scale[i]);
+      *(Lds<u32x4>)(tile + row * D + 8 * (ch ^ swz)) = values8<T>(x[i][0], x[i][1], s);
+      *(Lds<u32x4>)(tile + row * D + 8 * ((ch + 1) ^ swz)) = values8<T>(x[i][2], x[i][3], s);
+    }
+  }
+};
+
+// How a wave's part of the tiles gets into LDS: copied straight, or (k8) through registers,
+// one tile further ahead. to(j, ...) brings tile j (kAhead: asked for before, and asks for the
+// next one, whose pages `spot` names).
+template <typename T, int D, int kBN, int kWaves, Keys kKeys, bool k8>
+struct Bring {
+  static constexpr int kAhead = 0;
+  typedef Spot<Tile<T, D, kBN, kWaves>, kKeys> Spots;
+  template <bool kV, bool kPast>
+  __device__ __forceinline__ void first(const TileArgs &, const Where &, const Spots &, int, int, int, int) {}
+  // k0: the tile's first key, k1: the next one's (below 0: there is none)
+  template <bool kV, bool kPast>
+  __device__ __forceinline__ void to(T *tile, const TileArgs &a, const Where &t, const Spots &spot,
+                                     int kvh, int k0, int, int lane, int w) {
+    if (k0 >= 0) get<T, D, kBN, kWaves, kKeys, kV, kPast>(a, t, spot, kvh, k0, tile, lane, w);
+  }
+};
+template <typename T, int D, int kBN, int kWaves, Keys kKeys>
+struct Bring<T, D, kBN, kWaves, kKeys, true> {
+  static constexpr int kAhead = 1;
+  typedef Codes<T, D, kBN, kWaves> Held;
+  typedef typename Held::Pages Spots;
+  Held k, v;
+  template <bool kV, bool kPast>
+  __device__ __forceinline__ void first(const TileArgs &a, const Where &t, const Spots &spot, int kvh,
+                                        int k0, int lane, int w) {
+    if (k0 < 0) return;
+    if constexpr (kV)
+      v.template ask<kPast>(a.v, a.v_scales, a, t, spot, kvh, k0, lane, w);
+    else
+      k.template ask<kPast>(a.k, a.k_scales, a, t, spot, kvh, k0, lane, w);
+  }
+  template <bool kV, bool kPast>
+  __device__ __forceinline__ void to(T *tile, const TileArgs &a, const Where &t, const Spots &spot,
+                                     int kvh, int k0, int k1, int lane, int w) {
+    if (k0 >= 0) {
+      if constexpr (kV)
+        v.template put<true>((Lds<T>)tile, lane, w);
+      else
+        k.template put<false>((Lds<T>)tile, lane, w);
+    }
+    first<kV, kPast>(a, t, spot, kvh, k1, lane, w);
+  }
+};
+// The wait before a barrier: codes that were asked for go on coming.
+template <bool k8>
+__device__ __forceinline__ void wait_tiles() {
+  if constexpr (k8) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    asm volatile("" ::: "memory");
+  } else {
+    wait_lds();
+  }
+}
+
 template <typename T>
 __device__ __forceinline__ const T *q_row(const TileArgs &a, const Where &t, int tok, int row, int D) {
   return static_cast<const T *>(a.q) + (int64_t)(t.qb + tok) * a.q_row +
@@ -510,7 +618,7 @@ __device__ __forceinline__ const T *q_row(const TileArgs &a, const Where &t, int
 // heads of 256: 2658 us with four waves, 2130 with eight, when this was built; now 1900).
 // Their steps have 64 keys, or 32 with heads of 256, which leaves registers to read
 // fragments ahead (1836 -> 1820).
-template <typename T, int D, int kWaves, Keys kKeys>
+template <typename T, int D, int kWaves, Keys kKeys, bool k8>
 __global__ __launch_bounds__(64 * kWaves, kWaves == 4 ? 3 : 2) void attn_tile_kernel(TileArgs a) {
   constexpr int kBM = 32 * kWaves, kBN = kWaves == 4 || D == 256 ? 32 : 64;
   // four arrays of their own, so that a tile in flight is known to be another
@@ -522,29 +630,37 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 4 ? 3 : 2) void attn_tile_ke
   const int col = lane & 31, hh = lane >> 5;
   Where t;
   const int share = a.share, tt = kBM / share;
-  if (!find<D, kKeys, false, 64 * kWaves>(a, tt, tid, t, scan)) return;
+  if (!find<kKeys, false, 64 * kWaves>(a, tt, D * (k8 ? 2 : 4), tid, t, scan)) return;
   t = t.uniform_();
   const int kvh = t.group * share / (a.h / a.hkv);
   const Sight see = sight_of<kKeys>(t, 32 * w, col, tt, share);
   const int tiles = see.keys > 0 ? (see.keys + kBN - 1) / kBN : 0;
 
-  typedef Spot<Tile<T, D, kBN, kWaves>, kKeys> Spots;
+  typedef Bring<T, D, kBN, kWaves, kKeys, k8> Brings;
+  typedef typename Brings::Spots Spots;
+  constexpr int kAhead = Brings::kAhead;
+  Brings bring;
   auto look = [&](int j) __attribute__((always_inline)) {
     Spots s = {};
     if (j < tiles) s.look(a, t, j * kBN, w);
     return s;
   };
+  auto key_of = [&](int j) { return j < tiles ? j * kBN : -1; };
+  // tile j into LDS; s: the pages of tile j + kAhead
   auto get_k = [&](int j, T *tile, const Spots &s) __attribute__((always_inline)) {
-    if (j < tiles) get<T, D, kBN, kWaves, kKeys, false>(a, t, s, kvh, j * kBN, tile, lane, w);
+    bring.template to<false, false>(tile, a, t, s, kvh, key_of(j), key_of(j + 1), lane, w);
   };
   auto get_v = [&](int j, T *tile, const Spots &s) __attribute__((always_inline)) {
-    if (j < tiles) get<T, D, kBN, kWaves, kKeys, true>(a, t, s, kvh, j * kBN, tile, lane, w);
+    bring.template to<true, false>(tile, a, t, s, kvh, key_of(j), key_of(j + 1), lane, w);
   };
   Rows<T, D, kBN> x;
   {
     const Spots s = look(0);
-    get_k(0, k_a, s);
-    get_v(0, v_a, s);
+    bring.template first<false, false>(a, t, s, kvh, key_of(0), lane, w);
+    bring.template first<true, false>(a, t, s, kvh, key_of(0), lane, w);
+    const Spots s1 = kAhead ? look(1) : s;
+    get_k(0, k_a, s1);
+    get_v(0, v_a, s1);
   }
   x.load(q_row<T>(a, t, see.tok, 32 * w + col, D), hh, a.scale_log2);
   auto score = [&](int j, T *kt) __attribute__((always_inline)) {
@@ -555,21 +671,21 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 4 ? 3 : 2) void attn_tile_ke
     if (j * kBN <= see.hi) x.weigh((Lds<T>)vt, a.scale_log2, lane);
   };
   if constexpr (kWaves == 4) {
-    Spots s = look(1);
+    Spots s = look(1 + kAhead);
     for (int j = 0; j < tiles; j += 2) {
-      wait_lds();
+      wait_tiles<k8>();
       barrier();  // tile j is there, and the other pair is no longer read
       get_k(j + 1, k_b, s);
       get_v(j + 1, v_b, s);
-      s = look(j + 2);
+      s = look(j + 2 + kAhead);
       score(j, k_a);
       weigh(j, v_a);
       if (j + 1 >= tiles) break;
-      wait_lds();
+      wait_tiles<k8>();
       barrier();
       get_k(j + 2, k_a, s);
       get_v(j + 2, v_a, s);
-      s = look(j + 3);
+      s = look(j + 3 + kAhead);
       score(j + 1, k_b);
       weigh(j + 1, v_b);
     }
@@ -580,17 +696,17 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 4 ? 3 : 2) void attn_tile_ke
     // first read in 2 j + 2; V of tile j + 1 from the end of 2 j + 1 (last read in
     // 2 j) for 2 j + 3: each has a whole phase, and is waited for at its end.
     auto k_end = [&](int j, T *kt, const Spots &s) __attribute__((always_inline)) {
-      wait_lds();
+      wait_tiles<k8>();
       get_k(j, kt, s);
       barrier();
     };
     auto v_end = [&](int j, T *vt, const Spots &s) __attribute__((always_inline)) {
-      wait_lds();
+      wait_tiles<k8>();
       get_v(j, vt, s);
       barrier();
     };
-    Spots s = look(1);
-    wait_lds();
+    Spots s = look(1 + kAhead);
+    wait_tiles<k8>();
     barrier();
     if (w < 4) {
       for (int j = 0; j < tiles; j += 2) {
@@ -599,12 +715,12 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 4 ? 3 : 2) void attn_tile_ke
         weigh(j, v_a);
         v_end(j + 1, v_b, s);
         if (j + 1 >= tiles) break;
-        s = look(j + 2);
+        s = look(j + 2 + kAhead);
         score(j + 1, k_b);
         k_end(j + 2, k_a, s);
         weigh(j + 1, v_b);
         v_end(j + 2, v_a, s);
-        s = look(j + 3);
+        s = look(j + 3 + kAhead);
       }
       barrier();
     } else {
@@ -612,13 +728,13 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 4 ? 3 : 2) void attn_tile_ke
       for (int j = 0; j < tiles; j += 2) {
         score(j, k_a);
         v_end(j + 1, v_b, s);
-        s = look(j + 2);
+        s = look(j + 2 + kAhead);
         weigh(j, v_a);
         k_end(j + 2, k_a, s);
         if (j + 1 >= tiles) break;
         score(j + 1, k_b);
         v_end(j + 2, v_a, s);
-        s = look(j + 3);
+        s = look(j + 3 + kAhead);
         weigh(j + 1, v_b);
         k_end(j + 3, k_b, s);
       }
@@ -640,7 +756,7 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 4 ? 3 : 2) void attn_tile_ke
 // above cost more in barriers than they gain (39 against 36 us for 1024 rows on 8192
 // keys of two heads). The second set's state is added to the first's through LDS at
 // the end.
-template <typename T, int D, Keys kKeys>
+template <typename T, int D, Keys kKeys, bool k8>
 __global__ __launch_bounds__(512, 2) void attn_part_kernel(TileArgs a) {
   constexpr int kBM = 128, kBN = D == 256 ? 32 : 64;
   constexpr int kTile = kBN * D;
@@ -654,7 +770,7 @@ __global__ __launch_bounds__(512, 2) void attn_part_kernel(TileArgs a) {
   const int col = lane & 31, hh = lane >> 5;
   Where t;
   const int share = a.share, tt = kBM / share;
-  if (!find<D, kKeys, true, 512>(a, tt, tid, t, scan)) return;
+  if (!find<kKeys, true, 512>(a, tt, D * (k8 ? 2 : 4), tid, t, scan)) return;
   t = t.uniform_();
   const int kvh = t.group * share / (a.h / a.hkv);
   const Sight see = sight_of<kKeys>(t, 32 * w, col, tt, share);
@@ -664,28 +780,33 @@ __global__ __launch_bounds__(512, 2) void attn_part_kernel(TileArgs a) {
   const int steps = max((end - t.split * per + 1) / 2, 0);  // of either set
   // this set's tile of step j, if it has one
   auto has = [&](int j) { return j0 + 2 * j < end; };
-  typedef Spot<Tile<T, D, kBN, 4>, kKeys> Spots;
+  typedef Bring<T, D, kBN, 4, kKeys, k8> Brings;
+  typedef typename Brings::Spots Spots;
+  constexpr int kAhead = Brings::kAhead;
   auto look = [&](int j) __attribute__((always_inline)) {
     Spots s = {};
     if (has(j)) s.look(a, t, (j0 + 2 * j) * kBN, w);
     return s;
   };
+  auto key_of = [&](int j) { return has(j) ? (j0 + 2 * j) * kBN : -1; };
   Rows<T, D, kBN> x;
   auto walk = [&](auto past) __attribute__((always_inline)) {
+    constexpr bool kPast = decltype(past)::value;
+    Brings bring;
+    // tile j into LDS; s: the pages of tile j + kAhead
     auto get_k = [&](int j, T *tile, const Spots &s) __attribute__((always_inline)) {
-      if (has(j))
-        get<T, D, kBN, 4, kKeys, false, decltype(past)::value>(a, t, s, kvh, (j0 + 2 * j) * kBN,
-                                                               tile + set * kTile, lane, w);
+      bring.template to<false, kPast>(tile + set * kTile, a, t, s, kvh, key_of(j), key_of(j + 1), lane, w);
     };
     auto get_v = [&](int j, T *tile, const Spots &s) __attribute__((always_inline)) {
-      if (has(j))
-        get<T, D, kBN, 4, kKeys, true, decltype(past)::value>(a, t, s, kvh, (j0 + 2 * j) * kBN,
-                                                              tile + set * kTile, lane, w);
+      bring.template to<true, kPast>(tile + set * kTile, a, t, s, kvh, key_of(j), key_of(j + 1), lane, w);
     };
     {
       const Spots s = look(0);
-      get_k(0, k_a, s);
-      get_v(0, v_a, s);
+      bring.template first<false, kPast>(a, t, s, kvh, key_of(0), lane, w);
+      bring.template first<true, kPast>(a, t, s, kvh, key_of(0), lane, w);
+      const Spots s1 = kAhead ? look(1) : s;
+      get_k(0, k_a, s1);
+      get_v(0, v_a, s1);
     }
     x.load(q_row<T>(a, t, see.tok, 32 * w + col, D), hh, a.scale_log2);
     auto score = [&](int j, T *kt) __attribute__((always_inline)) {
@@ -697,21 +818,21 @@ __global__ __launch_bounds__(512, 2) void attn_part_kernel(TileArgs a) {
       if (has(j) && (j0 + 2 * j) * kBN <= see.hi)
         x.weigh((Lds<T>)(vt + set * kTile), a.scale_log2, lane);
     };
-    Spots s = look(1);
+    Spots s = look(1 + kAhead);
     for (int j = 0; j < steps; j += 2) {
-      wait_lds();
+      wait_tiles<k8>();
       barrier();
       get_k(j + 1, k_b, s);
       get_v(j + 1, v_b, s);
-      s = look(j + 2);
+      s = look(j + 2 + kAhead);
       score(j, k_a);
       weigh(j, v_a);
       if (j + 1 >= steps) break;
-      wait_lds();
+      wait_tiles<k8>();
       barrier();
       get_k(j + 2, k_a, s);
       get_v(j + 2, v_a, s);
-      s = look(j + 3);
+      s = look(j + 3 + kAhead);
       score(j + 1, k_b);
       weigh(j + 1, v_b);
     }
@@ -814,7 +935,13 @@ hipError_t run_whole(const gdn_attn_config *cfg, const TileArgs &a, hipStream_t 
   dim3 grid;
   if (!flat_grid((int64_t)a.slots * (cfg->h / a.share), 64 * kWaves, grid))
     return hipErrorInvalidValue;
-  hipLaunchKernelGGL((attn_tile_kernel<T, D, kWaves, kKeys>), grid, dim3(64 * kWaves), 0, stream, a);
+  if constexpr (kKeys != Keys::kRows) {
+    if (a.k_scales) {
+      hipLaunchKernelGGL((attn_tile_kernel<T, D, kWaves, kKeys, true>), grid, dim3(64 * kWaves), 0, stream, a);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((attn_tile_kernel<T, D, kWaves, kKeys, false>), grid, dim3(64 * kWaves), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -824,7 +951,14 @@ hipError_t run_parts(const gdn_attn_config *cfg, const TileArgs &a, int tt, hipS
   if (!flat_grid((int64_t)a.slots * (cfg->h / a.share) * a.splits, 512, grid) ||
       !flat_grid(((int64_t)cfg->t_max * cfg->h + 3) / 4, 256, join))
     return hipErrorInvalidValue;
-  hipLaunchKernelGGL((attn_part_kernel<T, D, kKeys>), grid, dim3(512), 0, stream, a);
+  if constexpr (kKeys != Keys::kRows) {
+    if (a.k_scales)
+      hipLaunchKernelGGL((attn_part_kernel<T, D, kKeys, true>), grid, dim3(512), 0, stream, a);
+    else
+      hipLaunchKernelGGL((attn_part_kernel<T, D, kKeys, false>), grid, dim3(512), 0, stream, a);
+  } else {
+    hipLaunchKernelGGL((attn_part_kernel<T, D, kKeys, false>), grid, dim3(512), 0, stream, a);
+  }
   if (kKeys == Keys::kShared) return hipGetLastError();  // the caller joins them
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

@@ -447,6 +447,19 @@ gdn_status gdn_qk_norm_rope(const gdn_attn_config *cfg, const void *qkv, int64_t
                             const int32_t *cu_seqlens, const int32_t *kv_lens, void *q, void *k,
                             void *stream);
 
+/* gdn_qk_norm_rope with positions of several axes (time, height and width of images and
+ * video, say): each pair of channels is turned by the position along one of them.
+ *   positions (device) int32 [n_axes, t_max]: token t lies at positions[a][t] along axis a
+ *            (any values; a token's place in its sequence plays no part)
+ *   pair_axis (device) int32 [rot_dim / 2]: the axis that turns pair i (an entry outside
+ *            0 .. n_axes - 1 counts as the nearest of them)
+ *   n_axes   1 .. GDN_AXES_LIMIT; rot_dim must not be 0 */
+#define GDN_AXES_LIMIT 16
+gdn_status gdn_qk_norm_rope_axes(const gdn_attn_config *cfg, const void *qkv, int64_t qkv_row,
+                                 const float *q_w, const float *k_w, const float *inv_freq,
+                                 const int32_t *positions, const int32_t *pair_axis, int32_t n_axes,
+                                 const int32_t *cu_seqlens, void *q, void *k, void *stream);
+
 /* gdn_qk_norm_rope that writes the rotated keys, and v as it is, into the
  * cache pages of their positions in the same pass.
  *   q (nullable = not wanted), k (nullable = only the pages are written)
@@ -459,6 +472,44 @@ gdn_status gdn_kv_append(const gdn_attn_config *cfg, const void *qkv, int64_t qk
                          const int32_t *cu_seqlens, const int32_t *kv_lens,
                          const int32_t *block_table, void *q, void *k, void *k_pages,
                          void *v_pages, void *stream);
+
+/* gdn_kv_append with positions of several axes as in gdn_qk_norm_rope_axes; kv_lens says, as
+ * ever, which cache rows the tokens are written to. */
+gdn_status gdn_kv_append_axes(const gdn_attn_config *cfg, const void *qkv, int64_t qkv_row,
+                              const float *q_w, const float *k_w, const float *inv_freq,
+                              const int32_t *positions, const int32_t *pair_axis, int32_t n_axes,
+                              const int32_t *cu_seqlens, const int32_t *kv_lens,
+                              const int32_t *block_table, void *q, void *k, void *k_pages,
+                              void *v_pages, void *stream);
+
+/* gdn_kv_append into a cache of 8-bit numbers: half the memory, and half the bytes that a
+ * decode step reads (gdn_attn_paged8).
+ *   k_pages, v_pages (device) [n_pages, hkv, page_size, d] e4m3 codes (OCP: 448 the largest,
+ *            no infinity)
+ *   k_scales, v_scales (device) uint8 [n_pages, hkv, page_size / 16]: a power of two for each
+ *            16 positions (a block) of a page and key head: a byte e stands for
+ *            2^(e - 127), and row r of a page holds code * 2^(e[r / 16] - 127)
+ *   positions, pair_axis, n_axes: several axes, or NULL, NULL, 0
+ * For every block that gets tokens, of each key head, with x the tokens' values (k in fp32
+ * after norm and rotation, v as it is) and a = max |x| over them:
+ *   e = the least one >= 15 with a <= 448 * 2^(e - 127); but where the call does not write
+ *       the block's first position, the block's scale if that is larger
+ *   new rows: the codes nearest to x * 2^(127 - e), ties to even
+ *   rows that the block had, if its scale grew: their values by the new scale, rounded again
+ *       (exact but for codes that get subnormal, below 2^-6)
+ * So e only grows while a block fills, and a block whose first position is written begins
+ * anew whatever it held. Values past the largest number of four significant bits of the 16-bit
+ * type (61440, 1.875 * 2^127) count as that; NaN and infinities are stored as NaN and
+ * count for nothing in a.
+ *   Scales of blocks that a call appends to must be at most 253 (the library writes 15 ..
+ *   247). Two sequences of one call must not write to the same block. Tokens without a place
+ *   in the cache are left out as in gdn_kv_append. q, k (nullable): 16-bit, as there. */
+gdn_status gdn_kv_append8(const gdn_attn_config *cfg, const void *qkv, int64_t qkv_row,
+                          const float *q_w, const float *k_w, const float *inv_freq,
+                          const int32_t *positions, const int32_t *pair_axis, int32_t n_axes,
+                          const int32_t *cu_seqlens, const int32_t *kv_lens,
+                          const int32_t *block_table, void *q, void *k, void *k_pages, void *v_pages,
+                          uint8_t *k_scales, uint8_t *v_scales, void *stream);
 
 /* Causal attention over packed prompts:  o_r = sum_c softmax_c(scale q_r . k_c) v_c
  * over the keys c of the row's sequence up to its own position. Sequence s has
@@ -504,6 +555,22 @@ gdn_status gdn_attn_paged(const gdn_attn_config *cfg, const void *q, int64_t q_r
                           const int32_t *kv_lens, const int32_t *block_table,
                           const int32_t *shared_len, void *o, void *workspace, size_t ws_bytes,
                           void *stream);
+
+/* Bytes of workspace gdn_attn_paged8 needs, as gdn_attn_workspace_size says of the 16-bit
+ * calls. */
+gdn_status gdn_attn_paged8_workspace_size(const gdn_attn_config *cfg, size_t *bytes);
+
+/* gdn_attn_paged over an 8-bit cache as gdn_kv_append8 writes it: k and v are code *
+ * 2^(e - 127), rounded to the 16-bit type (exact wherever that type has the number: four
+ * significant bits). q and o are in the 16-bit type; everything else as gdn_attn_paged
+ * says. A byte of 255 in a scale is NaN, like the codes 127 and 255; rows past a sequence's
+ * length and the scales of blocks without a row of it may hold anything. */
+gdn_status gdn_attn_paged8(const gdn_attn_config *cfg, const void *q, int64_t q_row,
+                           const void *k_pages, const void *v_pages, const uint8_t *k_scales,
+                           const uint8_t *v_scales, const int32_t *cu_seqlens,
+                           const int32_t *kv_lens, const int32_t *block_table,
+                           const int32_t *shared_len, void *o, void *workspace, size_t ws_bytes,
+                           void *stream);
 
 /* Static string for a status code (never NULL). */
 const char *gdn_status_str(gdn_status status);

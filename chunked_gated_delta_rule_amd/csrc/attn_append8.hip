@@ -13,10 +13,11 @@
 // subnormal: they are read, rounded and written again by the wave that appends.
 //
 // HBM-bound. A work-group takes the call's tokens of one block, 16 at most: so the block's
-// scale is one wave's own, found in registers, without atomics and the same from run to
-// run. Queries go row by row, as in the 16-bit front. A wave takes the 16 rows of one key
-// head (64 / (D / 8) rows per step, a lane's eight channels of all of them in registers)
-// or, with a single token, one row of several heads.
+// scale is its own, found in registers and LDS, without atomics and the same from run to run.
+// It goes through the heads in passes of 16 rows, D / 8 lanes and eight channels a lane, the
+// next pass's loads in flight: first k and v, a pass having the rows of one head (of 16 /
+// P heads, where P, the power of two that holds the tokens, is less than 16), then q
+// token by token.
 #include "attn_common.hpp"
 #include "attn_launch.hpp"
 #include "attn_row.hpp"
@@ -27,6 +28,7 @@ namespace {
 
 constexpr int kAppendThreads = 256;
 constexpr int kBlock = 16;  // positions that share a scale
+constexpr int kPartPasses = 4;
 
 // Largest finite value of the cache: the largest number of four significant bits that the
 // 16-bit type holds, so that whoever reads the cache in that type finds no infinity.
@@ -56,21 +58,44 @@ __device__ __forceinline__ uint32_t again4(uint32_t w, float by) {
   return codes4(a[0] * by, a[1] * by, b[0] * by, b[1] * by);
 }
 
+// Maximum of the lanes of a row, in all of them (as sum16 and sum16x go).
+template <int kLanes>
+__device__ __forceinline__ float max_row(float x) {
+  x = fmaxf(x, dpp_in<0xB1, 0xf>(x));
+  x = fmaxf(x, dpp_in<0x4E, 0xf>(x));
+  x = fmaxf(x, dpp_in<0x141, 0xf>(x));
+  x = fmaxf(x, dpp_in<0x140, 0xf>(x));
+  return kLanes == 32 ? max16(x) : x;
+}
+
+// A barrier for what is in LDS; loads go on coming (__syncthreads would wait for them).
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 template <typename T, int D, Pairs kPairs, bool kAxes>
-__global__ __launch_bounds__(kAppendThreads) void attn_append8_kernel(FrontArgs a) {
-  constexpr int kLanes = D / 8;          // lanes per row
-  constexpr int kStep = 64 / kLanes;     // rows of a wave at a time
-  constexpr int kSteps = kBlock / kStep;
+__global__ __launch_bounds__(kAppendThreads, 4) void attn_append8_kernel(FrontArgs a) {
+  constexpr int kLanes = D / 8;                    // lanes per row
+  constexpr int kRows = kAppendThreads / kLanes;   // rows at a time
+  constexpr int kSub = kBlock / kRows;             // rows of a pass per thread: 1 or 2
   __shared__ __attribute__((aligned(16))) float cs[kBlock][D / 2], sn[kBlock][D / 2];
-  const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
-  const int li = lane % kLanes, sub = lane / kLanes;
+  __shared__ __attribute__((aligned(16))) float most[2][kBlock];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int li = tid % kLanes, at = tid / kLanes;
   const int half = a.rot_dim >> 1;
   const Channels<kPairs> ch(li, a.rot_dim);
   const int c0 = ch.c0, c1 = ch.c1;
 
   // ---- the block: block i of sequence s has slot floor(cu[s] / 16) + 2 s + i, distinct for
   // all (n tokens lie in (n + 30) / 16 blocks at most), and its tokens are lo .. hi - 1
-  const int slot = flat_block();
+  // (a.group blocks at a time, part by part. With groups of eight a block's parts are near in
+  // time and all XCDs get as many of each; which part is first changes from group to group,
+  // so that the shader engines do too)
+  const int wg = flat_block(), group = wg / (a.group * a.parts), in = wg - group * a.group * a.parts;
+  const int slot = a.group * group + in % a.group, part = (in / a.group + group) % a.parts;
   int lens[1];
   const Packed p = locate(
       a.cu, a.n_max, a.t_max, slot, lane, [](int s, int b) { return b / kBlock + 2 * s; },
@@ -82,21 +107,94 @@ __global__ __launch_bounds__(kAppendThreads) void attn_append8_kernel(FrontArgs 
   const int lo = (int)max(first - pos0, (int64_t)0);
   const int hi = (int)min(first + kBlock - pos0, (int64_t)p.n);
   if (i < 0 || lo >= hi) return;
-  const int nt = hi - lo, t0 = p.b + lo;
-  const int had = (int)max(pos0 - first, (int64_t)0);       // rows of the block before this call
+  const int nt = uniform(hi - lo), t0 = uniform(p.b + lo);
+  const int had = uniform((int)max(pos0 - first, (int64_t)0));  // rows of the block before this call
   const T *const base = static_cast<const T *>(a.qkv) + (int64_t)t0 * a.qkv_row;
 
-  // its place in a pool of one head, in rows, and its scale's in the scales of one head
-  int64_t row0 = -1, at_scale = 0;
-  const int per_page = 1 << (a.page_shift - 4);
-  const int64_t col = first >> a.page_shift;
-  if (first >= 0 && col < a.max_pages) {
-    const int page = a.table[(int64_t)p.s * a.max_pages + col];
-    if (page >= 0 && page < a.n_pages) {
-      const int in = (int)(first & ((1 << a.page_shift) - 1));
-      row0 = (((int64_t)page * a.hkv) << a.page_shift) + in;
-      at_scale = ((int64_t)page * a.hkv) * per_page + in / kBlock;
+  // ---- passes: kp of k and as many of v, P token slots per head, then q; this work-group's
+  // share of them
+  const int shift = nt > 1 ? 32 - __builtin_clz(nt - 1) : 0;  // P = 1 << shift
+  const int kp = (a.hkv + (kBlock >> shift) - 1) >> (4 - shift), kvp = 2 * kp;
+  const int all = kvp + (a.q ? (nt * a.h + kBlock - 1) / kBlock : 0);
+  const int per = (all + a.parts - 1) / a.parts, pass0 = part * per, passes = min(pass0 + per, all);
+  if (pass0 >= passes) return;
+  // (offsets are in 32 bits: 16 rows of 2^24 values at most, heads of 256 in pages of 256)
+  const int row_len = (int)a.qkv_row;
+  u32x2 y[kSub][2];
+  auto load = [&](int u, int tk, int head) __attribute__((always_inline)) {
+    const uint32_t r = (uint32_t)(tk * row_len + head * D);
+    y[u][0] = *reinterpret_cast<const u32x2 *>(base + (r + c0));
+    y[u][1] = *reinterpret_cast<const u32x2 *>(base + (r + c1));
+  };
+  auto unpack = [&](int u, float(&x)[8]) __attribute__((always_inline)) {
+    unpack4<T>(y[u][0], x);
+    unpack4<T>(y[u][1], x + 4);
+  };
+  typedef f32x4 weights __attribute__((aligned(4)));
+  f32x4 w0, w1;  // the weights of the lane's channels
+  auto weigh = [&](const float *w) __attribute__((always_inline)) {
+    w0 = w ? *reinterpret_cast<const weights *>(w + c0) : f32x4{1.f, 1.f, 1.f, 1.f};
+    w1 = w ? *reinterpret_cast<const weights *>(w + c1) : f32x4{1.f, 1.f, 1.f, 1.f};
+  };
+  // the row of token tk and head `head` of the packed row, weights w
+  auto normed = [&](float(&x)[8], const float *w, int tk, int head, bool in) __attribute__((always_inline)) {
+    norm_rope_row<T, D, kPairs>(
+        x, ch, w != nullptr, true, in, a.eps, a.rot_dim,
+        [&](int j) __attribute__((always_inline)) { return j < 4 ? w0[j & 3] : w1[j & 3]; },
+        [&](const float *&ct, const float *&st) __attribute__((always_inline)) {
+          ct = cs[tk];
+          st = sn[tk];
+        },
+        [&]() __attribute__((always_inline)) { return base + (uint32_t)(tk * row_len + head * D); },
+        [&]() __attribute__((always_inline)) { return w; });
+  };
+  auto store = [&](T *out, uint32_t to, const float(&x)[8]) __attribute__((always_inline)) {
+    const u32x2 z0{Elem<T>::pack(x[0], x[1]), Elem<T>::pack(x[2], x[3])};
+    const u32x2 z1{Elem<T>::pack(x[4], x[5]), Elem<T>::pack(x[6], x[7])};
+    u32x2 *const p0 = reinterpret_cast<u32x2 *>(out + (to + c0)), *const p1 = reinterpret_cast<u32x2 *>(out + (to + c1));
+    if (a.past_cache) {
+      asm volatile("" ::: "memory");  // (the compiler would make one pair of the two)
+      __builtin_nontemporal_store(z0, p0);
+      __builtin_nontemporal_store(z1, p1);
+      asm volatile("" ::: "memory");
+    } else {
+      *p0 = z0;
+      *p1 = z1;
     }
+  };
+
+  // ---- keys and values. A slot without a token has its head all the same: it takes part
+  // in what the head's block had
+  auto kv_head = [&](int pass, int u) __attribute__((always_inline)) {
+    return ((pass < kp ? pass : pass - kp) << (4 - shift)) + ((at + kRows * u) >> shift);
+  };
+  auto load_kv = [&](int pass) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < kSub; ++u) {
+      const int tk = (at + kRows * u) & ((1 << shift) - 1);
+      load(u, tk < nt ? tk : 0, min(kv_head(pass, u), a.hkv - 1) + a.h + (pass < kp ? 0 : a.hkv));
+    }
+  };
+  const int q0 = max(pass0 - kvp, 0), q_end = passes - kvp;  // passes of q
+  int q_tok[kSub], q_head[kSub];
+  auto load_q = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < kSub; ++u) load(u, q_tok[u] < nt ? q_tok[u] : 0, q_tok[u] < nt ? q_head[u] : 0);
+  };
+  if (pass0 < kvp) {
+    load_kv(pass0);
+    weigh(a.k_w);
+  } else {
+    weigh(a.q_w);
+  }
+  if (q0 < q_end) {
+#pragma unroll
+    for (int u = 0; u < kSub; ++u) {
+      const int r = q0 * kBlock + at + kRows * u;
+      q_tok[u] = r / a.h;
+      q_head[u] = r - q_tok[u] * a.h;
+    }
+    if (pass0 >= kvp) load_q();
   }
 
   for (int x = tid; x < nt * half; x += kAppendThreads) {
@@ -110,137 +208,116 @@ __global__ __launch_bounds__(kAppendThreads) void attn_append8_kernel(FrontArgs 
     cs[k][j] = turn[0];
     sn[k][j] = turn[1];
   }
-  typedef f32x4 weights __attribute__((aligned(4)));
-  f32x4 wq0{1.f, 1.f, 1.f, 1.f}, wq1 = wq0, wk0 = wq0, wk1 = wq0;
-  if (a.q_w) {
-    wq0 = *reinterpret_cast<const weights *>(a.q_w + c0);
-    wq1 = *reinterpret_cast<const weights *>(a.q_w + c1);
-  }
-  if (a.k_w) {
-    wk0 = *reinterpret_cast<const weights *>(a.k_w + c0);
-    wk1 = *reinterpret_cast<const weights *>(a.k_w + c1);
-  }
-  __syncthreads();
+  lds_barrier();
 
-  // a row's values in fp32, of token tk and head hd (q, k and v in order)
-  auto normed = [&](float(&x)[8], int tk, int hd, bool in) __attribute__((always_inline)) {
-    const bool is_q = hd < a.h, is_v = hd >= a.h + a.hkv;
-    if (is_v) return;
-    norm_rope_row<T, D, kPairs>(
-        x, ch, (is_q ? a.q_w : a.k_w) != nullptr, true, in, a.eps, a.rot_dim,
-        [&](int j) __attribute__((always_inline)) {
-          return j < 4 ? (is_q ? wq0[j & 3] : wk0[j & 3]) : (is_q ? wq1[j & 3] : wk1[j & 3]);
-        },
-        [&](const float *&ct, const float *&st) __attribute__((always_inline)) {
-          ct = cs[tk];
-          st = sn[tk];
-        },
-        [&]() __attribute__((always_inline)) { return base + tk * a.qkv_row + hd * D; },
-        [&]() __attribute__((always_inline)) { return is_q ? a.q_w : a.k_w; });
-  };
-  auto store16 = [&](T *out, const float(&x)[8]) __attribute__((always_inline)) {
-    *reinterpret_cast<u32x2 *>(out + c0) = u32x2{Elem<T>::pack(x[0], x[1]), Elem<T>::pack(x[2], x[3])};
-    *reinterpret_cast<u32x2 *>(out + c1) = u32x2{Elem<T>::pack(x[4], x[5]), Elem<T>::pack(x[6], x[7])};
-  };
-
-  // ---- keys and values: `heads` rows of heads side by side (a single token), or the rows
-  // of one head
-  auto keys = [&](auto single) __attribute__((always_inline)) {
-    constexpr bool kOne = decltype(single)::value;
-    constexpr int kR = kOne ? 1 : kSteps;
-    const int items = kOne ? (2 * a.hkv + kStep - 1) / kStep : 2 * a.hkv;
-    for (int item = w; item < items; item += kAppendThreads / 64) {
-      const int kv = kOne ? item * kStep + sub : item;  // k of every head, then v
-      const bool real = kv < 2 * a.hkv, is_v = kv >= a.hkv;
-      const int kh = is_v ? kv - a.hkv : kv, hd = a.h + (real ? kv : 0);
-      u32x2 y[kR][2];
-#pragma unroll
-      for (int r = 0; r < kR; ++r) {
-        const int tk = kOne ? 0 : r * kStep + sub;
-        y[r][0] = y[r][1] = u32x2{0u, 0u};
-        if (tk < nt && real) {
-          const T *row = base + tk * a.qkv_row + hd * D;
-          y[r][0] = *reinterpret_cast<const u32x2 *>(row + c0);
-          y[r][1] = *reinterpret_cast<const u32x2 *>(row + c1);
-        }
+  if (pass0 < kvp) {
+    // the block's place in a pool, in rows of head 0, and its scale's
+    int64_t row0 = -1, at_scale = 0;
+    const int page_size = 1 << a.page_shift, per_page = page_size / kBlock;
+    const int64_t col = first >> a.page_shift;
+    if (first >= 0 && col < a.max_pages) {
+      const int page = a.table[(int64_t)p.s * a.max_pages + col];
+      if (page >= 0 && page < a.n_pages) {
+        const int in = (int)(first & (page_size - 1));
+        row0 = (((int64_t)page * a.hkv) << a.page_shift) + in;
+        at_scale = ((int64_t)page * a.hkv) * per_page + in / kBlock;
       }
-      uint8_t *const pool = static_cast<uint8_t *>(is_v ? a.v_pages : a.k_pages);
-      uint8_t *const scales = is_v ? a.v_scales : a.k_scales;
-      const bool placed = row0 >= 0 && real;
-      const int64_t rows = row0 + ((int64_t)kh << a.page_shift);
-      const int64_t my_scale = at_scale + (int64_t)kh * per_page;
-      const int before = placed && had > 0 ? scales[my_scale] : 0;
-      float x[kR][8], most = 0.f;
+    }
+    row0 = uniform(row0);
+    at_scale = uniform(at_scale);
+    for (int pass = pass0; pass < min(passes, kvp); ++pass) {
+      const bool is_v = pass >= kp;
+      float x[kSub][8];
+      int head[kSub], before[kSub];
+      uint8_t *const scales = (is_v ? a.v_scales : a.k_scales) + at_scale;
 #pragma unroll
-      for (int r = 0; r < kR; ++r) {
-        const int tk = kOne ? 0 : r * kStep + sub;
-        const bool in = tk < nt && real;
-        unpack4<T>(y[r][0], x[r]);
-        unpack4<T>(y[r][1], x[r] + 4);
-        if (kOne || !is_v) {
-          float z[8];
+      for (int u = 0; u < kSub; ++u) {
+        unpack(u, x[u]);
+        head[u] = min(kv_head(pass, u), a.hkv - 1);
+        before[u] = row0 >= 0 && had > 0 ? scales[(uint32_t)(head[u] * per_page)] : 0;
+      }
+      if (pass + 1 < min(passes, kvp))
+        load_kv(pass + 1);
+      else if (q0 < q_end)
+        load_q();
 #pragma unroll
-          for (int j = 0; j < 8; ++j) z[j] = x[r][j];
-          normed(z, in ? tk : 0, is_v ? a.h : hd, in);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[r][j] = is_v ? x[r][j] : z[j];
-          if (a.k && in && !is_v)
-            store16(static_cast<T *>(a.k) + ((int64_t)(t0 + tk) * a.hkv + kh) * D, x[r]);
+      for (int u = 0; u < kSub; ++u) {
+        const int slot_tk = (at + kRows * u) & ((1 << shift) - 1), tk = slot_tk < nt ? slot_tk : 0;
+        const bool in = slot_tk < nt && kv_head(pass, u) < a.hkv;
+        if (!is_v) {
+          normed(x[u], a.k_w, tk, a.h + head[u], in);
+          if (a.k && in)
+            store(static_cast<T *>(a.k) + (int64_t)t0 * a.hkv * D, (uint32_t)((tk * a.hkv + head[u]) * D), x[u]);
         }
         // what is not finite becomes NaN and does not count
+        float m = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const bool finite = fabsf(x[r][j]) <= FLT_MAX;
-          const float z = fminf(fmaxf(x[r][j], -kTop<T>), kTop<T>);
-          if (in) most = fmaxf(most, finite ? fabsf(z) : 0.f);
-          x[r][j] = finite ? z : __builtin_nanf("");
+          const bool finite = fabsf(x[u][j]) <= FLT_MAX;
+          const float v = fminf(fmaxf(x[u][j], -kTop<T>), kTop<T>);
+          m = fmaxf(m, finite ? fabsf(v) : 0.f);
+          x[u][j] = finite ? v : __builtin_nanf("");
         }
+        m = max_row<kLanes>(m);
+        if (li == 0) most[pass & 1][at + kRows * u] = in ? m : 0.f;
       }
+      lds_barrier();
+      if (row0 < 0) continue;
+      uint8_t *const pool = static_cast<uint8_t *>(is_v ? a.v_pages : a.k_pages) + row0 * D;
 #pragma unroll
-      for (int off = 1; off < (kOne ? kLanes : 64); off <<= 1) most = fmaxf(most, __shfl_xor(most, off, 64));
-      if (!placed) continue;
-      const int e = max(scale_for(most), before);
-      // the rows that the block had, by the new scale
-      if (had > 0 && e > before) {
-        const float by = __uint_as_float((uint32_t)max(before - e + 127, 1) << 23);
-        for (int r = kOne ? 0 : sub; r < had; r += kOne ? 1 : kStep) {
-          u32x2 *const at = reinterpret_cast<u32x2 *>(pool + (rows + r) * D + 8 * li);
-          const u32x2 c = *at;
-          *at = u32x2{again4(c[0], by), again4(c[1], by)};
+      for (int u = 0; u < kSub; ++u) {
+        const int s = at + kRows * u, tk = s & ((1 << shift) - 1);
+        float m = 0.f;
+        const float *of = &most[pass & 1][s - tk];
+        for (int r = 0; r < 1 << shift; ++r) m = fmaxf(m, of[r]);
+        const int e = max(scale_for(m), before[u]);
+        if (kv_head(pass, u) >= a.hkv) continue;
+        const uint32_t row = (uint32_t)(head[u] << a.page_shift);  // the head's first, from row0
+        // the rows that the block had, by the new scale
+        if (had > 0 && e > before[u]) {
+          const float by = __uint_as_float((uint32_t)max(before[u] - e + 127, 1) << 23);
+          for (int r = tk; r < had; r += 1 << shift) {
+            u32x2 *const old = reinterpret_cast<u32x2 *>(pool + (row + r) * D + 8 * li);
+            const u32x2 c = *old;
+            *old = u32x2{again4(c[0], by), again4(c[1], by)};
+          }
         }
-      }
-      if (e != before && (kOne ? li == 0 : lane == 0)) scales[my_scale] = (uint8_t)e;
-      const float by = unscale(e);
-#pragma unroll
-      for (int r = 0; r < kR; ++r) {
-        const int tk = kOne ? 0 : r * kStep + sub;
+        if (e != before[u] && tk == 0 && li == 0) scales[(uint32_t)(head[u] * per_page)] = (uint8_t)e;
         if (tk < nt) {
-          uint8_t *const out = pool + (rows + had + tk) * D;
-          const float *v = x[r];
-          *reinterpret_cast<uint32_t *>(out + c0) = codes4(v[0] * by, v[1] * by, v[2] * by, v[3] * by);
-          *reinterpret_cast<uint32_t *>(out + c1) = codes4(v[4] * by, v[5] * by, v[6] * by, v[7] * by);
+          const float by = unscale(e), *v = x[u];
+          const uint32_t to = (row + had + tk) * D;
+          *reinterpret_cast<uint32_t *>(pool + (to + c0)) = codes4(v[0] * by, v[1] * by, v[2] * by, v[3] * by);
+          *reinterpret_cast<uint32_t *>(pool + (to + c1)) = codes4(v[4] * by, v[5] * by, v[6] * by, v[7] * by);
         }
       }
     }
-  };
-  if (nt == 1)
-    keys(std::true_type{});
-  else
-    keys(std::false_type{});
+    weigh(a.q_w);
+  }
 
   // ---- queries, token by token, its heads in order
-  if (!a.q) return;
-  const int rows = nt * a.h;
-  for (int at = 0; at < rows; at += kAppendThreads / kLanes) {
-    const int r = at + tid / kLanes;
-    const bool in = r < rows;
-    const int tk = in ? r / a.h : 0, hd = in ? r - tk * a.h : 0;
-    const T *row = base + tk * a.qkv_row + hd * D;
-    float x[8];
-    unpack4<T>(*reinterpret_cast<const u32x2 *>(row + c0), x);
-    unpack4<T>(*reinterpret_cast<const u32x2 *>(row + c1), x + 4);
-    normed(x, tk, hd, in);
-    if (in) store16(static_cast<T *>(a.q) + ((int64_t)(t0 + tk) * a.h + hd) * D, x);
+  T *const out = static_cast<T *>(a.q) + (int64_t)t0 * a.h * D;
+  for (int pass = q0; pass < q_end; ++pass) {
+    float x[kSub][8];
+    int tok[kSub], head[kSub];
+#pragma unroll
+    for (int u = 0; u < kSub; ++u) {
+      unpack(u, x[u]);
+      tok[u] = q_tok[u];
+      head[u] = q_head[u];
+      q_head[u] += kBlock;
+      while (q_head[u] >= a.h) {
+        q_head[u] -= a.h;
+        ++q_tok[u];
+      }
+    }
+    if (pass + 1 < q_end) load_q();
+#pragma unroll
+    for (int u = 0; u < kSub; ++u) {
+      const bool in = tok[u] < nt;
+      const int tk = in ? tok[u] : 0;
+      normed(x[u], a.q_w, tk, in ? head[u] : 0, in);
+      if (in) store(out, (uint32_t)((tk * a.h + head[u]) * D), x[u]);
+    }
   }
 }
 
@@ -265,8 +342,23 @@ void run_of(const FrontArgs &a, bool interleaved, dim3 grid, hipStream_t stream)
 
 hipError_t launch_attn_append8(const gdn_attn_config *cfg, FrontArgs a, hipStream_t stream) {
   if (cfg->t_max == 0) return hipSuccess;
+  // a block is shared by several work-groups, down to kPartPasses passes apiece, until there
+  // are many per CU (32768 tokens of 20 heads of 256 in one part 153 us, 2: 141, 3 to 5: 133;
+  // 2500 tokens of 40 heads of 128 in one 33, in ten 18)
+  const int64_t each = (cfg->t_max + cfg->n_max - 1) / cfg->n_max;  // tokens of an average sequence
+  const int64_t blocks = cfg->n_max * ((each + kBlock - 1) / kBlock);
+  const int64_t passes = ((each < kBlock ? each : kBlock) * (cfg->h + 2 * cfg->hkv) + kBlock - 1) / kBlock;
+  int64_t parts = 32 * cu_count() / blocks;
+  if (parts > passes / kPartPasses) parts = passes / kPartPasses;
+  a.parts = parts > 1 ? (int)parts : 1;
+  // where all of them run at once, the parts with k and v, which take longer, come first (the
+  // 2500 tokens 18 -> 16; the 32768 would go from 133 to 138)
+  const int64_t slots = (cfg->t_max / kBlock + 2 * (int64_t)cfg->n_max + 7) / 8 * 8;
+  a.group = slots * a.parts <= 16 * cu_count() ? (int)slots : 8;
+  const int64_t heads = (a.q ? cfg->h : 0) + (a.k ? cfg->hkv : 0) + cfg->hkv;  // (codes: two in one)
+  a.past_cache = heads * cfg->t_max * cfg->d * 2 > kPastCache;
   dim3 grid;
-  if (!flat_grid((int64_t)cfg->t_max / kBlock + 2 * (int64_t)cfg->n_max, kAppendThreads, grid))
+  if (!flat_grid(slots * a.parts, kAppendThreads, grid))
     return hipErrorInvalidValue;
   const bool interleaved = cfg->rot_interleaved != 0;
   if (cfg->dtype == GDN_BF16)

@@ -30,6 +30,8 @@ struct FrontArgs {
   // any cache
   int tokens;
   bool past_cache;
+  // 8-bit cache: work-groups per block of tokens, and how many blocks are numbered together
+  int parts, group;
 };
 hipError_t launch_attn_front(const gdn_attn_config *cfg, FrontArgs a, hipStream_t stream);
 // The same into an 8-bit cache.

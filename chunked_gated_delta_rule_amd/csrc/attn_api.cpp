@@ -84,10 +84,10 @@ PrefillLayout prefill_layout(const gdn_attn_config *cfg, gdn::Keys keys) {
   return l;
 }
 
-PagedLayout paged_layout(const gdn_attn_config *cfg) {
+PagedLayout paged_layout(const gdn_attn_config *cfg, bool k8) {
   const size_t d = static_cast<size_t>(cfg->d);
   const size_t slots = static_cast<size_t>(gdn::stream_grid(cfg)) * 2 * 16 * gdn::stream_row_tiles(cfg);
-  const bool shared = gdn::shares(cfg);
+  const bool shared = gdn::shares(cfg, k8);
   const size_t done = shared ? static_cast<size_t>(cfg->t_max) * static_cast<size_t>(cfg->h) : 0;
   const size_t pre = shared ? static_cast<size_t>(gdn::tile_part_rows(
                                   cfg, gdn::tile_shape(cfg, gdn::Keys::kShared), gdn::Keys::kShared))
@@ -106,14 +106,14 @@ PagedLayout paged_layout(const gdn_attn_config *cfg) {
   return l;
 }
 
-size_t paged_bytes(const gdn_attn_config *cfg) {
-  const size_t paged = gdn::streams(cfg) ? paged_layout(cfg).total
+size_t paged_bytes(const gdn_attn_config *cfg, bool k8) {
+  const size_t paged = gdn::streams(cfg, k8) ? paged_layout(cfg, k8).total
                                          : prefill_layout(cfg, gdn::Keys::kPages).total;
   return paged > kAlign ? paged : kAlign;
 }
 
 size_t workspace_bytes(const gdn_attn_config *cfg) {
-  const size_t prefill = prefill_layout(cfg, gdn::Keys::kRows).total, paged = paged_bytes(cfg);
+  const size_t prefill = prefill_layout(cfg, gdn::Keys::kRows).total, paged = paged_bytes(cfg, false);
   return prefill > paged ? prefill : paged;
 }
 
@@ -226,12 +226,13 @@ gdn_status paged(const gdn_attn_config *cfg, const void *q, int64_t q_row, const
       !aligned(cu_seqlens, 4) || !aligned(kv_lens, 4) || !aligned(block_table, 4) ||
       !aligned(shared_len, 4))
     return GDN_ERR_INVALID_ARG;
+  const bool k8 = k_scales != nullptr;
   char *at = static_cast<char *>(workspace);
   gdn::PagedBatch pg;
   pg.cu = cu_seqlens;
   pg.kv_lens = kv_lens;
   pg.table = block_table;
-  pg.shared_len = gdn::shares(cfg) ? shared_len : nullptr;
+  pg.shared_len = gdn::shares(cfg, k8) ? shared_len : nullptr;
   pg.t_max = cfg->t_max;
   pg.n_max = cfg->n_max;
   pg.page_shift = page_shift(cfg);
@@ -248,12 +249,12 @@ gdn_status paged(const gdn_attn_config *cfg, const void *q, int64_t q_row, const
   t.cu_q = cu_seqlens;
   t.pg = pg;
   t.o = o;
-  if (!gdn::streams(cfg)) {
+  if (!gdn::streams(cfg, k8)) {
     const PrefillLayout l = prefill_layout(cfg, gdn::Keys::kPages);
     tile_common(cfg, t, at, l.part_o, l.part_ml);
     return from_hip(gdn::launch_attn_tiles(cfg, gdn::Keys::kPages, t, as_stream(stream)));
   }
-  const PagedLayout l = paged_layout(cfg);
+  const PagedLayout l = paged_layout(cfg, k8);
   gdn::StreamArgs a = {};
   if (pg.shared_len) {
     tile_common(cfg, t, at, l.pre_o, l.pre_ml);
@@ -412,7 +413,7 @@ gdn_status gdn_attn_paged8_workspace_size(const gdn_attn_config *cfg, size_t *by
   const gdn_status st = check_config(cfg);
   if (st != GDN_OK) return st;
   if (!bytes) return GDN_ERR_INVALID_ARG;
-  *bytes = paged_bytes(cfg);
+  *bytes = paged_bytes(cfg, true);
   return GDN_OK;
 }
 
@@ -426,7 +427,7 @@ gdn_status gdn_attn_paged8(const gdn_attn_config *cfg, const void *q, int64_t q_
   if (st != GDN_OK) return st;
   if (!k_scales || !v_scales) return GDN_ERR_INVALID_ARG;
   return paged(cfg, q, q_row, k_pages, v_pages, k_scales, v_scales, cu_seqlens, kv_lens, block_table,
-               shared_len, o, workspace, paged_bytes(cfg), ws_bytes, stream);
+               shared_len, o, workspace, paged_bytes(cfg, true), ws_bytes, stream);
 }
 
 }  // extern "C"

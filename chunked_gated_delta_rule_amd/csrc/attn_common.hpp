@@ -100,6 +100,13 @@ __device__ __forceinline__ int opaque(int x) {
   return x;
 }
 
+// The lane's number, formed where it is asked for: what goes by it costs no register along a loop.
+__device__ __forceinline__ int fresh_lane() {
+  int x;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(x));
+  return x;
+}
+
 constexpr float kNegInf = -__builtin_inff();
 
 // Bytes from which what a pass reads or writes once goes past the caches: what the last
@@ -408,8 +415,31 @@ __device__ __forceinline__ u32x4 values8(uint32_t lo, uint32_t hi, float scale) 
   return u32x4{values2<T, false>(lo, scale), values2<T, true>(lo, scale),
                values2<T, false>(hi, scale), values2<T, true>(hi, scale)};
 }
-// A scale as the conversions take it (0 stands for 2^-127, 255 for NaN).
-__device__ __forceinline__ float scale_of(uint32_t e) { return __uint_as_float(e << 23); }
+// A scale as the conversions take it (0 stands for 2^-127, 255 for NaN), formed here: the
+// compiler would move the shift to the load, and wait for it there.
+__device__ __forceinline__ float scale_of(uint32_t e) {
+  asm volatile("" : "+v"(e));
+  return __uint_as_float(e << 23);
+}
+
+// A descriptor of values that are one per wave, in scalar registers whatever the compiler thinks
+// of them (it would read it in a loop over the wave's values).
+__device__ __forceinline__ rsrc_t uniform_rsrc(const void *p, int bytes) {
+  return make_rsrc(reinterpret_cast<const void *>(uniform((int64_t)reinterpret_cast<uintptr_t>(p))),
+                   uniform(bytes));
+}
+
+// Page of position `key` of sequence s (uniform both) in two halves, so that a loop can ask for
+// it ahead: the table's word through the vector caches, and the page as an index into the pool
+// whatever the table says. Scalar loads come back in any order, so that reads of LDS beside one
+// in flight are all waited for together; these are counted.
+__device__ __forceinline__ int page_word(const PagedBatch &a, int s, int key) {
+  const rsrc_t row = uniform_rsrc(a.table + (int64_t)s * a.max_pages, a.max_pages * 4);
+  return __builtin_amdgcn_raw_buffer_load_b32(row, (key >> a.page_shift) * 4, 0, 0);
+}
+__device__ __forceinline__ int page_in(const PagedBatch &a, int word) {
+  return min(max(uniform(word), 0), a.n_pages - 1);
+}
 
 // Number of the scale of position `key` of a key head, in a pool of scales.
 __device__ __forceinline__ int64_t scale_at(const PagedBatch &a, int page, int key, int kh, int hkv) {

@@ -351,25 +351,32 @@ __global__ __launch_bounds__(256, kRT * D <= 256 ? 2 : 1) void attn_stream_kerne
         const int qrow = opaque<(kRT * D > 128)>(c);
         f32x4 sc[kRT][2];
   #pragma unroll
-        for (int t = 0; t < kRT; ++t) {
-          sc[t][0] = sc[t][1] = zero4();
+        for (int t = 0; t < kRT; ++t) sc[t][0] = sc[t][1] = zero4();
+        if constexpr (k8) {
+          // (a fragment is formed once, for all row tiles)
+          const T *const q0 = &qs[qrow][16 * g];
   #pragma unroll
-          for (int p = 0; p < D / 32; ++p) {
-            if constexpr (k8) {
-              const vec8 qf = *reinterpret_cast<const vec8 *>(
-                  &qs[16 * t + qrow][64 * (p >> 1) + 16 * g + 8 * (p & 1)]);
+          for (int p = 0; p < D / 32; ++p)
   #pragma unroll
-              for (int k = 0; k < 2; ++k)
-                sc[t][k] = mfma(__builtin_bit_cast(vec8, values8<T>(x.k[k][p >> 1][2 * (p & 1)],
-                                                                    x.k[k][p >> 1][2 * (p & 1) + 1],
-                                                                    scale_of(x.k_scale[k]))),
-                                qf, sc[t][k]);
-            } else {
+            for (int k = 0; k < 2; ++k) {
+              const vec8 kf = __builtin_bit_cast(
+                  vec8, values8<T>(x.k[k][p >> 1][2 * (p & 1)], x.k[k][p >> 1][2 * (p & 1) + 1],
+                                   scale_of(x.k_scale[k])));
+  #pragma unroll
+              for (int t = 0; t < kRT; ++t)
+                sc[t][k] = mfma(kf, *reinterpret_cast<const vec8 *>(
+                                        q0 + 16 * t * (D + 8) + 64 * (p >> 1) + 8 * (p & 1)),
+                                sc[t][k]);
+            }
+        } else {
+  #pragma unroll
+          for (int t = 0; t < kRT; ++t)
+  #pragma unroll
+            for (int p = 0; p < D / 32; ++p) {
               const vec8 qf = *reinterpret_cast<const vec8 *>(&qs[16 * t + qrow][32 * p + 8 * g]);
               sc[t][0] = mfma(x.k[0][p], qf, sc[t][0]);
               sc[t][1] = mfma(x.k[1][p], qf, sc[t][1]);
             }
-          }
         }
         if (i + 1 < mine_n) load_k(x, i + 1);
         __builtin_amdgcn_sched_barrier(0);
@@ -690,12 +697,14 @@ int64_t rows_per_seq(const gdn_attn_config *cfg) {
 // (about 12 us) against reads of it by every sequence, of which most hit a cache. Even
 // at 128 MiB of the latter (8 sequences on 16384 shared positions, 32 on 4096, 128 on
 // 1024: 29 / 28 / 36 us against 30 / 25 / 29), ahead at 512 MiB (128 on 4096: 44
-// against 57; with 4 times the heads and a quarter of the sequences 36 against 53).
-bool shares(const gdn_attn_config *cfg) {
+// against 57; with 4 times the heads and a quarter of the sequences 36 against 53). Over 8-bit
+// pages by their own bytes: 128 MiB 44 against 33, 256 (128 sequences on 1024 positions, 32 on
+// 4096, 8 on 16384) 48 / 35 / 33 against 57 / 53 / 54.
+bool shares(const gdn_attn_config *cfg, bool k8) {
   constexpr double kWorth = 256.0 * (1 << 20);
   const double room = (double)cfg->max_pages * cfg->page_size;
   const double shared = cfg->shared_max < room ? cfg->shared_max : room;
-  return shared * cfg->n_max * cfg->hkv * cfg->d * 4 >= kWorth;
+  return shared * cfg->n_max * cfg->hkv * cfg->d * (k8 ? 2 : 4) >= kWorth;
 }
 
 // Rows of an average sequence (new tokens times query heads per key head) up to which
@@ -704,7 +713,9 @@ bool shares(const gdn_attn_config *cfg) {
 // 86), with 64 the tiles are ahead (53 against 48, 116 against 90), except where only
 // streamed items can leave the prefix to its own pass (64 sequences behind 8192 shared
 // positions: 85 against 100; with 96 rows 124 against 102).
-bool streams(const gdn_attn_config *cfg) { return rows_per_seq(cfg) <= (shares(cfg) ? 64 : 32); }
+bool streams(const gdn_attn_config *cfg, bool k8) {
+  return rows_per_seq(cfg) <= (shares(cfg, k8) ? 64 : 32);
+}
 
 // One 16-row tile per item holds a decoding sequence's heads; where an average
 // sequence has more rows, wider items read the keys fewer times (32 rows on 2500 keys,

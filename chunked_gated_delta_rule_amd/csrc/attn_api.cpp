@@ -74,8 +74,8 @@ struct Taker {
   }
 };
 
-PrefillLayout prefill_layout(const gdn_attn_config *cfg, gdn::Keys keys) {
-  const size_t rows = static_cast<size_t>(gdn::tile_part_rows(cfg, gdn::tile_shape(cfg, keys), keys));
+PrefillLayout prefill_layout(const gdn_attn_config *cfg, gdn::Keys keys, bool k8) {
+  const size_t rows = static_cast<size_t>(gdn::tile_part_rows(cfg, gdn::tile_shape(cfg, keys, k8), keys));
   Taker take;
   PrefillLayout l;
   l.part_o = take(rows * cfg->d * 4);
@@ -90,7 +90,7 @@ PagedLayout paged_layout(const gdn_attn_config *cfg, bool k8) {
   const bool shared = gdn::shares(cfg, k8);
   const size_t done = shared ? static_cast<size_t>(cfg->t_max) * static_cast<size_t>(cfg->h) : 0;
   const size_t pre = shared ? static_cast<size_t>(gdn::tile_part_rows(
-                                  cfg, gdn::tile_shape(cfg, gdn::Keys::kShared), gdn::Keys::kShared))
+                                  cfg, gdn::tile_shape(cfg, gdn::Keys::kShared, k8), gdn::Keys::kShared))
                             : 0;
   Taker take;
   PagedLayout l;
@@ -108,12 +108,12 @@ PagedLayout paged_layout(const gdn_attn_config *cfg, bool k8) {
 
 size_t paged_bytes(const gdn_attn_config *cfg, bool k8) {
   const size_t paged = gdn::streams(cfg, k8) ? paged_layout(cfg, k8).total
-                                         : prefill_layout(cfg, gdn::Keys::kPages).total;
+                                         : prefill_layout(cfg, gdn::Keys::kPages, k8).total;
   return paged > kAlign ? paged : kAlign;
 }
 
 size_t workspace_bytes(const gdn_attn_config *cfg) {
-  const size_t prefill = prefill_layout(cfg, gdn::Keys::kRows).total, paged = paged_bytes(cfg, false);
+  const size_t prefill = prefill_layout(cfg, gdn::Keys::kRows, false).total, paged = paged_bytes(cfg, false);
   return prefill > paged ? prefill : paged;
 }
 
@@ -250,7 +250,7 @@ gdn_status paged(const gdn_attn_config *cfg, const void *q, int64_t q_row, const
   t.pg = pg;
   t.o = o;
   if (!gdn::streams(cfg, k8)) {
-    const PrefillLayout l = prefill_layout(cfg, gdn::Keys::kPages);
+    const PrefillLayout l = prefill_layout(cfg, gdn::Keys::kPages, k8);
     tile_common(cfg, t, at, l.part_o, l.part_ml);
     return from_hip(gdn::launch_attn_tiles(cfg, gdn::Keys::kPages, t, as_stream(stream)));
   }
@@ -260,7 +260,7 @@ gdn_status paged(const gdn_attn_config *cfg, const void *q, int64_t q_row, const
     tile_common(cfg, t, at, l.pre_o, l.pre_ml);
     const hipError_t e = gdn::launch_attn_tiles(cfg, gdn::Keys::kShared, t, as_stream(stream));
     if (e != hipSuccess) return GDN_ERR_HIP;
-    const gdn::TileShape s = gdn::tile_shape(cfg, gdn::Keys::kShared);
+    const gdn::TileShape s = gdn::tile_shape(cfg, gdn::Keys::kShared, k8);
     a.pre_share = s.share;
     a.pre_tt = s.tt;
     a.pre_slots = s.slots;
@@ -376,7 +376,7 @@ gdn_status gdn_attn_prefill(const gdn_attn_config *cfg, const void *q, int64_t q
   const gdn_status st = check_config(cfg);
   if (st != GDN_OK) return st;
   if (!q || !k || !v || !cu_q || !o) return GDN_ERR_INVALID_ARG;
-  const PrefillLayout l = prefill_layout(cfg, gdn::Keys::kRows);
+  const PrefillLayout l = prefill_layout(cfg, gdn::Keys::kRows, false);
   const gdn_status ws = check_workspace(workspace_bytes(cfg), workspace, ws_bytes);
   if (ws != GDN_OK) return ws;
   gdn::TileArgs a = {};

@@ -274,6 +274,58 @@ struct TiledBatch {
     at = __builtin_amdgcn_readlane(which, __ffsll(__ballot(any)) - 1);
     return true;
   }
+  // Work-groups for the parts of every tile's keys, `wgs` in all: each tile of a sequence is cut
+  // in `parts`, in proportion to the sequence's keys (extra[1]), at least one and at most
+  // `most`, no part of fewer than least_keys; numbered sequence by sequence, tile by tile.
+  // chosen(sequence, number of its first part, its parts) names one sequence; first and parts
+  // are its values. (Rounded down from wgs less one per tile: never more than wgs, if that is
+  // at least the batch's tiles. A search for the largest shares that fit lost 4 to 20 us to
+  // the search.)
+  template <typename F>
+  __device__ __forceinline__ bool in_parts(int lane, int wgs, int most, int least_keys, F chosen,
+                                           Tiled &out, int &first, int &parts) const {
+    int64_t keys = 0;
+    int count = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      keys += (int64_t)tiles[j] * seq[j].extra[1];
+      count += tiles[j];
+    }
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      keys += __shfl_xor(keys, off, 64);
+      count += __shfl_xor(count, off, 64);
+    }
+    const int64_t room = max(wgs - count, 0);
+    keys = max(keys, (int64_t)1);
+    int p[kPer], mine = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int lk = seq[j].extra[1];
+      p[j] = min(1 + (int)(room * lk / keys), max(min(most, lk / least_keys), 1));
+      mine += tiles[j] * p[j];
+    }
+    int end = mine;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int y = __shfl_up(end, off, 64);
+      if (lane >= off) end += y;
+    }
+    int at = end - mine, which = 0, what = 1;
+    bool found[kPer], any = false;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      found[j] = !any && seq[j].n > 0 && chosen(seq[j], at, p[j]);
+      if (found[j]) which = at, what = p[j];
+      any = any || found[j];
+      at += tiles[j] * p[j];
+    }
+    if (!pick(found, out)) return false;
+    const int hit = __ffsll(__ballot(any)) - 1;
+    first = __builtin_amdgcn_readlane(which, hit);
+    parts = __builtin_amdgcn_readlane(what, hit);
+    return true;
+  }
   // f over the wave's values: rows of 16 lanes (shifts by 1, 2, 4, 8), then the rows.
   template <typename F>
   static __device__ __forceinline__ int all(int v, F f) {

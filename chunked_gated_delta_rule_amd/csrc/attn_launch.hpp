@@ -59,16 +59,18 @@ struct TileArgs {
   // partial results of keys split over work-groups: [item][split][row]
   float *part_o, *part_ml;
   // filled in by the launcher (TileShape)
-  int share, splits, slots;
+  int share, splits, slots, by_keys;
 };
 
 // How a call is cut into tiles: rows per tile are tokens times `share` query heads
 // of one key head, tt tokens; `slots` token tiles at most, times h / share head
-// groups; each tile's keys in `splits` parts. `rows` rows (tt * share, rounded up).
+// groups; each tile's keys in `splits` parts. `rows` rows (tt * share, rounded up). by_keys (0:
+// not): parts in proportion to the sequences' keys instead, so many work-groups for each head
+// group.
 struct TileShape {
-  int waves, rows, share, tt, slots, splits;
+  int waves, rows, share, tt, slots, splits, by_keys;
 };
-TileShape tile_shape(const gdn_attn_config *cfg, Keys keys);
+TileShape tile_shape(const gdn_attn_config *cfg, Keys keys, bool k8);
 // Rows of partial results the shape needs (0 where o is written at once).
 int64_t tile_part_rows(const gdn_attn_config *cfg, const TileShape &s, Keys keys);
 // With more than one split, kRows and kPages are joined into o; the parts of

@@ -203,12 +203,13 @@ __global__ __launch_bounds__(512, 2) void attn_part_kernel(TileArgs a) {
   const int rg = k8 && set ? 3 - w : w;
   Where t;
   const int share = a.share, tt = kBM / share;
-  if (!find<kKeys, true, 512>(a, tt, D * (k8 ? 2 : 4), tid, t, scan)) return;
+  constexpr bool kByKeys = k8 && kKeys == Keys::kPages;
+  if (!find<kKeys, true, 512, kByKeys>(a, tt, D * (k8 ? 2 : 4), tid, t, scan)) return;
   t = t.uniform_();
   const int kvh = t.group * share / (a.h / a.hkv);
   const Sight see = sight_of<kKeys>(t, 32 * rg, col, tt, share);
   const int all = see.keys > 0 ? (see.keys + kBN - 1) / kBN : 0;
-  const int per = (all + a.splits - 1) / a.splits;
+  const int per = (all + t.splits - 1) / t.splits;
   const int j0 = t.split * per + set, end = min(t.split * per + per, all);
   const int steps = max((end - t.split * per + 1) / 2, 0);  // of either set
   // this set's tile of step j, if it has one
@@ -306,13 +307,14 @@ __global__ __launch_bounds__(512, 2) void attn_part_kernel(TileArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) x.o[i][4 * b + e] = x.o[i][4 * b + e] * f1 + y[e] * f2;
     }
-  const int64_t at = (item_of(t.group, t.slot, a.h / share, a.slots) * a.splits + t.split) * kBM +
-                     32 * rg + col;
+  const int64_t item = kByKeys ? (int64_t)t.slot * (a.h / share) + t.group
+                               : item_of(t.group, t.slot, a.h / share, a.slots) * a.splits + t.split;
+  const int64_t at = item * kBM + 32 * rg + col;
   x.store_part(a.part_o + at * D, a.part_ml + at * 2, hh);
 }
 
 // Joins the parts of a row's keys: one wave per row.
-template <typename T, int D>
+template <typename T, int D, bool kByKeys>
 __global__ __launch_bounds__(256) void attn_tile_join_kernel(TileArgs a, int tt, int bm) {
   constexpr int kPer = D / 64;  // dims per lane
   typedef float vec __attribute__((ext_vector_type(kPer)));
@@ -320,40 +322,67 @@ __global__ __launch_bounds__(256) void attn_tile_join_kernel(TileArgs a, int tt,
   const int64_t i = (int64_t)flat_block() * 4 + w;
   const int t = (int)(i / a.h), head = (int)(i % a.h);
   if (t >= cu_at(a.cu_q, a.n_max, a.t_max)) return;
+  // the row's parts: item(i) of the partial results, `splits` of them
   Tiled p;
-  int first, total;
-  auto none = [](int, int(&o)[2]) { o[0] = o[1] = 0; };
-  auto in = [&](const auto &batch) {
-    return batch.in_order(
-        lane, [&](const Tiled &x, int, int) { return t >= x.b && t < x.b + x.n; }, p, first, total);
-  };
-  if (!(a.n_max <= 64 ? in(TiledBatch<1>(a.cu_q, a.n_max, a.t_max, tt, lane, none))
-                      : in(TiledBatch<4>(a.cu_q, a.n_max, a.t_max, tt, lane, none))))
-    return;  // an unsorted cu_seqlens: a row of no sequence
-  const int tile = (t - p.b) / tt, slot = first + tile;
-  if (slot >= a.slots) return;  // or sequences that overlap
-  const int64_t item = item_of(head / a.share, slot, a.h / a.share, a.slots) * a.splits;
-  const int row = (t - p.b - tile * tt) * a.share + head % a.share;
+  int splits, row;
+  int64_t item, step;
+  if constexpr (kByKeys) {
+    int first;
+    auto keys = [&](int i, int(&o)[2]) {
+      o[0] = 0;
+      o[1] = kv_of(a.pg, i);
+    };
+    auto in = [&](const auto &batch) {
+      return batch.in_parts(
+          lane, a.by_keys, kMostParts, kLeastKeys,
+          [&](const Tiled &x, int, int) { return t >= x.b && t < x.b + x.n; }, p, first, splits);
+    };
+    if (!(a.n_max <= 64 ? in(TiledBatch<1>(a.cu_q, a.n_max, a.t_max, tt, lane, keys))
+                        : in(TiledBatch<4>(a.cu_q, a.n_max, a.t_max, tt, lane, keys))))
+      return;  // an unsorted cu_seqlens: a row of no sequence
+    const int tile = (t - p.b) / tt;
+    const int64_t at = first + (int64_t)tile * splits;
+    if (at < 0 || at + splits > a.by_keys) return;  // or sequences that overlap
+    step = a.h / a.share;
+    item = at * step + head / a.share;
+    row = (t - p.b - tile * tt) * a.share + head % a.share;
+  } else {
+    int first, total;
+    auto none = [](int, int(&o)[2]) { o[0] = o[1] = 0; };
+    auto in = [&](const auto &batch) {
+      return batch.in_order(
+          lane, [&](const Tiled &x, int, int) { return t >= x.b && t < x.b + x.n; }, p, first, total);
+    };
+    if (!(a.n_max <= 64 ? in(TiledBatch<1>(a.cu_q, a.n_max, a.t_max, tt, lane, none))
+                        : in(TiledBatch<4>(a.cu_q, a.n_max, a.t_max, tt, lane, none))))
+      return;  // an unsorted cu_seqlens: a row of no sequence
+    const int tile = (t - p.b) / tt, slot = first + tile;
+    if (slot >= a.slots) return;  // or sequences that overlap
+    splits = a.splits;
+    step = 1;
+    item = item_of(head / a.share, slot, a.h / a.share, a.slots) * splits;
+    row = (t - p.b - tile * tt) * a.share + head % a.share;
+  }
   // the splits' statistics, one per lane
-  const float mine = lane < a.splits ? a.part_ml[((item + lane) * bm + row) * 2] : kNegInf;
+  const float mine = lane < splits ? a.part_ml[((item + lane * step) * bm + row) * 2] : kNegInf;
   float big = mine;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) big = fmaxf(big, __shfl_xor(big, off, 64));
   const float f = mine == kNegInf ? 0.f : fast_exp2(mine - big);
-  float l = lane < a.splits ? a.part_ml[((item + lane) * bm + row) * 2 + 1] * f : 0.f;
+  float l = lane < splits ? a.part_ml[((item + lane * step) * bm + row) * 2 + 1] * f : 0.f;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) l += __shfl_xor(l, off, 64);
   vec sum = {};
-  for (int k = 0; k < a.splits; k += 4) {  // four loads at a time
+  for (int k = 0; k < splits; k += 4) {  // four loads at a time
     vec x[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       x[e] = *reinterpret_cast<const vec *>(
-          a.part_o + ((item + min(k + e, a.splits - 1)) * bm + row) * D + kPer * lane);
+          a.part_o + ((item + min(k + e, splits - 1) * step) * bm + row) * D + kPer * lane);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float g = __shfl(f, (k + e) & 63, 64);
-      if (k + e < a.splits) sum += g * x[e];
+      if (k + e < splits) sum += g * x[e];
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -381,7 +410,8 @@ hipError_t run_whole(const gdn_attn_config *cfg, const TileArgs &a, hipStream_t 
 template <typename T, int D, Keys kKeys>
 hipError_t run_parts(const gdn_attn_config *cfg, const TileArgs &a, int tt, hipStream_t stream) {
   dim3 grid, join;
-  if (!flat_grid((int64_t)a.slots * (cfg->h / a.share) * a.splits, 512, grid) ||
+  const int64_t parts = a.by_keys > 0 ? a.by_keys : (int64_t)a.slots * a.splits;
+  if (!flat_grid(parts * (cfg->h / a.share), 512, grid) ||
       !flat_grid(((int64_t)cfg->t_max * cfg->h + 3) / 4, 256, join))
     return hipErrorInvalidValue;
   if constexpr (kKeys != Keys::kRows) {
@@ -395,7 +425,13 @@ hipError_t run_parts(const gdn_attn_config *cfg, const TileArgs &a, int tt, hipS
   if (kKeys == Keys::kShared) return hipGetLastError();  // the caller joins them
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attn_tile_join_kernel<T, D>), join, dim3(256), 0, stream, a, tt, kPartRows);
+  if constexpr (kKeys == Keys::kPages) {
+    if (a.by_keys > 0) {
+      hipLaunchKernelGGL((attn_tile_join_kernel<T, D, true>), join, dim3(256), 0, stream, a, tt, kPartRows);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((attn_tile_join_kernel<T, D, false>), join, dim3(256), 0, stream, a, tt, kPartRows);
   return hipGetLastError();
 }
 
@@ -448,7 +484,7 @@ constexpr int kTwoKeys = 2048;
 // sequences of 128 tokens on 2500 keys 165 us against 144, 64 of 32 on 1250: 130 against
 // 96). Beyond, sequence s starts at slot floor(cu[s] / tt) + s, which is distinct for
 // every tile of the batch and grows with s, and is found by a search.
-TileShape tile_shape(const gdn_attn_config *cfg, Keys keys) {
+TileShape tile_shape(const gdn_attn_config *cfg, Keys keys, bool k8) {
   TileShape s;
   const int group = cfg->h / cfg->hkv;
   s.share = group < kMostShare ? group : kMostShare;
@@ -475,6 +511,17 @@ TileShape tile_shape(const gdn_attn_config *cfg, Keys keys) {
   if (n > longest / kSplitKeys) n = longest / kSplitKeys;
   s.splits = n < 1 ? 1 : n > kMostSplits ? kMostSplits : static_cast<int>(n);
   if (keys != Keys::kShared && cfg->n_max > kMostTiled) s.splits = 1;
+  // Codes: the parts go by the sequences' keys, in as many work-groups as CUs, twice as many
+  // where the tiles alone are more than half of that (us, equal parts against parts by keys:
+  // 4 sequences of 8 tokens on 15000 to 60000 keys 61.6, 53.6; 16 of 16 on 1000 to 4000 35.6,
+  // 33.8; 16 of 77 on 750 to 3000, heads of 256, 107, 104; one of 512 tokens on 8192 88.8,
+  // 89.8. Twice the CUs throughout: 4 of 8 63, 16 of 16 43; once throughout: 16 of 77 124).
+  s.by_keys = 0;
+  if (k8 && keys == Keys::kPages && s.splits > 1) {
+    const int64_t groups = cfg->h / s.share;
+    const int64_t wgs = (tiles * 2 > cu_count() ? 2 : 1) * cu_count() / groups;
+    s.by_keys = static_cast<int>(wgs > s.slots ? wgs : s.slots);
+  }
   if (s.splits > 1 || keys == Keys::kShared) return s;
   s.waves = cfg->d == 256 || cfg->t_max / cfg->n_max >= kLongPrompt ? 8 : 4;
   s.rows = 32 * s.waves;
@@ -484,15 +531,17 @@ TileShape tile_shape(const gdn_attn_config *cfg, Keys keys) {
 
 int64_t tile_part_rows(const gdn_attn_config *cfg, const TileShape &s, Keys keys) {
   if (s.splits == 1 && keys != Keys::kShared) return 0;
+  if (s.by_keys > 0) return (int64_t)s.by_keys * (cfg->h / s.share) * s.rows;
   return (int64_t)s.slots * (cfg->h / s.share) * s.splits * s.rows;
 }
 
 hipError_t launch_attn_tiles(const gdn_attn_config *cfg, Keys keys, TileArgs a, hipStream_t stream) {
   if (cfg->t_max == 0) return hipSuccess;
-  const TileShape s = tile_shape(cfg, keys);
+  const TileShape s = tile_shape(cfg, keys, a.k_scales != nullptr);
   a.share = s.share;
   a.splits = s.splits;
   a.slots = s.slots;
+  a.by_keys = s.by_keys;
   if (cfg->dtype == GDN_BF16)
     return cfg->d == 128 ? run_of<__bf16, 128>(cfg, keys, a, s, stream)
                          : run_of<__bf16, 256>(cfg, keys, a, s, stream);

@@ -32,6 +32,9 @@ __device__ __forceinline__ u32x2 tr_read(Lds<T> tile, int at) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(tile + at)));
 }
 
+// Parts by keys: at most so many of a tile (one per lane of the join), of at least so many keys.
+constexpr int kMostParts = 64, kLeastKeys = 256;
+
 // Head group, tile slot and split of a work-group. The last (longest) tiles come
 // first. Unsplit, with a multiple of 8 groups, neighbouring groups (which may read
 // the same keys) go to one XCD, whose L2 then holds their keys and values; the
@@ -310,23 +313,60 @@ struct Rows {
 // The tile of a work-group: its heads and sequence, the sequence's rows and keys, the
 // tile's first token, and the part of its keys.
 struct Where {
-  int group, slot, split, s, qb, lq, kb, lk, q0, past;
+  int group, slot, split, splits, s, qb, lq, kb, lk, q0, past;
   int past_cache;  // pages read once, and too large in all for the caches
   // one value per wave, which the compiler does not see by itself
   __device__ __forceinline__ Where uniform_() const {
-    return {uniform(group), uniform(slot), uniform(split), uniform(s),  uniform(qb),
-            uniform(lq),    uniform(kb),   uniform(lk),    uniform(q0), uniform(past),
+    return {uniform(group), uniform(slot), uniform(split), uniform(splits), uniform(s),  uniform(qb),
+            uniform(lq),    uniform(kb),   uniform(lk),    uniform(q0),     uniform(past),
             uniform(past_cache)};
   }
 };
 // key_bytes: of a key and its value, of one key head.
-template <Keys kKeys, bool kSplit, int kThreads>
+// kByKeys: the tile's parts go by its sequence's keys (TileArgs::by_keys), and slot is the
+// part's number in its head group.
+template <Keys kKeys, bool kSplit, int kThreads, bool kByKeys = false>
 __device__ __forceinline__ bool find(const TileArgs &a, int tt, int key_bytes, int tid, Where &t,
                                      int (&lds)[kThreads / 64][2]) {
+  if constexpr (kByKeys) {
+    const int groups = a.h / a.share, wg = flat_block(), lane = tid & 63;
+    t.slot = wg / groups;
+    t.group = wg - t.slot * groups;
+    t.past_cache = 0;
+    Tiled p;
+    int first;
+    auto in = [&](const auto &batch) {
+      t.past_cache = batch.past_cache(a.hkv * key_bytes);
+      return batch.in_parts(
+          lane, a.by_keys, kMostParts, kLeastKeys,
+          [&](const Tiled &x, int first, int parts) {
+            return t.slot >= first && t.slot < first + (x.n + tt - 1) / tt * parts;
+          },
+          p, first, t.splits);
+    };
+    auto keys = [&](int i, int(&o)[2]) {
+      o[0] = 0;
+      o[1] = kv_of(a.pg, i);
+    };
+    if (!(a.n_max <= 64 ? in(TiledBatch<1>(a.cu_q, a.n_max, a.t_max, tt, lane, keys))
+                        : in(TiledBatch<4>(a.cu_q, a.n_max, a.t_max, tt, lane, keys))))
+      return false;
+    const int i = t.slot - first, tile = i / t.splits;
+    t.split = i - tile * t.splits;
+    t.q0 = tile * tt;
+    t.s = p.s;
+    t.qb = p.b;
+    t.lq = p.n;
+    t.kb = 0;
+    t.lk = p.extra[1];
+    t.past = t.lk - t.lq;
+    return true;
+  }
   const Place at = place(flat_block(), a.h / a.share, a.slots, a.splits);
   t.group = at.group;
   t.slot = at.slot;
   t.split = at.split;
+  t.splits = a.splits;
   t.past_cache = 0;
   if (at.slot < 0) return false;  // past the grid's count (last row)
   if constexpr (kKeys == Keys::kShared) {

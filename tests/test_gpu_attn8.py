@@ -363,6 +363,11 @@ PAGED = [
     ([8] * 9, [900 + 40 * i for i in range(9)], 8, 1, 128, 16, 400),   # four, behind a prefix
     ([8] * 9, [900 + 40 * i for i in range(9)], 16, 2, 256, 64, 400),  # and items of two row tiles
     ([1, 1], [90, 3], 2048, 1, 128, 16, 0),                            # very many heads
+    # tiles with as many parts as their keys ask for: none to many, of more sequences than lanes too
+    ([40, 0, 3, 64, 1], [2600, 900, 64, 300, 5], 8, 2, 128, 16, 0),
+    ([70, 33], [3100, 40], 12, 2, 256, 32, 0),
+    ([9 + i % 9 if i % 7 else 0 for i in range(70)], [20 + 45 * i for i in range(70)], 8, 1, 128, 64, 0),
+    ([60 + i for i in range(12)], [2100 + i % 5 * 300 for i in range(12)], 8, 2, 128, 128, 0),
 ]
 
 
@@ -553,6 +558,27 @@ def test_paged8_indexes_that_name_nothing_stay_inside():
             for kv in ([32, 31, 20, 2_000_000_000, 0], [-4, 1000, 32, 32, 32]):
                 gdn.gdn_attn_paged8(cfg, q, *pools, ints(cu), ints(kv), wide, sh, buf[4:4 + T], workspace(cfg))
                 assert (buf[:4] == MARK).all() and (buf[4 + T:] == MARK).all()
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_paged8_indexes_that_name_nothing_stay_inside_of_tiles_in_parts(d):
+    t, h, hkv, page, n, T, pages, cols = torch.bfloat16, 8, 1, 16, 3, 150, 3, 60
+    c = Cache8([page * pages], hkv, d, page, t, 2, spare=0)
+    pools = c.on()
+    table = np.arange(n * cols, dtype=np.int32).reshape(n, cols) % 7 - 2
+    table[1, ::5], table[2, ::3] = 2_000_000_000, -2_000_000_000
+    buf = torch.full((T + 8, h, d), MARK, dtype=t, device=DEV)
+    q = normal(3, T, h, d).to(DEV)
+    cfg = gdn.make_attn_config(T, n, h, hkv, d, t, page_size=page, n_pages=pages, max_pages=cols)
+    size = gdn.gdn_attn_paged8_workspace_size(cfg)
+    assert size > 256  # parts
+    for cu in ([0, 70, 80, 150], [0, 150, 0, 150], [0, 2_000_000_000, -5, 150], [7, 150, 149, 60]):
+        for kv in ([960, 900, 3], [-4, 2_000_000_000, 500], [2_000_000_000] * 3):
+            ws = torch.full((size + 512,), 0x55, dtype=torch.uint8, device=DEV)
+            gdn.gdn_attn_paged8(cfg, q, *pools, ints(cu), ints(kv), ints(table), None, buf[4:4 + T],
+                                ws[256:256 + size])
+            assert (buf[:4] == MARK).all() and (buf[4 + T:] == MARK).all()
+            assert (ws[:256] == 0x55).all() and (ws[256 + size:] == 0x55).all()
 
 
 @pytest.mark.parametrize("d", [128, 256])

@@ -126,6 +126,9 @@ __device__ __forceinline__ void norm_rope_row(float (&x)[8], const Channels<kPai
       }
     } else {
       if (in) {
+        // (formed ahead of the branch, the partners' addresses would take registers that six
+        // waves per SIMD do not have: 67 us instead of 53)
+        asm volatile("");
         const float *wp = weights();
         const T *values = row();
 #pragma unroll

@@ -260,6 +260,8 @@ __global__ __launch_bounds__(kAppendThreads, 4) void attn_append8_kernel(FrontAr
         }
         m = max_row<kLanes>(m);
         if (li == 0) most[pass & 1][at + kRows * u] = in ? m : 0.f;
+        // (here by now: after the barrier another wave of the head may write a new one)
+        asm volatile("" : "+v"(before[u]));
       }
       lds_barrier();
       if (row0 < 0) continue;

@@ -12,8 +12,12 @@
 // where a block's e grows, its rows by the new e are exact but for codes that get
 // subnormal: they are read, rounded and written again by the wave that appends.
 //
-// HBM-bound. A work-group takes the call's tokens of one block, 16 at most: so the block's
-// scale is its own, found in registers and LDS, without atomics and the same from run to run.
+// HBM-bound where there are many tokens (32768 of 16 + 2 + 2 heads of 256: 133 us, 4.8 TB/s,
+// where a large copy reaches 5.1; 2500 of 40 sequences, 32 + 4 + 4 heads of 128: 14.7, 3.3);
+// one token for each of 256 sequences takes 7.6, the latency of finding the sequence, its
+// page, the block's scale and rows, one after the other. A work-group takes the call's
+// tokens of one block, 16 at most: so the block's scale is its own, found in registers and
+// LDS, without atomics and the same from run to run.
 // It goes through the heads in passes of 16 rows, D / 8 lanes and eight channels a lane, the
 // next pass's loads in flight: first k and v, a pass having the rows of one head (of 16 /
 // P heads, where P, the power of two that holds the tokens, is less than 16), then q
@@ -28,7 +32,12 @@ namespace {
 
 constexpr int kAppendThreads = 256;
 constexpr int kBlock = 16;  // positions that share a scale
-constexpr int kPartPasses = 4;
+// Passes of a work-group where several share a block. What comes before the first pass is paid
+// for by each, so as many as leave four work-groups per CU, within these limits (us with 2,
+// 4, 6 and 8 throughout: 1024 tokens of 8 sequences, 16 + 2 + 2 heads of 256: 10.2, 13.4,
+// 16.4, 19.2; 512 of one, 32 + 8 + 8 of 128: 7.4, 9.1, 11.2, 13.8; 2500 of 40 sequences 20.7,
+// 16.9, 14.7, 15.3; 32768 of four 133, 133, 133, 141).
+constexpr int kLeastPasses = 2, kMostPasses = 6;
 
 // Largest finite value of the cache: the largest number of four significant bits that the
 // 16-bit type holds, so that whoever reads the cache in that type finds no infinity.
@@ -344,14 +353,16 @@ void run_of(const FrontArgs &a, bool interleaved, dim3 grid, hipStream_t stream)
 
 hipError_t launch_attn_append8(const gdn_attn_config *cfg, FrontArgs a, hipStream_t stream) {
   if (cfg->t_max == 0) return hipSuccess;
-  // a block is shared by several work-groups, down to kPartPasses passes apiece, until there
-  // are many per CU (32768 tokens of 20 heads of 256 in one part 153 us, 2: 141, 3 to 5: 133;
-  // 2500 tokens of 40 heads of 128 in one 33, in ten 18)
+  // a block is shared by several work-groups until there are many per CU (32768 tokens of 20
+  // heads of 256 in one part 153 us, 2: 141, 3 to 5: 133; 2500 tokens of 40 heads of 128 in
+  // one 33, in six 14.7)
   const int64_t each = (cfg->t_max + cfg->n_max - 1) / cfg->n_max;  // tokens of an average sequence
   const int64_t blocks = cfg->n_max * ((each + kBlock - 1) / kBlock);
   const int64_t passes = ((each < kBlock ? each : kBlock) * (cfg->h + 2 * cfg->hkv) + kBlock - 1) / kBlock;
+  const int64_t share = blocks * passes / (4 * cu_count());
+  const int64_t least = share < kLeastPasses ? kLeastPasses : share > kMostPasses ? kMostPasses : share;
   int64_t parts = 32 * cu_count() / blocks;
-  if (parts > passes / kPartPasses) parts = passes / kPartPasses;
+  if (parts > passes / least) parts = passes / least;
   a.parts = parts > 1 ? (int)parts : 1;
   // where all of them run at once, the parts with k and v, which take longer, come first (the
   // 2500 tokens 18 -> 16; the 32768 would go from 133 to 138)

@@ -865,7 +865,7 @@ def append_paged_kv(qkv, heads, cu_seqlens, kv_lens, block_table, k_pages, v_pag
     if k_scales is not None or v_scales is not None:
         _both_scales(k_scales, v_scales)
         gdn_kv_append8(*front, *axes, *cache, k_scales, v_scales)
-    elif axes != (None, None):
+    elif positions is not None or pair_axis is not None:
         gdn_kv_append_axes(*front, *axes, *cache)
     else:
         gdn_kv_append(*front, *cache)

@@ -100,7 +100,9 @@ __device__ __forceinline__ int opaque(int x) {
   return x;
 }
 
-// The lane's number, formed where it is asked for: what goes by it costs no register along a loop.
+// The lane's number, formed where it is asked for: what goes by it costs no register along a loop
+// (tiles of 8-bit codes with heads of 256, whose reads ahead spilled without: 16 sequences of
+// 77 tokens on 2000 keys 131 -> 107 us, a chunk of 2048 on 9000 388 -> 329).
 __device__ __forceinline__ int fresh_lane() {
   int x;
   asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(x));
@@ -451,9 +453,8 @@ __device__ __forceinline__ Prefix shared_prefix(const PagedBatch &a, int tid,
 
 // ---- an 8-bit cache: e4m3 codes, one exponent byte for 16 positions of a page and key head
 
-// Codes per 16-byte word pair and their values: two codes of a word (the lower or the upper)
-// times 2^(e - 127), in the 16-bit type; the conversion takes the scale's exponent, so this
-// is exact as far as the type reaches.
+// Two codes of a word (the lower or the upper) times 2^(e - 127), in the 16-bit type; the
+// conversion takes the scale's exponent, so this is exact as far as the type reaches.
 template <typename T, bool kUpper>
 __device__ __forceinline__ uint32_t values2(uint32_t codes, float scale) {
   if constexpr (__is_same(T, _Float16))
@@ -484,7 +485,9 @@ __device__ __forceinline__ rsrc_t uniform_rsrc(const void *p, int bytes) {
 // Page of position `key` of sequence s (uniform both) in two halves, so that a loop can ask for
 // it ahead: the table's word through the vector caches, and the page as an index into the pool
 // whatever the table says. Scalar loads come back in any order, so that reads of LDS beside one
-// in flight are all waited for together; these are counted.
+// in flight are all waited for together; these are counted (with the descriptors in scalar
+// registers 4 sequences of 8 tokens on 46000 keys 91 -> 63 us). The streaming kernel, which reads
+// no LDS in its loop, keeps scalar look-ups (263 us against 276).
 __device__ __forceinline__ int page_word(const PagedBatch &a, int s, int key) {
   const rsrc_t row = uniform_rsrc(a.table + (int64_t)s * a.max_pages, a.max_pages * 4);
   return __builtin_amdgcn_raw_buffer_load_b32(row, (key >> a.page_shift) * 4, 0, 0);

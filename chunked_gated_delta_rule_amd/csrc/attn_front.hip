@@ -35,7 +35,8 @@ constexpr int kMostTokens = 2;
 //
 // kAxes: positions of several axes come with the tokens, one axis for each pair of channels.
 // They and the pairs' axes are asked for with the first rows, and without a cache no sequence
-// is searched for.
+// is searched for: 8192 tokens of 40 heads of 128 35 us (4.8 TB/s), 512 of 18 of 256 5.9, as
+// with one position per token; 24000 of 24 of 128 into pages 64 (4.7 TB/s).
 template <typename T, int D, Pairs kPairs, bool kCache, bool kAxes>
 __global__ __launch_bounds__(kFrontThreads, 6) void attn_front_kernel(FrontArgs a) {
   constexpr int kLanes = D / 8;                    // lanes per head

@@ -659,19 +659,25 @@ _SCALES = (torch.float8_e8m0fnu, torch.uint8)
 
 
 def _bytes_at(x, name, types, elems, dev, last):
-    if x.__class__ is int or x is None:
+    if x is None or x.__class__ is int:
         return x
+    if x.dtype in types and x.get_device() == dev and x.is_contiguous() and \
+            x.numel() >= elems and x.size(-1) == last:
+        return x.data_ptr()
     if x.dtype not in types:
         raise ValueError(f"{name}: dtype {x.dtype}, {types[0]} or {types[1]} expected")
     return _at(x, name, x.dtype, elems, dev, last)
 
 
 def _cache8_args(cfg, k_pages, v_pages, k_scales, v_scales, dev):
-    rows, d, blocks = cfg.n_pages * cfg.hkv * cfg.page_size, cfg.d, cfg.page_size // 16
-    return (_bytes_at(k_pages, "k_pages", _CODES, rows * d, dev, d),
-            _bytes_at(v_pages, "v_pages", _CODES, rows * d, dev, d),
-            _bytes_at(k_scales, "k_scales", _SCALES, rows // 16, dev, blocks),
-            _bytes_at(v_scales, "v_scales", _SCALES, rows // 16, dev, blocks))
+    size, d = cfg.page_size, cfg.d
+    blocks = size // 16
+    scales = cfg.n_pages * cfg.hkv * blocks
+    codes = scales * 16 * d
+    return (_bytes_at(k_pages, "k_pages", _CODES, codes, dev, d),
+            _bytes_at(v_pages, "v_pages", _CODES, codes, dev, d),
+            _bytes_at(k_scales, "k_scales", _SCALES, scales, dev, blocks),
+            _bytes_at(v_scales, "v_scales", _SCALES, scales, dev, blocks))
 
 
 def gdn_kv_append8(cfg, qkv, q_w, k_w, inv_freq, positions, pair_axis, cu_seqlens, kv_lens,

@@ -263,6 +263,22 @@ def test_append8_token_by_token(t, d):
 
 
 @pytest.mark.parametrize("t", TYPES)
+def test_append8_of_several_sequences_into_blocks_of_one_page(t):
+    """Sequences may share a page, as long as each block is written by one of them."""
+    h, hkv, d, page = 2, 2, 128, 64
+    lens, kv = [5, 16, 1, 9], [16, 32, 40, 64]
+    c = Cache8([64], hkv, d, page, t, 19)
+    c.table = np.repeat(c.table[:1, :1], 4, 0)
+    x = normal(20, sum(lens), (h + 2 * hkv) * d, dtype=t, scale=3.0)
+    cfg = gdn.make_attn_config(sum(lens), 4, h, hkv, d, t, page_size=page, n_pages=c.n_pages, max_pages=1)
+    say(f"append8, blocks of one page {t}")
+    pools = run_append(cfg, c, x.to(DEV), None, None, cu_of(lens), kv, None, None)
+    rows = f64(x).reshape(sum(lens), -1, d)
+    check_append(c, pools, rows, lens, kv, cu_of(lens), rows[:, h:h + hkv],
+                 np.zeros((sum(lens), hkv, d)), top_of(t))
+
+
+@pytest.mark.parametrize("t", TYPES)
 def test_append8_at_the_ends_of_the_types(t):
     """Zeros, the largest and the smallest numbers, NaN and infinities, single tokens and
     several, beside rows that a block had."""
@@ -846,6 +862,44 @@ def test_a_captured_decode_step_replays_with_other_lengths():
         torch.cuda.synchronize()
         assert torch.equal(o, o2) and torch.equal(q, q2), i
         assert all(torch.equal(a.view(torch.uint8), b) for a, b in zip(pools, other)), i
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_captured_tiles_in_parts_replay_with_other_lengths(d):
+    """How many parts a tile's keys are cut in goes by lengths on the device: one capture
+    serves uneven, empty and short sequences, and a workspace of any content."""
+    t, h, hkv, page, n, T, cols = torch.bfloat16, 8, 2, 32, 5, 120, 90
+    rng = np.random.Generator(np.random.PCG64(9))
+    c = Cache8([cols * page] * n, hkv, d, page, t, 6, extra_cols=0)
+    pools, table = c.on(), on(c.table)
+    cfg = gdn.make_attn_config(T, n, h, hkv, d, t, page_size=page, n_pages=c.n_pages, max_pages=cols)
+    q, o = (torch.zeros(T, h, d, dtype=t, device=DEV) for _ in range(2))
+    cu, kv = on(cu_of([24] * n)), ints([100] * n)
+    ws = workspace(cfg)
+    args = (cfg, q, *pools, cu, kv, table, None)
+    gdn.gdn_attn_paged8(*args, o, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gdn.gdn_attn_paged8(*args, o, ws)
+    for i, (new, full) in enumerate([([24] * n, [2880] * n), ([100, 0, 3, 16, 1], [2880, 7, 900, 16, 300]),
+                                     ([1, 1, 1, 1, 80], [5, 2880, 600, 0, 2500]), ([0] * n, [0] * n),
+                                     ([17, 40, 16, 20, 27], rng.integers(30, 2880, n))]):
+        cu.copy_(on(cu_of(new)))
+        kv.copy_(ints(full))
+        q.copy_(normal(70 + i, T, h, d, dtype=t))
+        say(f"captured tiles in parts d={d} {new}")
+        o.fill_(MARK)
+        graph.replay()
+        torch.cuda.synchronize()
+        for s in range(n):
+            at = slice(sum(new[:s]), sum(new[:s + 1]))
+            k, v = c.rows(s, int(full[s]))
+            check_attention(o[at], f64(q[at]), k, v, d ** -0.5, t)
+        assert (o[sum(new):] == MARK).all()
+        o2 = torch.full_like(o, MARK)
+        gdn.gdn_attn_paged8(*args, o2, torch.zeros_like(ws))
+        assert torch.equal(o, o2)
 
 
 @pytest.mark.parametrize("d", [128, 256])

@@ -1,0 +1,152 @@
+"""Launch shapes of the append to an 8-bit cache that only many tokens reach, each test
+asserting the one its sizes take. Bounds: attn8_helpers.py."""
+
+import numpy as np
+import pytest
+import torch
+
+import attn8_shapes
+import chunked_gated_delta_rule_amd as gdn
+from attn8_helpers import bytes_of, check_codes, top_of
+from attn_helpers import DEV, TYPES, cu_of, f64, on
+from oracle import attention, cache8
+
+pytestmark = pytest.mark.gpu
+
+
+def say(msg):
+    print(msg, flush=True)
+
+
+def ints(x):
+    return on(np.asarray(x, np.int32))
+
+
+def cus():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+# ---------------------------------------------------------------- append: long prompts
+
+LONG = [
+    # tokens, older ones of each sequence; h, hkv, d, page, rot, axes; parts, past the caches
+    ([9007, 6600, 16, 17145], [5, 0, 33, 300], 16, 2, 256, 64, 64, 0, 3, True),
+    ([14000, 1, 16003], [7, 30, 2], 32, 4, 128, 32, 128, 3, 4, True),
+    ([11001, 13000], [0, 21], 16, 2, 128, 16, 66, 0, 3, False),
+]
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("lens,past,h,hkv,d,page,rot,axes,parts,past_cache", LONG)
+def test_append8_of_long_prompts(t, lens, past, h, hkv, d, page, rot, axes, parts, past_cache):
+    """Blocks numbered eight at a time with several work-groups each, q and k stored past the
+    caches or not: q and k are the 16-bit pass's, the cache is what calls of 1600 tokens (other
+    parts, all blocks numbered together) leave, and sampled blocks are the oracle's."""
+    T, n = sum(lens), len(lens)
+    full = [a + b for a, b in zip(lens, past)]
+    cu = cu_of(lens)
+    need = [-(-x // page) for x in full]
+    table = np.full((n, max(need)), -1, np.int32)
+    order, at = np.random.Generator(np.random.PCG64(4)).permutation(sum(need)), 0
+    for i, u in enumerate(need):
+        table[i, :u] = order[at:at + u]
+        at += u
+
+    def cfg_of(tokens, seqs):
+        return gdn.make_attn_config(tokens, seqs, h, hkv, d, t, rot_dim=rot, page_size=page, n_pages=at,
+                                    max_pages=table.shape[1])
+
+    shape = attn8_shapes.append8(cfg_of(T, n), cus())
+    assert (shape.parts, shape.group, shape.past_cache) == (parts, 8, past_cache), shape
+    small = attn8_shapes.append8(cfg_of(1600, 1), cus())
+    assert small.whole and small.parts != parts and not small.past_cache, small
+    say(f"long append8 {t} T={T} h={h} hkv={hkv} d={d} axes={axes} {shape}")
+
+    g = torch.Generator(device=DEV).manual_seed(T + d)
+    x = torch.randn(T, (h + 2 * hkv) * d, device=DEV, generator=g)
+    x = (x * torch.exp2(torch.randint(-3, 4, (T, 1), device=DEV, generator=g).float())).to(t)
+    w = 1.0 + 0.3 * torch.randn(d, device=DEV, generator=g)
+    f = gdn.rope_inv_freq(rot).to(DEV)
+    places = torch.randint(0, 100000, (axes, T), device=DEV, generator=g, dtype=torch.int32) if axes else None
+    axis = (torch.arange(rot // 2) % axes).int().to(DEV) if axes else None
+    # (rows that the first blocks have: any codes but NaN)
+    codes = torch.randint(0, 127, (at, hkv, page, d), device=DEV, generator=g, dtype=torch.uint8)
+    scales = torch.randint(110, 118, (at, hkv, page // 16), device=DEV, generator=g, dtype=torch.uint8)
+    before = [codes, codes.flip(0).contiguous(), scales, scales.flip(0).contiguous()]
+    whole, pieces = ([y.clone() for y in before] for _ in range(2))
+    kw = dict(inv_freq=f, output_k=True, pair_axis=axis)
+    q, k = gdn.append_paged_kv(x, h, on(cu), ints(full), on(table), *whole[:2], w, w, k_scales=whole[2],
+                               v_scales=whole[3], positions=places, **kw)
+    q2, k2 = gdn.qk_norm_rope(x, h, hkv, on(cu), w, w, f, kv_lens=None if axes else ints(full),
+                              positions=places, pair_axis=axis)
+    assert torch.equal(q, q2) and torch.equal(k, k2)
+    del q2, k2
+    for s in range(n):
+        p = past[s]
+        while p < full[s]:
+            end = min((p // 16 + 100) * 16, full[s])
+            a, b = (int(cu[s]) + y - past[s] for y in (p, end))
+            qs, ks = gdn.append_paged_kv(x[a:b], h, on(cu_of([b - a])), ints([end]), on(table[s:s + 1]),
+                                         *pieces[:2], w, w, k_scales=pieces[2], v_scales=pieces[3],
+                                         positions=places[:, a:b].contiguous() if axes else None, **kw)
+            assert torch.equal(q[a:b], qs) and torch.equal(k[a:b], ks)
+            p = end
+    assert all(torch.equal(a, b) for a, b in zip(whole, pieces))
+
+    # blocks of the oracle: each sequence's first and last, and some between
+    rng = np.random.Generator(np.random.PCG64(5))
+    w64, f64_, top = f64(w), f64(f), top_of(t)
+    for s in range(n):
+        first, last = past[s] // 16, (full[s] - 1) // 16
+        for b in sorted({first, last, *rng.integers(first, last + 1, 6).tolist()}):
+            lo, hi = max(16 * b, past[s]), min(16 * b + 16, full[s])
+            rows = slice(int(cu[s]) + lo - past[s], int(cu[s]) + hi - past[s])
+            xs = f64(x[rows]).reshape(hi - lo, -1, d)
+            if axes:
+                want, mag = cache8.norm_rope_axes(xs[:, h:h + hkv], w64, f64(places[:, rows]), axis.cpu().numpy(),
+                                                  f64_, 1e-6)
+            else:
+                want, mag = attention.norm_rope(xs[:, h:h + hkv], w64, np.arange(lo, hi), f64_, 1e-6)
+            page_, r0 = int(table[s, 16 * b // page]), 16 * b % page
+            for i, y in ((0, want), (1, xs[:, h + hkv:])):
+                one = [bytes_of(z[i][page_:page_ + 1]).copy() for z in (before, whole)]
+                sc = [bytes_of(z[2 + i][page_:page_ + 1]).copy() for z in (before, whole)]
+                cache8.append(one[0], sc[0], [0], r0 + lo - 16 * b, y, top)
+                assert np.array_equal(sc[0][..., r0 // 16], sc[1][..., r0 // 16])
+                new = slice(r0 + lo - 16 * b, r0 + hi - 16 * b)
+                if i:
+                    assert np.array_equal(one[0][0, :, r0:new.stop], one[1][0, :, r0:new.stop])
+                else:
+                    assert np.array_equal(one[0][0, :, r0:new.start], one[1][0, :, r0:new.start])
+                    e = np.broadcast_to(sc[0][0, :, r0 // 16], (hi - lo, hkv))
+                    check_codes(one[1][0, :, new].transpose(1, 0, 2), e, np.clip(y, -top, top), mag)
+    torch.cuda.empty_cache()
+
+
+def test_append8_of_the_most_tokens_and_sequences_gives_q_and_k():
+    """t_max = 2^24 rows and n_max = 16384 sequences, most of them without a page: q and k of every
+    row are the 16-bit pass's."""
+    t, d, h, hkv, page = torch.bfloat16, 128, 1, 1, 256
+    T, n = gdn.GDN_T_MAX_LIMIT, gdn.GDN_N_MAX_LIMIT
+    cfg = gdn.make_attn_config(T, n, h, hkv, d, t)
+    shape = attn8_shapes.append8(cfg, cus())
+    assert shape.group == 8 and shape.parts == 1 and shape.past_cache
+    say(f"append8 of {T} rows, {n} sequences {shape}")
+    cu = np.linspace(0, T, n + 1).astype(np.int64)
+    x = torch.randint(-2 ** 15, 2 ** 15, (T, 3 * d), device=DEV, dtype=torch.int16).view(t)
+    x = torch.where(x.isfinite(), x, torch.ones((), dtype=t, device=DEV))
+    f, w = gdn.rope_inv_freq(64).to(DEV), torch.full((d,), 1.5, device=DEV)
+    table = np.full((n, 1), -1, np.int32)
+    table[-2:, 0] = 1, 0
+    kv = np.diff(cu) - 700  # the first rows' positions are below zero
+    pools = [torch.zeros(2, hkv, page, d, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    scales = [torch.zeros(2, hkv, page // 16, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    cud, kvd = on(cu.astype(np.int32)), ints(kv)
+    q, k = gdn.append_paged_kv(x, h, cud, kvd, on(table), *pools, w, w, f, output_k=True,
+                               k_scales=scales[0], v_scales=scales[1])
+    q2, k2 = gdn.qk_norm_rope(x, h, hkv, cud, w, w, f, kvd)
+    assert torch.equal(q.view(torch.int16), q2.view(torch.int16))
+    assert torch.equal(k.view(torch.int16), k2.view(torch.int16))
+    assert all(p.any(-1).sum() == 2 * 256 for p in pools)
+    del x, q, k, q2, k2
+    torch.cuda.empty_cache()

@@ -683,7 +683,9 @@ def _cache8_args(cfg, k_pages, v_pages, k_scales, v_scales, dev):
 def gdn_kv_append8(cfg, qkv, q_w, k_w, inv_freq, positions, pair_axis, cu_seqlens, kv_lens,
                    block_table, q, k, k_pages, v_pages, k_scales, v_scales, stream=None):
     """gdn_kv_append into 8-bit pages: e4m3 codes [n_pages, hkv, page_size, d] and scales (e8m0)
-    [n_pages, hkv, page_size / 16]; positions and pair_axis may be None (one axis)."""
+    [n_pages, hkv, page_size / 16]; positions and pair_axis may be None (one axis). A scale only
+    grows until its block begins anew: what a rejected draft leaves, and what sequences that
+    share a partly filled block see, is said in include/gdn.h."""
     dev, t, d, cols, hkv = _dev(qkv, k_pages), _GDN_DTYPE.get(cfg.dtype), cfg.d, cfg.max_pages, cfg.hkv
     n = cfg.t_max * d
     front = _front_args(cfg, qkv, q_w, k_w, inv_freq, cu_seqlens, kv_lens, t, dev)
@@ -851,8 +853,9 @@ def append_paged_kv(qkv, heads, cu_seqlens, kv_lens, block_table, k_pages, v_pag
     sequence in all, these included). positions (int32 [axes, T]) with pair_axis
     (rope_pair_axis): rotation by positions of several axes. k_scales, v_scales
     (float8_e8m0fnu or uint8 [pages, kv_heads, page_size / 16]): the pages hold 8-bit
-    numbers (float8_e4m3fn or uint8; gdn_kv_append8). Returns q [T, heads, d], or (q, k)
-    with output_k."""
+    numbers (float8_e4m3fn or uint8; gdn_kv_append8), and a large value, a rejected draft's
+    too, coarsens the small ones of its block of 16 positions. Returns q [T, heads, d], or
+    (q, k) with output_k."""
     pages, hkv, size, d = _pages(k_pages, v_pages, block_table)
     T, dq = _packed_qkv(qkv, heads, hkv)
     if dq != d:

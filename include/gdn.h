@@ -498,9 +498,19 @@ gdn_status gdn_kv_append_axes(const gdn_attn_config *cfg, const void *qkv, int64
  *   rows that the block had, if its scale grew: their values by the new scale, rounded again
  *       (exact but for codes that get subnormal, below 2^-6)
  * So e only grows while a block fills, and a block whose first position is written begins
- * anew whatever it held. Values past the largest number of four significant bits of the 16-bit
- * type (61440, 1.875 * 2^127) count as that; NaN and infinities are stored as NaN and
- * count for nothing in a.
+ * anew whatever it held. Two things follow that a 16-bit cache does not know:
+ *   A token that is taken back (a rejected draft) leaves the scale that it asked for: the
+ *   block's other rows, and those written after it, are multiples of 2^(e - 136) by that e.
+ *   Each growth to e moves a row that is there by 2^(e - 137) at most (2^-17 of the largest
+ *   value that asked for it). A caller that wants the cache as if the draft had never been
+ *   keeps the codes of the 16 rows and the scale of the block in which it begins, of every
+ *   key head, puts them back, and appends the accepted tokens again. (Where the draft begins
+ *   a block, there is nothing to keep: appending again begins it anew.)
+ *   An append to a partly filled block may round its rows again for every sequence whose
+ *   table has its page. Sequences that are to read the same numbers whatever the others
+ *   append share full blocks only, or copy the last one.
+ * Values past the largest number of four significant bits of the 16-bit type (61440, 1.875 *
+ * 2^127) count as that; NaN and infinities are stored as NaN and count for nothing in a.
  *   Scales of blocks that a call appends to must be at most 253 (the library writes 15 ..
  *   247). Two sequences of one call must not write to the same block. Tokens without a place
  *   in the cache are left out as in gdn_kv_append. q, k (nullable): 16-bit, as there. */

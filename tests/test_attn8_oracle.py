@@ -124,3 +124,30 @@ def test_rope_pair_axis_refuses():
     for bad in ((), (1, -1)):
         with pytest.raises(ValueError, match="sections"):
             gdn.rope_pair_axis(bad)
+
+
+def test_a_growing_scale_moves_a_row_by_half_its_smallest_step():
+    """Rows of a block, then others of any size: each growth to e moves what is there by
+    2^(e - 137) at most, which is below 2^-17 of the value that asked for it; and a block that
+    is put back and appended to again is what it would have been."""
+    moved = 0
+    for seed in range(8):
+        rng = np.random.Generator(np.random.PCG64(seed))
+        codes, scales = np.zeros((1, 1, 16, 64), np.uint8), np.zeros((1, 1, 1), np.uint8)
+        top, at = 1.875 * 2.0 ** 127, 0
+        while at < 15:
+            n = min(int(rng.integers(1, 4)), 16 - at)
+            x = rng.standard_normal((n, 1, 64)) * 2.0 ** rng.integers(-4, 12)
+            was, old = cache8.values(codes, scales)[0, 0, :at], scales.copy()
+            kept = codes.copy()
+            cache8.append(codes, scales, [0], at, x, top)
+            off, e = np.abs(cache8.values(codes, scales)[0, 0, :at] - was), int(scales[0, 0, 0])
+            if at and e > old[0, 0, 0]:
+                assert np.all(off <= 2.0 ** (e - 137)) and 2.0 ** (e - 137) < 2.0 ** -17 * np.abs(x).max()
+                moved += np.any(off > 0)
+            else:
+                assert not off.any()
+            cache8.append(kept, old, [0], at, x, top)
+            assert np.array_equal(kept, codes) and np.array_equal(old, scales)
+            at += n
+    assert moved

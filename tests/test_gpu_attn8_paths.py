@@ -1,5 +1,6 @@
 """Launch shapes of the append to an 8-bit cache that only many tokens reach, each test
-asserting the one its sizes take. Bounds: attn8_helpers.py."""
+asserting the one its sizes take; and the cache after a draft that is taken back. Bounds:
+attn8_helpers.py."""
 
 import numpy as np
 import pytest
@@ -7,8 +8,8 @@ import torch
 
 import attn8_shapes
 import chunked_gated_delta_rule_amd as gdn
-from attn8_helpers import bytes_of, check_codes, top_of
-from attn_helpers import DEV, TYPES, cu_of, f64, on
+from attn8_helpers import Cache8, bytes_of, check_codes, top_of
+from attn_helpers import DEV, TYPES, cu_of, f64, normal, on
 from oracle import attention, cache8
 
 pytestmark = pytest.mark.gpu
@@ -150,3 +151,70 @@ def test_append8_of_the_most_tokens_and_sequences_gives_q_and_k():
     assert all(p.any(-1).sum() == 2 * 256 for p in pools)
     del x, q, k, q2, k2
     torch.cuda.empty_cache()
+
+
+# ---------------------------------------------------------------- append: drafts that are taken back
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("had", [5, 14, 16])
+def test_append8_after_a_rejected_draft(t, d, had):
+    """Of eight draft tokens three are accepted; the fifth was large. Its mark on the accepted
+    rows is less than the smallest step of the block's grown scale, and the block put back as it
+    was takes it away to the bit (one that begins with a draft token begins anew by itself)."""
+    h, hkv, page, draft, keep, more = 2, 2, 32, 8, 3, 2
+    c = Cache8([had], hkv, d, page, t, 31, extra_cols=2)
+    c.table[0, :2] = np.random.Generator(np.random.PCG64(1)).permutation(c.n_pages)[:2]
+    x = normal(32, had + draft + more, (h + 2 * hkv) * d, dtype=t)
+    x[had + 4] *= 1000.0
+    say(f"rejected draft {t} d={d} had={had}")
+
+    def append(pools, rows, kv):
+        y = x[rows].to(DEV)
+        gdn.append_paged_kv(y, h, on(cu_of([len(y)])), ints([kv]), on(c.table), *pools[:2],
+                            k_scales=pools[2], v_scales=pools[3])
+
+    def start():
+        pools = [p.view(torch.uint8) for p in c.on()]
+        append(pools, slice(0, had), had)
+        return pools
+
+    accepted, later = slice(had, had + keep), slice(had + draft, None)
+    end = had + keep + more
+    plain = start()  # the draft never was
+    append(plain, accepted, had + keep)
+    append(plain, later, end)
+    marked = start()
+    append(marked, slice(had, had + draft), had + draft)
+    append(marked, later, end)
+    undone = start()
+    page_, row = int(c.table[0, had // page]), had % page // 16 * 16
+    blocks = [p[page_, :, row:row + 16] for p in undone[:2]] + [p[page_, :, row // 16] for p in undone[2:]]
+    saved = [b.clone() for b in blocks]
+    append(undone, slice(had, had + draft), had + draft)
+    for b, s in zip(blocks, saved):
+        b.copy_(s)
+    append(undone, accepted, had + keep)
+    append(undone, later, end)
+
+    def rows_of(pools):
+        c.k, c.v, c.ks, c.vs = (bytes_of(p) for p in pools)
+        return c.rows(0, end), [np.stack([e[c.table[0, p // page], :, p % page // 16] for p in range(end)])
+                                for e in (c.ks, c.vs)]
+
+    (pk, pv), _ = rows_of(plain)
+    (uk, uv), _ = rows_of(undone)
+    assert np.array_equal(pk, uk) and np.array_equal(pv, uv)
+    (mk, mv), es = rows_of(marked)
+    differ = False
+    for a, b, e in zip((pk, pv), (mk, mv), es):
+        # In steps of the smallest kind by the grown scale: a row that was there is off by half a
+        # step. An accepted row has its nearest multiple of a step, half a step off, where the
+        # step is larger than that of the number nearest to it alone, which is at most half a step
+        # apart (from four steps on; a quarter off): three quarters in all.
+        step = np.exp2(e.astype(np.float64) - 136.0)[..., None]
+        old = slice(0, had + keep)
+        assert np.all(np.abs(a - b)[old] <= 0.75 * step[old])
+        assert np.all(e[had + 4] >= 127)  # the large token's scale stays
+        differ = differ or not np.array_equal(a, b)
+    assert differ

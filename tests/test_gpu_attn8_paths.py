@@ -1,15 +1,17 @@
-"""Launch shapes of the append to an 8-bit cache that only many tokens reach, each test
-asserting the one its sizes take; and the cache after a draft that is taken back. Bounds:
-attn8_helpers.py."""
+"""The 8-bit cache where long prompts, drafts that are taken back and keys that are not finite
+lead: launch shapes of the append that only many tokens reach, each test asserting the one its
+sizes take; the cache after a rejected draft; NaN in codes and scales of keys. Bounds:
+attn_helpers.py, attn8_helpers.py."""
 
 import numpy as np
 import pytest
 import torch
 
 import attn8_shapes
+import attn_shapes
 import chunked_gated_delta_rule_amd as gdn
 from attn8_helpers import Cache8, bytes_of, check_codes, top_of
-from attn_helpers import DEV, TYPES, cu_of, f64, normal, on
+from attn_helpers import DEV, TYPES, check_attention, cu_of, f64, normal, on, widened
 from oracle import attention, cache8
 
 pytestmark = pytest.mark.gpu
@@ -218,3 +220,59 @@ def test_append8_after_a_rejected_draft(t, d, had):
         assert np.all(e[had + 4] >= 127)  # the large token's scale stays
         differ = differ or not np.array_equal(a, b)
     assert differ
+
+
+# ---------------------------------------------------------------- attention: keys that are not finite
+
+NAN = [
+    # where; new tokens, tokens in all; h, hkv, d, page, shared; whether keys are streamed
+    ("tokens", [1, 1], [9000, 700], 8, 2, 128, 16, 0, True),
+    ("tokens", [5, 3], [300, 77], 4, 2, 256, 32, 0, True),
+    ("tokens", [1, 2, 1], [900, 950, 1200], 16, 2, 256, 16, 700, True),
+    ("prefix", [1, 2, 1], [900, 950, 1200], 16, 2, 256, 16, 700, True),
+    ("tokens", [300, 120], [700, 333], 8, 2, 128, 16, 0, False),
+    ("tokens", [140], [4000], 4, 2, 256, 64, 0, False),
+    ("tokens", [60], [3000], 8, 2, 128, 128, 0, False),
+]
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("what", ["code", "scale"])
+@pytest.mark.parametrize("where,new,full,h,hkv,d,page,shared,streams", NAN)
+def test_paged8_of_keys_that_are_not_finite(t, what, where, new, full, h, hkv, d, page, shared, streams):
+    """NaN in a key's code, or 255 as the scale of a block of keys, of one key head, among the
+    last sequence's new tokens or in the prefix of all: the rows that see such a key are NaN in
+    that head's group, all others the oracle's; a key that the row's mask hides does nothing."""
+    c = Cache8(full, hkv, d, page, t, 7, shared)
+    n, T, last = len(new), sum(new), len(new) - 1
+    q = normal(8, T, h, d, dtype=t)
+    rows = [c.rows(s) for s in range(n)]  # before
+    at = 5 if where == "prefix" else full[last] - 1 - new[last] // 2
+    if what == "code":
+        c.k[c.table[last, at // page], 0, at % page, 3] = 255
+        first = at
+    else:
+        c.ks[c.table[last, at // page], 0, at % page // 16] = 255
+        first = at // 16 * 16
+    table = widened(c.table, -(-(1 << 28) // (2 * n * hkv * d * page))) if shared else c.table
+    cfg = gdn.make_attn_config(T, n, h, hkv, d, t, page_size=page, n_pages=c.n_pages, max_pages=table.shape[1],
+                               shared_max=table.shape[1] * page if shared else 0)
+    assert shared or attn_shapes.streams(cfg) == streams
+    say(f"NaN in keys {what} {t} {new} {full} d={d} shared={shared}")
+    kp, vp, ks, vs = c.on()
+    cu = cu_of(new)
+    o = gdn.paged_attention(q.to(DEV), kp, vp, on(cu), ints(full), on(table), ints([shared]) if shared else None,
+                            k_scales=ks, v_scales=vs)
+    G = h // hkv
+    for s in range(n):
+        a = o[int(cu[s]):int(cu[s + 1])]
+        qs, (k, v) = f64(q[int(cu[s]):int(cu[s + 1])]), rows[s]
+        hit = (full[s] - new[s] + np.arange(new[s]) >= first) & (s == last or where == "prefix")
+        assert a[torch.from_numpy(hit).to(DEV)][:, :G].isnan().all()
+        want = attention.attend(qs, k, v, d ** -0.5)
+        clean = np.broadcast_to(~hit[:, None], (new[s], h)).copy()
+        clean[:, G:] = True
+        pick = torch.from_numpy(clean).to(DEV)
+        assert a[pick].isfinite().all()
+        fixed = torch.where(pick[..., None], a, torch.from_numpy(want[0]).to(DEV).to(t))
+        check_attention(fixed, qs, k, v, d ** -0.5, t, want)

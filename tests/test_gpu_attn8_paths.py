@@ -1,7 +1,7 @@
 """The 8-bit cache where long prompts, drafts that are taken back and keys that are not finite
 lead: launch shapes of the append that only many tokens reach, each test asserting the one its
-sizes take; the cache after a rejected draft; NaN in codes and scales of keys. Bounds:
-attn_helpers.py, attn8_helpers.py."""
+sizes take; the cache after a rejected draft; NaN in codes and scales of keys; and the call
+against the 16-bit one on the same numbers. Bounds: attn_helpers.py, attn8_helpers.py."""
 
 import numpy as np
 import pytest
@@ -11,7 +11,8 @@ import attn8_shapes
 import attn_shapes
 import chunked_gated_delta_rule_amd as gdn
 from attn8_helpers import Cache8, bytes_of, check_codes, top_of
-from attn_helpers import DEV, TYPES, check_attention, cu_of, f64, normal, on, widened
+from attn_helpers import (DEV, TYPES, check_attention, cu_of, f64, half_step, normal, on, score_error,
+                          widened)
 from oracle import attention, cache8
 
 pytestmark = pytest.mark.gpu
@@ -276,3 +277,35 @@ def test_paged8_of_keys_that_are_not_finite(t, what, where, new, full, h, hkv, d
         assert a[pick].isfinite().all()
         fixed = torch.where(pick[..., None], a, torch.from_numpy(want[0]).to(DEV).to(t))
         check_attention(fixed, qs, k, v, d ** -0.5, t, want)
+
+
+# ---------------------------------------------------------------- attention: against 16-bit pages
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("new,full,h,hkv,d", [([1, 1, 1], [70, 900, 3000], 16, 2, 128),
+                                              ([5, 2], [600, 77], 8, 2, 256),
+                                              ([200, 130], [700, 900], 8, 2, 128),
+                                              ([300], [2000], 16, 2, 256)])
+def test_paged8_is_near_the_16_bit_call_row_by_row(t, new, full, h, hkv, d):
+    """On the same numbers either call is off by its bound (attn_helpers.py) at most: the two
+    differ by no more than both, value by value."""
+    c = Cache8(full, hkv, d, 32, t, 23)
+    q = normal(1, sum(new), h, d, dtype=t)
+    kp, vp, ks, vs = c.on()
+    say(f"8 and 16 bits row by row {t} {new} d={d}")
+    cu = cu_of(new)
+    batch = (on(cu), ints(full), on(c.table))
+    o = gdn.paged_attention(q.to(DEV), kp, vp, *batch, k_scales=ks, v_scales=vs)
+    wide = [(x.float() * s.float().repeat_interleave(16, 2)[..., None]).to(t) for x, s in ((kp, ks), (vp, vs))]
+    o16 = gdn.paged_attention(q.to(DEV), *wide, *batch)
+    u = half_step(t)
+    for s in range(len(new)):
+        a = slice(int(cu[s]), int(cu[s + 1]))
+        qs, (k, v) = f64(q[a]), c.rows(s)
+        want, mag, total = attention.attend(qs, k, v, d ** -0.5)
+        bound = 1.01 * (u * np.abs(want) + (u + 2 * score_error(qs, k, d, d ** -0.5) + 2.0 ** -18) * mag)
+        if t == torch.float16:
+            bound = bound + len(k) * 2.0 ** -25 * np.abs(v).max() / total[..., None] + 2.0 ** -25
+        off = np.abs(f64(o[a]) - f64(o16[a]))
+        say(f"  off / bound {np.max(off / (2 * bound)):.3f}")
+        assert np.all(off <= 2 * bound)

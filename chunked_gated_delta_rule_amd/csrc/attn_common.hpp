@@ -486,7 +486,7 @@ __device__ __forceinline__ rsrc_t uniform_rsrc(const void *p, int bytes) {
 // it ahead: the table's word through the vector caches, and the page as an index into the pool
 // whatever the table says. Scalar loads come back in any order, so that reads of LDS beside one
 // in flight are all waited for together; these are counted (with the descriptors in scalar
-// registers 4 sequences of 8 tokens on 46000 keys 91 -> 63 us). The streaming kernel, which reads
+// registers 4 sequences of 8 tokens on 43000 keys 91 -> 63 us). The streaming kernel, which reads
 // no LDS in its loop, keeps scalar look-ups (263 us against 276).
 __device__ __forceinline__ int page_word(const PagedBatch &a, int s, int key) {
   const rsrc_t row = uniform_rsrc(a.table + (int64_t)s * a.max_pages, a.max_pages * 4);

@@ -32,7 +32,7 @@
 //    16-bit values where it is used, two by an instruction. V's block is 8 keys x D / 16
 //    dims a lane, transposed as bytes before. The bytes halve and the vector unit's work
 //    grows by the conversions: 256 sequences of about 2500 keys 242 us (5.5 TB/s; 16-bit
-//    422), one token on 1000 keys 13.3, 128 tokens behind 8192 shared positions 65.
+//    422), one token on 1000 keys 12.9, 128 tokens behind 8192 shared positions 66.
 #include "attn_common.hpp"
 #include "attn_launch.hpp"
 

@@ -200,7 +200,7 @@ __global__ __launch_bounds__(512, 2) void attn_part_kernel(TileArgs a) {
   const int col = lane & 31, hh = lane >> 5;
   // The wave's rows: 32 from 32 rg on. Over codes the second set has them the other way round:
   // waves w and w + 4 share a SIMD, and a tile that is half full then keeps all four busy (4
-  // sequences of 8 tokens, 64 rows each, on 46000 keys 88 -> 83 us when this was built).
+  // sequences of 8 tokens, 64 rows each, on 43000 keys 88 -> 83 us when this was built).
   const int rg = k8 && set ? 3 - w : w;
   Where t;
   const int share = a.share, tt = kBM / share;

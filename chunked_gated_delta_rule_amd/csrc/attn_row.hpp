@@ -127,7 +127,8 @@ __device__ __forceinline__ void norm_rope_row(float (&x)[8], const Channels<kPai
     } else {
       if (in) {
         // (formed ahead of the branch, the partners' addresses would take registers that six
-        // waves per SIMD do not have: 67 us instead of 53)
+        // waves per SIMD do not have: 8192 tokens of 40 heads of 128, rot_dim 34, from HBM 98 us
+        // instead of 79)
         asm volatile("");
         const float *wp = weights();
         const T *values = row();

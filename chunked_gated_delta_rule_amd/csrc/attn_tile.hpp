@@ -514,9 +514,11 @@ __device__ __forceinline__ void get(const TileArgs &a, const Where &t,
 // has one scale. In registers, as only they can turn codes into values; so each code is
 // turned once for the 128 or 256 rows of a tile, and the products read what they read of a
 // 16-bit cache. The conversions and the writes (two of 16 bytes per load) cost a full tile
-// 5 to 10 % (a chunk of 2048 tokens on 9000 keys 284 us against 268 to 287 over 16-bit
-// pages, with heads of 256 329 against 302); half the bytes pay where keys are many and
-// rows few (4 sequences of 8 tokens on 46000 keys 54 against 81).
+// nothing that is seen with heads of 128 (a chunk of 2048 tokens on 8003 keys, back to back, 256
+// us against 255 over 16-bit pages; the first passes after a pause 283 and 285), and a sixth
+// with heads of 256 (312 against 268; 362 and 299), whose registers then leave no reads ahead.
+// Half the bytes pay where keys are many and rows few (4 sequences of 8 tokens on 43000 keys
+// 61 against 80).
 template <typename T, int D, int kBN, int kWaves>
 struct Codes {
   static constexpr int kPass = 1024 * kWaves;  // bytes the waves load at a time

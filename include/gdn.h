@@ -532,6 +532,8 @@ gdn_status gdn_kv_append8(const gdn_attn_config *cfg, const void *qkv, int64_t q
  *   cu_q, cu_k (device) int32 [n_max + 1]; cu_k NULL = cu_q
  *   o (device) [t_max, h, d], dense: valid rows written
  *   workspace (device) >= gdn_attn_workspace_size bytes, 256-byte aligned.
+ * Scores, maxima and sums are fp32; the weights are rounded to the 16-bit type for their
+ * products with v (half a step each), and so is the result, once (here and below).
  * A value that is not finite in k or v reaches at most the rows of its own
  * sequence (in v, also those whose weight for it is 0). A row whose every score
  * is -inf gives zeros, like one that sees no key. */
